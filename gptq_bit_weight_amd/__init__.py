@@ -20,7 +20,7 @@ from typing import Optional
 
 __all__ = [
     "Q4Matrix", "Q4Error", "load_library", "library_path", "check_shape", "plan_actorder",
-    "plan_gemv", "plan_gemv_gather", "plan_gemm", "PATH_NONE", "PATH_GEMV", "PATH_MFMA", "GEMV_MAX_M", "EXPORTED_SYMBOLS",
+    "plan_gemv", "plan_gemv_gather", "plan_gemm", "Rotary", "PagedCache", "PATH_NONE", "PATH_GEMV", "PATH_MFMA", "GEMV_MAX_M", "EXPORTED_SYMBOLS",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -41,6 +41,7 @@ EXPORTED_SYMBOLS = (
     "q4_matmul_bf16", "q4_matmul_ex_bf16", "q4_dequant_dump_bf16", "q4_make_bits", "q4_make_cat_bits",
     "q4_handle_bits", "q4_check_shape_bits", "q4_plan_gemm", "q4_plan_gemm_waves", "q4_read_probe",
     "q4_matmul_static",
+    "q4_rotary_make", "q4_rotary_free", "q4_rotary_plan", "q4_rotary_apply", "q4_cache_append",
 )
 
 _lib = None
@@ -118,6 +119,16 @@ def load_library():
     lib.q4_plan_gemm_waves.restype = I
     lib.q4_read_probe.argtypes = [P, ctypes.c_size_t, P, P]
     lib.q4_read_probe.restype = I
+    L, F = ctypes.c_int64, ctypes.c_double
+    lib.q4_rotary_make.argtypes = [I, I, I, I, F, F, I, F, F]
+    lib.q4_rotary_make.restype = P
+    lib.q4_rotary_free.argtypes = [P]
+    lib.q4_rotary_free.restype = None
+    lib.q4_rotary_plan.argtypes = [I, I, I, F, F, I, F, F, P, P]
+    lib.q4_rotary_apply.argtypes = [P, P, L, L, P, L, L, P, I, I, I, I, I, P]
+    lib.q4_cache_append.argtypes = [P, P, L, L, P, L, L, P, I, I, P, P, I, P, L, L, P, L, L, I, P]
+    for f in (lib.q4_rotary_plan, lib.q4_rotary_apply, lib.q4_cache_append):
+        f.restype = I
     _lib = lib
     return lib
 
@@ -432,3 +443,15 @@ class Q4Matrix:
             self.close()
         except Exception:
             pass
+
+
+_ATTENTION = ("Rotary", "PagedCache")
+
+
+def __getattr__(name):
+    # (torch is imported with the classes that work on its tensors, not with
+    # the package, whose host-only part needs none)
+    if name in _ATTENTION:
+        from . import attention
+        return getattr(attention, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,291 @@
+"""Rotary positions, a paged cache of keys and values, and attention of new
+tokens over it: what a decoder layer needs between its quantized
+projections.
+
+    rope = q4.Rotary(dim, scaling=dict(kind="linear", factor=8.0))
+    cache = q4.PagedCache(k_pages, v_pages)          # [pages, kv heads, page size, dim]
+    q = cache.append(k, v, slots, rotary=rope, positions=positions, q=q)
+    o = cache.attend(q, starts, lengths, table)
+
+Like the rest of the binding this only checks tensors and passes pointers and
+a HIP stream to the C ABI (``include/q4.h``).
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _check, _raise, load_library
+
+__all__ = ["Rotary", "PagedCache"]
+
+LAYOUTS = {"half": 0, "interleaved": 1}
+SCALINGS = {"none": 0, "linear": 1, "base": 2, "by_parts": 3}
+_SCALING_KEYS = {"none": set(), "linear": {"factor"}, "base": {"factor"},
+                 "by_parts": {"factor", "original_length", "low", "high"}}
+_HALVES = (torch.float16, torch.bfloat16)
+
+
+class _Cache(ctypes.Structure):
+    """q4_cache of include/q4.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_stride", ctypes.c_int64 * 3),
+                ("v_stride", ctypes.c_int64 * 3), ("pages", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("dim", ctypes.c_int), ("bf16", ctypes.c_int)]
+
+
+def _heads(t, name, device, dtype=None, tokens=None, heads=None, dim=None):
+    """Check a [tokens, heads, dim] tensor whose head values are dense."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _HALVES or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype or 'float16 or bfloat16'}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    s = t.shape
+    if len(s) != 3 or (tokens is not None and s[0] != tokens) or (heads is not None and s[1] != heads) \
+            or (dim is not None and s[2] != dim):
+        want = [("tokens" if tokens is None else tokens), ("heads" if heads is None else heads),
+                ("dim" if dim is None else dim)]
+        raise ValueError(f"{name} must be {want}, got {list(s)}")
+    if t.stride(2) != 1 and s[2] > 1:
+        raise ValueError(f"{name}: the values of a head must be contiguous")
+    return t
+
+
+def _index(t, name, device, n):
+    """Check an index vector of n int32 or int64; returns its width in bits."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    bits = 64 if t.dtype == torch.int64 else 32
+    if bits == 32 and t.dtype != torch.int32:
+        raise ValueError(f"{name} must be int32 or int64, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape [{n}], got {list(t.shape)}")
+    return bits
+
+
+def _distinct(t, name):
+    """An output's elements must be distinct places in memory."""
+    span = 1
+    for size, stride in sorted(zip(t.shape, t.stride()), key=lambda p: p[1]):
+        if size > 1:
+            if stride < span:
+                raise ValueError(f"{name} overlaps itself")
+            span = stride * (size - 1) + span
+
+
+def _overlap(a, b):
+    """Whether the address ranges of two tensors meet."""
+    def ends(t):
+        n = 1 + sum((s - 1) * st for s, st in zip(t.shape, t.stride()))
+        return t.data_ptr(), t.data_ptr() + n * t.element_size()
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+    (a0, a1), (b0, b1) = ends(a), ends(b)
+    return a0 < b1 and b0 < a1
+
+
+def _out_like(x, out, name, stream):
+    """The output for x: `out` checked, or a new dense tensor made on the
+    stream that the call runs on."""
+    if out is None:
+        if stream is None:
+            return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _heads(out, name, x.device, x.dtype, *x.shape)
+    _distinct(out, name)
+    same = out.data_ptr() == x.data_ptr() and out.stride() == x.stride()
+    if not same and _overlap(out, x):
+        raise ValueError(f"{name} overlaps its input without being the same view")
+    return out
+
+
+def _call(fn, what, device, stream, args, used=()):
+    """Call a C function on `stream` (the device's current one by default)."""
+    if stream is None:
+        sp = torch.cuda.current_stream(device).cuda_stream
+    else:
+        if stream.device != device:
+            raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on {device}")
+        sp = stream.cuda_stream
+        for t in used:          # their memory stays until the stream is done with it
+            t.record_stream(stream)
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, sp)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, sp)
+    if st:
+        _check(st, what)
+
+
+class _Rotate(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, rotary, positions, transpose, stream):
+        ctx.save_for_backward(positions)
+        ctx.rotary, ctx.transpose, ctx.stream = rotary, transpose, stream
+        return rotary._rotate(x.detach(), positions, transpose, None, stream)
+
+    @staticmethod
+    def backward(ctx, grad):
+        positions, = ctx.saved_tensors
+        if grad.stride(2) != 1:
+            grad = grad.contiguous()
+        return ctx.rotary._rotate(grad, positions, not ctx.transpose, None, ctx.stream), None, None, None, None
+
+
+class Rotary:
+    """Rotary positions for heads of `dim` values (at most 512) whose first
+    `rot` (default all) are rotated: pairs (i, i + rot/2) (layout "half") or
+    (2i, 2i + 1) ("interleaved"), pair i by base^(-2i / rot) radians a position.
+
+    scaling: None, or a dict with "kind" and
+      "linear": factor -- every frequency divided by it;
+      "base": factor -- base times factor^(rot / (rot - 2));
+      "by_parts": factor, original_length, low, high -- pairs that turn at least
+        `high` times in original_length positions keep their frequency, those
+        under `low` turns are divided by factor, a ramp between; the result is
+        multiplied by 0.1 ln(factor) + 1.
+
+    Positions are int32 or int64 of any sign; angles are exact modulo a turn.
+    The table lives on `device` (default: the current one).
+    """
+
+    def __init__(self, dim: int, rot: int | None = None, *, layout: str = "half", base: float = 10000.0,
+                 scaling: dict | None = None, device=None):
+        self._h = None
+        if layout not in LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(LAYOUTS)}, got {layout!r}")
+        s = dict(scaling or {"kind": "none"})
+        kind = s.pop("kind", None)
+        if kind not in SCALINGS:
+            raise ValueError(f"scaling kind must be one of {sorted(SCALINGS)}, got {kind!r}")
+        if set(s) != _SCALING_KEYS[kind]:
+            raise ValueError(f"scaling {kind!r} takes {sorted(_SCALING_KEYS[kind])}, got {sorted(s)}")
+        self.dim, self.rot = int(dim), int(dim if rot is None else rot)
+        self.layout = layout
+        lib = load_library()
+        args = (self.dim, self.rot, SCALINGS[kind], base, s.get("factor", 1.0), s.get("original_length", 0),
+                s.get("low", 0.0), s.get("high", 0.0))
+        # (the arguments' own checks need no device)
+        turns, mag = (ctypes.c_uint64 * 256)(), ctypes.c_float(1.0)
+        _check(lib.q4_rotary_plan(*args, turns, ctypes.byref(mag)), "Rotary")
+        self.magnitude = float(mag.value)
+        dev = torch.device("cuda" if device is None else device)
+        self.device = torch.device(dev.type, torch.cuda.current_device()) if dev.index is None else dev
+        with torch.cuda.device(self.device):
+            h = lib.q4_rotary_make(self.dim, self.rot, LAYOUTS[layout], *args[2:])
+        if not h:
+            _raise(lib.q4_last_status(), "q4_rotary_make")
+        self._h = ctypes.c_void_p(h)
+
+    def _handle(self):
+        if self._h is None:
+            raise ValueError("Rotary is closed")
+        return self._h
+
+    def _rotate(self, x, positions, transpose, out, stream):
+        dev = self.device
+        _heads(x, "x", dev, None, None, None, self.dim)
+        T, H, _ = x.shape
+        bits = _index(positions, "positions", dev, T)
+        out = _out_like(x, out, "out", stream)
+        xs, os_ = x.stride(), out.stride()
+        _call(load_library().q4_rotary_apply, "q4_rotary_apply", dev, stream,
+              (self._handle(), x.data_ptr(), xs[0], xs[1], out.data_ptr(), os_[0], os_[1], positions.data_ptr(), bits,
+               T, H, 1 if transpose else 0, 1 if x.dtype == torch.bfloat16 else 0), (x, positions, out))
+        return out
+
+    def rotate(self, x, positions, *, transpose: bool = False, out=None, stream=None):
+        """x [tokens, heads, dim] (float16 or bfloat16, any token and head
+        strides) turned by positions [tokens]; with `transpose` the other way
+        with the same factor: the gradient's pass. fp32, rounded once. out may
+        be x itself. Without `out` the call is differentiable in x."""
+        if out is None and isinstance(x, torch.Tensor) and x.requires_grad and torch.is_grad_enabled():
+            return _Rotate.apply(x, self, positions, transpose, stream)
+        return self._rotate(x, positions, transpose, out, stream)
+
+    def close(self):
+        if getattr(self, "_h", None) is not None:
+            torch.cuda.synchronize(self.device)
+            load_library().q4_rotary_free(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class PagedCache:
+    """Keys and values in pages: two tensors [pages, kv heads, page size, dim]
+    (float16 or bfloat16, any strides of the first three dimensions, dense
+    values), which stay the caller's and are written in place."""
+
+    def __init__(self, k, v):
+        for t, nm in ((k, "k"), (v, "v")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{nm} must be a torch.Tensor")
+            if t.dtype not in _HALVES:
+                raise ValueError(f"{nm} must be float16 or bfloat16, got {t.dtype}")
+            if t.dim() != 4 or 0 in t.shape:
+                raise ValueError(f"{nm} must be [pages, kv heads, page size, dim], got {list(t.shape)}")
+            if t.stride(3) != 1 and t.shape[3] > 1:
+                raise ValueError(f"{nm}: the values of a row must be contiguous")
+            if t.device.type != "cuda":
+                raise ValueError(f"{nm} must be on the GPU, got {t.device}")
+            _distinct(t, nm)
+        if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device:
+            raise ValueError("k and v must have the same shape, dtype and device")
+        self.k, self.v, self.device, self.dtype = k, v, k.device, k.dtype
+        self.pages, self.kv_heads, self.page_size, self.dim = (int(n) for n in k.shape)
+        if self.pages * self.page_size > 2 ** 31 - 1:
+            raise NotImplementedError("more than 2^31 - 1 rows in the cache")
+        self._c = _Cache(k.data_ptr(), v.data_ptr(), (ctypes.c_int64 * 3)(*k.stride()[:3]),
+                         (ctypes.c_int64 * 3)(*v.stride()[:3]), self.pages, self.kv_heads, self.page_size,
+                         self.dim, 1 if k.dtype == torch.bfloat16 else 0)
+        self._ref = ctypes.byref(self._c)
+
+    def append(self, k, v, slots, *, rotary=None, positions=None, q=None, q_out=None, stream=None):
+        """Write the keys (turned by `rotary` at `positions`, copied without
+        it) and values [tokens, kv heads, dim] of new tokens to rows slots
+        [tokens]: slot s is row s % page_size of page s // page_size; a slot
+        outside the cache (-1 for padding) is not written. With q [tokens,
+        heads, dim], returns it turned too (in q_out, which may be q)."""
+        dev, dt, D, kv = self.device, self.dtype, self.dim, self.kv_heads
+        _heads(k, "k", dev, dt, None, kv, D)
+        T = k.shape[0]
+        _heads(v, "v", dev, dt, T, kv, D)
+        sb = _index(slots, "slots", dev, T)
+        pb, pp, rh, qa = 32, None, None, (None, 0, 0, None, 0, 0, 0)
+        used = (k, v, slots)
+        if rotary is not None:
+            if rotary.dim != D:
+                raise ValueError(f"rotary turns heads of {rotary.dim} values, the cache has {D}")
+            if rotary.device != dev:
+                raise ValueError(f"rotary is on {rotary.device}, the cache on {dev}")
+            if positions is None:
+                raise ValueError("positions are needed with rotary")
+            pb, pp, rh = _index(positions, "positions", dev, T), positions.data_ptr(), rotary._handle()
+            used += (positions,)
+        if q is not None:
+            if rotary is None:
+                raise ValueError("q is given without rotary")
+            _heads(q, "q", dev, dt, T, None, D)
+            q_out = _out_like(q, q_out, "q_out", stream)
+            if q.shape[1]:
+                qs, os_ = q.stride(), q_out.stride()
+                qa = (q.data_ptr(), qs[0], qs[1], q_out.data_ptr(), os_[0], os_[1], q.shape[1])
+            used += (q, q_out)
+        elif q_out is not None:
+            raise ValueError("q_out is given without q")
+        ks, vs = k.stride(), v.stride()
+        _call(load_library().q4_cache_append, "q4_cache_append", dev, stream,
+              (self._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], slots.data_ptr(), sb, T, rh, pp, pb)
+              + qa, used if stream is None else used + (self.k, self.v))
+        return q_out

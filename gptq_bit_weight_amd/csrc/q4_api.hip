@@ -2,6 +2,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cstring>
 #include <map>
@@ -9,6 +10,7 @@
 #include <vector>
 
 #include "q4_internal.h"
+#include "q4_ops.h"
 
 // The allocation-free entry point's workspace (q4_matmul_static): one copy
 // per GPU. Host code never passes this name to a kernel or a copy; it uses
@@ -557,6 +559,22 @@ q4_status matmul_impl(const q4_matrix* h, const uint16_t* x, const uint16_t* bia
 }
 
 }  // namespace
+
+q4_status device_info(int* dev, int* num_cu)
+{
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices];   // CUs of a device that check_device has accepted
+    Q4_HIP(hipGetDevice(dev), "hipGetDevice");
+    if (*dev >= 0 && *dev < kDevices)
+        if (int n = known[*dev].load(std::memory_order_relaxed)) {
+            *num_cu = n;
+            return Q4_OK;
+        }
+    q4_status st = check_device(dev, num_cu);
+    if (st == Q4_OK && *dev >= 0 && *dev < kDevices) known[*dev].store(*num_cu, std::memory_order_relaxed);
+    return st;
+}
+
 }  // namespace q4
 
 extern "C" {

@@ -468,6 +468,86 @@ q4_status q4_plan_gemv(int M, int K, int N, int groupsize, int num_cu, int* col_
  */
 int q4_plan_gemv_gather(int M, int K, int splits);
 
+/* ------------------------------------------------------------------------
+ * Operators around the product: rotary positions, a paged cache of keys and
+ * values. All take 16-bit data: binary16 or (bf16 != 0) bfloat16 patterns.
+ * Token and head strides count values; the values of a head are dense.
+ * ---------------------------------------------------------------------- */
+
+typedef struct q4_rotary q4_rotary;   /* opaque, immutable after q4_rotary_make */
+
+#define Q4_ROTARY_MAX_DIM 512
+enum { Q4_ROTARY_HALF = 0, Q4_ROTARY_INTERLEAVED = 1 };
+enum { Q4_ROTARY_NONE = 0, Q4_ROTARY_LINEAR = 1, Q4_ROTARY_BASE = 2, Q4_ROTARY_BY_PARTS = 3 };
+
+/*
+ * q4_rotary_make -- rotary positions for heads of `dim` values (at most
+ * Q4_ROTARY_MAX_DIM) whose first `rot` (even, 2 .. dim) are rotated. With
+ * n = rot / 2, pair i is values (i, i + n) (Q4_ROTARY_HALF) or (2i, 2i + 1)
+ * (Q4_ROTARY_INTERLEAVED) and turns by w_i radians a position:
+ *   NONE      w_i = base^(-i / n)
+ *   LINEAR    w_i = base^(-i / n) / factor
+ *   BASE      the same as NONE with base * factor^(rot / (rot - 2))
+ *   BY_PARTS  w_i keep_i + w_i / factor (1 - keep_i), w_i as for NONE, where
+ *             keep_i = clamp((original_length w_i / 2 pi - low) / (high - low), 0, 1):
+ *             pairs that turn at least `high` times within the original length
+ *             keep their frequency, those below `low` turns are stretched;
+ *             the result is multiplied by 0.1 ln(factor) + 1.
+ * factor >= 1, base > 1. The table lives on the current device, on which the
+ * handle is then used. Returns NULL on error (q4_last_status/q4_last_error).
+ */
+q4_rotary* q4_rotary_make(int dim, int rot, int layout, int scaling, double base, double factor,
+                          int original_length, double low, double high);
+/* q4_rotary_free -- release it (NULL allowed); the caller has synchronized
+ * every stream that used it. */
+void q4_rotary_free(q4_rotary* r);
+
+/*
+ * q4_rotary_plan -- host-only: the checks of q4_rotary_make and its table,
+ * turns[rot / 2] = w_i / (2 pi) * 2^64 rounded, and the factor on the result.
+ */
+q4_status q4_rotary_plan(int dim, int rot, int scaling, double base, double factor, int original_length,
+                         double low, double high, uint64_t* turns, float* magnitude);
+
+/*
+ * q4_rotary_apply -- out[t][h] = rotation by positions[t] of x[t][h], or with
+ * `transpose` its transpose (the gradient of the input from the gradient of
+ * the output). Positions are device integers of 32 or 64 bits, negative ones
+ * allowed; the angle is exact modulo a turn (64-bit fixed point). fp32, one
+ * rounding. out may be x itself (same strides), else they must not overlap.
+ */
+q4_status q4_rotary_apply(const q4_rotary* r, const uint16_t* x, int64_t x_token, int64_t x_head, uint16_t* out,
+                          int64_t out_token, int64_t out_head, const void* positions, int position_bits,
+                          int tokens, int heads, int transpose, int bf16, hipStream_t stream);
+
+/*
+ * A paged cache: `pages` pages of `page_size` rows for each of `kv_heads`
+ * heads. Row r of head h of page p lies at k + p k_stride[0] + h k_stride[1]
+ * + r k_stride[2] (in values, non-negative), `dim` dense values; v likewise.
+ * Device memory is the caller's.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    int64_t k_stride[3];
+    int64_t v_stride[3];
+    int pages, kv_heads, page_size, dim, bf16;
+} q4_cache;
+
+/*
+ * q4_cache_append -- write `tokens` tokens to the cache: token t's keys
+ * (rotated by positions[t] when `rotary` is given, copied when it is NULL)
+ * and its values go to row slots[t] % page_size of page slots[t] / page_size.
+ * A token whose slot is negative or not below pages * page_size is not
+ * written; two tokens with one slot leave either's row. With q, its `heads`
+ * heads are rotated too, into q_out (which may be q itself), for every token.
+ */
+q4_status q4_cache_append(const q4_cache* c, const uint16_t* k, int64_t k_token, int64_t k_head, const uint16_t* v,
+                          int64_t v_token, int64_t v_head, const void* slots, int slot_bits, int tokens,
+                          const q4_rotary* rotary, const void* positions, int position_bits, const uint16_t* q,
+                          int64_t q_token, int64_t q_head, uint16_t* q_out, int64_t out_token, int64_t out_head,
+                          int heads, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
