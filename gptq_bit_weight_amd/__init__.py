@@ -42,6 +42,7 @@ EXPORTED_SYMBOLS = (
     "q4_handle_bits", "q4_check_shape_bits", "q4_plan_gemm", "q4_plan_gemm_waves", "q4_read_probe",
     "q4_matmul_static",
     "q4_rotary_make", "q4_rotary_free", "q4_rotary_plan", "q4_rotary_apply", "q4_cache_append",
+    "q4_attend_workspace", "q4_attend",
 )
 
 _lib = None
@@ -127,7 +128,10 @@ def load_library():
     lib.q4_rotary_plan.argtypes = [I, I, I, F, F, I, F, F, P, P]
     lib.q4_rotary_apply.argtypes = [P, P, L, L, P, L, L, P, I, I, I, I, I, P]
     lib.q4_cache_append.argtypes = [P, P, L, L, P, L, L, P, I, I, P, P, I, P, L, L, P, L, L, I, P]
-    for f in (lib.q4_rotary_plan, lib.q4_rotary_apply, lib.q4_cache_append):
+    lib.q4_attend_workspace.argtypes = [P, I]
+    lib.q4_attend_workspace.restype = ctypes.c_size_t
+    lib.q4_attend.argtypes = [P, P, L, L, I, I, P, P, P, I, L, I, I, ctypes.c_float, P, L, L, P, ctypes.c_size_t, P]
+    for f in (lib.q4_rotary_plan, lib.q4_rotary_apply, lib.q4_cache_append, lib.q4_attend):
         f.restype = I
     _lib = lib
     return lib

@@ -250,6 +250,7 @@ class PagedCache:
                          (ctypes.c_int64 * 3)(*v.stride()[:3]), self.pages, self.kv_heads, self.page_size,
                          self.dim, 1 if k.dtype == torch.bfloat16 else 0)
         self._ref = ctypes.byref(self._c)
+        self._need = {}
 
     def append(self, k, v, slots, *, rotary=None, positions=None, q=None, q_out=None, stream=None):
         """Write the keys (turned by `rotary` at `positions`, copied without
@@ -289,3 +290,88 @@ class PagedCache:
               (self._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], slots.data_ptr(), sb, T, rh, pp, pb)
               + qa, used if stream is None else used + (self.k, self.v))
         return q_out
+
+    def attend(self, q, starts, lengths, table, *, window: int = 0, scale=None, out=None, stream=None):
+        """Attention of new tokens over the cache: q [tokens, heads, dim] holds
+        the new tokens of every request one after the other, request b's are
+        rows starts[b] .. starts[b + 1] - 1 (starts int32 [requests + 1]) and
+        the last of its lengths[b] cached tokens (lengths int32 [requests]);
+        key j is row j % page_size of page table[b, j // page_size] (table int32
+        [requests, width]). A token sees the keys up to its own, with `window`
+        only the last `window` of them; one that sees none gives zeros. heads is
+        a multiple of the cached heads, scale defaults to dim ** -0.5. Lengths
+        stay on the device; nothing waits for it."""
+        dev, dt = self.device, self.dtype
+        _heads(q, "q", dev, dt, None, None, self.dim)
+        T, H, D = q.shape
+        if H % self.kv_heads or not H:
+            raise ValueError(f"q has {H} heads, the cache {self.kv_heads}")
+        for t, nm, nd in ((starts, "starts", 1), (lengths, "lengths", 1), (table, "table", 2)):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{nm} must be a torch.Tensor")
+            if t.dtype != torch.int32 or t.dim() != nd or t.device != dev:
+                raise ValueError(f"{nm} must be int32 with {nd} dimensions on {dev}, got {t.dtype} {list(t.shape)} on {t.device}")
+        B = lengths.shape[0]
+        if starts.shape[0] != B + 1 or table.shape[0] != B:
+            raise ValueError(f"starts must be [{B + 1}] and table [{B}, width], got {list(starts.shape)} and {list(table.shape)}")
+        width = table.shape[1]
+        if (B and width == 0) or (T and not B):
+            raise ValueError("table has no pages" if B else f"{T} tokens of no request")
+        if not (starts.is_contiguous() and lengths.is_contiguous()) or (width > 1 and table.stride(1) != 1):
+            raise ValueError("starts, lengths and the rows of table must be contiguous")
+        window = int(window)
+        if window < 0:
+            raise ValueError(f"window must not be negative, got {window}")
+        if q.data_ptr() % 16 or q.stride(0) % 8 or q.stride(1) % 8:
+            q = q.contiguous() if stream is None else _on(stream, q.contiguous)
+        if out is None:
+            out = _out_like(q, None, "out", stream)
+        else:
+            _heads(out, "out", dev, dt, T, H, D)
+            _distinct(out, "out")
+            if _overlap(out, q):
+                raise ValueError("out overlaps q")
+        ws = self._workspace(H, stream)
+        qs, os_ = q.stride(), out.stride()
+        _call(load_library().q4_attend, "q4_attend", dev, stream,
+              (self._ref, q.data_ptr(), qs[0], qs[1], H, T, starts.data_ptr(), lengths.data_ptr(), table.data_ptr(),
+               width, max(table.stride(0), width), B, window, D ** -0.5 if scale is None else scale, out.data_ptr(),
+               os_[0], os_[1], ws.data_ptr(), ws.numel()),
+              (q, out, starts, lengths, table, self.k, self.v))
+        return out
+
+    def _workspace(self, heads, stream):
+        """The workspace of a call: one a stream, shared by every cache, or
+        under capture one of the call's own (a graph may replay beside other
+        work of the stream it was captured on)."""
+        need = self._need.get(heads)
+        if need is None:
+            with torch.cuda.device(self.device):
+                need = load_library().q4_attend_workspace(self._ref, heads)
+            if not need:
+                _raise(load_library().q4_last_status(), "q4_attend_workspace")
+            self._need[heads] = need
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+            make = _zeros
+        else:
+            make = lambda *a: _on(stream, _zeros, *a)  # noqa: E731
+        if torch.cuda.is_current_stream_capturing():
+            return make(need, self.device)
+        key = (self.device.index, stream.cuda_stream)
+        ws = _workspaces.get(key)
+        if ws is None or ws.numel() < need:
+            ws = _workspaces[key] = make(need, self.device)
+        return ws
+
+
+_workspaces: dict = {}      # (device, stream) -> q4_attend's workspace
+
+
+def _zeros(n, device):
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _on(stream, f, *args):
+    with torch.cuda.stream(stream):
+        return f(*args)

@@ -1,0 +1,132 @@
+// C ABI of attention over a paged cache: argument checks and dispatch.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+
+#include "q4_attend.h"
+
+namespace q4 {
+
+hipError_t launch_attend_rows(const q4attend::Args& p, int row_blocks, bool bf16, bool pages_of_16, hipStream_t stream);
+
+namespace {
+
+// Workgroups of the few-row kernel: as many as the CUs hold by its LDS (66 KiB
+// at 128 values a head).
+int rows_workers(int dim, int num_cu) { return num_cu * (dim <= 64 ? 4 : dim <= 128 ? 2 : 1); }
+
+int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
+// The workspace: one arrival counter a workgroup, then the partial results.
+constexpr size_t kCounterBytes = 1 << 14;
+
+size_t rows_bytes(int dim, int row_blocks, int workers)
+{
+    return kCounterBytes + (size_t)workers * 2 * (16 * row_blocks) * (padded_dim(dim) + 2) * sizeof(float);
+}
+
+q4_status check_attend(const q4_cache* c, int heads, const char* who)
+{
+    if (q4_status st = check_cache(c, who); st != Q4_OK) return st;
+    if (c->dim % 8 || c->dim > 256)
+        return fail(Q4_ERR_UNSUPPORTED, "%s: heads of %d values (a multiple of 8, at most 256)", who, c->dim);
+    if (heads < 1 || heads % c->kv_heads)
+        return fail(Q4_ERR_INVALID_ARG, "%s: %d heads over %d cached heads", who, heads, c->kv_heads);
+    return Q4_OK;
+}
+
+bool at16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+}  // namespace
+}  // namespace q4
+
+extern "C" {
+
+size_t q4_attend_workspace(const q4_cache* c, int heads)
+{
+    int dev = -1, cu = 0;
+    if (q4::check_attend(c, heads, "q4_attend_workspace") != Q4_OK || q4::device_info(&dev, &cu) != Q4_OK) return 0;
+    return q4::rows_bytes(c->dim, 2, q4::rows_workers(c->dim, cu));
+}
+
+q4_status q4_attend(const q4_cache* c, const uint16_t* q, int64_t q_token, int64_t q_head, int heads, int tokens,
+                    const int32_t* starts, const int32_t* lengths, const int32_t* table, int table_width,
+                    int64_t table_stride, int requests, int window, float scale, uint16_t* out, int64_t out_token,
+                    int64_t out_head, void* workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    using namespace q4;
+    const char* who = "q4_attend";
+    if (q4_status st = check_attend(c, heads, who); st != Q4_OK) return st;
+    if (tokens < 0 || requests < 0 || window < 0)
+        return fail(Q4_ERR_INVALID_ARG, "%s: %d tokens, %d requests, window %d", who, tokens, requests, window);
+    if (!std::isfinite(scale)) return fail(Q4_ERR_INVALID_ARG, "%s: scale is not finite", who);
+    if (tokens == 0 || requests == 0) return Q4_OK;
+    if (!q || !starts || !lengths || !table || !out) return fail(Q4_ERR_INVALID_ARG, "%s: null pointer", who);
+    if (table_width < 1 || table_stride < table_width || table_stride > 0x7fffffff)
+        return fail(Q4_ERR_INVALID_ARG, "%s: a table of %d pages a request, %lld apart", who, table_width, (long long)table_stride);
+    const int64_t strides[] = {q_token, q_head, c->k_stride[0], c->k_stride[1], c->k_stride[2], c->v_stride[0], c->v_stride[1], c->v_stride[2]};
+    for (int64_t s : strides)
+        if (s < 0 || s % 8) return fail(Q4_ERR_UNSUPPORTED, "%s: strides of q and the cache must be multiples of 8 values", who);
+    if (!at16(q) || !at16(c->k) || !at16(c->v) || (reinterpret_cast<uintptr_t>(out) & 1))
+        return fail(Q4_ERR_UNSUPPORTED, "%s: q and the cache must be 16-byte aligned", who);
+    if (c->k_stride[2] > (1 << 25) || c->v_stride[2] > (1 << 25))
+        return fail(Q4_ERR_UNSUPPORTED, "%s: rows of a page more than 2^25 values apart", who);
+    const int g = heads / c->kv_heads;
+    if ((long long)tokens * g > (1 << 30) || (long long)heads * c->dim > (1 << 30))
+        return fail(Q4_ERR_UNSUPPORTED, "%s: %d tokens of %d heads", who, tokens, heads);
+    int dev = -1, cu = 0;
+    if (q4_status st = device_info(&dev, &cu); st != Q4_OK) return st;
+
+    q4attend::Args p = {};
+    p.q = q;
+    p.out = out;
+    p.k = static_cast<const uint16_t*>(c->k);
+    p.v = static_cast<const uint16_t*>(c->v);
+    p.starts = starts;
+    p.lengths = lengths;
+    p.table = table;
+    p.q_t = q_token;
+    p.q_h = q_head;
+    p.o_t = out_token;
+    p.o_h = out_head;
+    p.ks0 = c->k_stride[0];
+    p.ks1 = c->k_stride[1];
+    p.ks2 = (int)c->k_stride[2] * 2;
+    p.vs0 = c->v_stride[0];
+    p.vs1 = c->v_stride[1];
+    p.vs2 = (int)c->v_stride[2] * 2;
+    p.T = tokens;
+    p.B = requests;
+    p.KV = c->kv_heads;
+    p.g = g;
+    p.dim = c->dim;
+    p.chunks = c->dim / 8;
+    p.pages = c->pages;
+    p.page_size = c->page_size;
+    p.table_stride = (int)table_stride;
+    const long long rows = (long long)table_width * c->page_size;
+    p.max_len = (int)(rows < (1 << 30) ? rows : (1 << 30));
+    p.window = window;
+    p.scale = scale * 1.4426950408889634f;
+    p.store8 = (reinterpret_cast<uintptr_t>(out) % 8 == 0) && out_token % 4 == 0 && out_head % 4 == 0;
+    p.div_g = make_fastdiv((uint32_t)g);
+    p.div_page = make_fastdiv((uint32_t)c->page_size);
+    const bool bf16 = c->bf16 != 0, pg = c->page_size % 16 == 0;
+
+    const long long mean_rows = ((long long)tokens * g + requests - 1) / requests;
+    const int rb = mean_rows <= 16 ? 1 : 2;
+    const long long row_tiles = (long long)tokens * g / (16 * rb) + requests;
+    if (row_tiles * c->kv_heads * (p.max_len / 32 + 2) >= (1LL << 31))
+        return fail(Q4_ERR_UNSUPPORTED, "%s: more than 2^31 tiles of keys", who);
+    p.workers = rows_workers(c->dim, cu);
+    p.least = 4;
+    const size_t need = rows_bytes(c->dim, rb, p.workers);
+    if (!workspace || workspace_bytes < need || !at16(workspace))
+        return fail(Q4_ERR_INVALID_ARG, "%s: the workspace needs %zu bytes on a 16-byte boundary (q4_attend_workspace)", who, need);
+    p.counters = static_cast<uint32_t*>(workspace);
+    p.slots = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
+    hipError_t e = launch_attend_rows(p, rb, bf16, pg, stream);
+    return e == hipSuccess ? Q4_OK : fail(Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
+}
+
+}  // extern "C"

@@ -548,6 +548,41 @@ q4_status q4_cache_append(const q4_cache* c, const uint16_t* k, int64_t k_token,
                           int64_t q_token, int64_t q_head, uint16_t* q_out, int64_t out_token, int64_t out_head,
                           int heads, hipStream_t stream);
 
+/* Bytes of workspace q4_attend needs for this cache and number of heads on
+ * the current device, whatever the call's other sizes; 0 on error
+ * (q4_last_error). */
+size_t q4_attend_workspace(const q4_cache* c, int heads);
+
+/*
+ * q4_attend -- attention of new tokens over the cache. q holds `tokens` new
+ * tokens of `requests` requests one after the other: request b's are tokens
+ * starts[b] .. starts[b + 1] - 1 (starts: requests + 1 values, from 0 to
+ * tokens), the last of its lengths[b] cached ones (their own keys and values
+ * are in the cache already). Key j of request b is row j % page_size of page
+ * table[b table_stride + j / page_size]. `heads` is a multiple of the cached
+ * heads; head h reads cached head h / (heads / kv_heads). Token i, at position
+ * p, sees keys j <= p, with window > 0 only p - window < j:
+ *   out[i][h] = sum_j softmax_j(scale q[i][h] . k[j]) v[j]
+ * and zeros where it sees none. fp32 scores, softmax and sums; the weights
+ * are rounded to the data's type for the second product.
+ *
+ * Only rows that some token of the tile sees are read, and of the table only
+ * the entries of pages that hold them. Entries outside [0, pages), lengths above
+ * table_width * page_size and starts outside the tokens do not lead outside
+ * the tensors, but the result then has no meaning. A key or value that is not
+ * finite reaches every row whose tile of keys it is in.
+ *
+ * dim is a multiple of 8, at most 256; strides of q and the cache are
+ * multiples of 8 values, their base 16-byte aligned. `workspace` is device
+ * memory of at least q4_attend_workspace bytes whose first 16 KiB are zero before
+ * its first use (each call leaves them so); calls that share it must not overlap
+ * in time. Host and device never synchronize; the call may be captured.
+ */
+q4_status q4_attend(const q4_cache* c, const uint16_t* q, int64_t q_token, int64_t q_head, int heads, int tokens,
+                    const int32_t* starts, const int32_t* lengths, const int32_t* table, int table_width,
+                    int64_t table_stride, int requests, int window, float scale, uint16_t* out, int64_t out_token,
+                    int64_t out_head, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

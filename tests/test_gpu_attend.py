@@ -1,0 +1,329 @@
+"""Attention of new tokens over the paged cache on the GPU, against the
+definition in 64 bits.
+
+Tolerance, derived. A weight w_j = exp(s_j - max) is off by its score's error,
+twice over (its own and the sum's): a score is a fp32 sum of dim products, off
+by at most (dim + 2) 2^-24 scale sum |q k|; the exponential, the running rescales
+and the fp32 sums add a few 2^-24 each, together below 2^-18 (the longest sums
+here have some ten thousand terms, summed in tiles of 32). Each weight is then
+rounded once for the second product: eps / 2 of itself, or 2^-25 where it is
+subnormal in binary16 (the largest weight is 1, so the sum is at least 1). The result is
+rounded once: eps / 2. With A = sum w |v| / sum w:
+  |y - ref| <= eps/2 |ref| + (eps/2 + 2 delta + 2^-18) A (1 + eps) + 2^-25 sum |v| / sum w + tiny
+"""
+import math
+
+import pytest
+
+from tests.gpu_util import announce, torch_mod
+
+torch = torch_mod()
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import gptq_bit_weight_amd as q4
+    q4.load_library()
+    yield
+
+
+def reference(q, kc, vc, news, lens, table, window=0, scale=None):
+    """(result, tolerance) in float64."""
+    dt, D = q.dtype, q.shape[2]
+    kv, ps = kc.shape[1], kc.shape[2]
+    g = q.shape[1] // kv
+    scale = D ** -0.5 if scale is None else scale
+    half = torch.finfo(dt).eps / 2
+    tiny = torch.finfo(dt).smallest_normal * half
+    outs, tols, at = [], [], 0
+    for b, (n, m) in enumerate(zip(news, lens)):
+        if n == 0:
+            continue
+        qq = q[at:at + n].double()
+        at += n
+        if m == 0:
+            outs.append(torch.zeros_like(qq))
+            tols.append(torch.zeros_like(qq))
+            continue
+        need = -(-m // ps)
+        pages = table[b, :need].long().to(kc.device)
+        k, v = (c[pages].transpose(0, 1).reshape(kv, -1, D)[:, :m].double() for c in (kc, vc))
+        i, j = torch.arange(m - n, m, device=q.device)[:, None], torch.arange(m, device=q.device)[None]
+        see = j <= i
+        if window:
+            see = see & (j > i - window)
+        ys, ts = [], []
+        for h in range(q.shape[1]):
+            s = qq[:, h] @ k[h // g].t() * scale
+            mag = (qq[:, h].abs() @ k[h // g].abs().t() * abs(scale)).masked_fill(~see, 0).amax(-1, keepdim=True)
+            s = s.masked_fill(~see, -math.inf)
+            top = s.amax(-1, keepdim=True)
+            w = torch.where(see, torch.exp(s - torch.where(top.isfinite(), top, 0)), 0.0)
+            l = w.sum(-1, keepdim=True)
+            inv = torch.where(l > 0, 1 / l, 0.0)
+            y = w @ v[h // g] * inv
+            A = w @ v[h // g].abs() * inv
+            delta = (D + 2) * 2.0 ** -24 * mag
+            tol = half * y.abs() + (half + 2 * delta + 2.0 ** -18) * A * (1 + 2 * half) + tiny * (l > 0)
+            if dt == torch.float16:
+                tol = tol + 2.0 ** -25 * (see.double() @ v[h // g].abs()) * inv
+            ys.append(y)
+            ts.append(tol)
+        outs.append(torch.stack(ys, 1))
+        tols.append(torch.stack(ts, 1))
+    return torch.cat(outs), torch.cat(tols)
+
+
+def make(dt, H, kv, D, ps, news, lens, seed=0, spread=1.0, spare=3):
+    """q, caches, starts, lengths, table: pages in random order; rows that no
+    token wrote hold NaN."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    need = [-(-m // ps) for m in lens]
+    pages = sum(need) + spare
+    order = torch.randperm(pages, generator=g, device="cuda").int().cpu()
+    table = torch.full((len(lens), max(max(need), 1)), -7, dtype=torch.int32)
+    q = (torch.randn(sum(news), H, D, generator=g, device="cuda") * spread).to(dt)
+    kc = torch.randn(pages, kv, ps, D, generator=g, device="cuda").to(dt)
+    vc = torch.randn(pages, kv, ps, D, generator=g, device="cuda").to(dt)
+    written = torch.zeros(pages, ps, dtype=torch.bool)
+    at = 0
+    for b, (n, m) in enumerate(zip(need, lens)):
+        mine = order[at:at + n]
+        table[b, :n] = mine
+        at += n
+        rows = torch.arange(m)
+        written[mine.long()[rows // ps], rows % ps] = True
+    dead = ~written.cuda()
+    kc[dead[:, None].expand(-1, kv, -1)] = math.nan
+    vc[dead[:, None].expand(-1, kv, -1)] = math.nan
+    starts = torch.tensor([0] + news).cumsum(0).int().cuda()
+    return q, kc, vc, starts, torch.tensor(lens, dtype=torch.int32, device="cuda"), table.cuda()
+
+
+def check(y, ref, tol, what=""):
+    err = (y.double() - ref).abs()
+    bad = ~(err <= tol)
+    if bad.any():
+        i = tuple(bad.nonzero()[0].tolist())
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} outside, first {i}: {y[i].item()} against "
+                             f"{ref[i].item()}, tolerance {tol[i].item()}")
+
+
+def run(dt, H, kv, D, ps, news, lens, window=0, seed=0, spread=1.0, scale=None):
+    import gptq_bit_weight_amd as q4
+    announce(f"attend {dt} H={H} kv={kv} D={D} ps={ps} news={news[:8]} lens={lens[:8]} window={window}")
+    q, kc, vc, starts, lengths, table = make(dt, H, kv, D, ps, news, lens, seed, spread)
+    y = q4.PagedCache(kc, vc).attend(q, starts, lengths, table, window=window, scale=scale)
+    check(y, *reference(q, kc, vc, news, lens, table, window, scale))
+    return y
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("H,kv,D", [(4, 4, 128), (8, 1, 64), (6, 2, 256), (16, 2, 128), (7, 1, 128), (3, 3, 64), (16, 1, 256)])
+@pytest.mark.parametrize("ps", [16, 64])
+def test_single_tokens(dt, H, kv, D, ps):
+    run(dt, H, kv, D, ps, [1] * 7, [1, 2, 31, 32, 33, 500, 1027], seed=D + ps)
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("D,ps", [(64, 1), (128, 5), (256, 8), (128, 24), (128, 48), (64, 128), (8, 16), (40, 32), (80, 16), (96, 7),
+                                  (136, 16), (200, 16)])
+def test_page_sizes_and_head_dims(dt, D, ps):
+    run(dt, 4, 2, D, ps, [1, 3, 1, 20], [77, 3, 301, 95], seed=D * ps)
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("window", [1, 2, 31, 32, 33, 64, 100, 1000])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_windows(dt, window, D):
+    run(dt, 4, 2, D, 16, [1, 1, 40, 7, 130], [300, 5, 333, 7, 450], window=window, seed=window)
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("H,kv,D", [(4, 4, 64), (8, 2, 128), (12, 4, 128), (4, 1, 256), (5, 1, 128)])
+@pytest.mark.parametrize("news,lens", [
+    ([64], [64]), ([128], [500]), ([257], [257]), ([1, 300, 17], [900, 300, 80]), ([65, 0, 2], [65, 40, 700]),
+    ([600], [2000]), ([33] * 9, [33, 40, 65, 100, 129, 200, 300, 400, 1000])])
+def test_chunks(dt, H, kv, D, news, lens):
+    run(dt, H, kv, D, 16, news, lens, seed=sum(lens))
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+def test_long_context(dt):
+    """One request whose keys many workgroups share."""
+    run(dt, 8, 1, 128, 64, [1], [40001], seed=5)
+    run(dt, 4, 4, 64, 16, [2], [20003], seed=6)
+    run(dt, 8, 2, 128, 32, [40, 1], [9001, 17], seed=7)
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+def test_sharp_and_flat(dt):
+    run(dt, 4, 2, 128, 16, [1, 100], [700, 400], spread=30.0, seed=8)      # one key takes nearly all
+    run(dt, 4, 2, 128, 16, [1, 100], [700, 400], spread=0.0, seed=9)       # the mean
+    run(dt, 4, 2, 128, 16, [1, 100], [700, 400], scale=-0.3, seed=10)
+    run(dt, 4, 2, 128, 16, [1, 100], [700, 400], scale=0.0, seed=11)
+
+
+def test_many_requests():
+    """More requests than a wave has lanes, some without tokens, all lengths."""
+    g = torch.Generator().manual_seed(2)
+    lens = torch.randint(1, 700, (200,), generator=g).tolist()
+    news = [0 if i % 5 == 3 else 1 for i in range(200)]
+    run(torch.bfloat16, 8, 2, 128, 16, news, lens)
+    news = [min(m, [0, 1, 3, 50][i % 4]) for i, m in enumerate(lens)]
+    run(torch.float16, 4, 2, 64, 16, news, lens, window=90)
+
+
+def test_tokens_that_see_nothing():
+    """More new tokens than cached ones: those at negative positions give zeros."""
+    for D in (64, 128, 256):
+        for news, lens in (([5], [3]), ([1, 2, 40], [0, 0, 9]), ([300], [20]), ([300, 1], [0, 0])):
+            y = run(torch.bfloat16, 4, 2, D, 16, news, lens)
+            at = 0
+            for n, m in zip(news, lens):
+                assert (y[at:at + max(n - m, 0)] == 0).all()
+                at += n
+
+
+def test_pages_before_the_window_may_be_gone():
+    """Table entries that no visible key needs are not used: they may be any
+    number, and their pages any content."""
+    import gptq_bit_weight_amd as q4
+    for news, lens, window in (([1], [1000], 100), ([200], [1000], 64), ([40, 1], [700, 333], 17)):
+        q, kc, vc, starts, lengths, table = make(torch.float16, 8, 2, 128, 16, news, lens)
+        ref, tol = reference(q, kc, vc, news, lens, table, window)
+        for b, (n, m) in enumerate(zip(news, lens)):
+            first = max(0, m - n - window + 1) // 16
+            kc[table[b, :first].long()] = math.nan
+            vc[table[b, :first].long()] = math.nan
+            table[b, :first] = -(1 << 31) if b % 2 else 2 ** 31 - 1
+        check(q4.PagedCache(kc, vc).attend(q, starts, lengths, table, window=window), ref, tol)
+
+
+def test_strides():
+    """q as a view of a fused row, out as a view, a cache of another order,
+    a table that is a view of a wider one."""
+    import gptq_bit_weight_amd as q4
+    news, lens = [1, 90, 3], [200, 90, 50]
+    q, kc, vc, starts, lengths, table = make(torch.bfloat16, 8, 2, 128, 16, news, lens)
+    ref, tol = reference(q, kc, vc, news, lens, table)
+    T = q.shape[0]
+    wide = torch.zeros(T, 12, 128, dtype=q.dtype, device="cuda")
+    wide[:, 2:10] = q
+    store = torch.stack([kc, vc], 2).permute(0, 3, 2, 1, 4).contiguous()     # [pages, rows, k or v, heads, dim]
+    k2, v2 = (store[:, :, i].transpose(1, 2) for i in (0, 1))
+    t2 = torch.full((3, table.shape[1] + 9), -1, dtype=torch.int32, device="cuda")
+    t2[:, :table.shape[1]] = table
+    out = torch.full((T, 10, 130), 7.0, dtype=q.dtype, device="cuda")
+    cache = q4.PagedCache(k2, v2)
+    y = cache.attend(wide[:, 2:10], starts, lengths, t2[:, :table.shape[1]], out=out[:, 1:9, 1:129])
+    check(y, ref, tol)
+    assert (out[:, 0] == 7).all() and (out[:, 9] == 7).all() and (out[:, :, 0] == 7).all() and (out[:, :, 129] == 7).all()
+    # queries that 16 bytes do not divide are copied first
+    odd = torch.zeros(T, 8, 129, dtype=q.dtype, device="cuda")[:, :, 1:]
+    odd.copy_(q)
+    check(cache.attend(odd, starts, lengths, table), ref, tol)
+
+
+def test_runs_agree_to_the_bit():
+    import gptq_bit_weight_amd as q4
+    for news, lens in (([1, 1], [30000, 77]), ([300, 1], [5000, 900])):
+        q, kc, vc, starts, lengths, table = make(torch.bfloat16, 8, 2, 128, 64, news, lens)
+        cache = q4.PagedCache(kc, vc)
+        a = cache.attend(q, starts, lengths, table)
+        for _ in range(5):
+            assert torch.equal(a, cache.attend(q, starts, lengths, table))
+
+
+def test_cache_beyond_31_bits():
+    """Pages whose offsets pass 2^32 bytes and 2^31 values."""
+    import gptq_bit_weight_amd as q4
+    pages = (1 << 31) // (8 * 64 * 128) + 40
+    kc = torch.zeros(pages, 8, 64, 128, dtype=torch.float16, device="cuda")
+    vc = torch.zeros_like(kc)
+    kc[-32:].normal_()
+    vc[-32:].normal_()
+    for n, H in ((1, 16), (200, 8)):
+        table = torch.arange(pages - 1, pages - 33, -1, dtype=torch.int32, device="cuda")[None].contiguous()
+        lens = [2000]
+        q = torch.randn(n, H, 128, device="cuda").half()
+        starts = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        y = q4.PagedCache(kc, vc).attend(q, starts, torch.tensor(lens, dtype=torch.int32, device="cuda"), table)
+        check(y, *reference(q, kc, vc, [n], lens, table))
+
+
+def test_graph_replays():
+    """Captured once; lengths, table and data change between replays, with
+    eager calls of the same stream beside them."""
+    import gptq_bit_weight_amd as q4
+    for news, lens, H in (([1, 1, 1], [900, 5000, 64], 16), ([100, 1, 60], [900, 5000, 64], 8)):
+        q, kc, vc, starts, lengths, table = make(torch.float16, H, 2, 128, 16, news, lens)
+        cache = q4.PagedCache(kc, vc)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y = cache.attend(q, starts, lengths, table)
+        for i in range(4):
+            q.normal_()
+            cur = [m - 3 * i for m in lens]
+            cur = [max(m, n) for m, n in zip(cur, news)]
+            lengths.copy_(torch.tensor(cur, dtype=torch.int32))
+            graph.replay()
+            eager = cache.attend(q, starts, lengths, table)
+            torch.cuda.synchronize()
+            assert torch.equal(y, eager), i
+            check(y, *reference(q, kc, vc, news, cur, table), what=f"replay {i}")
+
+
+def test_other_stream():
+    import gptq_bit_weight_amd as q4
+    q, kc, vc, starts, lengths, table = make(torch.float16, 8, 2, 128, 16, [1, 1], [3000, 77])
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    y = q4.PagedCache(kc, vc).attend(q, starts, lengths, table, stream=s)
+    s.synchronize()
+    check(y, *reference(q, kc, vc, [1, 1], [3000, 77], table))
+
+
+def test_bad_tables_stay_inside():
+    """Entries, lengths and starts outside their ranges read and write nothing
+    outside the tensors (the result has no meaning)."""
+    import gptq_bit_weight_amd as q4
+    q, kc, vc, starts, lengths, table = make(torch.float16, 8, 2, 128, 16, [1, 40], [300, 200])
+    kc.nan_to_num_()
+    vc.nan_to_num_()
+    cache = q4.PagedCache(kc, vc)
+    guard = torch.full((43, 8, 128), 5.0, dtype=q.dtype, device="cuda")
+    out = guard[1:42]
+    for tb, ln, st in ((torch.full_like(table, 10 ** 9), lengths, starts), (torch.full_like(table, -5), lengths, starts),
+                       (table, torch.full_like(lengths, 10 ** 9), starts), (table, torch.full_like(lengths, -3), starts),
+                       (table, lengths, torch.tensor([-4, 99, 7], dtype=torch.int32, device="cuda"))):
+        cache.attend(q, st, ln, tb, out=out)
+        torch.cuda.synchronize()
+        assert (guard[0] == 5).all() and (guard[42] == 5).all()
+
+
+def test_refusals():
+    import gptq_bit_weight_amd as q4
+    q, kc, vc, starts, lengths, table = make(torch.float16, 8, 2, 128, 16, [1, 1], [30, 20])
+    c = q4.PagedCache(kc, vc)
+    good = dict(q=q, starts=starts, lengths=lengths, table=table)
+    bad = [dict(q=q.bfloat16()), dict(q=q[:, :7]), dict(q=q[..., :64]), dict(q=q[0]), dict(q=q.cpu()), dict(starts=starts.long()),
+           dict(starts=starts[:2]), dict(lengths=lengths[:1]), dict(table=table[:1]), dict(table=table[:, :0]),
+           dict(lengths=lengths.cpu()), dict(table=table.float()), dict(window=-1), dict(scale=math.nan), dict(scale=math.inf),
+           dict(out=q), dict(out=torch.empty_like(q)[:1]), dict(out=torch.empty_like(q).bfloat16()), dict(table=table[0])]
+    for i, kw in enumerate(bad):
+        with pytest.raises((ValueError, TypeError)):
+            c.attend(**{**good, **kw})
+            pytest.fail(f"case {i} was taken")
+    k9 = torch.zeros(2, 2, 16, 72 + 4, dtype=torch.float16, device="cuda")
+    with pytest.raises(NotImplementedError):
+        q4.PagedCache(k9, k9.clone()).attend(torch.zeros(2, 2, 76, dtype=torch.float16, device="cuda"), starts, lengths, table)
+    k9 = torch.zeros(2, 2, 16, 264, dtype=torch.float16, device="cuda")
+    with pytest.raises(NotImplementedError):
+        q4.PagedCache(k9, k9.clone()).attend(torch.zeros(2, 2, 264, dtype=torch.float16, device="cuda"), starts, lengths, table)
+    e = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert c.attend(q[:0], e, lengths[:0], table[:0]).shape == (0, 8, 128)
+    assert c.attend(q[:0], torch.zeros(3, dtype=torch.int32, device="cuda"), lengths, table).shape == (0, 8, 128)
