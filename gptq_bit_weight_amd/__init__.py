@@ -20,7 +20,7 @@ from typing import Optional
 
 __all__ = [
     "Q4Matrix", "Q4Error", "load_library", "library_path", "check_shape", "plan_actorder",
-    "plan_gemv", "plan_gemv_gather", "plan_gemm", "Rotary", "PagedCache", "PATH_NONE", "PATH_GEMV", "PATH_MFMA", "GEMV_MAX_M", "EXPORTED_SYMBOLS",
+    "plan_gemv", "plan_gemv_gather", "plan_gemm", "Q4Adapters", "Rotary", "PagedCache", "PATH_NONE", "PATH_GEMV", "PATH_MFMA", "GEMV_MAX_M", "EXPORTED_SYMBOLS",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -43,6 +43,8 @@ EXPORTED_SYMBOLS = (
     "q4_matmul_static",
     "q4_rotary_make", "q4_rotary_free", "q4_rotary_plan", "q4_rotary_apply", "q4_cache_append",
     "q4_attend_workspace", "q4_attend",
+    "q4_check_adapters", "q4_adapters_make", "q4_adapters_free", "q4_adapters_load", "q4_adapters_clear",
+    "q4_matmul_adapters",
 )
 
 _lib = None
@@ -131,7 +133,16 @@ def load_library():
     lib.q4_attend_workspace.argtypes = [P, I]
     lib.q4_attend_workspace.restype = ctypes.c_size_t
     lib.q4_attend.argtypes = [P, P, L, L, I, I, P, P, P, I, L, I, I, ctypes.c_float, P, L, L, P, ctypes.c_size_t, P]
-    for f in (lib.q4_rotary_plan, lib.q4_rotary_apply, lib.q4_cache_append, lib.q4_attend):
+    lib.q4_check_adapters.argtypes = [I, I]
+    lib.q4_adapters_make.argtypes = [P, I, I, I]
+    lib.q4_adapters_make.restype = P
+    lib.q4_adapters_free.argtypes = [P]
+    lib.q4_adapters_free.restype = None
+    lib.q4_adapters_load.argtypes = [P, I, P, P, I, ctypes.c_float, P]
+    lib.q4_adapters_clear.argtypes = [P, I, P]
+    lib.q4_matmul_adapters.argtypes = [P, P, P, P, P, P, I, I, P]
+    for f in (lib.q4_rotary_plan, lib.q4_rotary_apply, lib.q4_cache_append, lib.q4_attend, lib.q4_check_adapters,
+              lib.q4_adapters_load, lib.q4_adapters_clear, lib.q4_matmul_adapters):
         f.restype = I
     _lib = lib
     return lib
@@ -420,6 +431,50 @@ class Q4Matrix:
         _check(st, "q4_matmul_static")
         return out
 
+    def matmul_adapters(self, x, bank, index, bias=None, out=None, *, stream=None):
+        """matmul(x, bias, out) with the adapters of the rows' requests: row m
+        also gets c B (A x[m]) of slot index[m] of `bank` (a Q4Adapters made for
+        this matrix, of x's dtype); an index outside the slots (-1) adds nothing.
+        index: int32 [M]. One rounding, of the whole sum (q4_matmul_adapters)."""
+        torch = _torch()
+        h = self._handle()
+        if getattr(x, "dtype", None) not in (torch.float16, torch.bfloat16):
+            raise ValueError(f"x must be float16 or bfloat16, got {getattr(x, 'dtype', type(x))}")
+        dt, dev = x.dtype, self.device
+        _dev_tensor(x, dt, "x")
+        if x.dim() != 2 or x.shape[1] != self.K:
+            raise ValueError(f"x must be [M, {self.K}], got {tuple(x.shape)}")
+        M = x.shape[0]
+        if bank.dtype != dt:
+            raise ValueError(f"the adapters are {bank.dtype}, x is {dt}")
+        if bank.N != self.N or bank.K != self.K or bank.part_n != self.part_n:
+            raise ValueError("the adapters were made for another matrix")
+        _dev_tensor(index, torch.int32, "index", (M,))
+        if out is None:
+            if stream is None:
+                out = torch.empty((M, self.N), dtype=dt, device=dev)
+            else:
+                with torch.cuda.stream(stream):
+                    out = torch.empty((M, self.N), dtype=dt, device=dev)
+        else:
+            _dev_tensor(out, dt, "out", (M, self.N))
+        if bias is not None:
+            _dev_tensor(bias, dt, "bias", (self.N,))
+        for t, nm in ((x, "x"), (index, "index"), (out, "out"), (bias, "bias")):
+            if t is not None and t.device != dev:
+                raise ValueError(f"{nm} is on {t.device}, the matrix on {dev}")
+        if stream is not None:
+            for t in (x, index, out, bias):
+                if t is not None:
+                    t.record_stream(stream)
+        with torch.cuda.device(dev):
+            st = load_library().q4_matmul_adapters(h, bank._handle(), x.data_ptr(),
+                                                   bias.data_ptr() if bias is not None else None, index.data_ptr(),
+                                                   out.data_ptr(), M, 1 if dt == torch.bfloat16 else 0,
+                                                   _stream_ptr(stream))
+        _check(st, "q4_matmul_adapters")
+        return out
+
     def dequant_dump(self, path: int = PATH_GEMV, stream=None, dtype=None):
         """[K, N] in dtype (float16, or bfloat16 for the bfloat16 kernels): the
         dequantized values the kernel of `path` computes."""
@@ -440,6 +495,76 @@ class Q4Matrix:
             torch = _torch()
             torch.cuda.synchronize(self.device)
             load_library().q4_free(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class Q4Adapters:
+    """Low-rank adapters for one Q4Matrix: `slots` of them, each of rank at most
+    `rank`, in the activations' dtype. load() puts one into a slot;
+    Q4Matrix.matmul_adapters(x, bank, index) applies to each row its own. For a
+    matrix of concatenated layers every layer has its own A."""
+
+    def __init__(self, matrix: Q4Matrix, slots: int, rank: int, dtype=None):
+        self._h = None
+        torch = _torch()
+        dtype = dtype or torch.float16
+        if dtype not in (torch.float16, torch.bfloat16):
+            raise ValueError(f"dtype must be float16 or bfloat16, got {dtype}")
+        lib = load_library()
+        _check(lib.q4_check_adapters(slots, rank), "Q4Adapters")
+        with torch.cuda.device(matrix.device):
+            h = lib.q4_adapters_make(matrix._handle(), slots, rank, 1 if dtype == torch.bfloat16 else 0)
+        if not h:
+            _raise(lib.q4_last_status(), "q4_adapters_make")
+        self._h = ctypes.c_void_p(h)
+        self.K, self.N, self.part_n, self.device = matrix.K, matrix.N, matrix.part_n, matrix.device
+        self.slots, self.rank, self.dtype = int(slots), int(rank), dtype
+
+    def _handle(self):
+        if self._h is None:
+            raise ValueError("Q4Adapters is closed")
+        return self._h
+
+    def load(self, slot: int, A, B, c: float = 1.0, stream=None):
+        """Copy an adapter into a slot: A [parts, r, K] (or [r, K] for a matrix
+        of one part), B [N, r], r at most the bank's rank, the product's factor c
+        (alpha / r, often)."""
+        torch = _torch()
+        if getattr(A, "ndim", 0) == 2 and len(self.part_n) == 1:
+            A = A[None]
+        _dev_tensor(A, self.dtype, "A")
+        if A.dim() != 3 or A.shape[0] != len(self.part_n) or A.shape[2] != self.K:
+            raise ValueError(f"A must be [{len(self.part_n)}, rank, {self.K}], got {list(A.shape)}")
+        r = int(A.shape[1])
+        if not 1 <= r <= self.rank:
+            raise ValueError(f"rank {r} outside [1, {self.rank}]")
+        _dev_tensor(B, self.dtype, "B", (self.N, r))
+        for t, nm in ((A, "A"), (B, "B")):
+            if t.device != self.device:
+                raise ValueError(f"{nm} is on {t.device}, the adapters on {self.device}")
+            if stream is not None:
+                t.record_stream(stream)
+        with torch.cuda.device(self.device):
+            st = load_library().q4_adapters_load(self._handle(), slot, A.data_ptr(), B.data_ptr(), r, float(c),
+                                                 _stream_ptr(stream))
+        _check(st, "q4_adapters_load")
+
+    def clear(self, slot: int, stream=None):
+        """Empty a slot: its rows get nothing."""
+        with _torch().cuda.device(self.device):
+            st = load_library().q4_adapters_clear(self._handle(), slot, _stream_ptr(stream))
+        _check(st, "q4_adapters_clear")
+
+    def close(self):
+        if getattr(self, "_h", None) is not None:
+            _torch().cuda.synchronize(self.device)
+            load_library().q4_adapters_free(self._h)
             self._h = None
 
     def __del__(self):

@@ -1,0 +1,503 @@
+// The adapters' bank and the first of a call's two products, c A x.
+//
+// Few rows (the skinny kernel's M): a workgroup for each (row, value of rank),
+// whose four waves share K. It reads rank * K values a row and is bound by them;
+// nothing is sorted, since each row reads its own adapter whatever the others do.
+//
+// Many rows: the rows of one adapter are multiplied together. Each workgroup
+// counts the index (the same counting sort in all, a few microseconds for
+// thousands of rows, in place of a launch of its own) and takes 16 rows of one
+// adapter, 32 of its values; its eight waves share K (16 x 16 x 32 matrix
+// instructions, both operands straight from memory, where the rows of x and
+// A are dense along K) and their sums are joined in LDS. The workgroups also leave
+// the order of the rows for the product's launch.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <memory>
+#include <mutex>
+#include <new>
+#include <vector>
+
+#include "q4_adapters.h"
+#include "q4_ops.h"
+
+namespace {
+
+using namespace q4dev;
+
+constexpr int kMaxSlots = 4096;
+constexpr int kMaxRank = 1024;
+
+// ---- bank -------------------------------------------------------------------
+// A [parts][r][K] -> slot's [parts][rank][K], B [N][r] -> slot's [N][rp], zeros
+// past r; null A clears the slot.
+__global__ void q4_adapter_load_kernel(const uint16_t* A, const uint16_t* B, uint16_t* dA, uint16_t* dB, float* scale,
+                                       float c, int parts, int r, int rank, int rp, int K, int N)
+{
+    const long long na = (long long)parts * rank * K, nb = (long long)N * rp, step = (long long)gridDim.x * blockDim.x;
+    const long long id = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    for (long long i = id; i < na; i += step) {
+        const long long row = i / K;
+        const int p = (int)(row / rank), j = (int)(row % rank);
+        dA[i] = A && j < r ? A[((long long)p * r + j) * K + i % K] : (uint16_t)0;
+    }
+    for (long long i = id; i < nb; i += step) {
+        const long long n = i / rp;
+        const int j = (int)(i % rp);
+        dB[i] = A && j < r ? B[n * r + j] : (uint16_t)0;
+    }
+    if (id == 0) *scale = c;
+}
+
+// ---- few rows ---------------------------------------------------------------
+constexpr int DW = 4;      // waves of a workgroup
+
+template <bool BF>
+__global__ __launch_bounds__(64 * DW) void q4_adapter_few_kernel(const uint16_t* x, const int* index, const uint16_t* A,
+                                                                 const float* scale, float* t, int K, int slots,
+                                                                 int rank, int rp, int parts)
+{
+    __shared__ float part_sum[DW];
+    const int m = blockIdx.y, w = blockIdx.x, p = w / rp, j = w - p * rp;
+    const int s = index[m];
+    if ((unsigned)s >= (unsigned)slots) return;     // (its t is not read)
+    const int lane = threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+    const bool live = j < rank;
+    const uint16_t* xr = x + (size_t)m * K;
+    const uint16_t* ar = A + (((size_t)s * parts + p) * rank + (live ? j : 0)) * K;
+    float y = 0.f;
+    constexpr int U = 4;       // loads of each operand under way
+    for (int k0 = 8 * (int)threadIdx.x; live && k0 < K; k0 += U * 512 * DW) {
+        u4 a[U], b[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = k0 + u * 512 * DW;
+            a[u] = k < K ? *reinterpret_cast<const u4*>(ar + k) : u4{0, 0, 0, 0};
+            b[u] = k < K ? *reinterpret_cast<const u4*>(xr + k) : u4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                y = __builtin_fmaf(act_to_f32<BF>((uint16_t)a[u][e]), act_to_f32<BF>((uint16_t)b[u][e]), y);
+                y = __builtin_fmaf(act_to_f32<BF>((uint16_t)(a[u][e] >> 16)), act_to_f32<BF>((uint16_t)(b[u][e] >> 16)), y);
+            }
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) y += __shfl_xor(y, d);
+    if (lane == 0) part_sum[wave] = y;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float z = part_sum[0];
+#pragma unroll
+        for (int v = 1; v < DW; ++v) z += part_sum[v];
+        t[((size_t)m * parts + p) * rp + j] = live ? z * scale[s] : 0.f;
+    }
+}
+
+// ---- many rows --------------------------------------------------------------
+constexpr int MW = 8, MT = 64 * MW;    // waves, threads
+constexpr int MR = 16, MC = 32;        // rows and values of a workgroup
+
+struct ManyArgs {
+    const uint16_t* x;
+    const int* index;
+    const uint16_t* A;
+    const float* scale;
+    int *rows, *slot_of, *seg;
+    uint16_t *hi, *lo;
+    int M, K, slots, rank, rp, parts;
+};
+
+template <bool BF>
+__global__ __launch_bounds__(MT) void q4_adapter_many_kernel(ManyArgs p)
+{
+    extern __shared__ int count[];               // [slots + 1]: rows of each adapter; of none
+    __shared__ float red[MW][MR][MC];
+    __shared__ int wave_n[MW], tile_row[MR];
+    __shared__ int s_slot, s_first, s_pos;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int bins = p.slots + 1;
+    auto bin_of = [&](int i) {
+        const int s = p.index[i];
+        return (unsigned)s < (unsigned)p.slots ? s : p.slots;
+    };
+    for (int i = tid; i < bins; i += MT) count[i] = 0;
+    __syncthreads();
+    for (int i0 = 64 * wave; i0 < p.M; i0 += MT) {
+        // one addition for each run of equal neighbours
+        const int i = i0 + lane;
+        const int s = i < p.M ? bin_of(i) : -1;
+        const int before = __shfl_up(s, 1);
+        const bool head = lane == 0 || s != before;
+        const unsigned long long heads = __ballot(head);
+        if (head && s >= 0) {
+            const unsigned long long after = lane == 63 ? 0 : heads >> (lane + 1) << (lane + 1);
+            atomicAdd(&count[s], (after ? (int)__builtin_ctzll(after) : 64) - lane);
+        }
+    }
+    __syncthreads();
+    // ---- this workgroup's tile: of all bins' tiles of MR rows, the blockIdx.x-th
+    if (wave == 0) {
+        int tiles = 0, pos = 0, slot = -1, first = 0, at = 0;
+        for (int b0 = 0; b0 < bins; b0 += 64) {
+            const int n = b0 + lane < bins ? count[b0 + lane] : 0;
+            int t = (n + MR - 1) / MR, r = n;
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) {
+                const int to = __shfl_up(t, d), ro = __shfl_up(r, d);
+                if (lane >= d) t += to, r += ro;
+            }
+            if (blockIdx.x == 0 && blockIdx.y == 0 && b0 + lane < bins) p.seg[b0 + lane] = pos + r - n;
+            const unsigned long long past = __ballot(tiles + t > (int)blockIdx.x);
+            if (past && slot < 0) {
+                const int f = (int)__builtin_ctzll(past);
+                const int mine = __builtin_amdgcn_readlane(n, f);
+                slot = b0 + f;
+                first = ((int)blockIdx.x - (tiles + __builtin_amdgcn_readlane(t, f) - (mine + MR - 1) / MR)) * MR;
+                at = pos + __builtin_amdgcn_readlane(r, f) - mine;
+                if (blockIdx.x) break;           // (the first workgroup goes through all bins)
+            }
+            tiles += __builtin_amdgcn_readlane(t, 63);
+            pos += __builtin_amdgcn_readlane(r, 63);
+        }
+        if (lane == 0) {
+            s_slot = slot;
+            s_first = first;
+            s_pos = at + first;
+            if (blockIdx.x == 0 && blockIdx.y == 0) p.seg[bins] = p.M;
+        }
+    }
+    __syncthreads();
+    const int slot = __builtin_amdgcn_readfirstlane(s_slot), first = __builtin_amdgcn_readfirstlane(s_first);
+    if (slot < 0) return;
+    const int n_rows = min(MR, count[slot] - first);
+    // ---- its rows: those of the bin ranked first .. first + MR - 1
+    int seen = 0;
+    for (int i0 = 0; i0 < p.M && seen < first + n_rows; i0 += MT) {
+        const int i = i0 + tid;
+        const bool mine = i < p.M && bin_of(i) == slot;
+        const unsigned long long b = __ballot(mine);
+        if (lane == 0) wave_n[wave] = (int)__builtin_popcountll(b);
+        __syncthreads();
+        int rank = seen + (int)__builtin_popcountll(b & ((1ull << lane) - 1));
+        for (int w = 0; w < MW; ++w) {
+            if (w < wave) rank += wave_n[w];
+            seen += wave_n[w];
+        }
+        if (mine && rank >= first && rank < first + MR) tile_row[rank - first] = i;
+        __syncthreads();
+    }
+    const int pos = __builtin_amdgcn_readfirstlane(s_pos);
+    if (blockIdx.y == 0 && tid < n_rows) {
+        p.rows[pos + tid] = tile_row[tid];
+        p.slot_of[pos + tid] = slot;
+    }
+    if (slot == p.slots) return;                 // rows without an adapter
+    // ---- 16 rows x 32 values, the waves' shares of K
+    const int c16 = lane & 15, quad = lane >> 4, width = p.parts * p.rp, col0 = (int)blockIdx.y * MC;
+    const uint16_t* xr = p.x + (size_t)tile_row[min(c16, n_rows - 1)] * p.K + 8 * quad;
+    const uint16_t* ar[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int w = min(col0 + 16 * h + c16, width - 1), part = w / p.rp, j = min(w - part * p.rp, p.rank - 1);
+        ar[h] = p.A + (((size_t)slot * p.parts + part) * p.rank + j) * p.K + 8 * quad;
+    }
+    f4 acc[2] = {f4{0.f, 0.f, 0.f, 0.f}, f4{0.f, 0.f, 0.f, 0.f}};
+    const int steps = p.K / 32, k0 = steps * wave / MW, k1 = steps * (wave + 1) / MW;
+    constexpr int U = 4;
+    for (int k = k0; k < k1; k += U) {
+        u4 a[U], b[U][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int at = min(k + u, k1 - 1) * 32;
+            a[u] = *reinterpret_cast<const u4*>(xr + at);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) b[u][h] = *reinterpret_cast<const u4*>(ar[h] + at);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (k + u >= k1) continue;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (BF) acc[h] = mfma16(bitcast<b8>(a[u]), bitcast<b8>(b[u][h]), acc[h]);
+                else acc[h] = mfma16(bitcast<h8>(a[u]), bitcast<h8>(b[u][h]), acc[h]);
+            }
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) red[wave][4 * quad + e][16 * h + c16] = acc[h][e];
+    __syncthreads();
+    const int row = tid / MC, w = col0 + tid % MC;
+    static_assert(MT == MR * MC, "one value a thread");
+    if (row >= n_rows || w >= width) return;
+    float z = red[0][row][tid % MC];
+#pragma unroll
+    for (int v = 1; v < MW; ++v) z += red[v][row][tid % MC];
+    // (values past the rank meet zeros of B: they must be finite)
+    z = w % p.rp < p.rank ? z * p.scale[slot] : 0.f;
+    const uint16_t hi = f32_to_act<BF>(z);
+    // what the rounding leaves; nothing of a value beyond the type's range
+    const float rest = z - act_to_f32<BF>(hi);
+    const size_t o = (size_t)(pos + row) * width + w;
+    p.hi[o] = hi;
+    p.lo[o] = f32_to_act<BF>(__builtin_isfinite(rest) ? rest : 0.f);
+}
+
+}  // namespace
+
+struct q4_adapters {
+    int slots = 0, rank = 0, rp = 0, parts = 0, K = 0, N = 0, device = -1;
+    bool bf16 = false;
+    uint16_t *A = nullptr, *B = nullptr;
+    float* scale = nullptr;
+    uint8_t* part8 = nullptr;
+    float* t = nullptr;                // few rows: [Q4_GEMV_MAX_M][parts * rp]
+    std::mutex mutex;
+    char* many = nullptr;              // many rows' workspace, and the rows it holds
+    int many_rows = 0;
+    std::vector<char*> retired;        // outgrown ones, freed with the bank
+};
+
+namespace q4 {
+
+namespace {
+
+struct ManySpace {
+    int *rows, *slot_of, *seg;
+    uint16_t *hi, *lo;
+    size_t bytes;
+};
+
+// The many-row workspace of a bank: rows padded to whole output tiles.
+ManySpace many_space(const q4_adapters* a, char* base, int rows)
+{
+    const size_t m = ((size_t)rows + 255) / 256 * 256, width = (size_t)a->parts * a->rp;
+    ManySpace s;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        char* p = base + at;
+        at += (bytes + 255) / 256 * 256;
+        return p;
+    };
+    s.rows = reinterpret_cast<int*>(take(m * 4));
+    s.slot_of = reinterpret_cast<int*>(take(m * 4));
+    s.seg = reinterpret_cast<int*>(take((size_t)(a->slots + 2) * 4));
+    s.hi = reinterpret_cast<uint16_t*>(take(m * width * 2));
+    s.lo = reinterpret_cast<uint16_t*>(take(m * width * 2));
+    s.bytes = at;
+    return s;
+}
+
+q4_status load_slot(q4_adapters* a, int slot, const uint16_t* A, const uint16_t* B, int rank, float c,
+                    hipStream_t stream, const char* who)
+{
+    if (!a) return fail(Q4_ERR_INVALID_ARG, "%s: null bank", who);
+    if (slot < 0 || slot >= a->slots) return fail(Q4_ERR_INVALID_ARG, "%s: slot %d outside [0, %d)", who, slot, a->slots);
+    int cur = -1;
+    hipError_t e = hipGetDevice(&cur);
+    if (e != hipSuccess) return fail(Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
+    if (cur != a->device) return fail(Q4_ERR_INVALID_ARG, "%s: the bank is on device %d, the current device is %d", who, a->device, cur);
+    const size_t sa = (size_t)a->parts * a->rank * a->K, sb = (size_t)a->N * a->rp;
+    const int grid = (int)std::min<size_t>((std::max(sa, sb) + 255) / 256, 4096);
+    hipLaunchKernelGGL(q4_adapter_load_kernel, dim3(grid), dim3(256), 0, stream, A, B, a->A + slot * sa, a->B + slot * sb,
+                       a->scale + slot, c, a->parts, rank, a->rank, a->rp, a->K, a->N);
+    e = hipGetLastError();
+    return e == hipSuccess ? Q4_OK : fail(Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
+}
+
+}  // namespace
+
+q4_status adapters_check(const q4_adapters* a, const q4_matrix* h, const int* index, bool bf16, const char* who)
+{
+    if (!a || !index) return fail(Q4_ERR_INVALID_ARG, "%s: null bank or index", who);
+    if (a->K != h->K || a->N != h->N || a->device != h->device || a->parts != (int)h->part_n.size())
+        return fail(Q4_ERR_INVALID_ARG, "%s: the bank was made for another matrix", who);
+    if (a->bf16 != bf16)
+        return fail(Q4_ERR_INVALID_ARG, "%s: the bank holds %s, the activations are %s", who, a->bf16 ? "bfloat16" : "float16",
+                    bf16 ? "bfloat16" : "float16");
+    return Q4_OK;
+}
+
+// Grow a bank's workspace to M rows before anything of a call is launched.
+q4_status adapters_reserve(q4_adapters* a, int M, hipStream_t stream)
+{
+    const char* who = "q4_matmul_adapters";
+    std::lock_guard<std::mutex> lock(a->mutex);
+    if (a->many_rows >= M) return Q4_OK;
+    hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
+    hipError_t e = hipStreamIsCapturing(stream, &cap);
+    if (e != hipSuccess) return fail(Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
+    if (cap != hipStreamCaptureStatusNone)
+        return fail(Q4_ERR_INVALID_ARG, "%s: the bank's workspace must grow to M=%d under stream capture; make one "
+                    "uncaptured call with this M (or larger) first", who, M);
+    char* fresh = nullptr;
+    e = hipMalloc(&fresh, many_space(a, nullptr, M).bytes);
+    if (e != hipSuccess) return fail(e == hipErrorOutOfMemory ? Q4_ERR_OOM : Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
+    // (earlier launches, and graphs, may still use the outgrown one)
+    try {
+        if (a->many) a->retired.push_back(a->many);
+    } catch (const std::bad_alloc&) {
+        (void)hipFree(fresh);
+        return fail(Q4_ERR_OOM, "%s: out of memory", who);
+    }
+    a->many = fresh;
+    a->many_rows = M;
+    return Q4_OK;
+}
+
+// c A x for the rows of a call, and the arguments of the product's launch.
+q4_status adapters_prepare(q4_adapters* a, const uint16_t* x, const int* index, int M, bool few,
+                           q4dev::AdapterArgs* args, hipStream_t stream)
+{
+    const char* who = "q4_matmul_adapters";
+    *args = {};
+    args->B = a->B;
+    args->part8 = a->part8;
+    args->slots = a->slots;
+    args->rp = a->rp;
+    args->width = a->parts * a->rp;
+    args->index = index;
+    hipError_t e;
+    if (few) {
+        args->t = a->t;
+        const dim3 grid(args->width, M), block(64 * DW);
+        if (a->bf16)
+            hipLaunchKernelGGL((q4_adapter_few_kernel<true>), grid, block, 0, stream, x, index, a->A, a->scale, a->t, a->K, a->slots, a->rank, a->rp, a->parts);
+        else
+            hipLaunchKernelGGL((q4_adapter_few_kernel<false>), grid, block, 0, stream, x, index, a->A, a->scale, a->t, a->K, a->slots, a->rank, a->rp, a->parts);
+        e = hipGetLastError();
+        return e == hipSuccess ? Q4_OK : fail(Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
+    }
+    const int held = a->many_rows;
+    char* base = a->many;
+    const ManySpace s = many_space(a, base, held);
+    args->rows = s.rows;
+    args->slot_of = s.slot_of;
+    args->seg = s.seg;
+    args->hi = s.hi;
+    args->lo = s.lo;
+    ManyArgs p;
+    p.x = x;
+    p.index = index;
+    p.A = a->A;
+    p.scale = a->scale;
+    p.rows = s.rows;
+    p.slot_of = s.slot_of;
+    p.seg = s.seg;
+    p.hi = s.hi;
+    p.lo = s.lo;
+    p.M = M;
+    p.K = a->K;
+    p.slots = a->slots;
+    p.rank = a->rank;
+    p.rp = a->rp;
+    p.parts = a->parts;
+    // tiles: a whole one each MR rows, and a partial one each bin with rows
+    const dim3 grid(M / MR + std::min(a->slots + 1, M), (args->width + MC - 1) / MC), block(MT);
+    const size_t lds = (size_t)(a->slots + 1) * sizeof(int);
+    if (a->bf16) hipLaunchKernelGGL((q4_adapter_many_kernel<true>), grid, block, lds, stream, p);
+    else hipLaunchKernelGGL((q4_adapter_many_kernel<false>), grid, block, lds, stream, p);
+    e = hipGetLastError();
+    return e == hipSuccess ? Q4_OK : fail(Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
+}
+
+}  // namespace q4
+
+extern "C" {
+
+q4_status q4_check_adapters(int slots, int rank)
+{
+    if (slots < 1 || rank < 1)
+        return q4::fail(Q4_ERR_INVALID_ARG, "q4_adapters_make: %d slots of rank %d", slots, rank);
+    if (slots > kMaxSlots || rank > kMaxRank)
+        return q4::fail(Q4_ERR_UNSUPPORTED, "q4_adapters_make: %d slots of rank %d (at most %d of %d)", slots, rank, kMaxSlots, kMaxRank);
+    return Q4_OK;
+}
+
+q4_adapters* q4_adapters_make(const q4_matrix* h, int slots, int rank, int bf16)
+{
+    const char* who = "q4_adapters_make";
+    if (!h) {
+        q4::fail(Q4_ERR_INVALID_ARG, "%s: null handle", who);
+        return nullptr;
+    }
+    if (q4_check_adapters(slots, rank) != Q4_OK) return nullptr;
+    int cur = -1;
+    hipError_t e = hipGetDevice(&cur);
+    if (e != hipSuccess || cur != h->device) {
+        q4::fail(e != hipSuccess ? Q4_ERR_HIP : Q4_ERR_INVALID_ARG, "%s: the handle was made on device %d, the current device is %d", who, h->device, cur);
+        return nullptr;
+    }
+    q4_adapters* a = new (std::nothrow) q4_adapters;
+    if (!a) {
+        q4::fail(Q4_ERR_OOM, "%s: out of memory", who);
+        return nullptr;
+    }
+    a->slots = slots;
+    a->rank = rank;
+    a->rp = (rank + 7) / 8 * 8;
+    a->parts = (int)h->part_n.size();
+    a->K = h->K;
+    a->N = h->N;
+    a->device = h->device;
+    a->bf16 = bf16 != 0;
+    const size_t na = (size_t)slots * a->parts * rank * a->K * 2, nb = (size_t)slots * a->N * a->rp * 2;
+    e = hipMalloc(&a->A, na);
+    if (e == hipSuccess) e = hipMalloc(&a->B, nb);
+    if (e == hipSuccess) e = hipMalloc(&a->scale, (size_t)slots * 4);
+    if (e == hipSuccess) e = hipMalloc(&a->t, (size_t)q4::kGemvMaxM * a->parts * a->rp * 4);
+    if (e == hipSuccess && a->parts > 1) e = hipMalloc(&a->part8, (size_t)a->N / 8);
+    if (e == hipSuccess) e = hipMemset(a->A, 0, na);
+    if (e == hipSuccess) e = hipMemset(a->B, 0, nb);
+    if (e == hipSuccess) e = hipMemset(a->scale, 0, (size_t)slots * 4);
+    if (e == hipSuccess && a->parts > 1) {
+        std::unique_ptr<uint8_t[]> part(new (std::nothrow) uint8_t[(size_t)a->N / 8]);
+        if (!part) {
+            e = hipErrorOutOfMemory;
+        } else {
+            size_t at = 0;
+            for (int i = 0; i < a->parts; ++i)
+                for (int n = 0; n < h->part_n[i]; n += 8) part[at++] = (uint8_t)i;
+            e = hipMemcpy(a->part8, part.get(), (size_t)a->N / 8, hipMemcpyHostToDevice);
+        }
+    }
+    if (e == hipSuccess) e = hipDeviceSynchronize();
+    if (e != hipSuccess) {
+        q4_adapters_free(a);
+        q4::fail(e == hipErrorOutOfMemory ? Q4_ERR_OOM : Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
+        return nullptr;
+    }
+    return a;
+}
+
+void q4_adapters_free(q4_adapters* a)
+{
+    if (!a) return;
+    (void)hipFree(a->A);
+    (void)hipFree(a->B);
+    (void)hipFree(a->scale);
+    (void)hipFree(a->t);
+    (void)hipFree(a->part8);
+    (void)hipFree(a->many);
+    for (char* p : a->retired) (void)hipFree(p);
+    delete a;
+}
+
+q4_status q4_adapters_load(q4_adapters* a, int slot, const uint16_t* A, const uint16_t* B, int rank, float c, hipStream_t stream)
+{
+    const char* who = "q4_adapters_load";
+    if (!A || !B) return q4::fail(Q4_ERR_INVALID_ARG, "%s: null A or B", who);
+    if (a && (rank < 1 || rank > a->rank)) return q4::fail(Q4_ERR_INVALID_ARG, "%s: rank %d outside [1, %d]", who, rank, a->rank);
+    return q4::load_slot(a, slot, A, B, rank, c, stream, who);
+}
+
+q4_status q4_adapters_clear(q4_adapters* a, int slot, hipStream_t stream)
+{
+    return q4::load_slot(a, slot, nullptr, nullptr, 0, 0.f, stream, "q4_adapters_clear");
+}
+
+}  // extern "C"

@@ -9,6 +9,7 @@
 #include <utility>
 #include <vector>
 
+#include "q4_adapters.h"
 #include "q4_internal.h"
 #include "q4_ops.h"
 
@@ -25,6 +26,16 @@ hipError_t launch_gemv(const q4_matrix* h, const uint16_t* x, const uint16_t* bi
 hipError_t launch_gemm_stream(const q4_matrix* h, const uint16_t* x, const uint16_t* bias, uint16_t* out,
                               int M, bool bf16, int waves, int workers, float* partials, uint32_t* counters,
                               hipStream_t stream);
+hipError_t launch_gemv_adapters(const q4_matrix* h, const uint16_t* x, const uint16_t* bias, uint16_t* out, int M,
+                                int col_tiles, int splits, bool gather_x, bool bf16, float* partials,
+                                uint32_t* counters, const q4dev::AdapterArgs& ad, hipStream_t stream);
+hipError_t launch_gemm_adapters(const q4_matrix* h, const uint16_t* x, const uint16_t* bias, uint16_t* out, int M,
+                                bool bf16, int waves, int workers, float* partials, uint32_t* counters,
+                                const q4dev::AdapterArgs& ad, hipStream_t stream);
+q4_status adapters_check(const q4_adapters* a, const q4_matrix* h, const int* index, bool bf16, const char* who);
+q4_status adapters_reserve(q4_adapters* a, int M, hipStream_t stream);
+q4_status adapters_prepare(q4_adapters* a, const uint16_t* x, const int* index, int M, bool few,
+                           q4dev::AdapterArgs* args, hipStream_t stream);
 hipError_t launch_repack(const uint32_t* src, const int32_t* perm, uint32_t* dst, int K, int N,
                          int n_total, int col_off, int bits, hipStream_t stream);
 hipError_t launch_permute_x(const uint16_t* x, const int32_t* perm, uint16_t* xp, int M, int K,
@@ -182,6 +193,7 @@ q4_status make_impl(int parts, const int32_t* const* qweight, const int32_t* con
     h->bits = bits;
     h->device = dev;
     h->num_cu = num_cu;
+    h->part_n.assign(Np, Np + parts);
     auto bail = [&](q4_status s) {
         destroy(h);
         return s;
@@ -412,10 +424,10 @@ q4_status check_current(const q4_matrix* h, const char* who)
 
 // `stat`: q4_matmul_static (every workspace from the device's scratch
 // array, nothing allocated); otherwise workspaces are the handle's and the
-// stream's, allocated or grown on demand.
+// stream's, allocated or grown on demand. `bank`: adapters by `index`.
 q4_status matmul_impl(const q4_matrix* h, const uint16_t* x, const uint16_t* bias, uint16_t* out,
                       int M, int path, int variant, int splits, bool bf16, hipStream_t stream,
-                      bool stat = false)
+                      bool stat = false, q4_adapters* bank = nullptr, const int* index = nullptr)
 {
     if (!h) return fail(Q4_ERR_INVALID_ARG, "q4_matmul: null handle");
     if (q4_status st = check_current(h, "q4_matmul"); st != Q4_OK) return st;
@@ -452,6 +464,13 @@ q4_status matmul_impl(const q4_matrix* h, const uint16_t* x, const uint16_t* bia
         if (splits < 0 || splits > Q4_GEMM_MAX_WORKERS)
             return fail(Q4_ERR_INVALID_ARG, "q4_matmul: GEMM workgroups %d outside [0, %d]", splits,
                         Q4_GEMM_MAX_WORKERS);
+    }
+
+    q4dev::AdapterArgs ad = {};
+    if (bank) {
+        if (q4_status st = adapters_check(bank, h, index, bf16, "q4_matmul_adapters"); st != Q4_OK) return st;
+        if (kind == Q4_PATH_MFMA)
+            if (q4_status st = adapters_reserve(bank, M, stream); st != Q4_OK) return st;
     }
 
     int ct = 0, s = 0;
@@ -513,6 +532,13 @@ q4_status matmul_impl(const q4_matrix* h, const uint16_t* x, const uint16_t* bia
             if (st != Q4_OK) return st;
             partials = h->partials;
         }
+        if (bank) {
+            // (of the activations in their own order, which A is in too)
+            if (q4_status st = adapters_prepare(bank, x, index, M, true, &ad, stream); st != Q4_OK) return st;
+            Q4_HIP(launch_gemv_adapters(h, xe, bias, out, M, ct, s, gather, bf16, partials, counters, ad, stream),
+                   "q4_matmul: gemv launch");
+            return Q4_OK;
+        }
         Q4_HIP(launch_gemv(h, xe, bias, out, M, ct, s, gather, bf16, partials, counters, stream),
                "q4_matmul: gemv launch");
     } else {
@@ -551,6 +577,12 @@ q4_status matmul_impl(const q4_matrix* h, const uint16_t* x, const uint16_t* bia
                                 "under no stream capture; make one uncaptured call first", workers);
                 workers = tiles;   // planned call under capture: one workgroup per tile
             }
+        }
+        if (bank) {
+            if (q4_status st = adapters_prepare(bank, x, index, M, false, &ad, stream); st != Q4_OK) return st;
+            Q4_HIP(launch_gemm_adapters(h, xe, bias, out, M, bf16, waves, workers, ws.partials, ws.counters, ad, stream),
+                   "q4_matmul: gemm launch");
+            return Q4_OK;
         }
         Q4_HIP(launch_gemm_stream(h, xe, bias, out, M, bf16, waves, workers, ws.partials, ws.counters, stream),
                "q4_matmul: gemm launch");
@@ -656,6 +688,13 @@ q4_status q4_matmul_ex_bf16(const q4_matrix* h, const uint16_t* x, const uint16_
     if (path != 0 && path != Q4_PATH_GEMV && path != Q4_PATH_MFMA)
         return q4::fail(Q4_ERR_INVALID_ARG, "q4_matmul_ex_bf16: unknown path %d", path);
     return q4::matmul_impl(h, x, bias, out, M, path, variant, splits, true, stream);
+}
+
+q4_status q4_matmul_adapters(const q4_matrix* h, q4_adapters* bank, const uint16_t* x, const uint16_t* bias,
+                             const int32_t* index, uint16_t* out, int M, int bf16, hipStream_t stream)
+{
+    if (!bank) return q4::fail(Q4_ERR_INVALID_ARG, "q4_matmul_adapters: null bank");
+    return q4::matmul_impl(h, x, bias, out, M, 0, 0, 0, bf16 != 0, stream, false, bank, index);
 }
 
 void q4_free(q4_matrix* h) { q4::destroy(h); }

@@ -119,6 +119,7 @@ struct q4_matrix {
     int bits = 4;                  // 4 or 8
     int device = -1;
     int num_cu = 256;
+    std::vector<int> part_n;       // columns of each part
     uint32_t* qweight = nullptr;   // packed_words(K, N, bits): private block layout (above)
     // One device allocation holds every buffer below but the grown
     // workspaces (256-byte aligned regions, in this order).

@@ -583,6 +583,56 @@ q4_status q4_attend(const q4_cache* c, const uint16_t* q, int64_t q_token, int64
                     int64_t table_stride, int requests, int window, float scale, uint16_t* out, int64_t out_token,
                     int64_t out_head, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Adapters of many requests beside one quantized product.
+ * ---------------------------------------------------------------------- */
+
+typedef struct q4_adapters q4_adapters;   /* opaque bank of slots */
+
+/* The argument checks of q4_adapters_make that need no device: 1 .. 4096
+ * slots, rank 1 .. 1024. */
+q4_status q4_check_adapters(int slots, int rank);
+
+/*
+ * q4_adapters_make -- a bank of `slots` adapters of rank at most `rank` for
+ * handle h, in binary16 or (bf16 != 0) bfloat16, on h's device (the current
+ * one). Every slot is empty (adds nothing). The bank holds slots * (parts * rank *
+ * K + N * rank rounded up to 8) values and the workspace of its calls; it does not keep
+ * h. NULL on error.
+ */
+q4_adapters* q4_adapters_make(const q4_matrix* h, int slots, int rank, int bf16);
+/* q4_adapters_free -- NULL allowed; the caller has synchronized its streams. */
+void q4_adapters_free(q4_adapters* a);
+
+/*
+ * q4_adapters_load -- copy an adapter of `rank` (at most the bank's) into a slot,
+ * in `stream`'s order: A [parts][rank][K] (a part for each layer the handle
+ * concatenates, K in the checkpoint's order), B [N][rank], factor c.
+ * q4_adapters_clear empties a slot.
+ */
+q4_status q4_adapters_load(q4_adapters* a, int slot, const uint16_t* A, const uint16_t* B, int rank, float c,
+                           hipStream_t stream);
+q4_status q4_adapters_clear(q4_adapters* a, int slot, hipStream_t stream);
+
+/*
+ * q4_matmul_adapters -- q4_matmul_bias / q4_matmul_bf16 with the adapters of
+ * the rows' requests:
+ *   out[m][n] = (x[m] W)[n] + bias[n] + sum_j B[n][j] (c sum_k A[p][j][k] x[m][k])
+ * with A, B, c of slot index[m] and p the part of column n; an index outside
+ * [0, slots) (-1) adds nothing. index is int32 [M] on the device. fp32 sums, one
+ * rounding of the result. Up to Q4_GEMV_MAX_M rows c A x is kept in fp32; above, as
+ * two values of the activations' type (its rounding and the rest: 16 bits of
+ * bfloat16, 22 of binary16), so in binary16 its magnitude must stay below
+ * 65504. Rows of other adapters, or of none, are not touched by one's values
+ * that are not finite.
+ *
+ * Errors, graph capture and concurrency as q4_matmul, for the handle and the bank alike: a
+ * bank's workspace for M > Q4_GEMV_MAX_M grows on the first call with a larger
+ * M, which cannot be captured, and calls on one bank are ordered on one stream.
+ */
+q4_status q4_matmul_adapters(const q4_matrix* h, q4_adapters* bank, const uint16_t* x, const uint16_t* bias,
+                             const int32_t* index, uint16_t* out, int M, int bf16, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,61 @@
+"""What attention over the paged cache and the adapters refuse before any GPU
+call."""
+import ctypes
+import math
+
+import pytest
+
+import gptq_bit_weight_amd as q4
+
+
+def _attend(lib, cache=None, **kw):
+    from gptq_bit_weight_amd.attention import _Cache
+    c = _Cache(4096, 8192, (ctypes.c_int64 * 3)(2048, 1024, 64), (ctypes.c_int64 * 3)(2048, 1024, 64), 4, 2, 16, 64, 0)
+    for k, v in (cache or {}).items():
+        if k in ("k_stride", "v_stride"):
+            v = (ctypes.c_int64 * 3)(*v)
+        setattr(c, k, v)
+    a = dict(q=4096, q_token=512, q_head=64, heads=8, tokens=3, starts=4096, lengths=4096, table=4096, width=2, stride=2,
+             requests=2, window=0, scale=0.125, out=65536, o_token=512, o_head=64, ws=4096, ws_bytes=1 << 40)
+    a.update(kw)
+    return lib.q4_attend(ctypes.byref(c), a["q"], a["q_token"], a["q_head"], a["heads"], a["tokens"], a["starts"],
+                         a["lengths"], a["table"], a["width"], a["stride"], a["requests"], a["window"], a["scale"],
+                         a["out"], a["o_token"], a["o_head"], a["ws"], a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("cache,kw,status", [
+    (dict(k=None), {}, 1), (dict(dim=60), {}, 2), (dict(dim=264), {}, 2), (dict(pages=0), {}, 1),
+    (dict(k_stride=(2048, 1024, 60)), {}, 2), (dict(v_stride=(2044, 1024, 64)), {}, 2), (dict(k=4104), {}, 2),
+    (dict(k_stride=(2048, 1024, 1 << 26)), {}, 2), (dict(k_stride=(-2048, 1024, 64)), {}, 2),
+    ({}, dict(heads=0), 1), ({}, dict(heads=7), 1), ({}, dict(tokens=-1), 1), ({}, dict(requests=-1), 1),
+    ({}, dict(window=-1), 1), ({}, dict(scale=math.nan), 1), ({}, dict(scale=math.inf), 1), ({}, dict(q=None), 1),
+    ({}, dict(starts=None), 1), ({}, dict(lengths=None), 1), ({}, dict(table=None), 1), ({}, dict(out=None), 1),
+    ({}, dict(width=0), 1), ({}, dict(stride=1), 1), ({}, dict(q=4098), 2), ({}, dict(q_token=508), 2),
+    ({}, dict(tokens=1 << 30), 2),
+])
+def test_attend_refuses(cache, kw, status):
+    lib = q4.load_library()
+    assert _attend(lib, cache, **kw) == status
+    assert lib.q4_last_error()
+
+
+def test_attend_of_nothing():
+    lib = q4.load_library()
+    assert _attend(lib, tokens=0) == 0
+    assert _attend(lib, requests=0) == 0
+
+
+@pytest.mark.parametrize("slots,rank,status", [(0, 8, 1), (3, 0, 1), (-1, 8, 1), (4097, 8, 2), (3, 1025, 2), (4096, 1024, 0)])
+def test_adapters_sizes(slots, rank, status):
+    assert q4.load_library().q4_check_adapters(slots, rank) == status
+
+
+def test_adapters_null():
+    lib = q4.load_library()
+    assert lib.q4_adapters_make(None, 3, 8, 0) is None
+    assert lib.q4_last_status() == 1
+    assert lib.q4_adapters_load(None, 0, 4096, 4096, 8, 1.0, None) == 1
+    assert lib.q4_adapters_load(None, 0, None, 4096, 8, 1.0, None) == 1
+    assert lib.q4_adapters_clear(None, 0, None) == 1
+    assert lib.q4_matmul_adapters(None, None, 4096, None, 4096, 8192, 1, 0, None) == 1
+    lib.q4_adapters_free(None)
