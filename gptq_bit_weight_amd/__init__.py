@@ -460,19 +460,12 @@ class Q4Matrix:
             _dev_tensor(out, dt, "out", (M, self.N))
         if bias is not None:
             _dev_tensor(bias, dt, "bias", (self.N,))
-        for t, nm in ((x, "x"), (index, "index"), (out, "out"), (bias, "bias")):
-            if t is not None and t.device != dev:
-                raise ValueError(f"{nm} is on {t.device}, the matrix on {dev}")
-        if stream is not None:
-            for t in (x, index, out, bias):
-                if t is not None:
-                    t.record_stream(stream)
-        with torch.cuda.device(dev):
-            st = load_library().q4_matmul_adapters(h, bank._handle(), x.data_ptr(),
-                                                   bias.data_ptr() if bias is not None else None, index.data_ptr(),
-                                                   out.data_ptr(), M, 1 if dt == torch.bfloat16 else 0,
-                                                   _stream_ptr(stream))
-        _check(st, "q4_matmul_adapters")
+        if x.device != dev or index.device != dev or out.device != dev or (bias is not None and bias.device != dev):
+            raise ValueError(f"x, index, out and bias must be on {dev}, the matrix's device")
+        from .attention import _call
+        _call(load_library().q4_matmul_adapters, "q4_matmul_adapters", dev, stream,
+              (h, bank._handle(), x.data_ptr(), bias.data_ptr() if bias is not None else None, index.data_ptr(),
+               out.data_ptr(), M, 1 if dt == torch.bfloat16 else 0), [t for t in (x, index, out, bias) if t is not None])
         return out
 
     def dequant_dump(self, path: int = PATH_GEMV, stream=None, dtype=None):

@@ -27,6 +27,13 @@ _SCALING_KEYS = {"none": set(), "linear": {"factor"}, "base": {"factor"},
 _HALVES = (torch.float16, torch.bfloat16)
 
 
+# (A call's Python costs as much as a small kernel, so what is looked up for
+# each is kept cheap: the current stream's handle without a Stream object is
+# 0.1 us against 1.8.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+_dense = torch.contiguous_format
+
+
 class _Cache(ctypes.Structure):
     """q4_cache of include/q4.h."""
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_stride", ctypes.c_int64 * 3),
@@ -67,6 +74,13 @@ def _index(t, name, device, n):
     return bits
 
 
+def _int32(t, name, device, dims):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.int32 or t.dim() != dims or t.device != device:
+        raise ValueError(f"{name} must be int32 with {dims} dimensions on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
+
+
 def _distinct(t, name):
     """An output's elements must be distinct places in memory."""
     span = 1
@@ -93,9 +107,9 @@ def _out_like(x, out, name, stream):
     stream that the call runs on."""
     if out is None:
         if stream is None:
-            return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            return torch.empty_like(x, memory_format=_dense)
         with torch.cuda.stream(stream):
-            return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            return torch.empty_like(x, memory_format=_dense)
     _heads(out, name, x.device, x.dtype, *x.shape)
     _distinct(out, name)
     same = out.data_ptr() == x.data_ptr() and out.stride() == x.stride()
@@ -107,7 +121,7 @@ def _out_like(x, out, name, stream):
 def _call(fn, what, device, stream, args, used=()):
     """Call a C function on `stream` (the device's current one by default)."""
     if stream is None:
-        sp = torch.cuda.current_stream(device).cuda_stream
+        sp = _raw_stream(device.index)
     else:
         if stream.device != device:
             raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on {device}")
@@ -306,15 +320,13 @@ class PagedCache:
         T, H, D = q.shape
         if H % self.kv_heads or not H:
             raise ValueError(f"q has {H} heads, the cache {self.kv_heads}")
-        for t, nm, nd in ((starts, "starts", 1), (lengths, "lengths", 1), (table, "table", 2)):
-            if not isinstance(t, torch.Tensor):
-                raise TypeError(f"{nm} must be a torch.Tensor")
-            if t.dtype != torch.int32 or t.dim() != nd or t.device != dev:
-                raise ValueError(f"{nm} must be int32 with {nd} dimensions on {dev}, got {t.dtype} {list(t.shape)} on {t.device}")
-        B = lengths.shape[0]
-        if starts.shape[0] != B + 1 or table.shape[0] != B:
-            raise ValueError(f"starts must be [{B + 1}] and table [{B}, width], got {list(starts.shape)} and {list(table.shape)}")
-        width = table.shape[1]
+        _int32(starts, "starts", dev, 1)
+        _int32(lengths, "lengths", dev, 1)
+        _int32(table, "table", dev, 2)
+        B, width = table.shape
+        if lengths.shape[0] != B or starts.shape[0] != B + 1:
+            raise ValueError(f"table [{B}, {width}] takes lengths [{B}] and starts [{B + 1}], got {list(lengths.shape)} "
+                             f"and {list(starts.shape)}")
         if (B and width == 0) or (T and not B):
             raise ValueError("table has no pages" if B else f"{T} tokens of no request")
         if not (starts.is_contiguous() and lengths.is_contiguous()) or (width > 1 and table.stride(1) != 1):
@@ -332,11 +344,11 @@ class PagedCache:
             if _overlap(out, q):
                 raise ValueError("out overlaps q")
         ws = self._workspace(H, stream)
-        qs, os_ = q.stride(), out.stride()
+        qs, os_, ts = q.stride(), out.stride(), table.stride(0)
         _call(load_library().q4_attend, "q4_attend", dev, stream,
               (self._ref, q.data_ptr(), qs[0], qs[1], H, T, starts.data_ptr(), lengths.data_ptr(), table.data_ptr(),
-               width, max(table.stride(0), width), B, window, D ** -0.5 if scale is None else scale, out.data_ptr(),
-               os_[0], os_[1], ws.data_ptr(), ws.numel()),
+               width, ts if ts > width else width, B, window, D ** -0.5 if scale is None else scale, out.data_ptr(),
+               os_[0], os_[1], ws[0], ws[1]),
               (q, out, starts, lengths, table, self.k, self.v))
         return out
 
@@ -351,21 +363,18 @@ class PagedCache:
             if not need:
                 _raise(load_library().q4_last_status(), "q4_attend_workspace")
             self._need[heads] = need
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-            make = _zeros
-        else:
-            make = lambda *a: _on(stream, _zeros, *a)  # noqa: E731
         if torch.cuda.is_current_stream_capturing():
-            return make(need, self.device)
-        key = (self.device.index, stream.cuda_stream)
-        ws = _workspaces.get(key)
-        if ws is None or ws.numel() < need:
-            ws = _workspaces[key] = make(need, self.device)
-        return ws
+            ws = _zeros(need, self.device) if stream is None else _on(stream, _zeros, need, self.device)
+            return ws.data_ptr(), need, ws
+        key = (self.device.index, _raw_stream(self.device.index) if stream is None else stream.cuda_stream)
+        held = _workspaces.get(key)
+        if held is None or held[1] < need:
+            ws = _zeros(need, self.device) if stream is None else _on(stream, _zeros, need, self.device)
+            held = _workspaces[key] = (ws.data_ptr(), need, ws)
+        return held
 
 
-_workspaces: dict = {}      # (device, stream) -> q4_attend's workspace
+_workspaces: dict = {}      # (device, stream) -> q4_attend's workspace: address, bytes, tensor
 
 
 def _zeros(n, device):

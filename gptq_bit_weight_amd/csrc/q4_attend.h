@@ -18,6 +18,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "q4_device.h"
 #include "q4_fastdiv.h"
 #include "q4_ops.h"
@@ -37,7 +39,8 @@ struct Args {
     int T, B, KV, g;                       // tokens, requests, cached heads, heads of a group
     int dim, chunks;                       // values of a head and its 16-byte pieces
     int pages, page_size, table_stride, max_len, window;
-    float scale;                           // on the scores, times log2 e
+    float scale;                           // on the scores, times log2 e; positive
+    uint32_t q_and, q_xor;                 // on two of q's values: a scale of 0 clears them, a negative one turns them
     int store8;                            // 8-byte stores reach every output row
     float* slots;                          // partial results
     uint32_t* counters;

@@ -9,6 +9,8 @@ namespace q4 {
 
 hipError_t launch_attend_rows(const q4attend::Args& p, int row_blocks, bool bf16, bool pages_of_16, hipStream_t stream);
 
+hipError_t launch_attend_tiles(const q4attend::Args& p, int grid, bool bf16, bool pages_of_16, hipStream_t stream);
+
 namespace {
 
 // Workgroups of the few-row kernel: as many as the CUs hold by its LDS (66 KiB
@@ -23,6 +25,18 @@ constexpr size_t kCounterBytes = 1 << 14;
 size_t rows_bytes(int dim, int row_blocks, int workers)
 {
     return kCounterBytes + (size_t)workers * 2 * (16 * row_blocks) * (padded_dim(dim) + 2) * sizeof(float);
+}
+
+// The many-row kernel: rows of a workgroup, workgroups that it splits a call's
+// work for, least key tiles of one, and its partial results. (A request is split
+// where a row tile has more than 1 / target of all tiles: at most `target` row
+// tiles are, into at most 2 target units.)
+int tile_rows(int dim) { return dim <= 128 ? 256 : 128; }
+int tile_target(int num_cu) { return 2 * num_cu; }
+constexpr int kTileLeast = 8;
+size_t tiles_bytes(int dim, int num_cu)
+{
+    return kCounterBytes + (size_t)2 * tile_target(num_cu) * tile_rows(dim) * (padded_dim(dim) + 2) * sizeof(float);
 }
 
 q4_status check_attend(const q4_cache* c, int heads, const char* who)
@@ -46,7 +60,8 @@ size_t q4_attend_workspace(const q4_cache* c, int heads)
 {
     int dev = -1, cu = 0;
     if (q4::check_attend(c, heads, "q4_attend_workspace") != Q4_OK || q4::device_info(&dev, &cu) != Q4_OK) return 0;
-    return q4::rows_bytes(c->dim, 2, q4::rows_workers(c->dim, cu));
+    const size_t rows = q4::rows_bytes(c->dim, 2, q4::rows_workers(c->dim, cu)), tiles = q4::tiles_bytes(c->dim, cu);
+    return rows > tiles ? rows : tiles;
 }
 
 q4_status q4_attend(const q4_cache* c, const uint16_t* q, int64_t q_token, int64_t q_head, int heads, int tokens,
@@ -107,25 +122,32 @@ q4_status q4_attend(const q4_cache* c, const uint16_t* q, int64_t q_token, int64
     const long long rows = (long long)table_width * c->page_size;
     p.max_len = (int)(rows < (1 << 30) ? rows : (1 << 30));
     p.window = window;
-    p.scale = scale * 1.4426950408889634f;
+    // (a negative scale turns q's signs, a scale of zero clears q)
+    p.scale = scale == 0.f ? 1.f : std::fabs(scale) * 1.4426950408889634f;
+    p.q_and = scale == 0.f ? 0u : ~0u;
+    p.q_xor = scale < 0.f ? 0x80008000u : 0u;
     p.store8 = (reinterpret_cast<uintptr_t>(out) % 8 == 0) && out_token % 4 == 0 && out_head % 4 == 0;
     p.div_g = make_fastdiv((uint32_t)g);
     p.div_page = make_fastdiv((uint32_t)c->page_size);
     const bool bf16 = c->bf16 != 0, pg = c->page_size % 16 == 0;
 
+    // Few rows a request: the few-row kernel, above the many-row one.
     const long long mean_rows = ((long long)tokens * g + requests - 1) / requests;
-    const int rb = mean_rows <= 16 ? 1 : 2;
-    const long long row_tiles = (long long)tokens * g / (16 * rb) + requests;
+    const bool many = mean_rows > 32;
+    const int rb = mean_rows <= 16 ? 1 : 2, tile = many ? tile_rows(c->dim) : 16 * rb;
+    const long long row_tiles = (long long)tokens * g / tile + requests;
     if (row_tiles * c->kv_heads * (p.max_len / 32 + 2) >= (1LL << 31))
         return fail(Q4_ERR_UNSUPPORTED, "%s: more than 2^31 tiles of keys", who);
-    p.workers = rows_workers(c->dim, cu);
-    p.least = 4;
-    const size_t need = rows_bytes(c->dim, rb, p.workers);
+    p.workers = many ? tile_target(cu) : rows_workers(c->dim, cu);
+    p.least = many ? kTileLeast : 4;
+    const size_t need = many ? tiles_bytes(c->dim, cu) : rows_bytes(c->dim, rb, p.workers);
     if (!workspace || workspace_bytes < need || !at16(workspace))
         return fail(Q4_ERR_INVALID_ARG, "%s: the workspace needs %zu bytes on a 16-byte boundary (q4_attend_workspace)", who, need);
     p.counters = static_cast<uint32_t*>(workspace);
     p.slots = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
-    hipError_t e = launch_attend_rows(p, rb, bf16, pg, stream);
+    // (most units there can be: a whole one each share of the work, a partial one each row tile and head)
+    hipError_t e = many ? launch_attend_tiles(p, (int)(row_tiles * c->kv_heads + p.workers), bf16, pg, stream)
+                        : launch_attend_rows(p, rb, bf16, pg, stream);
     return e == hipSuccess ? Q4_OK : fail(Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
 }
 

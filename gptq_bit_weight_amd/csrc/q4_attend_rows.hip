@@ -24,8 +24,6 @@
 // in LDS. A segment that is its whole row tile is stored; else its partial
 // result goes to a slot of its workgroup, and the last workgroup of the row
 // tile to arrive joins them in key order (the same bits whichever it is).
-#include <type_traits>
-
 #include "q4_attend.h"
 
 namespace {
@@ -178,21 +176,20 @@ __global__ __launch_bounds__(NT, D == 64 ? (RB == 1 ? 4 : 3) : D == 128 ? 2 : 1)
                 const int pitch = values ? p.vs2 : p.ks2;
                 const long long off = values ? vo : ko;
                 if constexpr (PG) {
-                    // rows past the last key repeat it (nothing unwritten is read)
-                    const bool cut = first + KT > s.r.len;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int from = 2 * (i & 31) + h;
                         const uint32_t o0 = (uint32_t)__builtin_amdgcn_readlane((int)off, from);
                         const uint32_t o1 = (uint32_t)__builtin_amdgcn_readlane((int)(off >> 32), from);
                         const char* base = src + (long long)((uint64_t)o1 << 32 | o0);
-                        const int limit = min(max(s.r.len - 1 - first - 16 * h, 0), 15);
+                        // rows past the last key repeat it (nothing unwritten is read)
+                        const int limit = max(s.r.len - 1, 0) - 16 * min(max((first >> 4) + h, s.lo >> 4), last_block);
 #pragma unroll
                         for (int e0 = 0; e0 < NI / 2; e0 += NB) {
                             uint32_t at[NB];
 #pragma unroll
                             for (int e = 0; e < NB; ++e) at[e] = values ? voff[e0 + e] : koff[e0 + e];
-                            if (cut)
+                            if (limit < 15)
 #pragma unroll
                                 for (int e = 0; e < NB; ++e) {
                                     const int row = (e0 + e) * RPI + lane / CPR;
@@ -236,6 +233,8 @@ __global__ __launch_bounds__(NT, D == 64 ? (RB == 1 ? 4 : 3) : D == 128 ? 2 : 1)
                 for (int ks = 0; ks < KS; ++ks) {
                     const int at = 32 * ks + 8 * quad;
                     qf[rb][ks] = at < p.dim ? *reinterpret_cast<const u4*>(qp + at) : u4{0, 0, 0, 0};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) qf[rb][ks][e] = (qf[rb][ks][e] & p.q_and) ^ p.q_xor;
                 }
             }
             f4 acc[RB][DT];
@@ -364,7 +363,9 @@ __global__ __launch_bounds__(NT, D == 64 ? (RB == 1 ? 4 : 3) : D == 128 ? 2 : 1)
             constexpr int UNITS = ROWS * (D / 4), UPT = UNITS / NT;   // four values of a row each
             const bool whole = tile0 == 0 && tiles == s.nt;
             const uint32_t pair_at = before + pair * (uint32_t)s.nt;
-            const int wf = (int)(pair_at / per), wl = (int)((pair_at + (uint32_t)s.nt - 1) / per);
+            // (workgroups there are, whatever `starts` says)
+            const int wf = min((int)(pair_at / per), p.workers - 1);
+            const int wl = min((int)((pair_at + (uint32_t)s.nt - 1) / per), p.workers - 1);
             constexpr size_t SLOT = (size_t)ROWS * (D + 2);
             auto slot_of = [&](int w) {
                 return make_rsrc(p.slots + (size_t)(2 * w + (w == wf ? 1 : 0)) * SLOT, (uint32_t)(SLOT * 4));

@@ -142,6 +142,25 @@ def test_windows(dt, window, D):
     run(dt, 4, 2, D, 16, [1, 1, 40, 7, 130], [300, 5, 333, 7, 450], window=window, seed=window)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("window", [1, 3, 17])
+def test_windows_inside_the_last_rows(D, window):
+    """The first visible key in the last, half written 16 rows of a tile of keys."""
+    lens = list(range(1, 140, 3))
+    run(torch.float16, 4, 2, D, 16, [1] * len(lens), lens, window=window, seed=1)
+    run(torch.bfloat16, 4, 2, D, 64, [min(m, 30) for m in lens], lens, window=window, seed=2)
+    run(torch.bfloat16, 4, 2, D, 7, [min(m, 30) for m in lens], lens, window=window, seed=2)
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("H,kv,D", [(16, 1, 128), (2, 2, 64), (4, 2, 256)])
+def test_chunks_split_over_keys(dt, H, kv, D):
+    """Few row tiles over long contexts: their keys are split, joined in order."""
+    run(dt, H, kv, D, 64, [70], [12001], seed=3)
+    run(dt, H, kv, D, 16, [300, 1, 40], [9000, 4000, 60], seed=4)
+    run(dt, H, kv, D, 16, [300, 1, 40], [9000, 4000, 60], window=3000, seed=4)
+
+
 @pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("H,kv,D", [(4, 4, 64), (8, 2, 128), (12, 4, 128), (4, 1, 256), (5, 1, 128)])
 @pytest.mark.parametrize("news,lens", [
