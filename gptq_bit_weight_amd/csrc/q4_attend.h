@@ -28,6 +28,18 @@ namespace q4attend {
 
 using namespace q4dev;
 
+// Row tiles whose keys were split: where their rows and partial results are.
+struct Join {
+    int start, row0, rows, head, slot, parts;
+};
+constexpr int kMaxJoins = 1024;         // (at most one for each workgroup that work is split for)
+constexpr int kJoinGroups = 32;
+struct JoinList {
+    uint32_t count, done, pad[30];
+    struct { uint32_t done, pad[31]; } group[kJoinGroups];
+    Join item[kMaxJoins];
+};
+
 struct Args {
     const uint16_t* q;
     uint16_t* out;
@@ -43,7 +55,8 @@ struct Args {
     uint32_t q_and, q_xor;                 // on two of q's values: a scale of 0 clears them, a negative one turns them
     int store8;                            // 8-byte stores reach every output row
     float* slots;                          // partial results
-    uint32_t* counters;
+    uint32_t* counters;                    // few rows: arrivals
+    JoinList* joins;                       // many rows
     int workers, least;                    // workgroups, and least tiles of one
     q4::FastDiv div_g, div_page;           // by heads of a group; by rows of a page (or 16-row blocks of one)
 };

@@ -7,36 +7,38 @@
 
 namespace q4 {
 
-hipError_t launch_attend_rows(const q4attend::Args& p, int row_blocks, bool bf16, bool pages_of_16, hipStream_t stream);
+hipError_t launch_attend_rows(const q4attend::Args& p, bool bf16, bool pages_of_16, hipStream_t stream);
 
 hipError_t launch_attend_tiles(const q4attend::Args& p, int grid, bool bf16, bool pages_of_16, hipStream_t stream);
 
 namespace {
 
-// Workgroups of the few-row kernel: as many as the CUs hold by its LDS (66 KiB
-// at 128 values a head).
-int rows_workers(int dim, int num_cu) { return num_cu * (dim <= 64 ? 4 : dim <= 128 ? 2 : 1); }
-
 int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
-// The workspace: one arrival counter a workgroup, then the partial results.
-constexpr size_t kCounterBytes = 1 << 14;
+// The workspace: one arrival counter a workgroup, or the list of row tiles to
+// join, then the partial results. (Both leave what they used at zero, but a join's
+// entries are not: they lie past the counters.)
+constexpr size_t kCounterBytes = 1 << 16, kListAt = 1 << 14;
+static_assert(kListAt + sizeof(q4attend::JoinList) <= kCounterBytes, "workspace");
 
-size_t rows_bytes(int dim, int row_blocks, int workers)
+// The few-row kernel: rows of a tile, least tiles of a workgroup (of which there
+// is one a CU).
+constexpr int kFewRows = 16, kFewLeast = 4;
+size_t rows_bytes(int dim, int num_cu)
 {
-    return kCounterBytes + (size_t)workers * 2 * (16 * row_blocks) * (padded_dim(dim) + 2) * sizeof(float);
+    return kCounterBytes + (size_t)num_cu * 2 * kFewRows * (padded_dim(dim) + 2) * sizeof(float);
 }
 
 // The many-row kernel: rows of a workgroup, workgroups that it splits a call's
-// work for, least key tiles of one, and its partial results. (A request is split
-// where a row tile has more than 1 / target of all tiles: at most `target` row
-// tiles are, into at most 2 target units.)
-int tile_rows(int dim) { return dim <= 128 ? 256 : 128; }
-int tile_target(int num_cu) { return 2 * num_cu; }
-constexpr int kTileLeast = 8;
+// work for (one a CU: the chip holds twice as many, but splitting for those costs
+// more in joining than it fills), least key tiles of one, and its partial
+// results. (A request is split where a row tile has more than 1 / target of all
+// tiles: at most `target` row tiles are, into at most 2 target units.)
+constexpr int kTileRows = 128, kTileLeast = 8;
+int tile_target(int num_cu) { return num_cu < q4attend::kMaxJoins ? num_cu : q4attend::kMaxJoins; }
 size_t tiles_bytes(int dim, int num_cu)
 {
-    return kCounterBytes + (size_t)2 * tile_target(num_cu) * tile_rows(dim) * (padded_dim(dim) + 2) * sizeof(float);
+    return kCounterBytes + (size_t)2 * tile_target(num_cu) * kTileRows * (padded_dim(dim) + 2) * sizeof(float);
 }
 
 q4_status check_attend(const q4_cache* c, int heads, const char* who)
@@ -60,7 +62,7 @@ size_t q4_attend_workspace(const q4_cache* c, int heads)
 {
     int dev = -1, cu = 0;
     if (q4::check_attend(c, heads, "q4_attend_workspace") != Q4_OK || q4::device_info(&dev, &cu) != Q4_OK) return 0;
-    const size_t rows = q4::rows_bytes(c->dim, 2, q4::rows_workers(c->dim, cu)), tiles = q4::tiles_bytes(c->dim, cu);
+    const size_t rows = q4::rows_bytes(c->dim, cu), tiles = q4::tiles_bytes(c->dim, cu);
     return rows > tiles ? rows : tiles;
 }
 
@@ -131,23 +133,26 @@ q4_status q4_attend(const q4_cache* c, const uint16_t* q, int64_t q_token, int64
     p.div_page = make_fastdiv((uint32_t)c->page_size);
     const bool bf16 = c->bf16 != 0, pg = c->page_size % 16 == 0;
 
-    // Few rows a request: the few-row kernel, above the many-row one.
+    // Few rows a request: the few-row kernel, above the many-row one. (64 x 8
+    // rows over 4600 keys: 221 us and 237; 8 x 16 over 3000: 32 and 28; 20 x 32 over
+    // 6000: 115 and 102.)
     const long long mean_rows = ((long long)tokens * g + requests - 1) / requests;
-    const bool many = mean_rows > 32;
-    const int rb = mean_rows <= 16 ? 1 : 2, tile = many ? tile_rows(c->dim) : 16 * rb;
+    const bool many = mean_rows > 12;
+    const int tile = many ? kTileRows : kFewRows;
     const long long row_tiles = (long long)tokens * g / tile + requests;
     if (row_tiles * c->kv_heads * (p.max_len / 32 + 2) >= (1LL << 31))
         return fail(Q4_ERR_UNSUPPORTED, "%s: more than 2^31 tiles of keys", who);
-    p.workers = many ? tile_target(cu) : rows_workers(c->dim, cu);
-    p.least = many ? kTileLeast : 4;
-    const size_t need = many ? tiles_bytes(c->dim, cu) : rows_bytes(c->dim, rb, p.workers);
+    p.workers = many ? tile_target(cu) : cu;
+    p.least = many ? kTileLeast : kFewLeast;
+    const size_t need = many ? tiles_bytes(c->dim, cu) : rows_bytes(c->dim, cu);
     if (!workspace || workspace_bytes < need || !at16(workspace))
         return fail(Q4_ERR_INVALID_ARG, "%s: the workspace needs %zu bytes on a 16-byte boundary (q4_attend_workspace)", who, need);
     p.counters = static_cast<uint32_t*>(workspace);
+    p.joins = reinterpret_cast<q4attend::JoinList*>(static_cast<char*>(workspace) + kListAt);
     p.slots = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
     // (most units there can be: a whole one each share of the work, a partial one each row tile and head)
     hipError_t e = many ? launch_attend_tiles(p, (int)(row_tiles * c->kv_heads + p.workers), bf16, pg, stream)
-                        : launch_attend_rows(p, rb, bf16, pg, stream);
+                        : launch_attend_rows(p, bf16, pg, stream);
     return e == hipSuccess ? Q4_OK : fail(Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
 }
 

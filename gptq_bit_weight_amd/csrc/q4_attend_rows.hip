@@ -1,9 +1,9 @@
 // Attention over a paged cache for few rows a request: single tokens and
 // short runs of them.
 //
-// q4_attend_rows_kernel<D, RB, BF, PG>: head rows of D values in LDS (64, 128,
-// 256; a head's own dim may be less), RB blocks of 16 rows (token, head of
-// the group), BF (bfloat16), PG (pages of a multiple of 16 rows).
+// q4_attend_rows_kernel<D, BF, PG>: head rows of D values in LDS (64, 128,
+// 256; a head's own dim may be less), BF (bfloat16), PG (pages of a multiple
+// of 16 rows). A row tile is 16 rows (token, head of the group).
 //
 // Bound: HBM. Each key and value is read once for all rows of its tile and
 // does 4 rows flops a value, far under the matrix rate. So the work is split
@@ -17,8 +17,10 @@
 // keys and one of values in LDS of its own, filled by direct loads; the next
 // keys are under way as soon as the scores of the present ones are formed,
 // the next values when the present ones are multiplied, so the wave waits for
-// memory alone and no barrier stands in the loop. 64 KiB of such buffers a
-// workgroup (D = 128) lets two share a CU, with 64 to 128 KiB in flight.
+// memory alone and no barrier stands in the loop. One workgroup a CU has 32 to
+// 64 KiB under way (D = 128), which suffices: 64 single tokens over 4600 keys on
+// average take 221 us with one or with two (5.5 TB/s), and one token over 131000
+// 106 us against 114, since each workgroup's share is one more partial result to join.
 //
 // At a segment's end the waves' running maxima, sums and outputs are joined
 // in LDS. A segment that is its whole row tile is stored; else its partial
@@ -32,6 +34,7 @@ using namespace q4attend;
 
 constexpr int WV = 4, NT = 64 * WV;
 constexpr int KT = 32;                 // keys of a tile
+constexpr int ROWS = 16;               // rows of one
 
 // What of a request the kernel's split goes by: its row tiles, its first
 // visible key, where its tiles begin (a multiple of 32) and their number (at least
@@ -41,12 +44,11 @@ struct Span {
     int rt, lo, base, nt;
 };
 
-template <int RB>
 __device__ __forceinline__ Span span(const Args& p, int b)
 {
     Span s;
     s.r = request(p, b);
-    s.rt = (s.r.n * p.g + 16 * RB - 1) / (16 * RB);
+    s.rt = (s.r.n * p.g + ROWS - 1) / ROWS;
     s.lo = p.window ? max(s.r.len - s.r.n - p.window + 1, 0) : 0;
     s.lo = min(s.lo, max(s.r.len - 1, 0));
     s.base = s.lo & ~(KT - 1);
@@ -54,10 +56,9 @@ __device__ __forceinline__ Span span(const Args& p, int b)
     return s;
 }
 
-template <int D, int RB, bool BF, bool PG>
-__global__ __launch_bounds__(NT, D == 64 ? (RB == 1 ? 4 : 3) : D == 128 ? 2 : 1) void q4_attend_rows_kernel(Args p)
+template <int D, bool BF, bool PG>
+__global__ __launch_bounds__(NT, D == 64 ? 4 : D == 128 ? 2 : 1) void q4_attend_rows_kernel(Args p)
 {
-    constexpr int ROWS = 16 * RB;
     constexpr int PITCH = 2 * D;               // bytes of a row in LDS
     constexpr int CPR = D / 8;                 // 16-byte chunks of a row
     constexpr int RPI = 64 / CPR;              // rows one direct load fills
@@ -90,7 +91,7 @@ __global__ __launch_bounds__(NT, D == 64 ? (RB == 1 ? 4 : 3) : D == 128 ? 2 : 1)
     // ---- this workgroup's range of tiles
     auto cost = [&](int b) {
         if (b >= p.B) return 0u;
-        const Span s = span<RB>(p, b);
+        const Span s = span(p, b);
         return (uint32_t)s.rt * (uint32_t)p.KV * (uint32_t)s.nt;
     };
     auto scan = [&](uint32_t v) {              // inclusive, over the lanes
@@ -126,7 +127,7 @@ __global__ __launch_bounds__(NT, D == 64 ? (RB == 1 ? 4 : 3) : D == 128 ? 2 : 1)
     }
 
     for (; it < it_end && b < p.B; ++b) {
-        Span s = span<RB>(p, b);
+        Span s = span(p, b);
         s.r.start = uniform(s.r.start);
         s.r.n = uniform(s.r.n);
         s.r.len = uniform(s.r.len);
@@ -217,35 +218,29 @@ __global__ __launch_bounds__(NT, D == 64 ? (RB == 1 ? 4 : 3) : D == 128 ? 2 : 1)
             }
 
             // ---- queries: lane holds row c16 of each block, values 8 quad + 32 ks ..
-            u4 qf[RB][KS];
-            int klo[RB], khi[RB];              // the row's visible keys
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb) {
-                const int r = row0 + 16 * rb + c16;
-                const bool live = 16 * rb + c16 < rows;
+            u4 qf[KS];
+            int klo, khi;                      // the row's visible keys
+            {
+                const int r = row0 + c16;
+                const bool live = c16 < rows;
                 const int token = (int)q4::fast_div((uint32_t)r, p.div_g);
                 const int pos = pos0 + token;
-                khi[rb] = live ? pos : -1;
-                klo[rb] = p.window ? pos - p.window + 1 : 0;
+                khi = live ? pos : -1;
+                klo = p.window ? pos - p.window + 1 : 0;
                 const uint16_t* qp = p.q + (s.r.start + (live ? token : 0)) * p.q_t
                                    + (head * p.g + (live ? r - token * p.g : 0)) * p.q_h;
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
                     const int at = 32 * ks + 8 * quad;
-                    qf[rb][ks] = at < p.dim ? *reinterpret_cast<const u4*>(qp + at) : u4{0, 0, 0, 0};
+                    qf[ks] = at < p.dim ? *reinterpret_cast<const u4*>(qp + at) : u4{0, 0, 0, 0};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) qf[rb][ks][e] = (qf[rb][ks][e] & p.q_and) ^ p.q_xor;
+                    for (int e = 0; e < 4; ++e) qf[ks][e] = (qf[ks][e] & p.q_and) ^ p.q_xor;
                 }
             }
-            f4 acc[RB][DT];
-            float m[RB], l[RB];
+            f4 acc[DT];
+            float m = kLow, l = 0.f;
 #pragma unroll
-            for (int rb = 0; rb < RB; ++rb) {
-                m[rb] = kLow;
-                l[rb] = 0.f;
-#pragma unroll
-                for (int d = 0; d < DT; ++d) acc[rb][d] = f4{0.f, 0.f, 0.f, 0.f};
-            }
+            for (int d = 0; d < DT; ++d) acc[d] = f4{0.f, 0.f, 0.f, 0.f};
             // keys of a tile that every live row sees
             const int all_hi = pos0 + (int)q4::fast_div((uint32_t)row0, p.div_g);
             const int all_lo = p.window ? pos0 + (int)q4::fast_div((uint32_t)(row0 + rows - 1), p.div_g) - p.window + 1 : 0;
@@ -263,19 +258,14 @@ __global__ __launch_bounds__(NT, D == 64 ? (RB == 1 ? 4 : 3) : D == 128 ? 2 : 1)
                 // the keys have landed (the values' loads, issued later, may be out)
                 wait_loads<NI>();
                 __builtin_amdgcn_sched_barrier(0);
-                f4 sc[RB][2];
-#pragma unroll
-                for (int rb = 0; rb < RB; ++rb) sc[rb][0] = sc[rb][1] = f4{0.f, 0.f, 0.f, 0.f};
+                f4 sc[2] = {f4{0.f, 0.f, 0.f, 0.f}, f4{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const u4 a = *reinterpret_cast<const u4*>(kb + h * 16 * PITCH + (kx ^ (ks << 6)));
-#pragma unroll
-                        for (int rb = 0; rb < RB; ++rb) {
-                            if constexpr (BF) sc[rb][h] = mfma16(bitcast<b8>(a), bitcast<b8>(qf[rb][ks]), sc[rb][h]);
-                            else sc[rb][h] = mfma16(bitcast<h8>(a), bitcast<h8>(qf[rb][ks]), sc[rb][h]);
-                        }
+                        if constexpr (BF) sc[h] = mfma16(bitcast<b8>(a), bitcast<b8>(qf[ks]), sc[h]);
+                        else sc[h] = mfma16(bitcast<h8>(a), bitcast<h8>(qf[ks]), sc[h]);
                     }
                 // (every read of the keys issued before the first product)
                 __builtin_amdgcn_sched_group_barrier(0x100, 2 * KS, 0);
@@ -286,44 +276,39 @@ __global__ __launch_bounds__(NT, D == 64 ? (RB == 1 ? 4 : 3) : D == 128 ? 2 : 1)
                 }
                 __builtin_amdgcn_sched_barrier(0);
                 // ---- softmax: lane holds keys first + 16 h + 4 quad + e of row c16
-                u4 pt[RB];
-                const bool masked = first + KT - 1 > all_hi || first < all_lo;
-#pragma unroll
-                for (int rb = 0; rb < RB; ++rb) {
-                    sc[rb][0] *= p.scale;
-                    sc[rb][1] *= p.scale;
-                    if (masked) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int key = first + 16 * h + 4 * quad + e;
-                                sc[rb][h][e] = key >= klo[rb] && key <= khi[rb] ? sc[rb][h][e] : -INFINITY;
-                            }
-                    }
-                    float top = kLow;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[rb][h][e]);
-                    const float mn = fmaxf(m[rb], max_quarters(top));
-                    if (__any(mn > m[rb])) {
-                        const float a = exp2_fast(m[rb] - mn);
-                        l[rb] *= a;
-#pragma unroll
-                        for (int d = 0; d < DT; ++d) acc[rb][d] *= a;
-                        m[rb] = mn;
-                    }
-                    float w[8];
+                sc[0] *= p.scale;
+                sc[1] *= p.scale;
+                if (first + KT - 1 > all_hi || first < all_lo) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            w[4 * h + e] = exp2_fast(sc[rb][h][e] - m[rb]);
-                            l[rb] += w[4 * h + e];
+                            const int key = first + 16 * h + 4 * quad + e;
+                            sc[h][e] = key >= klo && key <= khi ? sc[h][e] : -INFINITY;
                         }
-                    pt[rb] = u4{pack2<BF>(w[0], w[1]), pack2<BF>(w[2], w[3]), pack2<BF>(w[4], w[5]), pack2<BF>(w[6], w[7])};
                 }
+                float top = kLow;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[h][e]);
+                const float mn = fmaxf(m, max_quarters(top));
+                if (__any(mn > m)) {
+                    const float a = exp2_fast(m - mn);
+                    l *= a;
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) acc[d] *= a;
+                    m = mn;
+                }
+                float w[8];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        w[4 * h + e] = exp2_fast(sc[h][e] - m);
+                        l += w[4 * h + e];
+                    }
+                const u4 pt = u4{pack2<BF>(w[0], w[1]), pack2<BF>(w[2], w[3]), pack2<BF>(w[4], w[5]), pack2<BF>(w[6], w[7])};
                 __builtin_amdgcn_sched_barrier(0);
                 if (more) wait_loads<NI>();
                 else wait_loads<0>();
@@ -334,11 +319,8 @@ __global__ __launch_bounds__(NT, D == 64 ? (RB == 1 ? 4 : 3) : D == 128 ? 2 : 1)
                     const char* at = vb + (vx ^ (d << 5));
                     const u2 a0 = read_tr(at), a1 = read_tr(at + 16 * PITCH);
                     const u4 a = u4{a0[0], a0[1], a1[0], a1[1]};
-#pragma unroll
-                    for (int rb = 0; rb < RB; ++rb) {
-                        if constexpr (BF) acc[rb][d] = mfma16(bitcast<b8>(a), bitcast<b8>(pt[rb]), acc[rb][d]);
-                        else acc[rb][d] = mfma16(bitcast<h8>(a), bitcast<h8>(pt[rb]), acc[rb][d]);
-                    }
+                    if constexpr (BF) acc[d] = mfma16(bitcast<b8>(a), bitcast<b8>(pt), acc[d]);
+                    else acc[d] = mfma16(bitcast<h8>(a), bitcast<h8>(pt), acc[d]);
                 }
                 __builtin_amdgcn_sched_barrier(0);
                 if (more) load(i + 1, VALUES);
@@ -347,17 +329,15 @@ __global__ __launch_bounds__(NT, D == 64 ? (RB == 1 ? 4 : 3) : D == 128 ? 2 : 1)
 
             // ---- join the waves: 16 rows of fp32 take a tile's buffer
             __syncthreads();
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb) {
-                const float ls = sum_quarters(l[rb]);
+            {
+                const float ls = sum_quarters(l);
                 if (quad == 0) {
-                    lds_m[wave][16 * rb + c16] = m[rb];
-                    lds_l[wave][16 * rb + c16] = ls;
+                    lds_m[wave][c16] = m;
+                    lds_l[wave][c16] = ls;
                 }
-                char* o = rb == 0 ? lds_k[wave] : lds_v[wave];
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
-                    *reinterpret_cast<f4*>(o + c16 * (4 * D) + (((4 * d + quad) ^ c16) << 4)) = acc[rb][d];
+                    *reinterpret_cast<f4*>(lds_k[wave] + c16 * (4 * D) + (((4 * d + quad) ^ c16) << 4)) = acc[d];
             }
             __syncthreads();
             constexpr int UNITS = ROWS * (D / 4), UPT = UNITS / NT;   // four values of a row each
@@ -384,8 +364,7 @@ __global__ __launch_bounds__(NT, D == 64 ? (RB == 1 ? 4 : 3) : D == 128 ? 2 : 1)
 #pragma unroll
                 for (int w = 0; w < WV; ++w) {
                     const float a = exp2_fast(lds_m[w][row] - mm);
-                    const char* src = row < 16 ? lds_k[w] : lds_v[w];
-                    const f4 x = *reinterpret_cast<const f4*>(src + (row & 15) * (4 * D) + ((c ^ (row & 15)) << 4));
+                    const f4 x = *reinterpret_cast<const f4*>(lds_k[w] + row * (4 * D) + ((c ^ row) << 4));
                     ll += a * lds_l[w][row];
                     v += a * x;
                 }
@@ -415,7 +394,7 @@ __global__ __launch_bounds__(NT, D == 64 ? (RB == 1 ? 4 : 3) : D == 128 ? 2 : 1)
                         const int unit = u * NT + tid, row = unit / (D / 4);
                         float mm = kLow, ll = 0.f;
                         f4 v = f4{0.f, 0.f, 0.f, 0.f};
-                        constexpr int FB = 4;      // slots whose loads are under way together
+                        constexpr int FB = 16;     // slots whose loads are under way together
                         for (int w0 = wf; row < rows && w0 <= wl; w0 += FB) {
                             float pm[FB], pl[FB];
                             f4 po[FB];
@@ -461,14 +440,14 @@ __global__ __launch_bounds__(NT, D == 64 ? (RB == 1 ? 4 : 3) : D == 128 ? 2 : 1)
     }
 }
 
-template <int D, int RB>
+template <int D>
 hipError_t launch_rows(const Args& p, bool bf16, bool pg, hipStream_t stream)
 {
     const dim3 grid(p.workers), block(NT);
-    if (bf16 && pg) hipLaunchKernelGGL((q4_attend_rows_kernel<D, RB, true, true>), grid, block, 0, stream, p);
-    else if (bf16) hipLaunchKernelGGL((q4_attend_rows_kernel<D, RB, true, false>), grid, block, 0, stream, p);
-    else if (pg) hipLaunchKernelGGL((q4_attend_rows_kernel<D, RB, false, true>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((q4_attend_rows_kernel<D, RB, false, false>), grid, block, 0, stream, p);
+    if (bf16 && pg) hipLaunchKernelGGL((q4_attend_rows_kernel<D, true, true>), grid, block, 0, stream, p);
+    else if (bf16) hipLaunchKernelGGL((q4_attend_rows_kernel<D, true, false>), grid, block, 0, stream, p);
+    else if (pg) hipLaunchKernelGGL((q4_attend_rows_kernel<D, false, true>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((q4_attend_rows_kernel<D, false, false>), grid, block, 0, stream, p);
     return hipGetLastError();
 }
 
@@ -476,14 +455,12 @@ hipError_t launch_rows(const Args& p, bool bf16, bool pg, hipStream_t stream)
 
 namespace q4 {
 
-hipError_t launch_attend_rows(const q4attend::Args& p, int row_blocks, bool bf16, bool pages_of_16, hipStream_t stream)
+hipError_t launch_attend_rows(const q4attend::Args& p, bool bf16, bool pages_of_16, hipStream_t stream)
 {
-    const int d = p.dim <= 64 ? 64 : p.dim <= 128 ? 128 : 256;
-    if (p.dim < 8 || p.dim > 256 || p.dim % 8 || p.workers < 1 || (row_blocks != 1 && row_blocks != 2))
-        return hipErrorInvalidValue;
-    if (d == 64) return row_blocks == 1 ? launch_rows<64, 1>(p, bf16, pages_of_16, stream) : launch_rows<64, 2>(p, bf16, pages_of_16, stream);
-    if (d == 128) return row_blocks == 1 ? launch_rows<128, 1>(p, bf16, pages_of_16, stream) : launch_rows<128, 2>(p, bf16, pages_of_16, stream);
-    return row_blocks == 1 ? launch_rows<256, 1>(p, bf16, pages_of_16, stream) : launch_rows<256, 2>(p, bf16, pages_of_16, stream);
+    if (p.dim < 8 || p.dim > 256 || p.dim % 8 || p.workers < 1) return hipErrorInvalidValue;
+    if (p.dim <= 64) return launch_rows<64>(p, bf16, pages_of_16, stream);
+    if (p.dim <= 128) return launch_rows<128>(p, bf16, pages_of_16, stream);
+    return launch_rows<256>(p, bf16, pages_of_16, stream);
 }
 
 }  // namespace q4

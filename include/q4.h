@@ -574,8 +574,8 @@ size_t q4_attend_workspace(const q4_cache* c, int heads);
  *
  * dim is a multiple of 8, at most 256; strides of q and the cache are
  * multiples of 8 values, their base 16-byte aligned. `workspace` is device
- * memory of at least q4_attend_workspace bytes whose first 16 KiB are zero before
- * its first use (each call leaves them so); calls that share it must not overlap
+ * memory of at least q4_attend_workspace bytes whose first 64 KiB are zero before
+ * its first use (each call leaves them fit for the next); calls that share it must not overlap
  * in time. Host and device never synchronize; the call may be captured.
  */
 q4_status q4_attend(const q4_cache* c, const uint16_t* q, int64_t q_token, int64_t q_head, int heads, int tokens,
