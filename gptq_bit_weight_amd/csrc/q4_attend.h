@@ -61,7 +61,7 @@ struct Args {
     q4::FastDiv div_g, div_page;           // by heads of a group; by rows of a page (or 16-row blocks of one)
 };
 
-constexpr float kLow = -1e30f;             // running maximum of a row that has seen no key
+constexpr float kLow = -3.4028234663852886e38f;   // running maximum of a row that has seen no key (the lowest finite value)
 
 typedef short s4v __attribute__((ext_vector_type(4)));
 typedef short s8v __attribute__((ext_vector_type(8)));
@@ -104,6 +104,28 @@ template <int N>
 __device__ __forceinline__ void wait_loads()
 {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// A weight of zero does not keep a value that is not finite out of a sum. Where a
+// tile of keys is not wholly visible to a tile's rows, the kernels therefore look
+// for such values, and multiply key by key if there are any: `lone` leaves one of
+// a fragment's eight keys, whose products only rows that see it take.
+template <bool BF>
+__device__ __forceinline__ bool not_finite(u2 v)
+{
+    constexpr uint32_t E = BF ? 0x7f80u : 0x7c00u;
+    bool r = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) r |= ((v[i] & E) == E) | ((v[i] >> 16 & E) == E);
+    return r;
+}
+__device__ __forceinline__ u4 lone(u2 a0, u2 a1, int key, bool mine)
+{
+    u4 a = u4{a0[0], a0[1], a1[0], a1[1]};
+    const uint32_t keep = key & 1 ? 0xffff0000u : 0xffffu;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = mine && i == key >> 1 ? a[i] & keep : 0u;
+    return a;
 }
 
 // A wave-uniform LDS address.

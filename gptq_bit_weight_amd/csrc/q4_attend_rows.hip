@@ -57,7 +57,7 @@ __device__ __forceinline__ Span span(const Args& p, int b)
 }
 
 template <int D, bool BF, bool PG>
-__global__ __launch_bounds__(NT, D == 64 ? 4 : D == 128 ? 2 : 1) void q4_attend_rows_kernel(Args p)
+__global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void q4_attend_rows_kernel(Args p)
 {
     constexpr int PITCH = 2 * D;               // bytes of a row in LDS
     constexpr int CPR = D / 8;                 // 16-byte chunks of a row
@@ -278,7 +278,8 @@ __global__ __launch_bounds__(NT, D == 64 ? 4 : D == 128 ? 2 : 1) void q4_attend_
                 // ---- softmax: lane holds keys first + 16 h + 4 quad + e of row c16
                 sc[0] *= p.scale;
                 sc[1] *= p.scale;
-                if (first + KT - 1 > all_hi || first < all_lo) {
+                const bool edge = first + KT - 1 > all_hi || first < all_lo;
+                if (edge) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -314,13 +315,41 @@ __global__ __launch_bounds__(NT, D == 64 ? 4 : D == 128 ? 2 : 1) void q4_attend_
                 else wait_loads<0>();
                 __builtin_amdgcn_sched_barrier(0);
                 // ---- O^T += V^T P^T: keys in the order in which the lanes hold P^T
+                auto mma = [&](u4 a, f4 c) {
+                    if constexpr (BF) return mfma16(bitcast<b8>(a), bitcast<b8>(pt), c);
+                    else return mfma16(bitcast<h8>(a), bitcast<h8>(pt), c);
+                };
+                bool apart = false;
+                if (edge) {
 #pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    const char* at = vb + (vx ^ (d << 5));
-                    const u2 a0 = read_tr(at), a1 = read_tr(at + 16 * PITCH);
-                    const u4 a = u4{a0[0], a0[1], a1[0], a1[1]};
-                    if constexpr (BF) acc[d] = mfma16(bitcast<b8>(a), bitcast<b8>(pt), acc[d]);
-                    else acc[d] = mfma16(bitcast<h8>(a), bitcast<h8>(pt), acc[d]);
+                    for (int d = 0; d < DT; ++d) {
+                        const char* at = vb + (vx ^ (d << 5));
+                        apart |= not_finite<BF>(read_tr(at)) | not_finite<BF>(read_tr(at + 16 * PITCH));
+                    }
+                    apart = __any(apart);
+                }
+                if (!apart) {
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) {
+                        const char* at = vb + (vx ^ (d << 5));
+                        const u2 a0 = read_tr(at), a1 = read_tr(at + 16 * PITCH);
+                        acc[d] = mma(u4{a0[0], a0[1], a1[0], a1[1]}, acc[d]);
+                    }
+                } else {
+                    // (key 16 h + 4 q + e of the tile is value 4 h + e of the lanes of quad q)
+#pragma clang loop unroll(disable)
+                    for (int x = 0; x < KT; ++x) {
+                        const bool sees = first + x >= klo && first + x <= khi;
+#pragma unroll
+                        for (int d = 0; d < DT; ++d) {
+                            const char* at = vb + (vx ^ (d << 5));
+                            const u4 a = lone(read_tr(at), read_tr(at + 16 * PITCH), x >> 4 << 2 | (x & 3), quad == (x >> 2 & 3));
+                            const f4 y = mma(a, f4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[d][e] += sees ? y[e] : 0.f;
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    }
                 }
                 __builtin_amdgcn_sched_barrier(0);
                 if (more) load(i + 1, VALUES);

@@ -411,6 +411,98 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
     if (alive) output((steps - 1) & (NS - 1));
     wait_loads<0>();      // (no load may land in LDS that is no longer this workgroup's)
 
+    // ---- outputs that are not finite, and keys that not all of the rows see: a
+    // row may have them from a key that it does not see (q4_attend.h). The workgroup
+    // then goes through its tiles again one by one, the partly visible ones key by key.
+    const bool edges = base + j0 * KT < all_lo || base + j1 * KT - 1 > all_hi;
+    bool again = false;
+    if (alive && edges) {
+        float z = 0.f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) z = __builtin_fmaf(acc[d][e], 0.f, z);
+        again = !(z == 0.f);
+    }
+    if (__syncthreads_or(again)) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[d][e] = 0.f;
+        m = kLow;
+        l = 0.f;
+#pragma clang loop unroll(disable)
+        for (int j = j0; j < j1; ++j) {
+            if (((j - j0) & 63) == 0) {
+                batch(j, KEYS);
+                batch(j, VALUES);
+            }
+            load(j, KEYS, 0);
+            load(j, VALUES, 0);
+            wait_loads<0>();
+            __syncthreads();
+            if (alive) {
+                scores(0, sa);
+                __builtin_amdgcn_sched_barrier(0);
+                const int first = base + j * KT;
+                float top = -INFINITY;
+#pragma unroll
+                for (int h = 0; h < HH; ++h)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int key = first + 32 * h + 8 * (e >> 2) + 4 * lhi + (e & 3);
+                        sa[h][e] = key >= klo && key <= pos ? sa[h][e] : -INFINITY;
+                        top = fmaxf(top, sa[h][e]);
+                    }
+                const float m1 = fmaxf(m, max_halves(top) * p.scale), a = exp2_fast(m - m1);
+                m = m1;
+                l *= a;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) acc[d][e] *= a;
+#pragma unroll
+                for (int h = 0; h < HH; ++h)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        sa[h][e] = exp2_fast(__builtin_fmaf(sa[h][e], p.scale, -m1));
+                        l += sa[h][e];
+                    }
+#pragma unroll
+                for (int s = 0; s < 2 * HH; ++s)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int at = 8 * (s & 1) + 2 * e;
+                        pt[s][e] = pack2<BF>(sa[s >> 1][at], sa[s >> 1][at + 1]);
+                    }
+                if (first + KT - 1 > all_hi || first < all_lo) {
+                    // (key 16 s + 8 q + 4 h + e of the tile is value 4 q + e of pt[s] in lanes of half h)
+#pragma unroll
+                    for (int s = 0; s < 2 * HH; ++s)
+#pragma clang loop unroll(disable)
+                        for (int x = 0; x < 16; ++x) {
+                            const int key = first + 16 * s + x;
+                            const bool sees = key >= klo && key <= pos;
+#pragma unroll
+                            for (int d = 0; d < DT; ++d) {
+                                f16x y;
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) y[e] = 0.f;
+                                y = mma(lone(read_tr(va[0][d] + s * 16 * PITCH), read_tr(va[1][d] + s * 16 * PITCH),
+                                             x >> 3 << 2 | (x & 3), lhi == (x >> 2 & 1)), pt[s], y);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) acc[d][e] += sees ? y[e] : 0.f;
+                                __builtin_amdgcn_sched_barrier(0);
+                            }
+                        }
+                } else {
+                    output(0);
+                }
+            }
+            __syncthreads();
+        }
+    }
+
     // ---- store, or leave a partial result
     const float ls = sum_halves(l);
     if (parts == 1) {

@@ -569,8 +569,8 @@ size_t q4_attend_workspace(const q4_cache* c, int heads);
  * Only rows that some token of the tile sees are read, and of the table only
  * the entries of pages that hold them. Entries outside [0, pages), lengths above
  * table_width * page_size and starts outside the tokens do not lead outside
- * the tensors, but the result then has no meaning. A key or value that is not
- * finite reaches every row whose tile of keys it is in.
+ * the tensors, but the result then has no meaning. Keys and values that are not
+ * finite reach the tokens that see them and no others.
  *
  * dim is a multiple of 8, at most 256; strides of q and the cache are
  * multiples of 8 values, their base 16-byte aligned. `workspace` is device

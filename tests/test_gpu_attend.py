@@ -222,6 +222,47 @@ def test_pages_before_the_window_may_be_gone():
         check(q4.PagedCache(kc, vc).attend(q, starts, lengths, table, window=window), ref, tol)
 
 
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("news,lens,window,ps", [
+    ([4], [40], 0, 16), ([200], [200], 0, 16), ([200], [333], 70, 16), ([5, 1], [50, 9], 7, 16), ([70], [6000], 0, 64),
+    ([130], [131], 0, 7), ([1], [500], 33, 16)])
+def test_values_that_are_not_finite_stay_with_those_who_see_them(dt, D, news, lens, window, ps):
+    """One value and one key of the cache infinite or NaN: tokens before it (or
+    past its window) are as without it, in every row of the same tile of keys;
+    of those that see the value, only its column changes, and a NaN key's
+    tokens are NaN."""
+    import gptq_bit_weight_amd as q4
+    q, kc, vc, starts, lengths, table = make(dt, 4, 2, D, ps, news, lens, spread=0.1)
+    n, m = news[0], lens[0]
+    pos = torch.arange(m - n, m, device="cuda")
+    for at in sorted({m - 1, m - max(1, n // 2), max(0, m - n), max(0, m - n - window)}):
+        page, row = int(table[0, at // ps]), at % ps
+        for bad, where in ((math.inf, vc), (-math.inf, vc), (math.nan, vc), (math.nan, kc)):
+            keep = where[page, 1, row, 3].item()
+            clean = reference(q, kc, vc, news, lens, table, window)
+            where[page, 1, row, 3] = bad
+            y = q4.PagedCache(kc, vc).attend(q, starts, lengths, table, window=window)
+            where[page, 1, row, 3] = keep
+            sees = torch.zeros(q.shape[0], dtype=torch.bool, device="cuda")
+            sees[:n] = (pos >= at) & (pos < at + window if window else True)
+            hit = torch.zeros_like(y, dtype=torch.bool)
+            hit[:, 2:, 3 if where is vc else slice(None)] = sees.view(-1, *([1] * (1 if where is vc else 2)))
+            got = y[hit]
+            assert (torch.isnan(got) if math.isnan(bad) else got == bad).all(), (at, bad)
+            check(torch.where(hit, 0, y), torch.where(hit, 0, clean[0]), clean[1], f"{bad} at key {at}")
+
+
+def test_very_low_scores():
+    """Scores far below zero, all of them the same number: a softmax goes by
+    differences, so the result is that of scores of zero."""
+    import gptq_bit_weight_amd as q4
+    q, kc, vc, starts, lengths, table = make(torch.bfloat16, 4, 2, 128, 16, [1, 40], [30, 90])
+    q[:], kc[:] = 2.0 ** 60, -(2.0 ** 50)
+    y = q4.PagedCache(kc, vc).attend(q, starts, lengths, table)
+    check(y, *reference(torch.zeros_like(q), kc, vc, [1, 40], [30, 90], table))
+
+
 def test_strides():
     """q as a view of a fused row, out as a view, a cache of another order,
     a table that is a view of a wider one."""
