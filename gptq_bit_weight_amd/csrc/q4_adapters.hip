@@ -30,12 +30,12 @@ constexpr int kMaxSlots = 4096;
 constexpr int kMaxRank = 1024;
 
 // ---- bank -------------------------------------------------------------------
-// A [parts][r][K] -> slot's [parts][rank][K], B [N][r] -> slot's [N][rp], zeros
-// past r; null A clears the slot.
+// A [parts][r][K] -> slot's [parts][rank][K], B [N][r] -> slot's [N / 32][rp / 8][32][8],
+// zeros past r and N; null A clears the slot.
 __global__ void q4_adapter_load_kernel(const uint16_t* A, const uint16_t* B, uint16_t* dA, uint16_t* dB, float* scale,
                                        float c, int parts, int r, int rank, int rp, int K, int N)
 {
-    const long long na = (long long)parts * rank * K, nb = (long long)N * rp, step = (long long)gridDim.x * blockDim.x;
+    const long long na = (long long)parts * rank * K, nb = (N + 31) / 32 * 32ll * rp, step = (long long)gridDim.x * blockDim.x;
     const long long id = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     for (long long i = id; i < na; i += step) {
         const long long row = i / K;
@@ -43,9 +43,9 @@ __global__ void q4_adapter_load_kernel(const uint16_t* A, const uint16_t* B, uin
         dA[i] = A && j < r ? A[((long long)p * r + j) * K + i % K] : (uint16_t)0;
     }
     for (long long i = id; i < nb; i += step) {
-        const long long n = i / rp;
-        const int j = (int)(i % rp);
-        dB[i] = A && j < r ? B[n * r + j] : (uint16_t)0;
+        const long long n = i / (32 * rp) * 32 + i / 8 % 32;
+        const int j = (int)(i % (32 * rp) / kChunk * 8 + i % 8);
+        dB[i] = A && n < N && j < r ? B[n * r + j] : (uint16_t)0;
     }
     if (id == 0) *scale = c;
 }
@@ -99,13 +99,14 @@ __global__ __launch_bounds__(64 * DW) void q4_adapter_few_kernel(const uint16_t*
 // ---- many rows --------------------------------------------------------------
 constexpr int MW = 8, MT = 64 * MW;    // waves, threads
 constexpr int MR = 16, MC = 32;        // rows and values of a workgroup
+constexpr int RPT = 4;                 // rows of the index that a thread looks at together
 
 struct ManyArgs {
     const uint16_t* x;
     const int* index;
     const uint16_t* A;
     const float* scale;
-    int *rows, *slot_of, *seg;
+    AdapterRow* rows;
     uint16_t *hi, *lo;
     int M, K, slots, rank, rp, parts;
 };
@@ -115,32 +116,50 @@ __global__ __launch_bounds__(MT) void q4_adapter_many_kernel(ManyArgs p)
 {
     extern __shared__ int count[];               // [slots + 1]: rows of each adapter; of none
     __shared__ float red[MW][MR][MC];
-    __shared__ int wave_n[MW], tile_row[MR];
-    __shared__ int s_slot, s_first, s_pos;
+    __shared__ int wave_n[RPT * MW], tile_row[MR];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int bins = p.slots + 1;
-    auto bin_of = [&](int i) {
-        const int s = p.index[i];
-        return (unsigned)s < (unsigned)p.slots ? s : p.slots;
+    // The index is gone through twice, RPT rows a thread at a time (row 2048 c + 512 u +
+    // tid); the first 2048 stay in registers.
+    auto bins_of = [&](int i0, int (&s)[RPT]) {
+#pragma unroll
+        for (int u = 0; u < RPT; ++u) {
+            const int i = i0 + u * MT + tid;
+            s[u] = i < p.M ? p.index[i] : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < RPT; ++u)
+            s[u] = i0 + u * MT + tid >= p.M ? -1 : (unsigned)s[u] < (unsigned)p.slots ? s[u] : p.slots;
     };
+    int bin0[RPT];
+    bins_of(0, bin0);
     for (int i = tid; i < bins; i += MT) count[i] = 0;
     __syncthreads();
-    for (int i0 = 64 * wave; i0 < p.M; i0 += MT) {
-        // one addition for each run of equal neighbours
-        const int i = i0 + lane;
-        const int s = i < p.M ? bin_of(i) : -1;
-        const int before = __shfl_up(s, 1);
-        const bool head = lane == 0 || s != before;
-        const unsigned long long heads = __ballot(head);
-        if (head && s >= 0) {
-            const unsigned long long after = lane == 63 ? 0 : heads >> (lane + 1) << (lane + 1);
-            atomicAdd(&count[s], (after ? (int)__builtin_ctzll(after) : 64) - lane);
+    auto add = [&](const int (&bin)[RPT]) {
+#pragma unroll
+        for (int u = 0; u < RPT; ++u) {
+            // one addition for each run of equal neighbours
+            const int s = bin[u], before = __shfl_up(s, 1);
+            const bool head = lane == 0 || s != before;
+            const unsigned long long heads = __ballot(head);
+            if (head && s >= 0) {
+                const unsigned long long after = lane == 63 ? 0 : heads >> (lane + 1) << (lane + 1);
+                atomicAdd(&count[s], (after ? (int)__builtin_ctzll(after) : 64) - lane);
+            }
         }
+    };
+    add(bin0);
+    for (int i0 = RPT * MT; i0 < p.M; i0 += RPT * MT) {
+        int bin[RPT];
+        bins_of(i0, bin);
+        add(bin);
     }
     __syncthreads();
     // ---- this workgroup's tile: of all bins' tiles of MR rows, the blockIdx.x-th
-    if (wave == 0) {
-        int tiles = 0, pos = 0, slot = -1, first = 0, at = 0;
+    // (in every wave, which needs no barrier)
+    int slot = -1, first = 0, pos = 0, n_rows = 0;
+    {
+        int tiles = 0, at = 0;
         for (int b0 = 0; b0 < bins; b0 += 64) {
             const int n = b0 + lane < bins ? count[b0 + lane] : 0;
             int t = (n + MR - 1) / MR, r = n;
@@ -149,51 +168,54 @@ __global__ __launch_bounds__(MT) void q4_adapter_many_kernel(ManyArgs p)
                 const int to = __shfl_up(t, d), ro = __shfl_up(r, d);
                 if (lane >= d) t += to, r += ro;
             }
-            if (blockIdx.x == 0 && blockIdx.y == 0 && b0 + lane < bins) p.seg[b0 + lane] = pos + r - n;
             const unsigned long long past = __ballot(tiles + t > (int)blockIdx.x);
-            if (past && slot < 0) {
+            if (past) {
                 const int f = (int)__builtin_ctzll(past);
                 const int mine = __builtin_amdgcn_readlane(n, f);
                 slot = b0 + f;
                 first = ((int)blockIdx.x - (tiles + __builtin_amdgcn_readlane(t, f) - (mine + MR - 1) / MR)) * MR;
-                at = pos + __builtin_amdgcn_readlane(r, f) - mine;
-                if (blockIdx.x) break;           // (the first workgroup goes through all bins)
+                pos = at + __builtin_amdgcn_readlane(r, f) - mine + first;
+                n_rows = min(MR, mine - first);
+                break;
             }
             tiles += __builtin_amdgcn_readlane(t, 63);
-            pos += __builtin_amdgcn_readlane(r, 63);
-        }
-        if (lane == 0) {
-            s_slot = slot;
-            s_first = first;
-            s_pos = at + first;
-            if (blockIdx.x == 0 && blockIdx.y == 0) p.seg[bins] = p.M;
+            at += __builtin_amdgcn_readlane(r, 63);
         }
     }
-    __syncthreads();
-    const int slot = __builtin_amdgcn_readfirstlane(s_slot), first = __builtin_amdgcn_readfirstlane(s_first);
     if (slot < 0) return;
-    const int n_rows = min(MR, count[slot] - first);
     // ---- its rows: those of the bin ranked first .. first + MR - 1
     int seen = 0;
-    for (int i0 = 0; i0 < p.M && seen < first + n_rows; i0 += MT) {
-        const int i = i0 + tid;
-        const bool mine = i < p.M && bin_of(i) == slot;
-        const unsigned long long b = __ballot(mine);
-        if (lane == 0) wave_n[wave] = (int)__builtin_popcountll(b);
-        __syncthreads();
-        int rank = seen + (int)__builtin_popcountll(b & ((1ull << lane) - 1));
-        for (int w = 0; w < MW; ++w) {
-            if (w < wave) rank += wave_n[w];
-            seen += wave_n[w];
+    auto pick = [&](int i0, const int (&bin)[RPT]) {
+        unsigned long long b[RPT];
+#pragma unroll
+        for (int u = 0; u < RPT; ++u) {
+            b[u] = __ballot(bin[u] == slot);
+            if (lane == 0) wave_n[u * MW + wave] = (int)__builtin_popcountll(b[u]);
         }
-        if (mine && rank >= first && rank < first + MR) tile_row[rank - first] = i;
         __syncthreads();
+        int before = seen;
+#pragma unroll
+        for (int u = 0; u < RPT; ++u) {
+            int rank = before;
+#pragma unroll
+            for (int w = 0; w < MW; ++w) {
+                if (w < wave) rank += wave_n[u * MW + w];
+                before += wave_n[u * MW + w];
+            }
+            rank += (int)__builtin_popcountll(b[u] & ((1ull << lane) - 1)) - first;
+            if (bin[u] == slot && rank >= 0 && rank < MR) tile_row[rank] = i0 + u * MT + tid;
+        }
+        seen = before;
+        __syncthreads();
+    };
+    pick(0, bin0);
+    for (int i0 = RPT * MT; i0 < p.M && seen < first + n_rows; i0 += RPT * MT) {
+        int bin[RPT];
+        bins_of(i0, bin);
+        pick(i0, bin);
     }
-    const int pos = __builtin_amdgcn_readfirstlane(s_pos);
-    if (blockIdx.y == 0 && tid < n_rows) {
-        p.rows[pos + tid] = tile_row[tid];
-        p.slot_of[pos + tid] = slot;
-    }
+    if (blockIdx.y == 0 && tid < n_rows)
+        p.rows[pos + tid] = AdapterRow{tile_row[tid], slot == p.slots ? -1 : slot, pos - first + count[slot], 0};
     if (slot == p.slots) return;                 // rows without an adapter
     // ---- 16 rows x 32 values, the waves' shares of K
     const int c16 = lane & 15, quad = lane >> 4, width = p.parts * p.rp, col0 = (int)blockIdx.y * MC;
@@ -206,7 +228,7 @@ __global__ __launch_bounds__(MT) void q4_adapter_many_kernel(ManyArgs p)
     }
     f4 acc[2] = {f4{0.f, 0.f, 0.f, 0.f}, f4{0.f, 0.f, 0.f, 0.f}};
     const int steps = p.K / 32, k0 = steps * wave / MW, k1 = steps * (wave + 1) / MW;
-    constexpr int U = 4;
+    constexpr int U = 8;       // k-steps whose loads are under way
     for (int k = k0; k < k1; k += U) {
         u4 a[U], b[U][2];
 #pragma unroll
@@ -242,7 +264,8 @@ __global__ __launch_bounds__(MT) void q4_adapter_many_kernel(ManyArgs p)
     const uint16_t hi = f32_to_act<BF>(z);
     // what the rounding leaves; nothing of a value beyond the type's range
     const float rest = z - act_to_f32<BF>(hi);
-    const size_t o = (size_t)(pos + row) * width + w;
+    const int at = pos + row;
+    const size_t o = ((size_t)(at >> 5) * width + (w & ~7)) * 32 + (at & 31) * 8 + (w & 7);
     p.hi[o] = hi;
     p.lo[o] = f32_to_act<BF>(__builtin_isfinite(rest) ? rest : 0.f);
 }
@@ -266,8 +289,11 @@ namespace q4 {
 
 namespace {
 
+// Values of a slot's B.
+size_t b_values(const q4_adapters* a) { return ((size_t)a->N + 31) / 32 * 32 * a->rp; }
+
 struct ManySpace {
-    int *rows, *slot_of, *seg;
+    AdapterRow* rows;
     uint16_t *hi, *lo;
     size_t bytes;
 };
@@ -283,9 +309,7 @@ ManySpace many_space(const q4_adapters* a, char* base, int rows)
         at += (bytes + 255) / 256 * 256;
         return p;
     };
-    s.rows = reinterpret_cast<int*>(take(m * 4));
-    s.slot_of = reinterpret_cast<int*>(take(m * 4));
-    s.seg = reinterpret_cast<int*>(take((size_t)(a->slots + 2) * 4));
+    s.rows = reinterpret_cast<AdapterRow*>(take(m * sizeof(AdapterRow)));
     s.hi = reinterpret_cast<uint16_t*>(take(m * width * 2));
     s.lo = reinterpret_cast<uint16_t*>(take(m * width * 2));
     s.bytes = at;
@@ -301,7 +325,7 @@ q4_status load_slot(q4_adapters* a, int slot, const uint16_t* A, const uint16_t*
     hipError_t e = hipGetDevice(&cur);
     if (e != hipSuccess) return fail(Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
     if (cur != a->device) return fail(Q4_ERR_INVALID_ARG, "%s: the bank is on device %d, the current device is %d", who, a->device, cur);
-    const size_t sa = (size_t)a->parts * a->rank * a->K, sb = (size_t)a->N * a->rp;
+    const size_t sa = (size_t)a->parts * a->rank * a->K, sb = b_values(a);
     const int grid = (int)std::min<size_t>((std::max(sa, sb) + 255) / 256, 4096);
     hipLaunchKernelGGL(q4_adapter_load_kernel, dim3(grid), dim3(256), 0, stream, A, B, a->A + slot * sa, a->B + slot * sb,
                        a->scale + slot, c, a->parts, rank, a->rank, a->rp, a->K, a->N);
@@ -358,6 +382,7 @@ q4_status adapters_prepare(q4_adapters* a, const uint16_t* x, const int* index, 
     args->B = a->B;
     args->part8 = a->part8;
     args->slots = a->slots;
+    args->b_slot = b_values(a);
     args->rp = a->rp;
     args->width = a->parts * a->rp;
     args->index = index;
@@ -376,8 +401,6 @@ q4_status adapters_prepare(q4_adapters* a, const uint16_t* x, const int* index, 
     char* base = a->many;
     const ManySpace s = many_space(a, base, held);
     args->rows = s.rows;
-    args->slot_of = s.slot_of;
-    args->seg = s.seg;
     args->hi = s.hi;
     args->lo = s.lo;
     ManyArgs p;
@@ -386,8 +409,6 @@ q4_status adapters_prepare(q4_adapters* a, const uint16_t* x, const int* index, 
     p.A = a->A;
     p.scale = a->scale;
     p.rows = s.rows;
-    p.slot_of = s.slot_of;
-    p.seg = s.seg;
     p.hi = s.hi;
     p.lo = s.lo;
     p.M = M;
@@ -445,7 +466,7 @@ q4_adapters* q4_adapters_make(const q4_matrix* h, int slots, int rank, int bf16)
     a->N = h->N;
     a->device = h->device;
     a->bf16 = bf16 != 0;
-    const size_t na = (size_t)slots * a->parts * rank * a->K * 2, nb = (size_t)slots * a->N * a->rp * 2;
+    const size_t na = (size_t)slots * a->parts * rank * a->K * 2, nb = (size_t)slots * q4::b_values(a) * 2;
     e = hipMalloc(&a->A, na);
     if (e == hipSuccess) e = hipMalloc(&a->B, nb);
     if (e == hipSuccess) e = hipMalloc(&a->scale, (size_t)slots * 4);

@@ -237,6 +237,9 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
     __shared__ __attribute__((aligned(1024))) char lds_a6[D > 6 ? A_TILE_BYTES : 1];
     __shared__ __attribute__((aligned(1024))) char lds_a7[D > 7 ? A_TILE_BYTES : 1];
     __shared__ int s_last;
+    // (AD) the present tile's positions: their rows, and their adapters and those' ends
+    __shared__ __attribute__((aligned(16))) uint32_t ad_row[AD ? BM : 1];
+    __shared__ int2 ad_seg[AD ? BM : 1];
 
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int wm = 0, wn = wave;   // (waves side by side along N)
@@ -486,7 +489,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
             const int chunk = (lane & 7) ^ ((row >> 1) & 7);
             c.a_k[e] = 8u * (uint32_t)chunk;
             if constexpr (AD) {
-                const uint32_t src = m0 + row < p.M ? (uint32_t)p.ad.rows[m0 + row] : 0u;
+                const uint32_t src = m0 + row < p.M ? (uint32_t)p.ad.rows[m0 + row].row : 0u;
                 c.a_off[e] = m0 + row < p.M ? (src * (uint32_t)p.K + c.a_k[e]) * 2u : kOOB;
             } else {
                 c.a_off[e] = ((uint32_t)(m0 + row) * (uint32_t)p.K + c.a_k[e]) * 2u;
@@ -517,6 +520,15 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
         // before they are refilled.
         if (!first_seg) lds_barrier();
         first_seg = false;
+        if constexpr (AD) {
+            static_assert(NT >= BM, "a thread for each position");
+            if (tid < BM) {
+                const bool in = m0 + tid < p.M;
+                const AdapterRow e = in ? p.ad.rows[m0 + tid] : AdapterRow{0, -1, 0, 0};
+                ad_row[tid] = (uint32_t)e.row;
+                ad_seg[tid] = int2{e.slot, e.end};
+            }
+        }
 #pragma unroll
         for (int d = 0; d + 1 < D; ++d) {
             const int kd = min(kb + d, ke - 1);
@@ -535,7 +547,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
         Q4S_VMCNT(0);
         if constexpr (AD) {
             if (kb == 0)
-                adapter_tile<BF, MI>(p.ad, m0, n0 + wn * 32, p.N, l32, lhi, [&](int i) -> f16x& { return acc[i][0]; });
+                adapter_tile<BF, MI>(p.ad, ad_seg, m0, n0 + wn * 32, p.N, l32, lhi, [&](int i) -> f16x& { return acc[i][0]; });
         }
 
         if (kb != 0 || ke != (int)ktiles) {
@@ -663,12 +675,12 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const int m = mb + 32 * i + 8 * g;    // (a multiple of 4)
-                        if (m >= p.M) continue;
-                        // (the map is padded to whole fours)
-                        const u4 to = *reinterpret_cast<const u4*>(p.ad.rows + m);
+                        const u4 to = *reinterpret_cast<const u4*>(ad_row + (m - m0));
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (m + e < p.M) p.out[(size_t)to[e] * p.N + n] = f32_to_act<BF>(acc[i][j][4 * g + e] + bv);
+                            // (row * N + n) * 2 < M * N * 2 <= 2^32 - 2: no wrap-around
+                            if (whole || m + e < p.M)
+                                buf_store2(ro, (to[e] * (uint32_t)p.N + (uint32_t)n) * 2u, 0u, f32_to_act<BF>(acc[i][j][4 * g + e] + bv));
                     }
             } else if (whole) {
                 // (m * N + n) * 2 < M * N * 2 <= 2^32 - 2: no wrap-around

@@ -563,7 +563,7 @@ __global__ __launch_bounds__(NT) void q4_gemv_kernel(const uint32_t* qweight, co
             const int m = idx / COLS, c = idx % COLS, n = n0 + c;
             if (n >= p.N) continue;
             float y = wg_sum(m, c);
-            if constexpr (AD) y += adapter_row<BF>(args.ad, m, n, p.N);
+            if constexpr (AD) y += adapter_row<BF>(args.ad, m, n);
             if (p.bias) y += act_to_f32<BF>(bias_h);
             p.out[(size_t)m * p.N + n] = f32_to_act<BF>(y);
         }
@@ -600,7 +600,7 @@ __global__ __launch_bounds__(NT) void q4_gemv_kernel(const uint32_t* qweight, co
         for (int s = 0; s < p.splits; ++s)
             y += __hip_atomic_load(&p.partials[((size_t)s * p.M + m) * p.N + n], __ATOMIC_RELAXED,
                                    __HIP_MEMORY_SCOPE_AGENT);
-        if constexpr (AD) y += adapter_row<BF>(args.ad, m, n, p.N);
+        if constexpr (AD) y += adapter_row<BF>(args.ad, m, n);
         if (p.bias) y += act_to_f32<BF>(bias_h);
         p.out[(size_t)m * p.N + n] = f32_to_act<BF>(y);
     }
