@@ -227,20 +227,23 @@ __global__ __launch_bounds__(MT) void q4_adapter_many_kernel(ManyArgs p)
         ar[h] = p.A + (((size_t)slot * p.parts + part) * p.rank + j) * p.K + 8 * quad;
     }
     f4 acc[2] = {f4{0.f, 0.f, 0.f, 0.f}, f4{0.f, 0.f, 0.f, 0.f}};
-    const int steps = p.K / 32, k0 = steps * wave / MW, k1 = steps * (wave + 1) / MW;
-    constexpr int U = 8;       // k-steps whose loads are under way
-    for (int k = k0; k < k1; k += U) {
+    // Steps of 32 values, in pairs (128 bytes of a row), dealt to the waves in turn: a
+    // workgroup reads a few KiB of each row side by side. (With a stretch of K for
+    // each wave all rows' reads, K values apart, fall on few of the L2's channels.)
+    const int steps = p.K / 32;
+    constexpr int U = 8;       // steps whose loads are under way
+    for (int k = 2 * wave; k < steps; k += U * MW) {
         u4 a[U], b[U][2];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int at = min(k + u, k1 - 1) * 32;
+            const int at = min(k + (u >> 1) * 2 * MW + (u & 1), steps - 1) * 32;
             a[u] = *reinterpret_cast<const u4*>(xr + at);
 #pragma unroll
             for (int h = 0; h < 2; ++h) b[u][h] = *reinterpret_cast<const u4*>(ar[h] + at);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (k + u >= k1) continue;
+            if (k + (u >> 1) * 2 * MW + (u & 1) >= steps) continue;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if constexpr (BF) acc[h] = mfma16(bitcast<b8>(a[u]), bitcast<b8>(b[u][h]), acc[h]);
