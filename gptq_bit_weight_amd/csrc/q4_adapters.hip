@@ -5,12 +5,14 @@
 // nothing is sorted, since each row reads its own adapter whatever the others do.
 //
 // Many rows: the rows of one adapter are multiplied together. Each workgroup
-// counts the index (the same counting sort in all, a few microseconds for
-// thousands of rows, in place of a launch of its own) and takes 16 rows of one
-// adapter, 32 of its values; its eight waves share K (16 x 16 x 32 matrix
-// instructions, both operands straight from memory, where the rows of x and
-// A are dense along K) and their sums are joined in LDS. The workgroups also leave
-// the order of the rows for the product's launch.
+// counts the index (the same counting sort in all, 2 us for 77 rows and 4 us for 2048,
+// in place of a launch of its own) and takes 32 rows of one adapter, 32 or 64 of
+// its values and a share of K. Bound: what one CU can fetch, about 45 GB/s where the
+// rows come from beyond its XCD's L2, so the shares of K spread a tile over CUs until
+// there are two workgroups each; x and A stream through a ring of LDS stages, 64 of
+// K each, filled by direct loads of whole 128-byte lines, and the last workgroup of a
+// tile to arrive adds the shares in order. The workgroups also leave the order
+// of the rows for the product's launch.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -97,9 +99,13 @@ __global__ __launch_bounds__(64 * DW) void q4_adapter_few_kernel(const uint16_t*
 }
 
 // ---- many rows --------------------------------------------------------------
-constexpr int MW = 8, MT = 64 * MW;    // waves, threads
-constexpr int MR = 16, MC = 32;        // rows and values of a workgroup
-constexpr int RPT = 4;                 // rows of the index that a thread looks at together
+constexpr int MW = 4, MT = 64 * MW;    // waves, threads
+constexpr int MR = 32;                 // rows of a workgroup
+constexpr int RPT = 8;                 // rows of the index that a thread looks at together
+constexpr int KC = 64;                 // values of K of a stage: a 16-value step for each wave
+constexpr int NS = 6;                  // stages
+constexpr int kMaxShares = 8;          // of K
+constexpr int kManyGroups = 512;       // workgroups that shares are made for (two a CU)
 
 struct ManyArgs {
     const uint16_t* x;
@@ -108,19 +114,25 @@ struct ManyArgs {
     const float* scale;
     AdapterRow* rows;
     uint16_t *hi, *lo;
+    float* partial;                    // [tile][columns' block][share][MR][64]
+    uint32_t* arrived;                 // [tile][columns' block], zero between calls
     int M, K, slots, rank, rp, parts;
 };
 
-template <bool BF>
-__global__ __launch_bounds__(MT) void q4_adapter_many_kernel(ManyArgs p)
+template <bool BF, int NB>
+__global__ __launch_bounds__(MT, 2) void q4_adapter_many_kernel(ManyArgs p)
 {
+    constexpr int MC = 32 * NB;                  // values of a workgroup
+    constexpr int STAGE = (MR + MC) * KC * 2;    // bytes
+    constexpr int LPW = (MR + MC) / 8 / MW;      // direct loads of a wave a stage, 8 rows each
     extern __shared__ int count[];               // [slots + 1]: rows of each adapter; of none
-    __shared__ float red[MW][MR][MC];
+    __shared__ __attribute__((aligned(1024))) char lds[NS * STAGE];
     __shared__ int wave_n[RPT * MW], tile_row[MR];
+    __shared__ int s_last;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int bins = p.slots + 1;
-    // The index is gone through twice, RPT rows a thread at a time (row 2048 c + 512 u +
-    // tid); the first 2048 stay in registers.
+    // The index is gone through twice, RPT rows a thread at a time; the first
+    // RPT MT of them stay in registers.
     auto bins_of = [&](int i0, int (&s)[RPT]) {
 #pragma unroll
         for (int u = 0; u < RPT; ++u) {
@@ -135,9 +147,10 @@ __global__ __launch_bounds__(MT) void q4_adapter_many_kernel(ManyArgs p)
     bins_of(0, bin0);
     for (int i = tid; i < bins; i += MT) count[i] = 0;
     __syncthreads();
-    auto add = [&](const int (&bin)[RPT]) {
+    auto add = [&](int i0, const int (&bin)[RPT]) {
 #pragma unroll
         for (int u = 0; u < RPT; ++u) {
+            if (i0 + u * MT >= p.M) continue;
             // one addition for each run of equal neighbours
             const int s = bin[u], before = __shfl_up(s, 1);
             const bool head = lane == 0 || s != before;
@@ -148,11 +161,11 @@ __global__ __launch_bounds__(MT) void q4_adapter_many_kernel(ManyArgs p)
             }
         }
     };
-    add(bin0);
+    add(0, bin0);
     for (int i0 = RPT * MT; i0 < p.M; i0 += RPT * MT) {
         int bin[RPT];
         bins_of(i0, bin);
-        add(bin);
+        add(i0, bin);
     }
     __syncthreads();
     // ---- this workgroup's tile: of all bins' tiles of MR rows, the blockIdx.x-th
@@ -183,6 +196,8 @@ __global__ __launch_bounds__(MT) void q4_adapter_many_kernel(ManyArgs p)
         }
     }
     if (slot < 0) return;
+    const bool none = slot == p.slots;           // rows without an adapter: only their order
+    if (none && (blockIdx.y || blockIdx.z)) return;
     // ---- its rows: those of the bin ranked first .. first + MR - 1
     int seen = 0;
     auto pick = [&](int i0, const int (&bin)[RPT]) {
@@ -214,63 +229,126 @@ __global__ __launch_bounds__(MT) void q4_adapter_many_kernel(ManyArgs p)
         bins_of(i0, bin);
         pick(i0, bin);
     }
-    if (blockIdx.y == 0 && tid < n_rows)
-        p.rows[pos + tid] = AdapterRow{tile_row[tid], slot == p.slots ? -1 : slot, pos - first + count[slot], 0};
-    if (slot == p.slots) return;                 // rows without an adapter
-    // ---- 16 rows x 32 values, the waves' shares of K
-    const int c16 = lane & 15, quad = lane >> 4, width = p.parts * p.rp, col0 = (int)blockIdx.y * MC;
-    const uint16_t* xr = p.x + (size_t)tile_row[min(c16, n_rows - 1)] * p.K + 8 * quad;
-    const uint16_t* ar[2];
+    if (blockIdx.y == 0 && blockIdx.z == 0 && tid < n_rows)
+        p.rows[pos + tid] = AdapterRow{tile_row[tid], none ? -1 : slot, pos - first + count[slot], 0};
+    if (none) return;
+    // ---- a stage is 128 bytes of each row of x and of A; its 16-byte chunk c lies at
+    // place c ^ row % 8, which spreads a product's operand over the banks
+    const int width = p.parts * p.rp, col0 = (int)blockIdx.y * MC, l32 = lane & 31, lhi = lane >> 5;
+    const char* src[LPW];
+    const int chunk = (lane & 7) ^ (lane >> 3);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int w = min(col0 + 16 * h + c16, width - 1), part = w / p.rp, j = min(w - part * p.rp, p.rank - 1);
-        ar[h] = p.A + (((size_t)slot * p.parts + part) * p.rank + j) * p.K + 8 * quad;
+    for (int i = 0; i < LPW; ++i) {
+        const int row = 8 * (wave + MW * i) + (lane >> 3);
+        const int w = min(col0 + max(row - MR, 0), width - 1), part = w / p.rp, j = min(w - part * p.rp, p.rank - 1);
+        const uint16_t* r = row < MR ? p.x + (size_t)tile_row[min(row, n_rows - 1)] * p.K
+                                     : p.A + (((size_t)slot * p.parts + part) * p.rank + j) * p.K;
+        src[i] = reinterpret_cast<const char*>(r);
     }
-    f4 acc[2] = {f4{0.f, 0.f, 0.f, 0.f}, f4{0.f, 0.f, 0.f, 0.f}};
-    // Steps of 32 values, in pairs (128 bytes of a row), dealt to the waves in turn: a
-    // workgroup reads a few KiB of each row side by side. (With a stretch of K for
-    // each wave all rows' reads, K values apart, fall on few of the L2's channels.)
-    const int steps = p.K / 32;
-    constexpr int U = 8;       // steps whose loads are under way
-    for (int k = 2 * wave; k < steps; k += U * MW) {
-        u4 a[U], b[U][2];
+    const uint32_t base = lds_address(lds) + (uint32_t)wave * 1024u;
+    const int shares = (int)gridDim.z, chunks = (p.K + KC - 1) / KC;
+    const int c0 = chunks * (int)blockIdx.z / shares, c1 = chunks * ((int)blockIdx.z + 1) / shares;
+    auto load = [&](int c, int stage) {
+        // (past K, whose multiple is 32, the first half repeats; it is not multiplied)
+        const int at = c * KC + chunk * 8 < p.K ? chunk : chunk & 3;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int at = min(k + (u >> 1) * 2 * MW + (u & 1), steps - 1) * 32;
-            a[u] = *reinterpret_cast<const u4*>(xr + at);
+        for (int i = 0; i < LPW; ++i) dma_lane(src[i] + ((size_t)c * KC * 2 + at * 16), base + (uint32_t)(stage * STAGE + i * MW * 1024));
+    };
+    f16x acc[NB];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) b[u][h] = *reinterpret_cast<const u4*>(ar[h] + at);
-        }
+    for (int h = 0; h < NB; ++h)
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (k + (u >> 1) * 2 * MW + (u & 1) >= steps) continue;
+        for (int e = 0; e < 16; ++e) acc[h][e] = 0.f;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if constexpr (BF) acc[h] = mfma16(bitcast<b8>(a[u]), bitcast<b8>(b[u][h]), acc[h]);
-                else acc[h] = mfma16(bitcast<h8>(a[u]), bitcast<h8>(b[u][h]), acc[h]);
+    for (int i = 0; i < NS - 1; ++i) load(min(c0 + i, c1 - 1), i);
+    int stage = 0;
+    const char* operand = lds + l32 * (KC * 2) + (((2 * wave + lhi) ^ (l32 & 7)) << 4);
+    for (int c = c0; c < c1; ++c) {
+        // this stage has landed, in every wave, and the one before is read
+        wait_loads<(NS - 2) * LPW>();
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        load(min(c + NS - 1, c1 - 1), stage == 0 ? NS - 1 : stage - 1);
+        __builtin_amdgcn_sched_barrier(0);
+        if (c * KC + 16 * wave < p.K) {
+            const u4 a = *reinterpret_cast<const u4*>(operand + stage * STAGE);
+#pragma unroll
+            for (int h = 0; h < NB; ++h) {
+                const u4 b = *reinterpret_cast<const u4*>(operand + stage * STAGE + (MR + 32 * h) * (KC * 2));
+                if constexpr (BF) acc[h] = mfma32(bitcast<b8>(a), bitcast<b8>(b), acc[h]);
+                else acc[h] = mfma32(bitcast<h8>(a), bitcast<h8>(b), acc[h]);
             }
         }
+        stage = stage + 1 == NS ? 0 : stage + 1;
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) red[wave][4 * quad + e][16 * h + c16] = acc[h][e];
+    wait_loads<0>();      // (the repeated last ones, before their stage is written)
     __syncthreads();
-    const int row = tid / MC, w = col0 + tid % MC;
-    static_assert(MT == MR * MC, "one value a thread");
-    if (row >= n_rows || w >= width) return;
-    float z = red[0][row][tid % MC];
+    // ---- the waves' sums: a thread takes 8 values of one row
+    constexpr int PITCH = MC + 4;
+    float(*red)[MR][PITCH] = reinterpret_cast<float(*)[MR][PITCH]>(lds);
+    static_assert(sizeof(float) * MW * MR * PITCH <= sizeof(lds), "sums in the stages");
 #pragma unroll
-    for (int v = 1; v < MW; ++v) z += red[v][row][tid % MC];
+    for (int h = 0; h < NB; ++h)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) red[wave][8 * (e >> 2) + 4 * lhi + (e & 3)][32 * h + l32] = acc[h][e];
+    __syncthreads();
+    const int row = tid % MR, c8 = tid / MR * 8, w0 = col0 + c8;
+    const bool mine = c8 < MC && row < n_rows && w0 < width;
+    f4 z[2] = {f4{0.f, 0.f, 0.f, 0.f}, f4{0.f, 0.f, 0.f, 0.f}};
+    if (mine)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            z[h] = *reinterpret_cast<const f4*>(&red[0][row][c8 + 4 * h]);
+#pragma unroll
+            for (int v = 1; v < MW; ++v) z[h] += *reinterpret_cast<const f4*>(&red[v][row][c8 + 4 * h]);
+        }
+    // ---- the shares of K, in order, by the last to arrive
+    if (shares > 1) {
+        const int block = (int)blockIdx.x * (int)gridDim.y + (int)blockIdx.y;
+        const rsrc_t r = make_rsrc(p.partial + (size_t)block * shares * (MR * 64), (uint32_t)shares * (MR * 64 * 4));
+        const uint32_t at = (uint32_t)(c8 * MR + row * 8) * 4u;
+        if (mine)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) put16(r, (uint32_t)blockIdx.z * (MR * 64 * 4) + at + 16u * h, z[h]);
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        if (tid == 0)
+            s_last = __hip_atomic_fetch_add(&p.arrived[block], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)(shares - 1);
+        __syncthreads();
+        if (!s_last) return;
+        if (tid == 0) __hip_atomic_store(&p.arrived[block], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        f4 o[kMaxShares][2];
+#pragma unroll
+        for (int s = 0; s < kMaxShares; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) o[s][h] = take16(r, (uint32_t)min(s, shares - 1) * (MR * 64 * 4) + at + 16u * h);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            z[h] = o[0][h];
+#pragma unroll
+            for (int s = 1; s < kMaxShares; ++s)
+                if (s < shares) z[h] += o[s][h];
+        }
+    }
+    if (!mine) return;
     // (values past the rank meet zeros of B: they must be finite)
-    z = w % p.rp < p.rank ? z * p.scale[slot] : 0.f;
-    const uint16_t hi = f32_to_act<BF>(z);
-    // what the rounding leaves; nothing of a value beyond the type's range
-    const float rest = z - act_to_f32<BF>(hi);
+    const float scale = p.scale[slot];
+    u4 hi, lo;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float y = (w0 + e) % p.rp < p.rank ? z[e >> 2][e & 3] * scale : 0.f;
+        const uint16_t t = f32_to_act<BF>(y);
+        // what the rounding leaves; nothing of a value beyond the type's range
+        const float rest = y - act_to_f32<BF>(t);
+        const uint16_t u = f32_to_act<BF>(__builtin_isfinite(rest) ? rest : 0.f);
+        hi[e >> 1] = e & 1 ? hi[e >> 1] | (uint32_t)t << 16 : t;
+        lo[e >> 1] = e & 1 ? lo[e >> 1] | (uint32_t)u << 16 : u;
+    }
     const int at = pos + row;
-    const size_t o = ((size_t)(at >> 5) * width + (w & ~7)) * 32 + (at & 31) * 8 + (w & 7);
-    p.hi[o] = hi;
-    p.lo[o] = f32_to_act<BF>(__builtin_isfinite(rest) ? rest : 0.f);
+    const size_t o = ((size_t)(at >> 5) * width + w0) * 32 + (at & 31) * 8;
+    *reinterpret_cast<u4*>(p.hi + o) = hi;
+    *reinterpret_cast<u4*>(p.lo + o) = lo;
 }
 
 }  // namespace
@@ -296,10 +374,15 @@ namespace {
 size_t b_values(const q4_adapters* a) { return ((size_t)a->N + 31) / 32 * 32 * a->rp; }
 
 struct ManySpace {
+    uint32_t* arrived;
+    float* partial;
     AdapterRow* rows;
     uint16_t *hi, *lo;
     size_t bytes;
 };
+
+// (a count for each tile whose K is shared, and their sums)
+constexpr size_t kArrivedBytes = kManyGroups * sizeof(uint32_t), kPartialBytes = (size_t)kManyGroups * MR * 64 * sizeof(float);
 
 // The many-row workspace of a bank: rows padded to whole output tiles.
 ManySpace many_space(const q4_adapters* a, char* base, int rows)
@@ -312,6 +395,8 @@ ManySpace many_space(const q4_adapters* a, char* base, int rows)
         at += (bytes + 255) / 256 * 256;
         return p;
     };
+    s.arrived = reinterpret_cast<uint32_t*>(take(kArrivedBytes));
+    s.partial = reinterpret_cast<float*>(take(kPartialBytes));
     s.rows = reinterpret_cast<AdapterRow*>(take(m * sizeof(AdapterRow)));
     s.hi = reinterpret_cast<uint16_t*>(take(m * width * 2));
     s.lo = reinterpret_cast<uint16_t*>(take(m * width * 2));
@@ -363,6 +448,7 @@ q4_status adapters_reserve(q4_adapters* a, int M, hipStream_t stream)
                     "uncaptured call with this M (or larger) first", who, M);
     char* fresh = nullptr;
     e = hipMalloc(&fresh, many_space(a, nullptr, M).bytes);
+    if (e == hipSuccess && (e = hipMemsetAsync(fresh, 0, kArrivedBytes, stream)) != hipSuccess) (void)hipFree(fresh);
     if (e != hipSuccess) return fail(e == hipErrorOutOfMemory ? Q4_ERR_OOM : Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
     // (earlier launches, and graphs, may still use the outgrown one)
     try {
@@ -420,11 +506,24 @@ q4_status adapters_prepare(q4_adapters* a, const uint16_t* x, const int* index, 
     p.rank = a->rank;
     p.rp = a->rp;
     p.parts = a->parts;
-    // tiles: a whole one each MR rows, and a partial one each bin with rows
-    const dim3 grid(M / MR + std::min(a->slots + 1, M), (args->width + MC - 1) / MC), block(MT);
+    p.partial = s.partial;
+    p.arrived = s.arrived;
+    // tiles: a whole one each MR rows, and a partial one each bin with rows; K is
+    // shared out while there are fewer workgroups than the chip holds, in shares of
+    // 256 values and more
+    const bool narrow = args->width <= 32;
+    const int tiles = M / MR + std::min(a->slots + 1, M), blocks = narrow ? 1 : (args->width + 63) / 64;
+    const int shares = (int)std::clamp<long long>(kManyGroups / ((long long)tiles * blocks), 1, std::min(kMaxShares, std::max(a->K / 256, 1)));
+    const dim3 grid(tiles, blocks, shares), block(MT);
     const size_t lds = (size_t)(a->slots + 1) * sizeof(int);
-    if (a->bf16) hipLaunchKernelGGL((q4_adapter_many_kernel<true>), grid, block, lds, stream, p);
-    else hipLaunchKernelGGL((q4_adapter_many_kernel<false>), grid, block, lds, stream, p);
+    auto launch = [&](auto bf, auto nb) {
+        hipLaunchKernelGGL((q4_adapter_many_kernel<decltype(bf)::value, decltype(nb)::value>), grid, block, lds, stream, p);
+    };
+    using std::integral_constant;
+    if (a->bf16 && narrow) launch(integral_constant<bool, true>{}, integral_constant<int, 1>{});
+    else if (a->bf16) launch(integral_constant<bool, true>{}, integral_constant<int, 2>{});
+    else if (narrow) launch(integral_constant<bool, false>{}, integral_constant<int, 1>{});
+    else launch(integral_constant<bool, false>{}, integral_constant<int, 2>{});
     e = hipGetLastError();
     return e == hipSuccess ? Q4_OK : fail(Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
 }

@@ -93,19 +93,6 @@ __device__ __forceinline__ void dma(const char* base, const uint32_t (&off)[N], 
                      ::"v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(b), "s"(dst) : "memory", "scc");
 }
 
-// The same with an address of its own for each lane.
-__device__ __forceinline__ void dma_lane(const char* src, uint32_t dst)
-{
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(dst) : "memory");
-}
-
-// All but the newest N vector-memory operations are done.
-template <int N>
-__device__ __forceinline__ void wait_loads()
-{
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
 // A weight of zero does not keep a value that is not finite out of a sum. Where a
 // tile of keys is not wholly visible to a tile's rows, the kernels therefore look
 // for such values, and multiply key by key if there are any: `lone` leaves one of
@@ -126,12 +113,6 @@ __device__ __forceinline__ u4 lone(u2 a0, u2 a1, int key, bool mine)
 #pragma unroll
     for (int i = 0; i < 4; ++i) a[i] = mine && i == key >> 1 ? a[i] & keep : 0u;
     return a;
-}
-
-// A wave-uniform LDS address.
-__device__ __forceinline__ uint32_t lds_address(const void* p)
-{
-    return (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p);
 }
 
 // A head's row lies in LDS as 16-byte chunks, chunk c of row r at place
@@ -200,26 +181,6 @@ __device__ __forceinline__ Request request(const Args& p, int b)
     r.n = min(max(p.starts[b + 1] - r.start, 0), p.T - r.start);
     r.len = min(max(p.lengths[b], 0), p.max_len);
     return r;
-}
-
-// Device-coherent stores and loads of partial results (scope bit sc1: past
-// the XCD's own L2), at a byte offset of a wave-uniform slot.
-constexpr int kDeviceScope = 16;
-__device__ __forceinline__ void put16(rsrc_t r, uint32_t off, f4 v)
-{
-    __builtin_amdgcn_raw_buffer_store_b128(bitcast<u4>(v), r, (int)off, 0, kDeviceScope);
-}
-__device__ __forceinline__ void put4(rsrc_t r, uint32_t off, float v)
-{
-    __builtin_amdgcn_raw_buffer_store_b32(bitcast<uint32_t>(v), r, (int)off, 0, kDeviceScope);
-}
-__device__ __forceinline__ f4 take16(rsrc_t r, uint32_t off)
-{
-    return bitcast<f4>(__builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, kDeviceScope));
-}
-__device__ __forceinline__ float take4(rsrc_t r, uint32_t off)
-{
-    return bitcast<float>(__builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, kDeviceScope));
 }
 
 // Four values of an output row.

@@ -339,4 +339,46 @@ __device__ __forceinline__ uint16_t f32_to_act(float v)
     else return f32_to_f16_bits(v);
 }
 
+// 16 bytes a lane from an address of its own straight into LDS: lane l's land at
+// dst + 16 l (dst is wave-uniform). In assembly, with no register result, so that the
+// kernel counts the loads out itself (wait_loads). (s_nop: one wait state after a
+// write of m0, and those of the write of dst's SGPR.)
+__device__ __forceinline__ void dma_lane(const char* src, uint32_t dst)
+{
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(dst) : "memory");
+}
+
+// All but the newest N vector-memory operations are done.
+template <int N>
+__device__ __forceinline__ void wait_loads()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// A wave-uniform LDS address.
+__device__ __forceinline__ uint32_t lds_address(const void* p)
+{
+    return (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p);
+}
+
+// Device-coherent stores and loads of partial results (scope bit sc1: past
+// the XCD's own L2), at a byte offset of a wave-uniform slot.
+constexpr int kDeviceScope = 16;
+__device__ __forceinline__ void put16(rsrc_t r, uint32_t off, f4 v)
+{
+    __builtin_amdgcn_raw_buffer_store_b128(bitcast<u4>(v), r, (int)off, 0, kDeviceScope);
+}
+__device__ __forceinline__ void put4(rsrc_t r, uint32_t off, float v)
+{
+    __builtin_amdgcn_raw_buffer_store_b32(bitcast<uint32_t>(v), r, (int)off, 0, kDeviceScope);
+}
+__device__ __forceinline__ f4 take16(rsrc_t r, uint32_t off)
+{
+    return bitcast<f4>(__builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, kDeviceScope));
+}
+__device__ __forceinline__ float take4(rsrc_t r, uint32_t off)
+{
+    return bitcast<float>(__builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, kDeviceScope));
+}
+
 }  // namespace q4dev
