@@ -60,89 +60,134 @@ __device__ __forceinline__ float adapter_row(const AdapterArgs& a, int m, int n)
     return y;
 }
 
-// Adds the adapters of positions m0 .. m0 + 32 MI - 1 to a wave's accumulators:
-// acc(i) is the 32 x 32 tile of positions m0 + 32 i .. and columns n0 .. n0 + 31
-// (lane: column n0 + l32, rows 8 (r / 4) + 4 lhi + r % 4). seg[i], in LDS, is the
-// adapter of position m0 + i (-1: none, or past the last) and where its rows end.
+// Adds the adapters of positions m0 .. m0 + 32 MI - 1 to the accumulators of a
+// workgroup of NW waves, whose columns are n0 .. n0 + 32 NW - 1, 32 a wave: acc(i) is
+// the 32 x 32 tile of positions m0 + 32 i .. (lane: column l32 of the wave's, rows 8 (r
+// / 4) + 4 lhi + r % 4). seg[i], in LDS, is the adapter of position m0 + i (-1: none,
+// or past the last) and where its rows end. lds_hi and lds_lo take 64 values of c A x
+// of every position each; no load into them is under way, and all waves come here.
 //
-// Bound: latency, so operands are asked for ahead: 32 values of rank at a time, the
-// next 32 positions' c A x and the next adapter's B while the present ones are
-// multiplied. Each operand is one dense KiB of its 32 positions or columns.
+// Bound: latency. 64 values of rank at a time, the positions' c A x comes to LDS once for
+// all waves; then each wave goes by runs, the positions of one adapter inside one tile,
+// with the B of the next PF runs under way. (With the operands straight from memory a
+// run at a time, 2048 rows of 8 adapters of rank 64 took 16 us on it, 77 rows of 12 took
+// 10.) The runs are bit masks, and their adapters lanes of a register: looking
+// each run up in LDS cost about as much as its products.
 //
-// A tile that is one adapter's takes its products directly; one that several
-// share (or whose columns are of several parts) takes each through a result of
-// its own, so that values of one request that are not finite stay its own.
-template <bool BF, int MI, class Acc>
-__device__ __forceinline__ void adapter_tile(const AdapterArgs& a, const int2* seg, int m0, int n0, int N, int l32, int lhi, Acc&& acc)
+// A run's products are a result of their own, of which only its rows (and its part's
+// columns) are added, so that values of one request that are not finite stay its own.
+template <bool BF, int MI, int NW, class Acc>
+__device__ __forceinline__ void adapter_tile(const AdapterArgs& a, const int2* seg, char* lds_hi, char* lds_lo, int m0, int n0, int N,
+                                             int wave, int lane, Acc&& acc)
 {
-    constexpr int KC = 2;               // 16-value steps of rank at a time
+    constexpr int RC = 64, KC = RC / 16;   // values of rank in LDS, and their 16-value steps
+    // steps that runs are gone through for, runs ahead (the accumulators of 256 rows
+    // leave room for less)
+    constexpr int KB = MI <= 2 ? 4 : 2, PF = MI <= 2 ? 3 : 2;
+    constexpr int J = MI / 2;              // groups of 64 positions
+    static_assert(MI % 2 == 0 && MI * 2 * KC % NW == 0, "whole groups; whole loads of a wave");
     auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
     if (uniform(seg[0].x) < 0) return;
-    int mine = 0, first = 0, last = 0;
+    const int l32 = lane & 31, lhi = lane >> 5, own = n0 + 32 * wave;
+    int mine = 0, first = 0, last = 0, wg_first = 0, wg_last = 0;
     if (a.part8) {
-        mine = a.part8[min(n0 + l32, N - 1) >> 3];
-        first = uniform(a.part8[min(n0, N - 1) >> 3]);
-        last = uniform(a.part8[min(n0 + 31, N - 1) >> 3]);
+        mine = a.part8[min(own + l32, N - 1) >> 3];
+        first = uniform(a.part8[min(own, N - 1) >> 3]);
+        last = uniform(a.part8[min(own + 31, N - 1) >> 3]);
+        wg_first = uniform(a.part8[n0 >> 3]);
+        wg_last = uniform(a.part8[min(n0 + 32 * NW - 1, N - 1) >> 3]);
+    }
+    // the adapters of 64 positions and where runs begin (the first position without
+    // one begins the last, which ends all)
+    int slot[J];
+    uint64_t starts[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        slot[j] = seg[64 * j + lane].x;
+        const int before = seg[max(64 * j + lane - 1, 0)].x;
+        starts[j] = __ballot((lane & 31) == 0 || slot[j] != before);
     }
     auto mma = [](u4 x, u4 y, f16x c) {
         if constexpr (BF) return mfma32(bitcast<b8>(x), bitcast<b8>(y), c);
         else return mfma32(bitcast<h8>(x), bitcast<h8>(y), c);
     };
     const u4 zero = u4{0, 0, 0, 0};
-    const uint16_t* bn = a.B + (size_t)(min(n0, N - 1) >> 5) * a.rp * 32 + l32 * 8;
-    const uint16_t* tn = a.hi + (size_t)(m0 >> 5) * a.width * 32 + l32 * 8;
-    const ptrdiff_t to_lo = a.lo - a.hi;
-    for (int part = first; part <= last; ++part)
-        for (int k = 8 * lhi; k - 8 * lhi < a.rp; k += 16 * KC) {
-            u4 h[KC], l[KC], nh[KC], nl[KC], nb[KC];
-            auto load_t = [&](int i) {
+    const uint16_t* bn = a.B + ((size_t)(min(own, N - 1) >> 5) * a.rp + 8 * lhi) * 32 + l32 * 8;
+    const uint32_t to_hi = lds_address(lds_hi), to_lo = lds_address(lds_lo);
+    bool fresh = true;
+    for (int part = wg_first; part <= wg_last; ++part)
+        for (int k = 0; k < a.rp; k += RC) {
+            const int chunks = min(RC, a.rp - k) >> 3;       // 8-value chunks of this stretch
+            if (!fresh) __syncthreads();
+            fresh = false;
 #pragma unroll
-                for (int c = 0; c < KC; ++c) {
-                    const bool in = k + 16 * c < a.rp;
-                    const uint16_t* t = tn + ((size_t)i * a.width + part * a.rp + k + 16 * c) * 32;
-                    nh[c] = in ? *reinterpret_cast<const u4*>(t) : zero;
-                    nl[c] = in ? *reinterpret_cast<const u4*>(t + to_lo) : zero;
-                }
-            };
-            auto load_b = [&](int s) {
+            for (int e = 0; e < MI * KC / NW; ++e) {
+                const int at = wave + NW * e, tile = at / KC, pair = at % KC;
+                if (2 * pair >= chunks) continue;
+                // (a chunk past an odd number's last repeats it; it meets zeros of B)
+                const size_t off = ((size_t)((m0 >> 5) + tile) * a.width + part * a.rp + k + 8 * min(2 * pair + lhi, chunks - 1)) * 32 + l32 * 8;
+                dma_lane(reinterpret_cast<const char*>(a.hi + off), to_hi + (uint32_t)at * 1024u);
+                dma_lane(reinterpret_cast<const char*>(a.lo + off), to_lo + (uint32_t)at * 1024u);
+            }
+            wait_loads<0>();
+            __syncthreads();
+            if (part < first || part > last) continue;
+            for (int c0 = 0; 2 * c0 < chunks; c0 += KB) {
 #pragma unroll
-                for (int c = 0; c < KC; ++c)
-                    nb[c] = k + 16 * c < a.rp && mine == part
-                                ? *reinterpret_cast<const u4*>(bn + s * a.b_slot + (size_t)(k + 16 * c) * 32) : zero;
-            };
-            int r = 0, s = uniform(seg[0].x);   // the next position, its adapter
-            load_t(0);
-            load_b(s);
+                for (int j = 0; j < J; ++j) {
+                    uint64_t runs = starts[j], ahead = runs;
+                    u4 b[PF][KB];
+                    auto load = [&](int q) {
+                        if (!ahead) return;
+                        const int s = __builtin_amdgcn_readlane(slot[j], (int)__builtin_ctzll(ahead));
+                        ahead &= ahead - 1;
+                        if (s < 0) return;
 #pragma unroll
-            for (int i = 0; i < MI; ++i) {
+                        for (int c = 0; c < KB; ++c)
+                            if (2 * (c0 + c) < chunks)
+                                b[q][c] = 2 * (c0 + c) + lhi < chunks && mine == part
+                                              ? *reinterpret_cast<const u4*>(bn + s * a.b_slot + (size_t)(k + 16 * (c0 + c)) * 32) : zero;
+                    };
 #pragma unroll
-                for (int c = 0; c < KC; ++c) h[c] = nh[c], l[c] = nl[c];
-                if (i + 1 < MI && s >= 0) load_t(i + 1);
+                    for (int q = 0; q < PF; ++q) load(q);
 #pragma clang loop unroll(disable)
-                while (s >= 0 && r < 32 * i + 32) {
-                    u4 b[KC];
+                    while (runs)
 #pragma unroll
-                    for (int c = 0; c < KC; ++c) b[c] = nb[c];
-                    const int from = r;
-                    r = min(32 * i + 32, uniform(seg[r].y) - m0);
-                    s = r < 32 * MI ? uniform(seg[r].x) : -1;
-                    if (s >= 0) load_b(s);
-                    if (first == last && r - from == 32) {
+                        for (int q = 0; q < PF; ++q) {
+                            if (!runs) continue;
+                            const int from = (int)__builtin_ctzll(runs);
+                            const int s = __builtin_amdgcn_readlane(slot[j], from);
+                            runs &= runs - 1;
+                            if (s < 0) {
+                                runs = 0;
+                                continue;
+                            }
+                            const int to = runs ? (int)__builtin_ctzll(runs) : 64;
+                            const int at = ((2 * j + (from >> 5)) * KC + c0) * 1024 + lane * 16;
+                            f16x y;
 #pragma unroll
-                        for (int c = 0; c < KC; ++c) acc(i) = mma(l[c], b[c], mma(h[c], b[c], acc(i)));
-                    } else {
-                        f16x y;
+                            for (int v = 0; v < 16; ++v) y[v] = 0.f;
 #pragma unroll
-                        for (int v = 0; v < 16; ++v) y[v] = 0.f;
+                            for (int c = 0; c < KB; ++c)
+                                if (2 * (c0 + c) < chunks)
+                                    y = mma(*reinterpret_cast<const u4*>(lds_lo + at + c * 1024), b[q][c],
+                                            mma(*reinterpret_cast<const u4*>(lds_hi + at + c * 1024), b[q][c], y));
+                            if (to - from < 32 || first != last) {
+                                const int lo = (from & 31) - 4 * lhi, hi = mine == part ? lo + to - from : -1;
 #pragma unroll
-                        for (int c = 0; c < KC; ++c) y = mma(l[c], b[c], mma(h[c], b[c], y));
-                        const int lo = from - 32 * i - 4 * lhi, hi = mine == part ? r - 32 * i - 4 * lhi : -1;
+                                for (int v = 0; v < 16; ++v) {
+                                    const int m = 8 * (v >> 2) + (v & 3);
+                                    y[v] = m >= lo && m < hi ? y[v] : 0.f;
+                                }
+                            }
+                            if (from < 32)
 #pragma unroll
-                        for (int v = 0; v < 16; ++v) {
-                            const int m = 8 * (v >> 2) + (v & 3);
-                            acc(i)[v] += m >= lo && m < hi ? y[v] : 0.f;
+                                for (int v = 0; v < 16; ++v) acc(2 * j)[v] += y[v];
+                            else
+#pragma unroll
+                                for (int v = 0; v < 16; ++v) acc(2 * j + 1)[v] += y[v];
+                            load(q);
                         }
-                    }
                 }
             }
         }

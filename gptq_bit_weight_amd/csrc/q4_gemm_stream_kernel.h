@@ -546,8 +546,12 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
         // Drain the last (unused) prefetch before the LDS is reused.
         Q4S_VMCNT(0);
         if constexpr (AD) {
-            if (kb == 0)
-                adapter_tile<BF, MI>(p.ad, ad_seg, m0, n0 + wn * 32, p.N, l32, lhi, [&](int i) -> f16x& { return acc[i][0]; });
+            if (kb == 0) {
+                lds_barrier();     // (every wave's loads have landed and its reads are done)
+                static_assert(G::A_TILE_BYTES == BM * 64 * 2 && G::BN == 32 * NW, "64 values of a position in a stage");
+                adapter_tile<BF, MI, NW>(p.ad, ad_seg, lds_a0, lds_a1, m0, n0, p.N, wave, lane,
+                                         [&](int i) -> f16x& { return acc[i][0]; });
+            }
         }
 
         if (kb != 0 || ke != (int)ktiles) {
