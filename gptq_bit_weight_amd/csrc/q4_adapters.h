@@ -15,9 +15,9 @@
 namespace q4dev {
 
 // A position in the order of the adapters: its row of the call, its adapter (-1:
-// none) and the position at which that adapter's rows end.
+// none) and whether that adapter's B has values that are not finite.
 struct AdapterRow {
-    int row, slot, end, pad;
+    int row, slot, wild, pad;
 };
 
 struct AdapterArgs {
@@ -64,8 +64,9 @@ __device__ __forceinline__ float adapter_row(const AdapterArgs& a, int m, int n)
 // workgroup of NW waves, whose columns are n0 .. n0 + 32 NW - 1, 32 a wave: acc(i) is
 // the 32 x 32 tile of positions m0 + 32 i .. (lane: column l32 of the wave's, rows 8 (r
 // / 4) + 4 lhi + r % 4). seg[i], in LDS, is the adapter of position m0 + i (-1: none,
-// or past the last) and where its rows end. lds_hi and lds_lo take 64 values of c A x
-// of every position each; no load into them is under way, and all waves come here.
+// or past the last; kWild added where its B has values that are not finite).
+// lds_hi and lds_lo take 64 values of c A x of every position each; no load into
+// them is under way, and all waves come here.
 //
 // Bound: latency. 64 values of rank at a time, the positions' c A x comes to LDS once for
 // all waves; then each wave goes by runs, the positions of one adapter inside one tile,
@@ -74,20 +75,22 @@ __device__ __forceinline__ float adapter_row(const AdapterArgs& a, int m, int n)
 // 10.) The runs are bit masks, and their adapters lanes of a register: looking
 // each run up in LDS cost about as much as its products.
 //
-// A run's products are a result of their own, of which only its rows (and its part's
-// columns) are added, so that values of one request that are not finite stay its own.
+// Other rows of a run's tile meet it with zeros for their c A x; where the run's B has
+// values that are not finite, its products are a result of their own, of which only
+// its rows are added: values of one request that are not finite stay its own.
+constexpr int kWild = 1 << 20;
 template <bool BF, int MI, int NW, class Acc>
-__device__ __forceinline__ void adapter_tile(const AdapterArgs& a, const int2* seg, char* lds_hi, char* lds_lo, int m0, int n0, int N,
+__device__ __forceinline__ void adapter_tile(const AdapterArgs& a, const int* seg, char* lds_hi, char* lds_lo, int m0, int n0, int N,
                                              int wave, int lane, Acc&& acc)
 {
     constexpr int RC = 64, KC = RC / 16;   // values of rank in LDS, and their 16-value steps
     // steps that runs are gone through for, runs ahead (the accumulators of 256 rows
     // leave room for less)
-    constexpr int KB = MI <= 2 ? 4 : 2, PF = MI <= 2 ? 3 : 2;
+    constexpr int KB = 2, PF = MI <= 2 ? 6 : 2;
     constexpr int J = MI / 2;              // groups of 64 positions
     static_assert(MI % 2 == 0 && MI * 2 * KC % NW == 0, "whole groups; whole loads of a wave");
     auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
-    if (uniform(seg[0].x) < 0) return;
+    if (uniform(seg[0]) < 0) return;
     const int l32 = lane & 31, lhi = lane >> 5, own = n0 + 32 * wave;
     int mine = 0, first = 0, last = 0, wg_first = 0, wg_last = 0;
     if (a.part8) {
@@ -103,8 +106,8 @@ __device__ __forceinline__ void adapter_tile(const AdapterArgs& a, const int2* s
     uint64_t starts[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-        slot[j] = seg[64 * j + lane].x;
-        const int before = seg[max(64 * j + lane - 1, 0)].x;
+        slot[j] = seg[64 * j + lane];
+        const int before = seg[max(64 * j + lane - 1, 0)];
         starts[j] = __ballot((lane & 31) == 0 || slot[j] != before);
     }
     auto mma = [](u4 x, u4 y, f16x c) {
@@ -129,27 +132,38 @@ __device__ __forceinline__ void adapter_tile(const AdapterArgs& a, const int2* s
                 dma_lane(reinterpret_cast<const char*>(a.hi + off), to_hi + (uint32_t)at * 1024u);
                 dma_lane(reinterpret_cast<const char*>(a.lo + off), to_lo + (uint32_t)at * 1024u);
             }
+            const bool wanted = part >= first && part <= last;
+            u4 b[PF][KB];
+            uint64_t ahead = 0;
+            int c0 = 0;
+            auto load = [&](int q, int j) {
+                if (!ahead) return;
+                const int s = __builtin_amdgcn_readlane(slot[j], (int)__builtin_ctzll(ahead));
+                ahead &= ahead - 1;
+                if (s < 0) return;
+#pragma unroll
+                for (int c = 0; c < KB; ++c)
+                    if (2 * (c0 + c) < chunks)
+                        b[q][c] = 2 * (c0 + c) + lhi < chunks && mine == part
+                                      ? *reinterpret_cast<const u4*>(bn + (s & (kWild - 1)) * a.b_slot + (size_t)(k + 16 * (c0 + c)) * 32) : zero;
+            };
+            if (wanted) {
+                ahead = starts[0];
+#pragma unroll
+                for (int q = 0; q < PF; ++q) load(q, 0);
+            }
             wait_loads<0>();
             __syncthreads();
-            if (part < first || part > last) continue;
-            for (int c0 = 0; 2 * c0 < chunks; c0 += KB) {
+            if (!wanted) continue;
+            for (; 2 * c0 < chunks; c0 += KB) {
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
-                    uint64_t runs = starts[j], ahead = runs;
-                    u4 b[PF][KB];
-                    auto load = [&](int q) {
-                        if (!ahead) return;
-                        const int s = __builtin_amdgcn_readlane(slot[j], (int)__builtin_ctzll(ahead));
-                        ahead &= ahead - 1;
-                        if (s < 0) return;
+                    uint64_t runs = starts[j];
+                    if (j || c0) {
+                        ahead = runs;
 #pragma unroll
-                        for (int c = 0; c < KB; ++c)
-                            if (2 * (c0 + c) < chunks)
-                                b[q][c] = 2 * (c0 + c) + lhi < chunks && mine == part
-                                              ? *reinterpret_cast<const u4*>(bn + s * a.b_slot + (size_t)(k + 16 * (c0 + c)) * 32) : zero;
-                    };
-#pragma unroll
-                    for (int q = 0; q < PF; ++q) load(q);
+                        for (int q = 0; q < PF; ++q) load(q, j);
+                    }
 #pragma clang loop unroll(disable)
                     while (runs)
 #pragma unroll
@@ -163,30 +177,45 @@ __device__ __forceinline__ void adapter_tile(const AdapterArgs& a, const int2* s
                                 continue;
                             }
                             const int to = runs ? (int)__builtin_ctzll(runs) : 64;
+                            const bool in = l32 >= (from & 31) && l32 < (from & 31) + to - from;
                             const int at = ((2 * j + (from >> 5)) * KC + c0) * 1024 + lane * 16;
-                            f16x y;
+                            auto products = [&](f16x y) {
 #pragma unroll
-                            for (int v = 0; v < 16; ++v) y[v] = 0.f;
+                                for (int c = 0; c < KB; ++c)
+                                    if (2 * (c0 + c) < chunks) {
+                                        u4 h = *reinterpret_cast<const u4*>(lds_hi + at + c * 1024);
+                                        u4 l = *reinterpret_cast<const u4*>(lds_lo + at + c * 1024);
 #pragma unroll
-                            for (int c = 0; c < KB; ++c)
-                                if (2 * (c0 + c) < chunks)
-                                    y = mma(*reinterpret_cast<const u4*>(lds_lo + at + c * 1024), b[q][c],
-                                            mma(*reinterpret_cast<const u4*>(lds_hi + at + c * 1024), b[q][c], y));
-                            if (to - from < 32 || first != last) {
-                                const int lo = (from & 31) - 4 * lhi, hi = mine == part ? lo + to - from : -1;
+                                        for (int v = 0; v < 4; ++v) h[v] = in ? h[v] : 0u, l[v] = in ? l[v] : 0u;
+                                        y = mma(l, b[q][c], mma(h, b[q][c], y));
+                                    }
+                                return y;
+                            };
+                            // (256 rows' accumulators as operands in two branches would spill)
+                            if (MI <= 2 && s < kWild && first == last) {
+                                if (from < 32) acc(2 * j) = products(acc(2 * j));
+                                else acc(2 * j + 1) = products(acc(2 * j + 1));
+                            } else {
+                                f16x y;
 #pragma unroll
-                                for (int v = 0; v < 16; ++v) {
-                                    const int m = 8 * (v >> 2) + (v & 3);
-                                    y[v] = m >= lo && m < hi ? y[v] : 0.f;
+                                for (int v = 0; v < 16; ++v) y[v] = 0.f;
+                                y = products(y);
+                                if (s >= kWild || first != last) {
+                                    const int lo = (from & 31) - 4 * lhi, hi = mine == part ? lo + to - from : -1;
+#pragma unroll
+                                    for (int v = 0; v < 16; ++v) {
+                                        const int m = 8 * (v >> 2) + (v & 3);
+                                        y[v] = m >= lo && m < hi ? y[v] : 0.f;
+                                    }
                                 }
+                                if (from < 32)
+#pragma unroll
+                                    for (int v = 0; v < 16; ++v) acc(2 * j)[v] += y[v];
+                                else
+#pragma unroll
+                                    for (int v = 0; v < 16; ++v) acc(2 * j + 1)[v] += y[v];
                             }
-                            if (from < 32)
-#pragma unroll
-                                for (int v = 0; v < 16; ++v) acc(2 * j)[v] += y[v];
-                            else
-#pragma unroll
-                                for (int v = 0; v < 16; ++v) acc(2 * j + 1)[v] += y[v];
-                            load(q);
+                            load(q, j);
                         }
                 }
             }

@@ -34,8 +34,15 @@ constexpr int kMaxRank = 1024;
 // ---- bank -------------------------------------------------------------------
 // A [parts][r][K] -> slot's [parts][rank][K], B [N][r] -> slot's [N / 32][rp / 8][32][8],
 // zeros past r and N; null A clears the slot.
-__global__ void q4_adapter_load_kernel(const uint16_t* A, const uint16_t* B, uint16_t* dA, uint16_t* dB, float* scale,
-                                       float c, int parts, int r, int rank, int rp, int K, int N)
+__global__ void q4_adapter_reset_kernel(float* scale, int* wild, float c)
+{
+    *scale = c;
+    *wild = 0;
+}
+
+template <bool BF>
+__global__ void q4_adapter_load_kernel(const uint16_t* A, const uint16_t* B, uint16_t* dA, uint16_t* dB, int* wild, int parts,
+                                       int r, int rank, int rp, int K, int N)
 {
     const long long na = (long long)parts * rank * K, nb = (N + 31) / 32 * 32ll * rp, step = (long long)gridDim.x * blockDim.x;
     const long long id = (long long)blockIdx.x * blockDim.x + threadIdx.x;
@@ -47,9 +54,11 @@ __global__ void q4_adapter_load_kernel(const uint16_t* A, const uint16_t* B, uin
     for (long long i = id; i < nb; i += step) {
         const long long n = i / (32 * rp) * 32 + i / 8 % 32;
         const int j = (int)(i % (32 * rp) / kChunk * 8 + i % 8);
-        dB[i] = A && n < N && j < r ? B[n * r + j] : (uint16_t)0;
+        const uint16_t v = A && n < N && j < r ? B[n * r + j] : (uint16_t)0;
+        constexpr uint16_t E = BF ? 0x7f80 : 0x7c00;
+        if ((v & E) == E) *wild = 1;       // (any of them)
+        dB[i] = v;
     }
-    if (id == 0) *scale = c;
 }
 
 // ---- few rows ---------------------------------------------------------------
@@ -112,6 +121,7 @@ struct ManyArgs {
     const int* index;
     const uint16_t* A;
     const float* scale;
+    const int* wild;
     AdapterRow* rows;
     uint16_t *hi, *lo;
     float* partial;                    // [tile][columns' block][share][MR][64]
@@ -230,7 +240,7 @@ __global__ __launch_bounds__(MT, 2) void q4_adapter_many_kernel(ManyArgs p)
         pick(i0, bin);
     }
     if (blockIdx.y == 0 && blockIdx.z == 0 && tid < n_rows)
-        p.rows[pos + tid] = AdapterRow{tile_row[tid], none ? -1 : slot, pos - first + count[slot], 0};
+        p.rows[pos + tid] = AdapterRow{tile_row[tid], none ? -1 : slot, none ? 0 : p.wild[slot], 0};
     if (none) return;
     // ---- a stage is 128 bytes of each row of x and of A; its 16-byte chunk c lies at
     // place c ^ row % 8, which spreads a product's operand over the banks
@@ -358,6 +368,7 @@ struct q4_adapters {
     bool bf16 = false;
     uint16_t *A = nullptr, *B = nullptr;
     float* scale = nullptr;
+    int* wild = nullptr;               // whether a slot's B has values that are not finite
     uint8_t* part8 = nullptr;
     float* t = nullptr;                // few rows: [Q4_GEMV_MAX_M][parts * rp]
     std::mutex mutex;
@@ -415,8 +426,9 @@ q4_status load_slot(q4_adapters* a, int slot, const uint16_t* A, const uint16_t*
     if (cur != a->device) return fail(Q4_ERR_INVALID_ARG, "%s: the bank is on device %d, the current device is %d", who, a->device, cur);
     const size_t sa = (size_t)a->parts * a->rank * a->K, sb = b_values(a);
     const int grid = (int)std::min<size_t>((std::max(sa, sb) + 255) / 256, 4096);
-    hipLaunchKernelGGL(q4_adapter_load_kernel, dim3(grid), dim3(256), 0, stream, A, B, a->A + slot * sa, a->B + slot * sb,
-                       a->scale + slot, c, a->parts, rank, a->rank, a->rp, a->K, a->N);
+    hipLaunchKernelGGL(q4_adapter_reset_kernel, dim3(1), dim3(1), 0, stream, a->scale + slot, a->wild + slot, c);
+    hipLaunchKernelGGL((a->bf16 ? q4_adapter_load_kernel<true> : q4_adapter_load_kernel<false>), dim3(grid), dim3(256), 0, stream, A, B,
+                       a->A + slot * sa, a->B + slot * sb, a->wild + slot, a->parts, rank, a->rank, a->rp, a->K, a->N);
     e = hipGetLastError();
     return e == hipSuccess ? Q4_OK : fail(Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
 }
@@ -497,6 +509,7 @@ q4_status adapters_prepare(q4_adapters* a, const uint16_t* x, const int* index, 
     p.index = index;
     p.A = a->A;
     p.scale = a->scale;
+    p.wild = a->wild;
     p.rows = s.rows;
     p.hi = s.hi;
     p.lo = s.lo;
@@ -572,11 +585,13 @@ q4_adapters* q4_adapters_make(const q4_matrix* h, int slots, int rank, int bf16)
     e = hipMalloc(&a->A, na);
     if (e == hipSuccess) e = hipMalloc(&a->B, nb);
     if (e == hipSuccess) e = hipMalloc(&a->scale, (size_t)slots * 4);
+    if (e == hipSuccess) e = hipMalloc(&a->wild, (size_t)slots * 4);
     if (e == hipSuccess) e = hipMalloc(&a->t, (size_t)q4::kGemvMaxM * a->parts * a->rp * 4);
     if (e == hipSuccess && a->parts > 1) e = hipMalloc(&a->part8, (size_t)a->N / 8);
     if (e == hipSuccess) e = hipMemset(a->A, 0, na);
     if (e == hipSuccess) e = hipMemset(a->B, 0, nb);
     if (e == hipSuccess) e = hipMemset(a->scale, 0, (size_t)slots * 4);
+    if (e == hipSuccess) e = hipMemset(a->wild, 0, (size_t)slots * 4);
     if (e == hipSuccess && a->parts > 1) {
         std::unique_ptr<uint8_t[]> part(new (std::nothrow) uint8_t[(size_t)a->N / 8]);
         if (!part) {
@@ -603,6 +618,7 @@ void q4_adapters_free(q4_adapters* a)
     (void)hipFree(a->A);
     (void)hipFree(a->B);
     (void)hipFree(a->scale);
+    (void)hipFree(a->wild);
     (void)hipFree(a->t);
     (void)hipFree(a->part8);
     (void)hipFree(a->many);

@@ -237,9 +237,9 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
     __shared__ __attribute__((aligned(1024))) char lds_a6[D > 6 ? A_TILE_BYTES : 1];
     __shared__ __attribute__((aligned(1024))) char lds_a7[D > 7 ? A_TILE_BYTES : 1];
     __shared__ int s_last;
-    // (AD) the present tile's positions: their rows, and their adapters and those' ends
+    // (AD) the present tile's positions: their rows and their adapters
     __shared__ __attribute__((aligned(16))) uint32_t ad_row[AD ? BM : 1];
-    __shared__ int2 ad_seg[AD ? BM : 1];
+    __shared__ int ad_seg[AD ? BM : 1];
 
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int wm = 0, wn = wave;   // (waves side by side along N)
@@ -526,7 +526,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
                 const bool in = m0 + tid < p.M;
                 const AdapterRow e = in ? p.ad.rows[m0 + tid] : AdapterRow{0, -1, 0, 0};
                 ad_row[tid] = (uint32_t)e.row;
-                ad_seg[tid] = int2{e.slot, e.end};
+                ad_seg[tid] = e.slot >= 0 && e.wild ? e.slot + kWild : e.slot;
             }
         }
 #pragma unroll
