@@ -437,35 +437,36 @@ class Q4Matrix:
         this matrix, of x's dtype); an index outside the slots (-1) adds nothing.
         index: int32 [M]. One rounding, of the whole sum (q4_matmul_adapters)."""
         torch = _torch()
-        h = self._handle()
+        h, dev, dt = self._handle(), self.device, bank.dtype
         if getattr(x, "dtype", None) not in (torch.float16, torch.bfloat16):
             raise ValueError(f"x must be float16 or bfloat16, got {getattr(x, 'dtype', type(x))}")
-        dt, dev = x.dtype, self.device
-        _dev_tensor(x, dt, "x")
+        if x.dtype is not dt:
+            raise ValueError(f"the adapters are {dt}, x is {x.dtype}")
         if x.dim() != 2 or x.shape[1] != self.K:
             raise ValueError(f"x must be [M, {self.K}], got {tuple(x.shape)}")
         M = x.shape[0]
-        if bank.dtype != dt:
-            raise ValueError(f"the adapters are {bank.dtype}, x is {dt}")
         if bank.N != self.N or bank.K != self.K or bank.part_n != self.part_n:
             raise ValueError("the adapters were made for another matrix")
-        _dev_tensor(index, torch.int32, "index", (M,))
+        checks = [(x, dt, "x", None), (index, torch.int32, "index", (M,))]
+        if bias is not None:
+            checks.append((bias, dt, "bias", (self.N,)))
+        if out is not None:
+            checks.append((out, dt, "out", (M, self.N)))
+        for t, want, name, shape in checks:
+            if not (isinstance(t, torch.Tensor) and t.dtype is want and t.device == dev and t.is_contiguous()
+                    and (shape is None or t.shape == shape)):
+                _dev_tensor(t, want, name, shape)
+                raise ValueError(f"{name} is on {t.device}, expected {dev}, the matrix's device")
         if out is None:
             if stream is None:
-                out = torch.empty((M, self.N), dtype=dt, device=dev)
+                out = x.new_empty((M, self.N))
             else:
                 with torch.cuda.stream(stream):
-                    out = torch.empty((M, self.N), dtype=dt, device=dev)
-        else:
-            _dev_tensor(out, dt, "out", (M, self.N))
-        if bias is not None:
-            _dev_tensor(bias, dt, "bias", (self.N,))
-        if x.device != dev or index.device != dev or out.device != dev or (bias is not None and bias.device != dev):
-            raise ValueError(f"x, index, out and bias must be on {dev}, the matrix's device")
+                    out = x.new_empty((M, self.N))
         from .attention import _call
         _call(load_library().q4_matmul_adapters, "q4_matmul_adapters", dev, stream,
               (h, bank._handle(), x.data_ptr(), bias.data_ptr() if bias is not None else None, index.data_ptr(),
-               out.data_ptr(), M, 1 if dt == torch.bfloat16 else 0), [t for t in (x, index, out, bias) if t is not None])
+               out.data_ptr(), M, 1 if dt is torch.bfloat16 else 0), () if stream is None else [t for t in (x, index, out, bias) if t is not None])
         return out
 
     def dequant_dump(self, path: int = PATH_GEMV, stream=None, dtype=None):

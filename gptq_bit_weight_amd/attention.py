@@ -31,7 +31,9 @@ _HALVES = (torch.float16, torch.bfloat16)
 # each is kept cheap: the current stream's handle without a Stream object is
 # 0.1 us against 1.8.)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _dense = torch.contiguous_format
+_Tensor, _int32_t, _int64_t = torch.Tensor, torch.int32, torch.int64
 
 
 class _Cache(ctypes.Structure):
@@ -42,42 +44,43 @@ class _Cache(ctypes.Structure):
 
 
 def _heads(t, name, device, dtype=None, tokens=None, heads=None, dim=None):
-    """Check a [tokens, heads, dim] tensor whose head values are dense."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in _HALVES or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name} must be {dtype or 'float16 or bfloat16'}, got {t.dtype}")
-    if t.device != device:
+    """Check a [tokens, heads, dim] tensor whose head values are dense; returns
+    its shape and strides."""
+    if isinstance(t, _Tensor):
+        d = t.dtype
+        if d in _HALVES and (dtype is None or d is dtype) and t.device == device:
+            s = t.shape
+            if len(s) == 3 and (tokens is None or s[0] == tokens) and (heads is None or s[1] == heads) and (dim is None or s[2] == dim):
+                st = t.stride()
+                if st[2] == 1 or s[2] <= 1:
+                    return s, st
+                raise ValueError(f"{name}: the values of a head must be contiguous")
+            want = [("tokens" if tokens is None else tokens), ("heads" if heads is None else heads), ("dim" if dim is None else dim)]
+            raise ValueError(f"{name} must be {want}, got {list(s)}")
+        if d not in _HALVES or (dtype is not None and d != dtype):
+            raise ValueError(f"{name} must be {dtype or 'float16 or bfloat16'}, got {d}")
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    s = t.shape
-    if len(s) != 3 or (tokens is not None and s[0] != tokens) or (heads is not None and s[1] != heads) \
-            or (dim is not None and s[2] != dim):
-        want = [("tokens" if tokens is None else tokens), ("heads" if heads is None else heads),
-                ("dim" if dim is None else dim)]
-        raise ValueError(f"{name} must be {want}, got {list(s)}")
-    if t.stride(2) != 1 and s[2] > 1:
-        raise ValueError(f"{name}: the values of a head must be contiguous")
-    return t
+    raise TypeError(f"{name} must be a torch.Tensor")
 
 
 def _index(t, name, device, n):
     """Check an index vector of n int32 or int64; returns its width in bits."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    bits = 64 if t.dtype == torch.int64 else 32
-    if bits == 32 and t.dtype != torch.int32:
-        raise ValueError(f"{name} must be int32 or int64, got {t.dtype}")
+    d = t.dtype
+    if d is not _int64_t and d is not _int32_t:
+        raise ValueError(f"{name} must be int32 or int64, got {d}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with shape [{n}], got {list(t.shape)}")
-    return bits
+    return 64 if d is _int64_t else 32
 
 
 def _int32(t, name, device, dims):
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.int32 or t.dim() != dims or t.device != device:
+    if t.dtype is not _int32_t or t.dim() != dims or t.device != device:
         raise ValueError(f"{name} must be int32 with {dims} dimensions on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
 
 
@@ -128,7 +131,7 @@ def _call(fn, what, device, stream, args, used=()):
         sp = stream.cuda_stream
         for t in used:          # their memory stays until the stream is done with it
             t.record_stream(stream)
-    if torch.cuda.current_device() == device.index:
+    if _device() == device.index:
         st = fn(*args, sp)
     else:
         with torch.cuda.device(device):
@@ -149,7 +152,17 @@ class _Rotate(torch.autograd.Function):
         positions, = ctx.saved_tensors
         if grad.stride(2) != 1:
             grad = grad.contiguous()
-        return ctx.rotary._rotate(grad, positions, not ctx.transpose, None, ctx.stream), None, None, None, None
+        # (on the forward pass's stream, between what makes the gradient and what
+        # takes it, which are on the one that was current then)
+        s = ctx.stream
+        if s is not None:
+            now = torch.cuda.current_stream(grad.device)
+            s.wait_stream(now)
+        out = _Rotate.apply(grad, ctx.rotary, positions, not ctx.transpose, s)
+        if s is not None:
+            now.wait_stream(s)
+            out.record_stream(now)
+        return out, None, None, None, None
 
 
 class Rotary:
@@ -204,11 +217,10 @@ class Rotary:
 
     def _rotate(self, x, positions, transpose, out, stream):
         dev = self.device
-        _heads(x, "x", dev, None, None, None, self.dim)
-        T, H, _ = x.shape
+        (T, H, _), xs = _heads(x, "x", dev, None, None, None, self.dim)
         bits = _index(positions, "positions", dev, T)
         out = _out_like(x, out, "out", stream)
-        xs, os_ = x.stride(), out.stride()
+        os_ = out.stride()
         _call(load_library().q4_rotary_apply, "q4_rotary_apply", dev, stream,
               (self._handle(), x.data_ptr(), xs[0], xs[1], out.data_ptr(), os_[0], os_[1], positions.data_ptr(), bits,
                T, H, 1 if transpose else 0, 1 if x.dtype == torch.bfloat16 else 0), (x, positions, out))
@@ -273,9 +285,8 @@ class PagedCache:
         outside the cache (-1 for padding) is not written. With q [tokens,
         heads, dim], returns it turned too (in q_out, which may be q)."""
         dev, dt, D, kv = self.device, self.dtype, self.dim, self.kv_heads
-        _heads(k, "k", dev, dt, None, kv, D)
-        T = k.shape[0]
-        _heads(v, "v", dev, dt, T, kv, D)
+        (T, _, _), ks = _heads(k, "k", dev, dt, None, kv, D)
+        _, vs = _heads(v, "v", dev, dt, T, kv, D)
         sb = _index(slots, "slots", dev, T)
         pb, pp, rh, qa = 32, None, None, (None, 0, 0, None, 0, 0, 0)
         used = (k, v, slots)
@@ -291,15 +302,14 @@ class PagedCache:
         if q is not None:
             if rotary is None:
                 raise ValueError("q is given without rotary")
-            _heads(q, "q", dev, dt, T, None, D)
+            (_, H, _), qs = _heads(q, "q", dev, dt, T, None, D)
             q_out = _out_like(q, q_out, "q_out", stream)
-            if q.shape[1]:
-                qs, os_ = q.stride(), q_out.stride()
-                qa = (q.data_ptr(), qs[0], qs[1], q_out.data_ptr(), os_[0], os_[1], q.shape[1])
+            if H:
+                os_ = q_out.stride()
+                qa = (q.data_ptr(), qs[0], qs[1], q_out.data_ptr(), os_[0], os_[1], H)
             used += (q, q_out)
         elif q_out is not None:
             raise ValueError("q_out is given without q")
-        ks, vs = k.stride(), v.stride()
         _call(load_library().q4_cache_append, "q4_cache_append", dev, stream,
               (self._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], slots.data_ptr(), sb, T, rh, pp, pb)
               + qa, used if stream is None else used + (self.k, self.v))
@@ -316,8 +326,7 @@ class PagedCache:
         a multiple of the cached heads, scale defaults to dim ** -0.5. Lengths
         stay on the device; nothing waits for it."""
         dev, dt = self.device, self.dtype
-        _heads(q, "q", dev, dt, None, None, self.dim)
-        T, H, D = q.shape
+        (T, H, D), qs = _heads(q, "q", dev, dt, None, None, self.dim)
         if H % self.kv_heads or not H:
             raise ValueError(f"q has {H} heads, the cache {self.kv_heads}")
         _int32(starts, "starts", dev, 1)
@@ -334,8 +343,11 @@ class PagedCache:
         window = int(window)
         if window < 0:
             raise ValueError(f"window must not be negative, got {window}")
-        if q.data_ptr() % 16 or q.stride(0) % 8 or q.stride(1) % 8:
-            q = q.contiguous() if stream is None else _on(stream, q.contiguous)
+        if q.data_ptr() % 16 or qs[0] % 8 or qs[1] % 8:
+            if stream is not None:
+                q.record_stream(stream)
+            q = _on(stream, torch.clone, q, memory_format=_dense)
+            qs = q.stride()
         if out is None:
             out = _out_like(q, None, "out", stream)
         else:
@@ -344,7 +356,7 @@ class PagedCache:
             if _overlap(out, q):
                 raise ValueError("out overlaps q")
         ws = self._workspace(H, stream)
-        qs, os_, ts = q.stride(), out.stride(), table.stride(0)
+        os_, ts = out.stride(), table.stride(0)
         _call(load_library().q4_attend, "q4_attend", dev, stream,
               (self._ref, q.data_ptr(), qs[0], qs[1], H, T, starts.data_ptr(), lengths.data_ptr(), table.data_ptr(),
                width, ts if ts > width else width, B, window, D ** -0.5 if scale is None else scale, out.data_ptr(),
@@ -364,12 +376,12 @@ class PagedCache:
                 _raise(load_library().q4_last_status(), "q4_attend_workspace")
             self._need[heads] = need
         if torch.cuda.is_current_stream_capturing():
-            ws = _zeros(need, self.device) if stream is None else _on(stream, _zeros, need, self.device)
+            ws = _on(stream, _zeros, need, self.device)
             return ws.data_ptr(), need, ws
         key = (self.device.index, _raw_stream(self.device.index) if stream is None else stream.cuda_stream)
         held = _workspaces.get(key)
         if held is None or held[1] < need:
-            ws = _zeros(need, self.device) if stream is None else _on(stream, _zeros, need, self.device)
+            ws = _on(stream, _zeros, need, self.device)
             held = _workspaces[key] = (ws.data_ptr(), need, ws)
         return held
 
@@ -381,6 +393,8 @@ def _zeros(n, device):
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def _on(stream, f, *args):
+def _on(stream, f, *args, **kw):
+    if stream is None:
+        return f(*args, **kw)
     with torch.cuda.stream(stream):
-        return f(*args)
+        return f(*args, **kw)

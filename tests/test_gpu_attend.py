@@ -288,6 +288,22 @@ def test_strides():
     check(cache.attend(odd, starts, lengths, table), ref, tol)
 
 
+def test_queries_off_sixteen_bytes():
+    """A dense q whose first value is not on 16 bytes."""
+    import gptq_bit_weight_amd as q4
+    q, kc, vc, starts, lengths, table = make(torch.float16, 8, 2, 128, 16, [1, 3], [200, 90])
+    odd = torch.zeros(q.numel() + 1, dtype=q.dtype, device="cuda")[1:].view(q.shape)
+    odd.copy_(q)
+    ref = reference(q, kc, vc, [1, 3], [200, 90], table)
+    cache = q4.PagedCache(kc, vc)
+    check(cache.attend(odd, starts, lengths, table), *ref)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    y = cache.attend(odd, starts, lengths, table, stream=s)
+    s.synchronize()
+    check(y, *ref)
+
+
 def test_runs_agree_to_the_bit():
     import gptq_bit_weight_amd as q4
     for news, lens in (([1, 1], [30000, 77]), ([300, 1], [5000, 900])):

@@ -209,6 +209,33 @@ def test_gradient():
     assert abs((x.grad.cpu().double() * d).sum() - diff) <= tol
 
 
+def test_gradient_on_another_stream():
+    """The backward pass of a call on a stream that is not the current one waits
+    for the gradient it takes, and what takes its result waits for it; and the
+    gradient of the gradient."""
+    import gptq_bit_weight_amd as q4
+    r = q4.Rotary(64, 32, scaling=SCALINGS["by_parts"])
+    g = torch.Generator().manual_seed(4)
+    pos = torch.arange(700, 705, device="cuda")
+    x = torch.randn(5, 3, 64, generator=g).bfloat16().cuda().requires_grad_()
+    up = torch.randn(5, 3, 64, generator=g).bfloat16().cuda()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y = r.rotate(x, pos, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    slow = torch.randn(4096, 4096, device="cuda")
+    for _ in range(4):
+        slow = slow @ slow * 1e-3       # what the gradient comes from takes a while
+    up2 = up + (slow[0, 0] * 0).nan_to_num().bfloat16()
+    y.backward(up2)
+    check(x.grad, *rotated(up, pos, 32, "half", "by_parts", True), "grad")
+    x2 = x.detach().clone().requires_grad_()
+    w = up.clone().requires_grad_()
+    gx, = torch.autograd.grad(r.rotate(x2, pos), x2, w, create_graph=True)
+    gw, = torch.autograd.grad(gx, w, x.detach())
+    check(gw, *rotated(x.detach(), pos, 32, "half", "by_parts"), "second")
+
+
 def test_graph_and_streams():
     """Captured, replayed with other data; and a call on a stream that is not
     the current one."""
