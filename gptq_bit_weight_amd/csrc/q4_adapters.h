@@ -10,6 +10,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "q4_device.h"
 
 namespace q4dev {
@@ -60,6 +62,15 @@ __device__ __forceinline__ float adapter_row(const AdapterArgs& a, int m, int n)
     return y;
 }
 
+template <int I, int N, class F>
+__device__ __forceinline__ void each(F&& f)
+{
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        each<I + 1, N>(f);
+    }
+}
+
 // Adds the adapters of positions m0 .. m0 + 32 MI - 1 to the accumulators of a
 // workgroup of NW waves, whose columns are n0 .. n0 + 32 NW - 1, 32 a wave: acc(i) is
 // the 32 x 32 tile of positions m0 + 32 i .. (lane: column l32 of the wave's, rows 8 (r
@@ -86,7 +97,7 @@ __device__ __forceinline__ void adapter_tile(const AdapterArgs& a, const int* se
     constexpr int RC = 64, KC = RC / 16;   // values of rank in LDS, and their 16-value steps
     // steps that runs are gone through for, runs ahead (the accumulators of 256 rows
     // leave room for less)
-    constexpr int KB = 2, PF = MI <= 2 ? 6 : 2;
+    constexpr int KB = 2, PF = MI <= 2 ? 4 : 2;
     constexpr int J = MI / 2;              // groups of 64 positions
     static_assert(MI % 2 == 0 && MI * 2 * KC % NW == 0, "whole groups; whole loads of a wave");
     auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
@@ -115,7 +126,7 @@ __device__ __forceinline__ void adapter_tile(const AdapterArgs& a, const int* se
         else return mfma32(bitcast<h8>(x), bitcast<h8>(y), c);
     };
     const u4 zero = u4{0, 0, 0, 0};
-    const uint16_t* bn = a.B + ((size_t)(min(own, N - 1) >> 5) * a.rp + 8 * lhi) * 32 + l32 * 8;
+    const uint16_t* bn = a.B + (size_t)(min(own, N - 1) >> 5) * a.rp * 32 + l32 * 8;
     const uint32_t to_hi = lds_address(lds_hi), to_lo = lds_address(lds_lo);
     bool fresh = true;
     for (int part = wg_first; part <= wg_last; ++part)
@@ -136,16 +147,19 @@ __device__ __forceinline__ void adapter_tile(const AdapterArgs& a, const int* se
             u4 b[PF][KB];
             uint64_t ahead = 0;
             int c0 = 0;
-            auto load = [&](int q, int j) {
-                if (!ahead) return;
-                const int s = __builtin_amdgcn_readlane(slot[j], (int)__builtin_ctzll(ahead));
+            // (64 rows: always as many loads, of something where there is no run left, so
+            // that the compiler can count those newer than the one it waits for; with a
+            // branch here every run waits for all, 77 rows of 12 adapters 35 us against
+            // 33. 256 rows mostly have long runs, for which the loads of nothing cost
+            // more: 2048 rows of 8 adapters 196 us against 184.)
+            auto load = [&](int q, int j) __attribute__((always_inline)) {
+                if (MI > 2 && !ahead) return;
+                const int s = ahead ? __builtin_amdgcn_readlane(slot[j], (int)__builtin_ctzll(ahead)) : 0;
                 ahead &= ahead - 1;
-                if (s < 0) return;
+                if (MI > 2 && s < 0) return;
+                const uint16_t* of = bn + (s < 0 ? 0 : s & (kWild - 1)) * a.b_slot + (size_t)k * 32;
 #pragma unroll
-                for (int c = 0; c < KB; ++c)
-                    if (2 * (c0 + c) < chunks)
-                        b[q][c] = 2 * (c0 + c) + lhi < chunks && mine == part
-                                      ? *reinterpret_cast<const u4*>(bn + (s & (kWild - 1)) * a.b_slot + (size_t)(k + 16 * (c0 + c)) * 32) : zero;
+                for (int c = 0; c < KB; ++c) b[q][c] = *reinterpret_cast<const u4*>(of + min(2 * (c0 + c) + lhi, chunks - 1) * kChunk);
             };
             if (wanted) {
                 ahead = starts[0];
@@ -156,68 +170,73 @@ __device__ __forceinline__ void adapter_tile(const AdapterArgs& a, const int* se
             __syncthreads();
             if (!wanted) continue;
             for (; 2 * c0 < chunks; c0 += KB) {
-#pragma unroll
-                for (int j = 0; j < J; ++j) {
+                each<0, J>([&](auto group) __attribute__((always_inline)) {
+                    constexpr int j = decltype(group)::value;
                     uint64_t runs = starts[j];
                     if (j || c0) {
                         ahead = runs;
 #pragma unroll
                         for (int q = 0; q < PF; ++q) load(q, j);
                     }
-#pragma clang loop unroll(disable)
-                    while (runs)
+                    auto run = [&](int q) __attribute__((always_inline)) {
+                        if (!runs) return false;
+                        const int from = (int)__builtin_ctzll(runs);
+                        const int s = __builtin_amdgcn_readlane(slot[j], from);
+                        runs &= runs - 1;
+                        if (s < 0) return false;
+                        const int to = runs ? (int)__builtin_ctzll(runs) : 64;
+                        const bool in = l32 >= (from & 31) && l32 < (from & 31) + to - from;
+                        const int at = ((2 * j + (from >> 5)) * KC + c0) * 1024 + lane * 16;
+                        auto products = [&](f16x y) __attribute__((always_inline)) {
 #pragma unroll
-                        for (int q = 0; q < PF; ++q) {
-                            if (!runs) continue;
-                            const int from = (int)__builtin_ctzll(runs);
-                            const int s = __builtin_amdgcn_readlane(slot[j], from);
-                            runs &= runs - 1;
-                            if (s < 0) {
-                                runs = 0;
-                                continue;
-                            }
-                            const int to = runs ? (int)__builtin_ctzll(runs) : 64;
-                            const bool in = l32 >= (from & 31) && l32 < (from & 31) + to - from;
-                            const int at = ((2 * j + (from >> 5)) * KC + c0) * 1024 + lane * 16;
-                            auto products = [&](f16x y) {
+                            for (int c = 0; c < KB; ++c)
+                                if (2 * (c0 + c) < chunks) {
+                                    u4 h = *reinterpret_cast<const u4*>(lds_hi + at + c * 1024);
+                                    u4 l = *reinterpret_cast<const u4*>(lds_lo + at + c * 1024);
 #pragma unroll
-                                for (int c = 0; c < KB; ++c)
-                                    if (2 * (c0 + c) < chunks) {
-                                        u4 h = *reinterpret_cast<const u4*>(lds_hi + at + c * 1024);
-                                        u4 l = *reinterpret_cast<const u4*>(lds_lo + at + c * 1024);
-#pragma unroll
-                                        for (int v = 0; v < 4; ++v) h[v] = in ? h[v] : 0u, l[v] = in ? l[v] : 0u;
-                                        y = mma(l, b[q][c], mma(h, b[q][c], y));
-                                    }
-                                return y;
-                            };
-                            // (256 rows' accumulators as operands in two branches would spill)
-                            if (MI <= 2 && s < kWild && first == last) {
-                                if (from < 32) acc(2 * j) = products(acc(2 * j));
-                                else acc(2 * j + 1) = products(acc(2 * j + 1));
-                            } else {
-                                f16x y;
-#pragma unroll
-                                for (int v = 0; v < 16; ++v) y[v] = 0.f;
-                                y = products(y);
-                                if (s >= kWild || first != last) {
-                                    const int lo = (from & 31) - 4 * lhi, hi = mine == part ? lo + to - from : -1;
-#pragma unroll
-                                    for (int v = 0; v < 16; ++v) {
-                                        const int m = 8 * (v >> 2) + (v & 3);
-                                        y[v] = m >= lo && m < hi ? y[v] : 0.f;
-                                    }
+                                    for (int v = 0; v < 4; ++v) h[v] = in ? h[v] : 0u, l[v] = in ? l[v] : 0u;
+                                    const u4 w = 2 * (c0 + c) + lhi < chunks ? b[q][c] : zero;
+                                    y = mma(l, w, mma(h, w, y));
                                 }
-                                if (from < 32)
+                            return y;
+                        };
+                        // (256 rows' accumulators as operands in two branches would spill)
+                        if (MI <= 2 && s < kWild && first == last) {
+                            if (from < 32) acc(2 * j) = products(acc(2 * j));
+                            else acc(2 * j + 1) = products(acc(2 * j + 1));
+                        } else {
+                            f16x y;
 #pragma unroll
-                                    for (int v = 0; v < 16; ++v) acc(2 * j)[v] += y[v];
-                                else
+                            for (int v = 0; v < 16; ++v) y[v] = 0.f;
+                            y = products(y);
+                            if (s >= kWild || first != last) {
+                                const int lo = (from & 31) - 4 * lhi, hi = mine == part ? lo + to - from : -1;
 #pragma unroll
-                                    for (int v = 0; v < 16; ++v) acc(2 * j + 1)[v] += y[v];
+                                for (int v = 0; v < 16; ++v) {
+                                    const int m = 8 * (v >> 2) + (v & 3);
+                                    y[v] = m >= lo && m < hi ? y[v] : 0.f;
+                                }
                             }
-                            load(q, j);
+                            // (the two ends differ, or the compiler makes one of them, of an
+                            // address of either tile, and keeps the accumulators in memory)
+                            if (from < 32) {
+#pragma unroll
+                                for (int v = 0; v < 16; ++v) acc(2 * j)[v] += y[v];
+                                asm volatile("; first tile");
+                            } else {
+#pragma unroll
+                                for (int v = 0; v < 16; ++v) acc(2 * j + 1)[v] += y[v];
+                                asm volatile("; second tile");
+                            }
                         }
-                }
+                        load(q, j);
+                        return true;
+                    };
+                    // (written out: as a loop it is not unrolled, and b is then in memory)
+                    static_assert(PF == 2 || PF == 4, "runs by name");
+#pragma clang loop unroll(disable)
+                    while (run(0) && run(1) && (PF == 2 || (run(PF / 2) && run(PF - 1)))) {}
+                });
             }
         }
 }
