@@ -5,14 +5,16 @@
 // nothing is sorted, since each row reads its own adapter whatever the others do.
 //
 // Many rows: the rows of one adapter are multiplied together. Each workgroup
-// counts the index (the same counting sort in all, 2 us for 77 rows and 4 us for 2048,
-// in place of a launch of its own) and takes 32 rows of one adapter, 32 or 64 of
+// counts the index (the same counting sort in all, in place of a launch of its own;
+// with nothing multiplied the launch takes 4 us for 77 rows, 7 for 2048) and takes 32 rows of one adapter, 32 or 64 of
 // its values and a share of K. Bound: what one CU can fetch, about 45 GB/s where the
 // rows come from beyond its XCD's L2, so the shares of K spread a tile over CUs until
 // there are two workgroups each; x and A stream through a ring of LDS stages, 64 of
 // K each, filled by direct loads of whole 128-byte lines, and the last workgroup of a
-// tile to arrive adds the shares in order. The workgroups also leave the order
-// of the rows for the product's launch.
+// tile to arrive adds the shares in order (K = 4096: 77 rows of 12 adapters of rank 32
+// 9.2 us, 2048 rows of 8 of rank 64 21 us; one workgroup a tile, operands straight from
+// memory: 13.4 and 33). The workgroups also leave the order of the rows for the
+// product's launch.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
