@@ -67,7 +67,7 @@ def log(*a):
 # (its code, the shared device helpers and geometry, the weight layout the
 # repack writes, the launch plan and the dispatch): counter figures taken for
 # it stay valid while their code (comments aside) is unchanged.
-GEMV_SOURCES = ("q4_gemv.hip", "q4_device.h", "q4_internal.h", "q4_prep.hip", "q4_plan.cpp",
+GEMV_SOURCES = ("q4_gemv.hip", "q4_gemv_kernel.h", "q4_device.h", "q4_internal.h", "q4_prep.hip", "q4_plan.cpp",
                 "q4_api.hip")
 
 
