@@ -183,6 +183,12 @@ __device__ __forceinline__ Request request(const Args& p, int b)
     return r;
 }
 
+// The same of lane `b`'s request.
+__device__ __forceinline__ Request request_of_lane(const Request& r, int b)
+{
+    return Request{__builtin_amdgcn_readlane(r.start, b), __builtin_amdgcn_readlane(r.n, b), __builtin_amdgcn_readlane(r.len, b)};
+}
+
 // Four values of an output row.
 template <bool BF>
 __device__ __forceinline__ void store_row4(uint16_t* o, f4 v, int left, int store8)

@@ -44,10 +44,10 @@ struct Span {
     int rt, lo, base, nt;
 };
 
-__device__ __forceinline__ Span span(const Args& p, int b)
+__device__ __forceinline__ Span span(const Args& p, const Request& r)
 {
     Span s;
-    s.r = request(p, b);
+    s.r = r;
     s.rt = (s.r.n * p.g + ROWS - 1) / ROWS;
     s.lo = p.window ? max(s.r.len - s.r.n - p.window + 1, 0) : 0;
     s.lo = min(s.lo, max(s.r.len - 1, 0));
@@ -89,9 +89,11 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void q4_attend_rows_kernel(Ar
     }
 
     // ---- this workgroup's range of tiles
-    auto cost = [&](int b) {
-        if (b >= p.B) return 0u;
-        const Span s = span(p, b);
+    // (the first 64 requests stay in the lanes: each look at them in memory is one
+    // more latency before the first key)
+    auto request_at = [&](int b) { return b < p.B ? request(p, b) : Request{0, 0, 0}; };
+    auto cost = [&](const Request& r) {        // (0 without tokens)
+        const Span s = span(p, r);
         return (uint32_t)s.rt * (uint32_t)p.KV * (uint32_t)s.nt;
     };
     auto scan = [&](uint32_t v) {              // inclusive, over the lanes
@@ -102,8 +104,10 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void q4_attend_rows_kernel(Ar
         }
         return v;
     };
-    uint32_t total = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 64) total += (uint32_t)__builtin_amdgcn_readlane((int)scan(cost(b0 + lane)), 63);
+    const Request first64 = request_at(lane);
+    const uint32_t cost64 = scan(cost(first64));
+    uint32_t total = (uint32_t)__builtin_amdgcn_readlane((int)cost64, 63);
+    for (int b0 = 64; b0 < p.B; b0 += 64) total += (uint32_t)__builtin_amdgcn_readlane((int)scan(cost(request_at(b0 + lane))), 63);
     // equal shares, in whole rounds of the waves
     uint32_t per = (total + (uint32_t)p.workers - 1) / (uint32_t)p.workers;
     per = (max(per, (uint32_t)p.least) + WV - 1) / WV * WV;
@@ -114,7 +118,7 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void q4_attend_rows_kernel(Ar
     int b = 0;
     uint32_t before = 0;                       // tiles of the requests before b
     for (int b0 = 0; b0 < p.B; b0 += 64) {
-        const uint32_t c = scan(cost(b0 + lane));
+        const uint32_t c = b0 ? scan(cost(request_at(b0 + lane))) : cost64;
         const unsigned long long past = __ballot(before + c > it);
         if (past) {
             const int f = (int)__builtin_ctzll(past);
@@ -127,10 +131,11 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void q4_attend_rows_kernel(Ar
     }
 
     for (; it < it_end && b < p.B; ++b) {
-        Span s = span(p, b);
-        s.r.start = uniform(s.r.start);
-        s.r.n = uniform(s.r.n);
-        s.r.len = uniform(s.r.len);
+        Request r = b < 64 ? request_of_lane(first64, b) : request(p, b);
+        r.start = uniform(r.start);
+        r.n = uniform(r.n);
+        r.len = uniform(r.len);
+        Span s = span(p, r);
         s.rt = uniform(s.rt);
         s.lo = uniform(s.lo);
         s.base = uniform(s.base);

@@ -53,10 +53,10 @@ struct Span {
 };
 
 template <class S>
-__device__ __forceinline__ Span span(const Args& p, int b)
+__device__ __forceinline__ Span span(const Args& p, const Request& r)
 {
     Span s;
-    s.r = request(p, b);
+    s.r = r;
     s.rt = (s.r.n * p.g + BR - 1) / BR;
     const int lo = p.window ? min(max(s.r.len - s.r.n - p.window + 1, 0), max(s.r.len - 1, 0)) : 0;
     s.nt = max((s.r.len - (lo & ~(S::KT - 1)) + S::KT - 1) / S::KT, 1);
@@ -89,15 +89,16 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
         return v;
     };
     auto last_of = [](uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane((int)v, 63); };
-    uint32_t total = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 64) {
-        uint32_t c = 0;
-        if (b0 + lane < p.B) {
-            const Span s = span<SH>(p, b0 + lane);
-            c = (uint32_t)s.rt * (uint32_t)s.nt * (uint32_t)p.KV;
-        }
-        total += last_of(scan(c));
-    }
+    // (the first 64 requests stay in the lanes: each look at them in memory is one
+    // more latency before the first key)
+    auto request_at = [&](int b) { return b < p.B ? request(p, b) : Request{0, 0, 0}; };
+    auto cost = [&](const Request& r) {        // (0 without tokens)
+        const Span s = span<SH>(p, r);
+        return (uint32_t)s.rt * (uint32_t)s.nt * (uint32_t)p.KV;
+    };
+    const Request first64 = request_at(lane);
+    uint32_t total = last_of(scan(cost(first64)));
+    for (int b0 = 64; b0 < p.B; b0 += 64) total += last_of(scan(cost(request_at(b0 + lane))));
     const int chunk = (int)max((total + (uint32_t)p.workers - 1) / (uint32_t)p.workers, (uint32_t)p.least);
     const uint32_t me = blockIdx.x;
     uint32_t before = 0, slots_before = 0;
@@ -105,7 +106,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
     for (int b0 = 0; b0 < p.B && b < 0; b0 += 64) {
         uint32_t u = 0, sl = 0;
         if (b0 + lane < p.B) {
-            const Span s = span<SH>(p, b0 + lane);
+            const Span s = span<SH>(p, b0 ? request(p, b0 + lane) : first64);
             const int splits = (s.nt + chunk - 1) / chunk;
             u = (uint32_t)s.rt * (uint32_t)splits * (uint32_t)p.KV;
             sl = splits > 1 ? u : 0;
@@ -123,7 +124,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
         }
     }
     if (b < 0) return;
-    const Span sp = span<SH>(p, b);
+    const Span sp = span<SH>(p, b < 64 ? request_of_lane(first64, b) : request(p, b));
     const int start = uniform(sp.r.start), n = uniform(sp.r.n), len = uniform(sp.r.len), rt = uniform(sp.rt);
     const int splits = (uniform(sp.nt) + chunk - 1) / chunk;
     const uint32_t unit = me - before;
