@@ -376,12 +376,12 @@ class PagedCache:
                 _raise(load_library().q4_last_status(), "q4_attend_workspace")
             self._need[heads] = need
         if torch.cuda.is_current_stream_capturing():
-            ws = _on(stream, _zeros, need, self.device)
+            ws = _on(stream, _new_workspace, need, self.device)
             return ws.data_ptr(), need, ws
         key = (self.device.index, _raw_stream(self.device.index) if stream is None else stream.cuda_stream)
         held = _workspaces.get(key)
         if held is None or held[1] < need:
-            ws = _on(stream, _zeros, need, self.device)
+            ws = _on(stream, _new_workspace, need, self.device)
             held = _workspaces[key] = (ws.data_ptr(), need, ws)
         return held
 
@@ -389,8 +389,14 @@ class PagedCache:
 _workspaces: dict = {}      # (device, stream) -> q4_attend's workspace: address, bytes, tensor
 
 
-def _zeros(n, device):
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+_WORKSPACE_ZEROS = 1 << 16  # bytes of it that q4_attend wants zero before the first call
+
+
+def _new_workspace(n, device):
+    # (a graph makes one at each replay: filling it all took longer than a small call)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:_WORKSPACE_ZEROS].zero_()
+    return ws
 
 
 def _on(stream, f, *args, **kw):
