@@ -7,6 +7,8 @@ sum, plus what the adapter's part adds, derived: c A x is a fp32 sum of K exact 
 (K 2^-24 c sum |A x|) and is kept in fp32 or in two halves (2^-16 of it at
 most); B's products are summed in fp32 (rank 2^-24, below the same 2^-16).
 """
+import math
+
 import numpy as np
 import pytest
 
@@ -199,6 +201,58 @@ def test_what_is_not_finite_stays_with_its_rows():
             xc[3] = 0
             c.check(torch.where(skip, torch.zeros_like(y), y), xc, b, index, f"M={M}", skip)
             assert y[3].isnan().all()
+
+
+def test_a_slot_loaded_again_is_as_new():
+    """Values that are not finite leave nothing behind when their slot is loaded
+    or cleared."""
+    for M in (8, 50, 600):
+        c = Case(256, [72, 64], 64, "f16", slots=3, rank=8)
+        c.bank.load(1, c.A[1], torch.full_like(c.B[1], math.nan), c.c[1])
+        x, b, index = c.inputs(M)
+        assert c.W.matmul_adapters(x, c.bank, index, b)[index == 1].isnan().all()
+        c.bank.load(1, c.A[1], c.B[1], c.c[1])
+        c.check(c.W.matmul_adapters(x, c.bank, index, b), x, b, index, f"M={M}")
+        c.bank.load(0, c.A[0], torch.full_like(c.B[0], math.inf), c.c[0])
+        c.bank.clear(0)
+        c.check(c.W.matmul_adapters(x, c.bank, torch.where(index == 0, -1, index), b), x, b, torch.where(index == 0, -1, index), "cleared")
+        zero = c.W.matmul_adapters(x, c.bank, index, b)
+        c.check(zero, x, b, torch.where(index == 0, -1, index), "empty")
+
+
+@pytest.mark.parametrize("fmt", ["f16", "bf16"])
+@pytest.mark.parametrize("rank", [72, 150, 200])
+def test_ranks_of_several_stretches(fmt, rank):
+    """Ranks past the 64 values that are in LDS at a time, over several parts
+    whose borders lie inside a wave's columns."""
+    c = Case(512, [72, 64, 120], 128, fmt, slots=3, rank=rank)
+    for M in (5, 33, 70, 600):
+        c.run(M)
+
+
+@pytest.mark.parametrize("fmt", ["f16", "bf16"])
+@pytest.mark.parametrize("K,G", [(4096, 128), (4128, 32), (288, 32)])
+def test_shared_k(fmt, K, G):
+    """Few tiles, whose K several workgroups share; K that ends inside a stage."""
+    c = Case(K, [264], G, fmt, slots=6, rank=40)
+    for M in (33, 77, 200):
+        c.run(M)
+        c.run(M, index=torch.full((M,), 4))
+
+
+@pytest.mark.parametrize("fmt", ["f16", "bf16"])
+def test_more_rows_than_stay_in_registers(fmt):
+    c = Case(256, [136], 128, fmt, slots=37, rank=20)
+    for M in (2049, 5003):
+        c.run(M)
+        c.run(M, index=torch.sort(torch.randint(-1, 37, (M,), generator=torch.Generator().manual_seed(M))).values)
+        c.run(M, index=torch.arange(M) % 40 - 1)
+
+
+def test_largest_bank():
+    c = Case(128, [64], 128, slots=4096, rank=1)
+    for M in (100, 5000):
+        c.run(M)
 
 
 def test_graph_and_repeats():
