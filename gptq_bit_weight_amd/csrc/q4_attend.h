@@ -58,6 +58,7 @@ struct Args {
     uint32_t* counters;                    // few rows: arrivals
     JoinList* joins;                       // many rows
     int workers, least;                    // workgroups, and least tiles of one
+    int unsplit;                           // many rows: no row tile has more than `least` tiles
     q4::FastDiv div_g, div_page;           // by heads of a group; by rows of a page (or 16-row blocks of one)
 };
 

@@ -617,8 +617,7 @@ hipError_t launch_tiles(const Args& p, int grid, bool bf16, bool pg, hipStream_t
     else if (pg) hipLaunchKernelGGL((q4_attend_tiles_kernel<D, false, true>), g, block, 0, stream, p);
     else hipLaunchKernelGGL((q4_attend_tiles_kernel<D, false, false>), g, block, 0, stream, p);
     hipError_t e = hipGetLastError();
-    // (no row tile can have more than `least` tiles of keys: none is split)
-    if (e != hipSuccess || p.max_len / Shape<D>::KT + 1 <= p.least) return e;
+    if (e != hipSuccess || p.unsplit) return e;
     if (bf16) hipLaunchKernelGGL((q4_attend_join_kernel<D, true>), dim3(kJoinGrid), dim3(64 * JW), 0, stream, p);
     else hipLaunchKernelGGL((q4_attend_join_kernel<D, false>), dim3(kJoinGrid), dim3(64 * JW), 0, stream, p);
     return hipGetLastError();
