@@ -12,7 +12,7 @@
 // there are two workgroups each; x and A stream through a ring of LDS stages, 64 of
 // K each, filled by direct loads of whole 128-byte lines, and the last workgroup of a
 // tile to arrive adds the shares in order (K = 4096: 77 rows of 12 adapters of rank 32
-// 9.2 us, 2048 rows of 8 of rank 64 21 us; one workgroup a tile, operands straight from
+// 8.8 us, 2048 rows of 8 of rank 64 21 us; one workgroup a tile, operands straight from
 // memory: 13.4 and 33). The workgroups also leave the order of the rows for the
 // product's launch.
 #include <hip/hip_runtime.h>
@@ -210,6 +210,9 @@ __global__ __launch_bounds__(MT, 2) void q4_adapter_many_kernel(ManyArgs p)
     if (slot < 0) return;
     const bool none = slot == p.slots;           // rows without an adapter: only their order
     if (none && (blockIdx.y || blockIdx.z)) return;
+    // (asked for here, used much later)
+    const float scale = none ? 0.f : p.scale[slot];
+    const int wild = none ? 0 : p.wild[slot];
     // ---- its rows: those of the bin ranked first .. first + MR - 1
     int seen = 0;
     auto pick = [&](int i0, const int (&bin)[RPT]) {
@@ -223,6 +226,7 @@ __global__ __launch_bounds__(MT, 2) void q4_adapter_many_kernel(ManyArgs p)
         int before = seen;
 #pragma unroll
         for (int u = 0; u < RPT; ++u) {
+            if (i0 + u * MT >= p.M) continue;
             int rank = before;
 #pragma unroll
             for (int w = 0; w < MW; ++w) {
@@ -242,7 +246,7 @@ __global__ __launch_bounds__(MT, 2) void q4_adapter_many_kernel(ManyArgs p)
         pick(i0, bin);
     }
     if (blockIdx.y == 0 && blockIdx.z == 0 && tid < n_rows)
-        p.rows[pos + tid] = AdapterRow{tile_row[tid], none ? -1 : slot, none ? 0 : p.wild[slot], 0};
+        p.rows[pos + tid] = AdapterRow{tile_row[tid], none ? -1 : slot, wild, 0};
     if (none) return;
     // ---- a stage is 128 bytes of each row of x and of A; its 16-byte chunk c lies at
     // place c ^ row % 8, which spreads a product's operand over the banks
@@ -345,7 +349,6 @@ __global__ __launch_bounds__(MT, 2) void q4_adapter_many_kernel(ManyArgs p)
     }
     if (!mine) return;
     // (values past the rank meet zeros of B: they must be finite)
-    const float scale = p.scale[slot];
     u4 hi, lo;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
