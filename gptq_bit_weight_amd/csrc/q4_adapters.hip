@@ -9,10 +9,10 @@
 // with nothing multiplied the launch takes 4 us for 77 rows, 7 for 2048) and takes 32 rows of one adapter, 32 or 64 of
 // its values and a share of K. Bound: what one CU can fetch, about 45 GB/s where the
 // rows come from beyond its XCD's L2, so the shares of K spread a tile over CUs until
-// there are two workgroups each; x and A stream through a ring of LDS stages, 64 of
+// each has a workgroup; x and A stream through a ring of LDS stages, 64 of
 // K each, filled by direct loads of whole 128-byte lines, and the last workgroup of a
 // tile to arrive adds the shares in order (K = 4096: 77 rows of 12 adapters of rank 32
-// 8.8 us, 2048 rows of 8 of rank 64 21 us; one workgroup a tile, operands straight from
+// 8.8 us, 2048 rows of 8 of rank 64 20.5 us; one workgroup a tile, operands straight from
 // memory: 13.4 and 33). The workgroups also leave the order of the rows for the
 // product's launch.
 #include <hip/hip_runtime.h>
@@ -116,7 +116,8 @@ constexpr int RPT = 8;                 // rows of the index that a thread looks 
 constexpr int KC = 64;                 // values of K of a stage: a 16-value step for each wave
 constexpr int NS = 6;                  // stages
 constexpr int kMaxShares = 8;          // of K
-constexpr int kManyGroups = 512;       // workgroups that shares are made for (two a CU)
+constexpr int kManyGroups = 256;       // workgroups that shares are made for (one a CU; 512: 21.4 us against 20.5
+                                       // at 2048 rows, whose sums are then twice as many)
 
 struct ManyArgs {
     const uint16_t* x;
