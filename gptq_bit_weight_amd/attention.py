@@ -283,7 +283,8 @@ class PagedCache:
         it) and values [tokens, kv heads, dim] of new tokens to rows slots
         [tokens]: slot s is row s % page_size of page s // page_size; a slot
         outside the cache (-1 for padding) is not written. With q [tokens,
-        heads, dim], returns it turned too (in q_out, which may be q)."""
+        heads, dim], returns it turned too (in q_out, which may be q). No
+        gradient goes through it (Rotary.rotate has one)."""
         dev, dt, D, kv = self.device, self.dtype, self.dim, self.kv_heads
         (T, _, _), ks = _heads(k, "k", dev, dt, None, kv, D)
         _, vs = _heads(v, "v", dev, dt, T, kv, D)
@@ -324,7 +325,7 @@ class PagedCache:
         [requests, width]). A token sees the keys up to its own, with `window`
         only the last `window` of them; one that sees none gives zeros. heads is
         a multiple of the cached heads, scale defaults to dim ** -0.5. Lengths
-        stay on the device; nothing waits for it."""
+        stay on the device; nothing waits for it. No gradient goes through it."""
         dev, dt = self.device, self.dtype
         (T, H, D), qs = _heads(q, "q", dev, dt, None, None, self.dim)
         if H % self.kv_heads or not H:

@@ -597,8 +597,9 @@ q4_status q4_check_adapters(int slots, int rank);
  * q4_adapters_make -- a bank of `slots` adapters of rank at most `rank` for
  * handle h, in binary16 or (bf16 != 0) bfloat16, on h's device (the current
  * one). Every slot is empty (adds nothing). The bank holds slots * (parts * rank *
- * K + N * rank rounded up to 8) values and the workspace of its calls; it does not keep
- * h. NULL on error.
+ * K + N rounded up to 32 * rank rounded up to 8) values and the workspace of its calls
+ * (2 MiB and 4 bytes a row and value of rank once M passes Q4_GEMV_MAX_M); it does not
+ * keep h. NULL on error.
  */
 q4_adapters* q4_adapters_make(const q4_matrix* h, int slots, int rank, int bf16);
 /* q4_adapters_free -- NULL allowed; the caller has synchronized its streams. */
