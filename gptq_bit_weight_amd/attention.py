@@ -105,6 +105,21 @@ def _overlap(a, b):
     return a0 < b1 and b0 < a1
 
 
+def _table_rows(table, stream=None):
+    """A page table and its row stride, at least its width. Rows that share memory
+    (one row expanded over the requests) are copied: the C call takes them apart only.
+    One row has no stride of its own."""
+    B, width = table.shape
+    ts = table.stride(0)
+    if B == 1:
+        return table, width
+    if ts < width:
+        if stream is not None:
+            table.record_stream(stream)
+        return _on(stream, torch.clone, table, memory_format=_dense), width
+    return table, ts
+
+
 def _out_like(x, out, name, stream):
     """The output for x: `out` checked, or a new dense tensor made on the
     stream that the call runs on."""
@@ -356,11 +371,12 @@ class PagedCache:
             _distinct(out, "out")
             if _overlap(out, q):
                 raise ValueError("out overlaps q")
+        table, ts = _table_rows(table, stream)
         ws = self._workspace(H, stream)
-        os_, ts = out.stride(), table.stride(0)
+        os_ = out.stride()
         _call(load_library().q4_attend, "q4_attend", dev, stream,
               (self._ref, q.data_ptr(), qs[0], qs[1], H, T, starts.data_ptr(), lengths.data_ptr(), table.data_ptr(),
-               width, ts if ts > width else width, B, window, D ** -0.5 if scale is None else scale, out.data_ptr(),
+               width, ts, B, window, D ** -0.5 if scale is None else scale, out.data_ptr(),
                os_[0], os_[1], ws[0], ws[1]),
               (q, out, starts, lengths, table, self.k, self.v))
         return out

@@ -59,3 +59,25 @@ def test_adapters_null():
     assert lib.q4_adapters_clear(None, 0, None) == 1
     assert lib.q4_matmul_adapters(None, None, 4096, None, 4096, 8192, 1, 0, None) == 1
     lib.q4_adapters_free(None)
+
+
+def test_table_rows_that_share_memory():
+    """The row stride handed to the C call is one that the tensor has: rows that
+    share memory are copied, a single row's stride does not count."""
+    import torch
+    from gptq_bit_weight_amd.attention import _table_rows
+    base = torch.arange(60, dtype=torch.int32)
+    cases = [base[:7].expand(5, 7), base[:7][None].expand(5, 7), base.as_strided((4, 6), (3, 1)), base[:3, None].expand(3, 1),
+             base[:1].expand(4, 1), base.view(10, 6), base.view(10, 6)[::2, :4], base.view(10, 6)[:1, :4], base.as_strided((1, 5), (0, 1)),
+             base.as_strided((1, 5), (2, 1))]
+    for t in cases:
+        got, stride = _table_rows(t)
+        B, width = t.shape
+        assert stride >= width and torch.equal(got, t)
+        # what the kernel reads: entry (b, i) at b * stride + i, inside the tensor's storage
+        at = got.storage_offset() + torch.arange(B)[:, None] * stride + torch.arange(width)
+        whole = torch.empty(0, dtype=torch.int32).set_(got.untyped_storage())
+        assert int(at.max()) < whole.numel()
+        assert torch.equal(whole[at], t)
+    t = base.view(10, 6)
+    assert _table_rows(t)[0] is t                # (rows apart are taken as they are)

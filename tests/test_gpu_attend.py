@@ -288,6 +288,31 @@ def test_strides():
     check(cache.attend(odd, starts, lengths, table), ref, tol)
 
 
+@pytest.mark.parametrize("news,H", [([1, 1, 1], 8), ([40, 33, 64], 8), ([200, 1, 90], 2)])
+def test_requests_that_share_a_row_of_the_table(news, H):
+    """One row of pages expanded over the requests, and rows that lie half over each
+    other, on both kernels, on the current stream and another."""
+    import gptq_bit_weight_amd as q4
+    lens = [300] * 3
+    q, kc, vc, starts, lengths, table = make(torch.float16, H, 2, 128, 16, news, lens)
+    kc.nan_to_num_()
+    vc.nan_to_num_()
+    cache = q4.PagedCache(kc, vc)
+    width = table.shape[1]
+    flat = table.flatten()
+    for t in (table[:1].expand(3, width), flat.as_strided((3, width), (5, 1))):
+        ref = reference(q, kc, vc, news, lens, t.cpu())
+        check(cache.attend(q, starts, lengths, t), *ref)
+        assert torch.equal(cache.attend(q, starts, lengths, t), cache.attend(q, starts, lengths, t.contiguous()))
+        s = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        y = cache.attend(q, starts, lengths, t, stream=s)
+        s.synchronize()
+        check(y, *ref)
+    one = table[:1].as_strided((1, width), (1, 1))          # (a single row's stride is any)
+    check(cache.attend(q[:news[0]], starts[:2], lengths[:1], one), *reference(q[:news[0]], kc, vc, news[:1], lens[:1], one.cpu()))
+
+
 def test_queries_off_sixteen_bytes():
     """A dense q whose first value is not on 16 bytes."""
     import gptq_bit_weight_amd as q4
