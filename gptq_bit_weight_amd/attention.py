@@ -13,6 +13,7 @@ a HIP stream to the C ABI (``include/q4.h``).
 from __future__ import annotations
 
 import ctypes
+import threading
 
 import torch
 
@@ -340,7 +341,8 @@ class PagedCache:
         [requests, width]). A token sees the keys up to its own, with `window`
         only the last `window` of them; one that sees none gives zeros. heads is
         a multiple of the cached heads, scale defaults to dim ** -0.5. Lengths
-        stay on the device; nothing waits for it. No gradient goes through it."""
+        stay on the device; nothing waits for it. No gradient goes through it.
+        Several threads may call at once, on one stream too."""
         dev, dt = self.device, self.dtype
         (T, H, D), qs = _heads(q, "q", dev, dt, None, None, self.dim)
         if H % self.kv_heads or not H:
@@ -372,38 +374,53 @@ class PagedCache:
             if _overlap(out, q):
                 raise ValueError("out overlaps q")
         table, ts = _table_rows(table, stream)
-        ws = self._workspace(H, stream)
         os_ = out.stride()
-        _call(load_library().q4_attend, "q4_attend", dev, stream,
-              (self._ref, q.data_ptr(), qs[0], qs[1], H, T, starts.data_ptr(), lengths.data_ptr(), table.data_ptr(),
-               width, ts, B, window, D ** -0.5 if scale is None else scale, out.data_ptr(),
-               os_[0], os_[1], ws[0], ws[1]),
-              (q, out, starts, lengths, table, self.k, self.v))
+        args = (self._ref, q.data_ptr(), qs[0], qs[1], H, T, starts.data_ptr(), lengths.data_ptr(), table.data_ptr(),
+                width, ts, B, window, D ** -0.5 if scale is None else scale, out.data_ptr(), os_[0], os_[1])
+        used = (q, out, starts, lengths, table, self.k, self.v)
+        fn, need = load_library().q4_attend, self._need.get(H) or self._workspace_bytes(H)
+        if torch.cuda.is_current_stream_capturing():
+            # (the call's own: a graph may replay beside other work of the stream it was captured on)
+            ws = _on(stream, _new_workspace, need, dev)
+            _call(fn, "q4_attend", dev, stream, args + (ws.data_ptr(), need), used)
+            return out
+        ws = _workspace(dev, stream)
+        with ws.lock:
+            if ws.bytes < need:
+                ws.hold(_on(stream, _new_workspace, need, dev))
+            _call(fn, "q4_attend", dev, stream, args + (ws.at, ws.bytes), used)
         return out
 
-    def _workspace(self, heads, stream):
-        """The workspace of a call: one a stream, shared by every cache, or
-        under capture one of the call's own (a graph may replay beside other
-        work of the stream it was captured on)."""
-        need = self._need.get(heads)
-        if need is None:
-            with torch.cuda.device(self.device):
-                need = load_library().q4_attend_workspace(self._ref, heads)
-            if not need:
-                _raise(load_library().q4_last_status(), "q4_attend_workspace")
-            self._need[heads] = need
-        if torch.cuda.is_current_stream_capturing():
-            ws = _on(stream, _new_workspace, need, self.device)
-            return ws.data_ptr(), need, ws
-        key = (self.device.index, _raw_stream(self.device.index) if stream is None else stream.cuda_stream)
-        held = _workspaces.get(key)
-        if held is None or held[1] < need:
-            ws = _on(stream, _new_workspace, need, self.device)
-            held = _workspaces[key] = (ws.data_ptr(), need, ws)
-        return held
+    def _workspace_bytes(self, heads):
+        with torch.cuda.device(self.device):
+            need = load_library().q4_attend_workspace(self._ref, heads)
+        if not need:
+            _raise(load_library().q4_last_status(), "q4_attend_workspace")
+        self._need[heads] = need
+        return need
 
 
-_workspaces: dict = {}      # (device, stream) -> q4_attend's workspace: address, bytes, tensor
+class _Workspace:
+    """A stream's workspace of q4_attend, shared by every cache. A call is up to two
+    launches that hand partial results over in it, and several threads may use one
+    stream (the default one is every thread's): the lock keeps a call's launches side by
+    side, and the memory until they are made."""
+    __slots__ = ("lock", "at", "bytes", "memory")
+
+    def __init__(self):
+        self.lock, self.at, self.bytes, self.memory = threading.Lock(), None, 0, None
+
+    def hold(self, memory):
+        self.at, self.bytes, self.memory = memory.data_ptr(), memory.numel(), memory
+
+
+_workspaces: dict = {}      # (device, stream) -> its _Workspace
+
+
+def _workspace(device, stream):
+    key = (device.index, _raw_stream(device.index) if stream is None else stream.cuda_stream)
+    # (setdefault: two threads that come first get one and the same)
+    return _workspaces.get(key) or _workspaces.setdefault(key, _Workspace())
 
 
 _WORKSPACE_ZEROS = 1 << 16  # bytes of it that q4_attend wants zero before the first call

@@ -81,3 +81,59 @@ def test_table_rows_that_share_memory():
         assert torch.equal(whole[at], t)
     t = base.view(10, 6)
     assert _table_rows(t)[0] is t                # (rows apart are taken as they are)
+
+
+def test_calls_of_two_threads_on_one_stream_follow_each_other(monkeypatch):
+    """The C call makes two launches that share the stream's workspace: another
+    thread's may not come between them, nor free the workspace before them."""
+    import threading
+    import time
+
+    import torch
+    from gptq_bit_weight_amd import attention
+
+    inside, most, sizes, errors = [], [], [], []
+
+    class Library:
+        @staticmethod
+        def q4_attend(*a):
+            inside.append(1)
+            most.append(len(inside))
+            at, n = a[-3], a[-2]
+            time.sleep(0.002)
+            sizes.append((at, n) if any(w.memory is not None and w.at == at and w.memory.numel() >= n
+                                        for w in attention._workspaces.values()) else None)
+            inside.pop()
+            return 0
+
+    monkeypatch.setattr(attention, "load_library", lambda: Library)
+    monkeypatch.setattr(attention, "_raw_stream", lambda i: 7)
+    monkeypatch.setattr(attention, "_device", lambda: None)
+    monkeypatch.setattr(attention, "_workspaces", {})
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+
+    def cache(need):
+        c = object.__new__(attention.PagedCache)
+        c.device, c.dtype, c.dim, c.kv_heads, c._need, c._ref = torch.device("cpu"), torch.float16, 64, 2, {4: need}, None
+        c.k = c.v = torch.zeros(2, 2, 16, 64, dtype=torch.float16)
+        return c
+
+    q = torch.zeros(3, 4, 64, dtype=torch.float16)
+    starts, lengths = torch.tensor([0, 3], dtype=torch.int32), torch.tensor([20], dtype=torch.int32)
+    table = torch.zeros(1, 2, dtype=torch.int32)
+
+    def work(c):
+        try:
+            for _ in range(20):
+                c.attend(q, starts, lengths, table)
+        except Exception as e:      # reported below
+            errors.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(cache(1 << 16 + i),)) for i in (1, 0, 2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    assert len(most) == 60 and max(most) == 1
+    assert None not in sizes

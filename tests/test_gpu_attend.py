@@ -428,3 +428,39 @@ def test_refusals():
     e = torch.zeros(1, dtype=torch.int32, device="cuda")
     assert c.attend(q[:0], e, lengths[:0], table[:0]).shape == (0, 8, 128)
     assert c.attend(q[:0], torch.zeros(3, dtype=torch.int32, device="cuda"), lengths, table).shape == (0, 8, 128)
+
+
+def test_two_threads_on_one_stream():
+    """Two threads with caches of their own on the same stream, chunks whose keys
+    are split (two launches a call) beside single tokens: each has what it has alone."""
+    import threading
+
+    import gptq_bit_weight_amd as q4
+    work = []
+    for i, (news, lens, D) in enumerate((([70], [9001], 128), ([300, 1, 40], [5000, 900, 60], 128), ([33], [6000], 256))):
+        q, kc, vc, starts, lengths, table = make(torch.bfloat16, 8, 2, D, 16, news, lens, seed=i)
+        c = q4.PagedCache(kc, vc)
+        y = c.attend(q, starts, lengths, table)
+        check(y, *reference(q, kc, vc, news, lens, table))
+        work.append((c, q, starts, lengths, table, y, []))
+    torch.cuda.synchronize()
+    errors = []
+
+    def run(c, q, starts, lengths, table, y, outs):
+        try:
+            for _ in range(200):
+                outs.append(c.attend(q, starts, lengths, table))
+        except Exception as e:      # reported below
+            errors.append(repr(e))
+
+    threads = [threading.Thread(target=run, args=w) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for w in work:
+        assert len(w[6]) == 200
+        for i, y in enumerate(w[6]):
+            assert torch.equal(y, w[5]), i
