@@ -379,7 +379,7 @@ class PagedCache:
                 width, ts, B, window, D ** -0.5 if scale is None else scale, out.data_ptr(), os_[0], os_[1])
         used = (q, out, starts, lengths, table, self.k, self.v)
         fn, need = load_library().q4_attend, self._need.get(H) or self._workspace_bytes(H)
-        if torch.cuda.is_current_stream_capturing():
+        if _capturing(dev, stream):
             # (the call's own: a graph may replay beside other work of the stream it was captured on)
             ws = _on(stream, _new_workspace, need, dev)
             _call(fn, "q4_attend", dev, stream, args + (ws.data_ptr(), need), used)
@@ -431,6 +431,15 @@ def _new_workspace(n, device):
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     ws[:_WORKSPACE_ZEROS].zero_()
     return ws
+
+
+def _capturing(device, stream):
+    """Whether the stream that a call runs on is being captured."""
+    if stream is None:
+        if _device() == device.index:
+            return torch.cuda.is_current_stream_capturing()
+        stream = torch.cuda.current_stream(device)
+    return _on(stream, torch.cuda.is_current_stream_capturing)
 
 
 def _on(stream, f, *args, **kw):

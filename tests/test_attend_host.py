@@ -137,3 +137,50 @@ def test_calls_of_two_threads_on_one_stream_follow_each_other(monkeypatch):
     assert not errors, errors
     assert len(most) == 60 and max(most) == 1
     assert None not in sizes
+
+
+@pytest.mark.parametrize("captured", ["given", "current", "neither"])
+def test_a_captured_stream_that_is_not_the_current_one(monkeypatch, captured):
+    """It is the stream the call runs on that counts: a graph gets a workspace of
+    its own, an eager call the stream's."""
+    import contextlib
+
+    import torch
+    from gptq_bit_weight_amd import attention
+
+    seen, now = [], ["current"]
+
+    class Library:
+        @staticmethod
+        def q4_attend(*a):
+            seen.append(a[-3])
+            return 0
+
+    class Stream:
+        device, cuda_stream = torch.device("cpu"), 9
+
+    @contextlib.contextmanager
+    def stream(s):
+        was, now[0] = now[0], "given" if isinstance(s, Stream) else s
+        yield
+        now[0] = was
+
+    monkeypatch.setattr(attention, "load_library", lambda: Library)
+    monkeypatch.setattr(attention, "_raw_stream", lambda i: 7)
+    monkeypatch.setattr(attention, "_device", lambda: None)
+    monkeypatch.setattr(attention, "_workspaces", {})
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now[0] == captured)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
+    c = object.__new__(attention.PagedCache)
+    c.device, c.dtype, c.dim, c.kv_heads, c._need, c._ref = torch.device("cpu"), torch.float16, 64, 2, {4: 1 << 16}, None
+    c.k = c.v = torch.zeros(2, 2, 16, 64, dtype=torch.float16)
+    q = torch.zeros(3, 4, 64, dtype=torch.float16)
+    starts, lengths = torch.tensor([0, 3], dtype=torch.int32), torch.tensor([20], dtype=torch.int32)
+    table = torch.zeros(1, 2, dtype=torch.int32)
+    c.attend(q, starts, lengths, table, stream=Stream())
+    c.attend(q, starts, lengths, table)
+    held = [attention._workspaces.get((None, h)) for h in (9, 7)]
+    for workspace, at, which in zip(held, seen, ("given", "current")):
+        assert (workspace is None) == (captured == which)
+        assert workspace is None or workspace.at == at

@@ -464,3 +464,30 @@ def test_two_threads_on_one_stream():
         assert len(w[6]) == 200
         for i, y in enumerate(w[6]):
             assert torch.equal(y, w[5]), i
+
+
+def test_captured_stream_that_is_not_the_current_one():
+    """A capture begun on a stream that the calls are given and that is not current:
+    replays on one stream beside eager calls on the captured one."""
+    import gptq_bit_weight_amd as q4
+    news, lens = [70, 1], [9001, 300]
+    q, kc, vc, starts, lengths, table = make(torch.float16, 8, 2, 128, 16, news, lens)
+    ref = reference(q, kc, vc, news, lens, table)
+    cache = q4.PagedCache(kc, vc)
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    cache.attend(q, starts, lengths, table, stream=s)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        graph.capture_begin()
+    y = cache.attend(q, starts, lengths, table, stream=s)
+    with torch.cuda.stream(s):
+        graph.capture_end()
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(20):
+        graph.replay()              # (on the current stream)
+        outs.append(cache.attend(q, starts, lengths, table, stream=s))
+    torch.cuda.synchronize()
+    check(y, *ref)
+    for o in outs:
+        assert torch.equal(o, y)
