@@ -18,6 +18,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <memory>
 #include <mutex>
 #include <new>
@@ -378,7 +379,8 @@ struct q4_adapters {
     uint8_t* part8 = nullptr;
     float* t = nullptr;                // few rows: [Q4_GEMV_MAX_M][parts * rp]
     std::mutex mutex;
-    char* many = nullptr;              // many rows' workspace, and the rows it holds
+    char* shares = nullptr;            // many rows' workspace: shares of K, and (many) what goes by rows,
+    char* many = nullptr;              // of which it holds many_rows
     int many_rows = 0;
     std::vector<char*> retired;        // outgrown ones, freed with the bank
 };
@@ -390,21 +392,20 @@ namespace {
 // Values of a slot's B.
 size_t b_values(const q4_adapters* a) { return ((size_t)a->N + 31) / 32 * 32 * a->rp; }
 
+// (a count for each tile whose K is shared, and their sums)
+constexpr size_t kArrivedBytes = kManyGroups * sizeof(uint32_t), kPartialBytes = (size_t)kManyGroups * MR * 64 * sizeof(float);
+
 struct ManySpace {
-    uint32_t* arrived;
-    float* partial;
     AdapterRow* rows;
     uint16_t *hi, *lo;
     size_t bytes;
 };
 
-// (a count for each tile whose K is shared, and their sums)
-constexpr size_t kArrivedBytes = kManyGroups * sizeof(uint32_t), kPartialBytes = (size_t)kManyGroups * MR * 64 * sizeof(float);
-
-// The many-row workspace of a bank: rows padded to whole output tiles.
+// What goes by rows of a bank's many-row workspace. The rows are whole output tiles.
+constexpr int kRowStep = 256;
 ManySpace many_space(const q4_adapters* a, char* base, int rows)
 {
-    const size_t m = ((size_t)rows + 255) / 256 * 256, width = (size_t)a->parts * a->rp;
+    const size_t m = (size_t)rows, width = (size_t)a->parts * a->rp;
     ManySpace s;
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -412,8 +413,6 @@ ManySpace many_space(const q4_adapters* a, char* base, int rows)
         at += (bytes + 255) / 256 * 256;
         return p;
     };
-    s.arrived = reinterpret_cast<uint32_t*>(take(kArrivedBytes));
-    s.partial = reinterpret_cast<float*>(take(kPartialBytes));
     s.rows = reinterpret_cast<AdapterRow*>(take(m * sizeof(AdapterRow)));
     s.hi = reinterpret_cast<uint16_t*>(take(m * width * 2));
     s.lo = reinterpret_cast<uint16_t*>(take(m * width * 2));
@@ -452,7 +451,7 @@ q4_status adapters_check(const q4_adapters* a, const q4_matrix* h, const int* in
     return Q4_OK;
 }
 
-// Grow a bank's workspace to M rows before anything of a call is launched.
+// Grow a bank's workspace to hold M rows before anything of a call is launched.
 q4_status adapters_reserve(q4_adapters* a, int M, hipStream_t stream)
 {
     const char* who = "q4_matmul_adapters";
@@ -464,10 +463,28 @@ q4_status adapters_reserve(q4_adapters* a, int M, hipStream_t stream)
     if (cap != hipStreamCaptureStatusNone)
         return fail(Q4_ERR_INVALID_ARG, "%s: the bank's workspace must grow to M=%d under stream capture; make one "
                     "uncaptured call with this M (or larger) first", who, M);
+    auto failed = [&](hipError_t e) { return fail(e == hipErrorOutOfMemory ? Q4_ERR_OOM : Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e)); };
+    if (!a->shares) {
+        char* shares = nullptr;
+        if ((e = hipMalloc(&shares, kArrivedBytes + kPartialBytes)) != hipSuccess) return failed(e);
+        if ((e = hipMemsetAsync(shares, 0, kArrivedBytes, stream)) != hipSuccess) {
+            (void)hipFree(shares);
+            return failed(e);
+        }
+        a->shares = shares;
+    }
+    // (twice the last at least, so that those outgrown hold no more together than the
+    // present one; as much as is needed where there is no room for that)
+    const long long need = ((long long)M + kRowStep - 1) / kRowStep * kRowStep;
+    long long rows = std::min<long long>(std::max(need, 2LL * a->many_rows), INT_MAX / kRowStep * kRowStep);
     char* fresh = nullptr;
-    e = hipMalloc(&fresh, many_space(a, nullptr, M).bytes);
-    if (e == hipSuccess && (e = hipMemsetAsync(fresh, 0, kArrivedBytes, stream)) != hipSuccess) (void)hipFree(fresh);
-    if (e != hipSuccess) return fail(e == hipErrorOutOfMemory ? Q4_ERR_OOM : Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
+    e = hipMalloc(&fresh, many_space(a, nullptr, (int)rows).bytes);
+    if (e == hipErrorOutOfMemory && rows > need) {
+        (void)hipGetLastError();
+        rows = need;
+        e = hipMalloc(&fresh, many_space(a, nullptr, (int)rows).bytes);
+    }
+    if (e != hipSuccess) return failed(e);
     // (earlier launches, and graphs, may still use the outgrown one)
     try {
         if (a->many) a->retired.push_back(a->many);
@@ -476,7 +493,7 @@ q4_status adapters_reserve(q4_adapters* a, int M, hipStream_t stream)
         return fail(Q4_ERR_OOM, "%s: out of memory", who);
     }
     a->many = fresh;
-    a->many_rows = M;
+    a->many_rows = (int)rows;
     return Q4_OK;
 }
 
@@ -525,8 +542,8 @@ q4_status adapters_prepare(q4_adapters* a, const uint16_t* x, const int* index, 
     p.rank = a->rank;
     p.rp = a->rp;
     p.parts = a->parts;
-    p.partial = s.partial;
-    p.arrived = s.arrived;
+    p.arrived = reinterpret_cast<uint32_t*>(a->shares);
+    p.partial = reinterpret_cast<float*>(a->shares + kArrivedBytes);
     // tiles: a whole one each MR rows, and a partial one each bin with rows; K is
     // shared out while there are fewer workgroups than the chip holds, in shares of
     // 256 values and more
@@ -627,6 +644,7 @@ void q4_adapters_free(q4_adapters* a)
     (void)hipFree(a->wild);
     (void)hipFree(a->t);
     (void)hipFree(a->part8);
+    (void)hipFree(a->shares);
     (void)hipFree(a->many);
     for (char* p : a->retired) (void)hipFree(p);
     delete a;

@@ -597,8 +597,10 @@ q4_status q4_check_adapters(int slots, int rank);
  * q4_adapters_make -- a bank of `slots` adapters of rank at most `rank` for
  * handle h, in binary16 or (bf16 != 0) bfloat16, on h's device (the current
  * one). Every slot is empty (adds nothing). The bank holds slots * (parts * rank *
- * K + N rounded up to 32 * rank rounded up to 8) values and the workspace of its calls
- * (2 MiB and 4 bytes a row and value of rank once M passes Q4_GEMV_MAX_M); it does not
+ * K + N rounded up to 32 * rank rounded up to 8) values and the workspace of its calls:
+ * once M passes Q4_GEMV_MAX_M, 2 MiB and, a row, 16 bytes and 4 for each part and value of
+ * rank (rounded up to 8). Rows come in 256s and at least double as M grows; what is
+ * outgrown stays until the bank is freed, which is at most as much again. It does not
  * keep h. NULL on error.
  */
 q4_adapters* q4_adapters_make(const q4_matrix* h, int slots, int rank, int bf16);

@@ -326,3 +326,23 @@ def test_refusals():
     bank.close()
     with pytest.raises(ValueError, match="closed"):
         W.matmul_adapters(x, bank, index)
+
+
+def test_growth_row_by_row_keeps_little_memory():
+    """A bank's workspace grows by doubling: calls of one row more each time do not
+    allocate each time, and what is outgrown is no more than what is held."""
+    c = Case(128, [64], 128, slots=3, rank=16)
+    x, b, index = c.inputs(700)
+    c.W.matmul(x, b)
+    c.W.matmul_adapters(x[:2], c.bank, index[:2], b)
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    least = free
+    for M in range(33, 700):
+        y = c.W.matmul_adapters(x[:M], c.bank, index[:M], b)
+        if M % 97 == 0:
+            c.check(y, x[:M], b, index[:M], f"M={M}")
+        least = min(least, torch.cuda.mem_get_info()[0])
+    torch.cuda.synchronize()
+    # 2 MiB of sums, 1024 rows of 80 bytes and as much outgrown, each allocation up to 2 MiB; and the checks' own
+    assert free - least < 100 << 20, (free - least) / 2 ** 20
