@@ -431,6 +431,7 @@ q4_status load_slot(q4_adapters* a, int slot, const uint16_t* A, const uint16_t*
     if (cur != a->device) return fail(Q4_ERR_INVALID_ARG, "%s: the bank is on device %d, the current device is %d", who, a->device, cur);
     const size_t sa = (size_t)a->parts * a->rank * a->K, sb = b_values(a);
     const int grid = (int)std::min<size_t>((std::max(sa, sb) + 255) / 256, 4096);
+    const std::lock_guard<std::mutex> lock(a->mutex);      // (two launches)
     hipLaunchKernelGGL(q4_adapter_reset_kernel, dim3(1), dim3(1), 0, stream, a->scale + slot, a->wild + slot, c);
     hipLaunchKernelGGL((a->bf16 ? q4_adapter_load_kernel<true> : q4_adapter_load_kernel<false>), dim3(grid), dim3(256), 0, stream, A, B,
                        a->A + slot * sa, a->B + slot * sb, a->wild + slot, a->parts, rank, a->rank, a->rp, a->K, a->N);
@@ -451,11 +452,14 @@ q4_status adapters_check(const q4_adapters* a, const q4_matrix* h, const int* in
     return Q4_OK;
 }
 
+// Held over all of a call's launches: they hand c A x over in the bank's workspace, and
+// two host threads may use one stream.
+std::unique_lock<std::mutex> adapters_lock(q4_adapters* a) { return std::unique_lock<std::mutex>(a->mutex); }
+
 // Grow a bank's workspace to hold M rows before anything of a call is launched.
 q4_status adapters_reserve(q4_adapters* a, int M, hipStream_t stream)
 {
     const char* who = "q4_matmul_adapters";
-    std::lock_guard<std::mutex> lock(a->mutex);
     if (a->many_rows >= M) return Q4_OK;
     hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
     hipError_t e = hipStreamIsCapturing(stream, &cap);

@@ -6,6 +6,7 @@
 #include <climits>
 #include <cstring>
 #include <map>
+#include <mutex>
 #include <utility>
 #include <vector>
 
@@ -33,6 +34,7 @@ hipError_t launch_gemm_adapters(const q4_matrix* h, const uint16_t* x, const uin
                                 bool bf16, int waves, int workers, float* partials, uint32_t* counters,
                                 const q4dev::AdapterArgs& ad, hipStream_t stream);
 q4_status adapters_check(const q4_adapters* a, const q4_matrix* h, const int* index, bool bf16, const char* who);
+std::unique_lock<std::mutex> adapters_lock(q4_adapters* a);
 q4_status adapters_reserve(q4_adapters* a, int M, hipStream_t stream);
 q4_status adapters_prepare(q4_adapters* a, const uint16_t* x, const int* index, int M, bool few,
                            q4dev::AdapterArgs* args, hipStream_t stream);
@@ -467,8 +469,10 @@ q4_status matmul_impl(const q4_matrix* h, const uint16_t* x, const uint16_t* bia
     }
 
     q4dev::AdapterArgs ad = {};
+    std::unique_lock<std::mutex> bank_lock;
     if (bank) {
         if (q4_status st = adapters_check(bank, h, index, bf16, "q4_matmul_adapters"); st != Q4_OK) return st;
+        bank_lock = adapters_lock(bank);
         if (kind == Q4_PATH_MFMA)
             if (q4_status st = adapters_reserve(bank, M, stream); st != Q4_OK) return st;
     }

@@ -631,7 +631,8 @@ q4_status q4_adapters_clear(q4_adapters* a, int slot, hipStream_t stream);
  *
  * Errors, graph capture and concurrency as q4_matmul, for the handle and the bank alike: a
  * bank's workspace for M > Q4_GEMV_MAX_M grows on the first call with a larger
- * M, which cannot be captured, and calls on one bank are ordered on one stream.
+ * M, which cannot be captured, and calls on one bank are ordered on one stream. (A call is
+ * several launches; those of two host threads on one stream and one bank follow each other.)
  */
 q4_status q4_matmul_adapters(const q4_matrix* h, q4_adapters* bank, const uint16_t* x, const uint16_t* bias,
                              const int32_t* index, uint16_t* out, int M, int bf16, hipStream_t stream);

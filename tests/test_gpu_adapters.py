@@ -346,3 +346,36 @@ def test_growth_row_by_row_keeps_little_memory():
     torch.cuda.synchronize()
     # 2 MiB of sums, 1024 rows of 80 bytes and as much outgrown, each allocation up to 2 MiB; and the checks' own
     assert free - least < 100 << 20, (free - least) / 2 ** 20
+
+
+def test_two_threads_on_one_bank_and_stream():
+    """A call's launches hand c A x over in the bank: another thread's on the same
+    stream do not come between them."""
+    import threading
+    c = Case(512, [264, 64], 64, "bf16", slots=6, rank=16)
+    work, errors = [], []
+    for M in (5, 70, 31, 300):
+        x, b, index = c.inputs(M)
+        y = c.W.matmul_adapters(x, c.bank, index, b)
+        c.check(y, x, b, index, f"M={M}")
+        work.append((x, b, index, y, []))
+    torch.cuda.synchronize()
+
+    def run(x, b, index, y, outs):
+        try:
+            for _ in range(200):
+                outs.append(c.W.matmul_adapters(x, c.bank, index, b))
+        except Exception as e:      # reported below
+            errors.append(repr(e))
+
+    threads = [threading.Thread(target=run, args=w) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for x, _, _, y, outs in work:
+        assert len(outs) == 200
+        for i, o in enumerate(outs):
+            assert torch.equal(o, y), (x.shape[0], i)
