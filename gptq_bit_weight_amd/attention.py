@@ -358,7 +358,7 @@ class PagedCache:
             raise ValueError("table has no pages" if B else f"{T} tokens of no request")
         if not (starts.is_contiguous() and lengths.is_contiguous()) or (width > 1 and table.stride(1) != 1):
             raise ValueError("starts, lengths and the rows of table must be contiguous")
-        window = int(window)
+        window = min(int(window), 2 ** 31 - 1)       # (more keys than any cache has)
         if window < 0:
             raise ValueError(f"window must not be negative, got {window}")
         if q.data_ptr() % 16 or qs[0] % 8 or qs[1] % 8:

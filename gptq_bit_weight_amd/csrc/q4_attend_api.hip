@@ -129,6 +129,9 @@ q4_status q4_attend(const q4_cache* c, const uint16_t* q, int64_t q_token, int64
     p.table_stride = (int)table_stride;
     const long long rows = (long long)table_width * c->page_size;
     p.max_len = (int)(rows < (1 << 30) ? rows : (1 << 30));
+    // (a window that no key can lie outside is none; the kernels' 32-bit positions less a
+    // window then stay in range)
+    if (window >= p.max_len) window = 0;
     p.window = window;
     // (a negative scale turns q's signs, a scale of zero clears q)
     p.scale = scale == 0.f ? 1.f : std::fabs(scale) * 1.4426950408889634f;

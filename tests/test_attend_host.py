@@ -184,3 +184,31 @@ def test_a_captured_stream_that_is_not_the_current_one(monkeypatch, captured):
     for workspace, at, which in zip(held, seen, ("given", "current")):
         assert (workspace is None) == (captured == which)
         assert workspace is None or workspace.at == at
+
+
+@pytest.mark.parametrize("window", [0, 7, 2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 5, 10 ** 30])
+def test_no_window_is_cut_to_32_bits(monkeypatch, window):
+    """What the C call gets, an int, is the window or at least every row of the cache."""
+    import torch
+    from gptq_bit_weight_amd import attention
+
+    seen = []
+
+    class Library:
+        @staticmethod
+        def q4_attend(*a):
+            seen.append(a[12])
+            return 0
+
+    monkeypatch.setattr(attention, "load_library", lambda: Library)
+    monkeypatch.setattr(attention, "_raw_stream", lambda i: 7)
+    monkeypatch.setattr(attention, "_device", lambda: None)
+    monkeypatch.setattr(attention, "_workspaces", {})
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    c = object.__new__(attention.PagedCache)
+    c.device, c.dtype, c.dim, c.kv_heads, c._need, c._ref = torch.device("cpu"), torch.float16, 64, 2, {4: 1 << 16}, None
+    c.k = c.v = torch.zeros(2, 2, 16, 64, dtype=torch.float16)
+    c.attend(torch.zeros(3, 4, 64, dtype=torch.float16), torch.tensor([0, 3], dtype=torch.int32),
+             torch.tensor([20], dtype=torch.int32), torch.zeros(1, 2, dtype=torch.int32), window=window)
+    got = ctypes.c_int(seen[0]).value
+    assert got == seen[0] and (got == window or got >= 2 * 16)

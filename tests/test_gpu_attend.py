@@ -491,3 +491,15 @@ def test_captured_stream_that_is_not_the_current_one():
     check(y, *ref)
     for o in outs:
         assert torch.equal(o, y)
+
+
+@pytest.mark.parametrize("window", [200, 201, 304, 2 ** 30, 2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5, 10 ** 30])
+def test_windows_past_the_cache(window):
+    """A window of all the keys there are, or of any larger number, is none, also for
+    tokens at negative positions (more new tokens than cached ones)."""
+    import gptq_bit_weight_amd as q4
+    for D in (64, 128, 256):
+        for news, lens in (([300], [200]), ([3], [2]), ([1, 1, 40], [200, 3, 9]), ([300, 1], [0, 190])):
+            q, kc, vc, starts, lengths, table = make(torch.bfloat16, 4, 2, D, 16, news, lens)
+            y = q4.PagedCache(kc, vc).attend(q, starts, lengths, table, window=window)
+            check(y, *reference(q, kc, vc, news, lens, table), what=f"{D} {news} {lens}")
