@@ -472,6 +472,9 @@ q4_status matmul_impl(const q4_matrix* h, const uint16_t* x, const uint16_t* bia
     std::unique_lock<std::mutex> bank_lock;
     if (bank) {
         if (q4_status st = adapters_check(bank, h, index, bf16, "q4_matmul_adapters"); st != Q4_OK) return st;
+        const View to = flat_view(out, (int64_t)M * h->N * 2);
+        if (meet(to, flat_view(index, (int64_t)M * 4)) || (bias && meet(to, flat_view(bias, (int64_t)h->N * 2))))
+            return fail(Q4_ERR_INVALID_ARG, "q4_matmul_adapters: out overlaps index or bias");
         bank_lock = adapters_lock(bank);
         if (kind == Q4_PATH_MFMA)
             if (q4_status st = adapters_reserve(bank, M, stream); st != Q4_OK) return st;

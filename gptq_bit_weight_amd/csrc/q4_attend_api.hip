@@ -97,6 +97,14 @@ q4_status q4_attend(const q4_cache* c, const uint16_t* q, int64_t q_token, int64
     const int g = heads / c->kv_heads;
     if ((long long)tokens * g > (1 << 30) || (long long)heads * c->dim > (1 << 30))
         return fail(Q4_ERR_UNSUPPORTED, "%s: %d tokens of %d heads", who, tokens, heads);
+    // (row tiles are stored while others still read)
+    const View to = head_view(out, out_token, out_head, tokens, heads, c->dim);
+    if (meet(to, head_view(q, q_token, q_head, tokens, heads, c->dim))) return fail(Q4_ERR_INVALID_ARG, "%s: out overlaps q", who);
+    if (meet(to, cache_view(c, false)) || meet(to, cache_view(c, true)))
+        return fail(Q4_ERR_INVALID_ARG, "%s: out overlaps the cache", who);
+    if (meet(to, flat_view(starts, ((int64_t)requests + 1) * 4)) || meet(to, flat_view(lengths, (int64_t)requests * 4)) ||
+        meet(to, View{table, (int64_t)table_width * 4, {{requests, table_stride * 4}, {1, 0}, {1, 0}}}))
+        return fail(Q4_ERR_INVALID_ARG, "%s: out overlaps starts, lengths or table", who);
     int dev = -1, cu = 0;
     if (q4_status st = device_info(&dev, &cu); st != Q4_OK) return st;
 

@@ -258,6 +258,12 @@ q4_status check_rotary(const q4_rotary* r, const void* positions, int position_b
     return Q4_OK;
 }
 
+// (of one token, or one head, the stride does not count)
+bool same_view(const uint16_t* a, int64_t at, int64_t ah, const uint16_t* b, int64_t bt, int64_t bh, int tokens, int heads)
+{
+    return a == b && (at == bt || tokens == 1) && (ah == bh || heads == 1);
+}
+
 }  // namespace
 
 extern "C" {
@@ -311,6 +317,12 @@ q4_status q4_rotary_apply(const q4_rotary* r, const uint16_t* x, int64_t x_token
     if (q4_status st = check_rotary(r, positions, position_bits, who); st != Q4_OK) return st;
     if (!x || !out) return q4::fail(Q4_ERR_INVALID_ARG, "%s: null pointer", who);
     if ((long long)heads * r->dim > (1 << 24)) return q4::fail(Q4_ERR_UNSUPPORTED, "%s: more than 2^24 values a token", who);
+    const q4::View to = q4::head_view(out, out_token, out_head, tokens, heads, r->dim);
+    if (!same_view(x, x_token, x_head, out, out_token, out_head, tokens, heads) &&
+        q4::meet(to, q4::head_view(x, x_token, x_head, tokens, heads, r->dim)))
+        return q4::fail(Q4_ERR_INVALID_ARG, "%s: out overlaps its input without being the same view", who);
+    if (q4::meet(to, q4::flat_view(positions, (int64_t)tokens * position_bits / 8)))
+        return q4::fail(Q4_ERR_INVALID_ARG, "%s: out overlaps the positions", who);
     RopeArgs p = {};
     set_rotary(p, r, transpose != 0);
     p.dim = r->dim;
@@ -355,6 +367,19 @@ q4_status q4_cache_append(const q4_cache* c, const uint16_t* k, int64_t k_token,
     if (q) {
         if (!r) return q4::fail(Q4_ERR_INVALID_ARG, "%s: q is given without a rotary", who);
         if (!q_out || heads < 1) return q4::fail(Q4_ERR_INVALID_ARG, "%s: q without heads or output", who);
+        // (a workgroup writes its part of q_out while others read k and v)
+        const q4::View to = q4::head_view(q_out, out_token, out_head, tokens, heads, c->dim);
+        if (!same_view(q, q_token, q_head, q_out, out_token, out_head, tokens, heads) &&
+            q4::meet(to, q4::head_view(q, q_token, q_head, tokens, heads, c->dim)))
+            return q4::fail(Q4_ERR_INVALID_ARG, "%s: q_out overlaps q without being the same view", who);
+        if (q4::meet(to, q4::head_view(k, k_token, k_head, tokens, c->kv_heads, c->dim)) ||
+            q4::meet(to, q4::head_view(v, v_token, v_head, tokens, c->kv_heads, c->dim)))
+            return q4::fail(Q4_ERR_INVALID_ARG, "%s: q_out overlaps k or v", who);
+        if (q4::meet(to, q4::cache_view(c, false)) || q4::meet(to, q4::cache_view(c, true)))
+            return q4::fail(Q4_ERR_INVALID_ARG, "%s: q_out overlaps the cache", who);
+        if (q4::meet(to, q4::flat_view(slots, (int64_t)tokens * slot_bits / 8)) ||
+            q4::meet(to, q4::flat_view(positions, (int64_t)tokens * position_bits / 8)))
+            return q4::fail(Q4_ERR_INVALID_ARG, "%s: q_out overlaps slots or positions", who);
         p.H = heads;
         p.q = q;
         p.q_t = q_token;

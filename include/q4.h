@@ -514,7 +514,8 @@ q4_status q4_rotary_plan(int dim, int rot, int scaling, double base, double fact
  * `transpose` its transpose (the gradient of the input from the gradient of
  * the output). Positions are device integers of 32 or 64 bits, negative ones
  * allowed; the angle is exact modulo a turn (64-bit fixed point). fp32, one
- * rounding. out may be x itself (same strides), else they must not overlap.
+ * rounding. out may be x itself (same strides), else they must not overlap (nor
+ * out and the positions): Q4_ERR_INVALID_ARG.
  */
 q4_status q4_rotary_apply(const q4_rotary* r, const uint16_t* x, int64_t x_token, int64_t x_head, uint16_t* out,
                           int64_t out_token, int64_t out_head, const void* positions, int position_bits,
@@ -540,7 +541,8 @@ typedef struct {
  * and its values go to row slots[t] % page_size of page slots[t] / page_size.
  * A token whose slot is negative or not below pages * page_size is not
  * written; two tokens with one slot leave either's row. With q, its `heads`
- * heads are rotated too, into q_out (which may be q itself), for every token.
+ * heads are rotated too, into q_out (which may be q itself), for every token; q_out
+ * must not overlap anything else of the call (Q4_ERR_INVALID_ARG).
  */
 q4_status q4_cache_append(const q4_cache* c, const uint16_t* k, int64_t k_token, int64_t k_head, const uint16_t* v,
                           int64_t v_token, int64_t v_head, const void* slots, int slot_bits, int tokens,
@@ -576,7 +578,8 @@ size_t q4_attend_workspace(const q4_cache* c, int heads);
  * multiples of 8 values, their base 16-byte aligned. `workspace` is device
  * memory of at least q4_attend_workspace bytes whose first 64 KiB are zero before
  * its first use (each call leaves them fit for the next); calls that share it must not overlap
- * in time. Host and device never synchronize; the call may be captured.
+ * in time. out must not overlap an input (Q4_ERR_INVALID_ARG). Host and device never
+ * synchronize; the call may be captured.
  */
 q4_status q4_attend(const q4_cache* c, const uint16_t* q, int64_t q_token, int64_t q_head, int heads, int tokens,
                     const int32_t* starts, const int32_t* lengths, const int32_t* table, int table_width,

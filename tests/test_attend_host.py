@@ -212,3 +212,18 @@ def test_no_window_is_cut_to_32_bits(monkeypatch, window):
              torch.tensor([20], dtype=torch.int32), torch.zeros(1, 2, dtype=torch.int32), window=window)
     got = ctypes.c_int(seen[0]).value
     assert got == seen[0] and (got == window or got >= 2 * 16)
+
+
+# out is 3 tokens of 8 heads of 64 at 65536: 1024 bytes a token. (Each call is refused
+# later on too, for its workspace or the missing device: nothing is launched.)
+@pytest.mark.parametrize("cache,kw,meets", [
+    ({}, {}, False), ({}, dict(q=65536), True), ({}, dict(q=65536 + 2048), True), ({}, dict(q=65536 + 1024, o_token=1024, q_token=1024), False),
+    ({}, dict(q=65536 + 1024, o_token=1024, q_token=1032), True), (dict(k=65536), {}, True), (dict(v=65536 - 1024), {}, True),
+    (dict(k=65536 - 16384), {}, False), (dict(v=65536 + 3072), {}, False), ({}, dict(starts=65536 - 8), True),
+    ({}, dict(starts=65536 - 12), False), ({}, dict(lengths=65536 + 3068), True), ({}, dict(table=65536 - 12, stride=3), True),
+    ({}, dict(table=65536 - 20, stride=3), False),
+])
+def test_attend_out_that_meets_an_input(cache, kw, meets):
+    lib = q4.load_library()
+    assert _attend(lib, cache, ws=None, **kw) != 0
+    assert (b"overlaps" in lib.q4_last_error()) == meets

@@ -379,3 +379,28 @@ def test_two_threads_on_one_bank_and_stream():
         assert len(outs) == 200
         for i, o in enumerate(outs):
             assert torch.equal(o, y), (x.shape[0], i)
+
+
+def test_out_that_meets_an_input_is_refused():
+    c = Case(128, [128], 128, rank=8)
+    for M in (4, 40):
+        x, b, index = c.inputs(M)
+        own = torch.zeros(3 * M * 128, dtype=c.dt, device="cuda")
+        out, ints = own[:M * 128].view(M, 128), own[M * 128 - 2 * M:M * 128].view(torch.int32)
+        ints.copy_(index)
+        for args, kw in (((x, c.bank, index, b), dict(out=x)), ((x, c.bank, ints, b), dict(out=out)),
+                         ((x, c.bank, index, own[64:192]), dict(out=out))):
+            with pytest.raises(ValueError, match="overlaps"):
+                c.W.matmul_adapters(*args, **kw)
+        y = c.W.matmul_adapters(x, c.bank, index, own[M * 128:M * 128 + 128], out=out)
+        c.check(y, x, own[M * 128:M * 128 + 128], index)
+
+
+def test_activations_off_sixteen_bytes_are_refused():
+    c = Case(128, [128], 128, rank=8)
+    for M in (4, 40):
+        x, b, index = c.inputs(M)
+        odd = torch.zeros(x.numel() + 1, dtype=c.dt, device="cuda")[1:].view(x.shape)
+        odd.copy_(x)
+        with pytest.raises(ValueError, match="16-byte aligned"):
+            c.W.matmul_adapters(odd, c.bank, index, b)

@@ -503,3 +503,23 @@ def test_windows_past_the_cache(window):
             q, kc, vc, starts, lengths, table = make(torch.bfloat16, 4, 2, D, 16, news, lens)
             y = q4.PagedCache(kc, vc).attend(q, starts, lengths, table, window=window)
             check(y, *reference(q, kc, vc, news, lens, table), what=f"{D} {news} {lens}")
+
+
+def test_out_that_meets_an_input_is_refused():
+    import gptq_bit_weight_amd as q4
+    q, kc, vc, starts, lengths, table = make(torch.float16, 8, 2, 128, 16, [1, 1], [30, 20])
+    c = q4.PagedCache(kc, vc)
+    flat = torch.zeros(2 * 8 * 128 + 64, dtype=torch.float16, device="cuda")
+    ints = flat[-8:].view(torch.int32)
+    ints[:2].copy_(lengths)
+    for kw in (dict(out=kc.view(-1)[:2048].view(2, 8, 128)), dict(out=vc.view(-1)[256:2304].view(2, 8, 128)),
+               dict(out=flat[64:].view(2, 8, 128), lengths=ints[:2])):
+        with pytest.raises(ValueError, match="overlaps"):
+            c.attend(**{**dict(q=q, starts=starts, lengths=lengths, table=table), **kw})
+    # parts of one wider row that lie side by side are not in each other's way
+    arena = torch.zeros(2, 3, 8, 128, dtype=torch.float16, device="cuda")
+    arena[:, 0] = q
+    check(c.attend(arena[:, 0], starts, lengths, table, out=arena[:, 1]), *reference(q, kc, vc, [1, 1], [30, 20], table))
+    assert (arena[:, 2] == 0).all() and torch.equal(arena[:, 0], q)
+    with pytest.raises(ValueError, match="overlaps"):
+        c.attend(arena[:, 0], starts, lengths, table, out=arena.view(2, 24, 128)[:, 7:15])

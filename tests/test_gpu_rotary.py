@@ -306,3 +306,38 @@ def test_nothing_to_do():
     assert r.rotate(torch.empty(0, 2, 64, dtype=torch.float16, device="cuda"), e).shape == (0, 2, 64)
     p = torch.arange(2, device="cuda")
     assert r.rotate(torch.empty(2, 0, 64, dtype=torch.float16, device="cuda"), p).shape == (2, 0, 64)
+
+
+def test_outputs_that_meet_inputs_are_refused():
+    """q_out against q, k, v, the cache and the indexes; parts of one row side by side pass."""
+    import gptq_bit_weight_amd as q4
+    T, H, kv, D, ps = 5, 4, 2, 64, 16
+    fused = torch.randn(T, H + 2 * kv + H, D, device="cuda").half()
+    q, k, v, rest = fused.split([H, kv, kv, H], 1)
+    kc, vc = torch.zeros(2, 3, kv, ps, D, dtype=torch.float16, device="cuda")
+    c, r = q4.PagedCache(kc, vc), q4.Rotary(D)
+    slots, pos = torch.arange(T, device="cuda"), torch.arange(T, device="cuda") + 3
+    args = dict(rotary=r, positions=pos)
+    own = torch.zeros(8 * T * H * D, dtype=torch.float16, device="cuda")
+    index = own[:4 * T].view(torch.int64)
+    index.copy_(slots)
+    bad = [
+        dict(q=q, q_out=fused[:, H - 1:2 * H - 1]), dict(q=q.clone(), q_out=fused[:, H:2 * H]), dict(q=q.clone(), q_out=fused[:, 2:2 + H]),
+        dict(q=q.clone(), q_out=kc.view(-1)[:T * H * D].view(T, H, D)), dict(q=q.clone(), q_out=vc.view(-1)[64:64 + T * H * D].view(T, H, D)),
+        dict(q=q, q_out=own[8:8 + T * H * D].view(T, H, D), slots=index), dict(q=q, q_out=own[8:8 + T * H * D].view(T, H, D), positions=index),
+    ]
+    for i, kw in enumerate(bad):
+        with pytest.raises(ValueError, match="overlaps"):
+            c.append(**{**dict(k=k, v=v, slots=slots, **args), **kw})
+            pytest.fail(f"case {i} was taken")
+    with pytest.raises(ValueError, match="overlaps"):
+        r.rotate(q.contiguous(), index, out=own[8:8 + T * H * D].view(T, H, D))
+    assert (kc == 0).all() and (vc == 0).all()
+    keep = fused.clone()
+    out = c.append(k, v, slots, q=q.clone(), q_out=rest, **args)
+    assert out is rest
+    check(rest, *rotated(keep[:, :H], pos, D, "half", "none"), "beside")
+    assert torch.equal(fused[:, :H + 2 * kv], keep[:, :H + 2 * kv])
+    c.append(k, v, slots, q=q, q_out=q, **args)
+    check(q, *rotated(keep[:, :H], pos, D, "half", "none"), "in place")
+    assert torch.equal(fused[:, H:H + 2 * kv], keep[:, H:H + 2 * kv])
