@@ -457,16 +457,20 @@ class Q4Matrix:
                     and (shape is None or t.shape == shape)):
                 _dev_tensor(t, want, name, shape)
                 raise ValueError(f"{name} is on {t.device}, expected {dev}, the matrix's device")
-        if out is None:
-            if stream is None:
+        from .attention import _call, _writable, _wrote
+        written = out is not None
+        if written:
+            _writable(out, "out")
+        elif stream is None:
+            out = x.new_empty((M, self.N))
+        else:
+            with torch.cuda.stream(stream):
                 out = x.new_empty((M, self.N))
-            else:
-                with torch.cuda.stream(stream):
-                    out = x.new_empty((M, self.N))
-        from .attention import _call
         _call(load_library().q4_matmul_adapters, "q4_matmul_adapters", dev, stream,
               (h, bank._handle(), x.data_ptr(), bias.data_ptr() if bias is not None else None, index.data_ptr(),
                out.data_ptr(), M, 1 if dt is torch.bfloat16 else 0), () if stream is None else [t for t in (x, index, out, bias) if t is not None])
+        if written:
+            _wrote(out)
         return out
 
     def dequant_dump(self, path: int = PATH_GEMV, stream=None, dtype=None):

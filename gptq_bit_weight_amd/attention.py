@@ -35,6 +35,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i:
 _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _dense = torch.contiguous_format
 _Tensor, _int32_t, _int64_t = torch.Tensor, torch.int32, torch.int64
+_wrote = torch.autograd.graph.increment_version      # tells autograd of tensors written in place
+
+
+def _writable(t, name):
+    """An output given by the caller, or the cache: no gradient goes through a write."""
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient and cannot be written in place (but under torch.no_grad())")
 
 
 class _Cache(ctypes.Structure):
@@ -119,6 +126,7 @@ def _out_like(x, out, name, stream):
         with torch.cuda.stream(stream):
             return torch.empty_like(x, memory_format=_dense)
     _heads(out, name, x.device, x.dtype, *x.shape)
+    _writable(out, name)
     _distinct(out, name)            # (the C call refuses one that meets an input)
     return out
 
@@ -221,18 +229,22 @@ class Rotary:
         dev = self.device
         (T, H, _), xs = _heads(x, "x", dev, None, None, None, self.dim)
         bits = _index(positions, "positions", dev, T)
+        written = out is not None
         out = _out_like(x, out, "out", stream)
         os_ = out.stride()
         _call(load_library().q4_rotary_apply, "q4_rotary_apply", dev, stream,
               (self._handle(), x.data_ptr(), xs[0], xs[1], out.data_ptr(), os_[0], os_[1], positions.data_ptr(), bits,
                T, H, 1 if transpose else 0, 1 if x.dtype == torch.bfloat16 else 0), (x, positions, out))
+        if written:
+            _wrote(out)
         return out
 
     def rotate(self, x, positions, *, transpose: bool = False, out=None, stream=None):
         """x [tokens, heads, dim] (float16 or bfloat16, any token and head
         strides) turned by positions [tokens]; with `transpose` the other way
         with the same factor: the gradient's pass. fp32, rounded once. out may
-        be x itself. Without `out` the call is differentiable in x."""
+        be x itself. Without `out` the call is differentiable in x; one that
+        requires a gradient is refused while gradients are recorded."""
         if out is None and isinstance(x, torch.Tensor) and x.requires_grad and torch.is_grad_enabled():
             return _Rotate.apply(x, self, positions, transpose, stream)
         return self._rotate(x, positions, transpose, out, stream)
@@ -292,7 +304,9 @@ class PagedCache:
         _, vs = _heads(v, "v", dev, dt, T, kv, D)
         sb = _index(slots, "slots", dev, T)
         pb, pp, rh, qa = 32, None, None, (None, 0, 0, None, 0, 0, 0)
-        used = (k, v, slots)
+        used, written = (k, v, slots), (self.k, self.v)
+        _writable(self.k, "the cache's k")
+        _writable(self.v, "the cache's v")
         if rotary is not None:
             if rotary.dim != D:
                 raise ValueError(f"rotary turns heads of {rotary.dim} values, the cache has {D}")
@@ -306,6 +320,8 @@ class PagedCache:
             if rotary is None:
                 raise ValueError("q is given without rotary")
             (_, H, _), qs = _heads(q, "q", dev, dt, T, None, D)
+            if q_out is not None:
+                written += (q_out,)
             q_out = _out_like(q, q_out, "q_out", stream)
             if H:
                 os_ = q_out.stride()
@@ -316,6 +332,7 @@ class PagedCache:
         _call(load_library().q4_cache_append, "q4_cache_append", dev, stream,
               (self._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], slots.data_ptr(), sb, T, rh, pp, pb)
               + qa, used if stream is None else used + (self.k, self.v))
+        _wrote(written)
         return q_out
 
     def attend(self, q, starts, lengths, table, *, window: int = 0, scale=None, out=None, stream=None):
@@ -352,10 +369,12 @@ class PagedCache:
                 q.record_stream(stream)
             q = _on(stream, torch.clone, q, memory_format=_dense)
             qs = q.stride()
-        if out is None:
+        written = out is not None
+        if not written:
             out = _out_like(q, None, "out", stream)
         else:
             _heads(out, "out", dev, dt, T, H, D)
+            _writable(out, "out")
             _distinct(out, "out")
         table, ts = _table_rows(table, stream)
         os_ = out.stride()
@@ -367,12 +386,16 @@ class PagedCache:
             # (the call's own: a graph may replay beside other work of the stream it was captured on)
             ws = _on(stream, _new_workspace, need, dev)
             _call(fn, "q4_attend", dev, stream, args + (ws.data_ptr(), need), used)
+            if written:
+                _wrote(out)
             return out
         ws = _workspace(dev, stream)
         with ws.lock:
             if ws.bytes < need:
                 ws.hold(_on(stream, _new_workspace, need, dev))
             _call(fn, "q4_attend", dev, stream, args + (ws.at, ws.bytes), used)
+        if written:
+            _wrote(out)
         return out
 
     def _workspace_bytes(self, heads):

@@ -227,3 +227,70 @@ def test_attend_out_that_meets_an_input(cache, kw, meets):
     lib = q4.load_library()
     assert _attend(lib, cache, ws=None, **kw) != 0
     assert (b"overlaps" in lib.q4_last_error()) == meets
+
+
+def _stand_in(monkeypatch):
+    """The binding over a library that does nothing, on CPU tensors."""
+    import torch
+    from gptq_bit_weight_amd import attention
+
+    class Library:
+        q4_attend = q4_cache_append = q4_rotary_apply = staticmethod(lambda *a: 0)
+
+    monkeypatch.setattr(attention, "load_library", lambda: Library)
+    monkeypatch.setattr(attention, "_raw_stream", lambda i: 7)
+    monkeypatch.setattr(attention, "_device", lambda: None)
+    monkeypatch.setattr(attention, "_workspaces", {})
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    c = object.__new__(attention.PagedCache)
+    c.device, c.dtype, c.dim, c.kv_heads, c._need, c._ref = torch.device("cpu"), torch.float16, 64, 2, {4: 1 << 16}, None
+    c.k, c.v = torch.zeros(2, 2, 2, 16, 64, dtype=torch.float16).clone().unbind(0)
+    r = object.__new__(attention.Rotary)
+    r.device, r.dim, r._h = torch.device("cpu"), 64, 1
+    monkeypatch.setattr(attention.Rotary, "close", lambda self: None)
+    return c, r
+
+
+def test_writes_in_place_are_told_to_autograd(monkeypatch):
+    """Outputs that the caller gives, and the cache: a tensor saved for a backward
+    pass is found changed, one that requires a gradient is refused."""
+    import torch
+    c, r = _stand_in(monkeypatch)
+    T = 3
+    make = lambda h: torch.randn(T, h, 64).half()  # noqa: E731
+    pos = torch.arange(T)
+    starts, lengths = torch.tensor([0, T], dtype=torch.int32), torch.tensor([20], dtype=torch.int32)
+    table = torch.zeros(1, 2, dtype=torch.int32)
+    calls = {
+        "rotate": lambda t: r.rotate(t, pos, out=t),
+        "append": lambda t: c.append(make(2), make(2), pos, rotary=r, positions=pos, q=t, q_out=t),
+        "attend": lambda t: c.attend(make(4), starts, lengths, table, out=t),
+    }
+    for name, call in calls.items():
+        w = torch.ones(T, 4, 64, dtype=torch.float16, requires_grad=True)
+        t = make(4)
+        y = (w * t).sum()                        # saves t
+        at = t._version
+        call(t)
+        assert t._version > at, name
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+        for leaf in (make(4).requires_grad_(), make(4).requires_grad_() * 1):
+            with pytest.raises(ValueError, match="requires a gradient"):
+                call(leaf)
+            with torch.no_grad():
+                at = leaf._version
+                call(leaf)
+                assert leaf._version > at, name
+        with torch.inference_mode():
+            call(make(4))
+    at = c.k._version, c.v._version
+    c.append(make(2), make(2), pos)
+    assert c.k._version > at[0] and c.v._version > at[1]
+    c.v.requires_grad_()
+    with pytest.raises(ValueError, match="requires a gradient"):
+        c.append(make(2), make(2), pos)
+    with torch.no_grad():
+        c.append(make(2), make(2), pos)
+    # what the calls make themselves is not written in place
+    assert r.rotate(make(4), pos)._version == 0 and c.attend(make(4), starts, lengths, table)._version == 0

@@ -404,3 +404,18 @@ def test_activations_off_sixteen_bytes_are_refused():
         odd.copy_(x)
         with pytest.raises(ValueError, match="16-byte aligned"):
             c.W.matmul_adapters(odd, c.bank, index, b)
+
+
+def test_out_is_told_to_autograd():
+    c = Case(128, [128], 128, rank=8)
+    x, b, index = c.inputs(4)
+    out = torch.zeros(4, 128, dtype=c.dt, device="cuda")
+    y = (torch.ones_like(out, requires_grad=True) * out).sum()      # saves out
+    c.W.matmul_adapters(x, c.bank, index, b, out=out)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    c.check(out, x, b, index)
+    with pytest.raises(ValueError, match="requires a gradient"):
+        c.W.matmul_adapters(x, c.bank, index, b, out=out.clone().requires_grad_())
+    with torch.no_grad():
+        c.check(c.W.matmul_adapters(x, c.bank, index, b, out=out.clone().requires_grad_()), x, b, index)
