@@ -16,6 +16,7 @@ import ctypes
 import threading
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _check, _raise, load_library
 
@@ -38,10 +39,17 @@ _Tensor, _int32_t, _int64_t = torch.Tensor, torch.int32, torch.int64
 _wrote = torch.autograd.graph.increment_version      # tells autograd of tensors written in place
 
 
+def _recorded(t):
+    """Whether a derivative goes by t: backward, or forward (it has a tangent)."""
+    return (t.requires_grad and torch.is_grad_enabled()) or (
+        forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None)
+
+
 def _writable(t, name):
-    """An output given by the caller, or the cache: no gradient goes through a write."""
-    if t.requires_grad and torch.is_grad_enabled():
-        raise ValueError(f"{name} requires a gradient and cannot be written in place (but under torch.no_grad())")
+    """An output given by the caller, or the cache: no derivative goes through a write."""
+    if _recorded(t):
+        raise ValueError(f"{name} requires a gradient, or has a tangent, and cannot be written in place "
+                         "(under torch.no_grad() a gradient's may)")
 
 
 class _Cache(ctypes.Structure):
@@ -151,28 +159,42 @@ def _call(fn, what, device, stream, args, used=()):
 
 
 class _Rotate(torch.autograd.Function):
+    """The rotation is linear: a tangent is turned as x is, a gradient the other way."""
+
     @staticmethod
-    def forward(ctx, x, rotary, positions, transpose, stream):
-        ctx.save_for_backward(positions)
-        ctx.rotary, ctx.transpose, ctx.stream = rotary, transpose, stream
+    def forward(x, rotary, positions, transpose, stream):
         return rotary._rotate(x.detach(), positions, transpose, None, stream)
 
     @staticmethod
-    def backward(ctx, grad):
+    def setup_context(ctx, inputs, output):
+        _, ctx.rotary, positions, ctx.transpose, ctx.stream = inputs
+        ctx.save_for_backward(positions)
+        ctx.save_for_forward(positions)
+
+    @staticmethod
+    def _turn(ctx, t, transpose):
         positions, = ctx.saved_tensors
-        if grad.stride(2) != 1:
-            grad = grad.contiguous()
+        if t.stride(2) != 1:
+            t = t.contiguous()
         # (on the forward pass's stream, between what makes the gradient and what
         # takes it, which are on the one that was current then)
         s = ctx.stream
         if s is not None:
-            now = torch.cuda.current_stream(grad.device)
+            now = torch.cuda.current_stream(t.device)
             s.wait_stream(now)
-        out = _Rotate.apply(grad, ctx.rotary, positions, not ctx.transpose, s)
+        out = _Rotate.apply(t, ctx.rotary, positions, transpose, s)
         if s is not None:
             now.wait_stream(s)
             out.record_stream(now)
-        return out, None, None, None, None
+        return out
+
+    @staticmethod
+    def backward(ctx, grad):
+        return _Rotate._turn(ctx, grad, not ctx.transpose), None, None, None, None
+
+    @staticmethod
+    def jvp(ctx, tangent, *rest):
+        return _Rotate._turn(ctx, tangent, ctx.transpose)
 
 
 class Rotary:
@@ -243,9 +265,9 @@ class Rotary:
         """x [tokens, heads, dim] (float16 or bfloat16, any token and head
         strides) turned by positions [tokens]; with `transpose` the other way
         with the same factor: the gradient's pass. fp32, rounded once. out may
-        be x itself. Without `out` the call is differentiable in x; one that
-        requires a gradient is refused while gradients are recorded."""
-        if out is None and isinstance(x, torch.Tensor) and x.requires_grad and torch.is_grad_enabled():
+        be x itself. Without `out` the call is differentiable in x (backward and
+        forward); one that requires a gradient is refused while gradients are recorded."""
+        if out is None and isinstance(x, torch.Tensor) and _recorded(x):
             return _Rotate.apply(x, self, positions, transpose, stream)
         return self._rotate(x, positions, transpose, out, stream)
 

@@ -341,3 +341,24 @@ def test_outputs_that_meet_inputs_are_refused():
     c.append(k, v, slots, q=q, q_out=q, **args)
     check(q, *rotated(keep[:, :H], pos, D, "half", "none"), "in place")
     assert torch.equal(fused[:, H:H + 2 * kv], keep[:, H:H + 2 * kv])
+
+
+def test_tangents():
+    """Forward derivatives: a tangent is turned as x is, on another stream too."""
+    import gptq_bit_weight_amd as q4
+    from torch.autograd import forward_ad
+    r = q4.Rotary(64, 32, scaling=SCALINGS["by_parts"])
+    g = torch.Generator().manual_seed(5)
+    x, v = torch.randn(2, 5, 3, 64, generator=g).bfloat16().cuda()
+    pos = torch.arange(700, 705, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for tr in (False, True):
+        for stream in (None, s):
+            with forward_ad.dual_level():
+                y, dy = forward_ad.unpack_dual(r.rotate(forward_ad.make_dual(x, v), pos, transpose=tr, stream=stream))
+            torch.cuda.synchronize()
+            check(y, *rotated(x, pos, 32, "half", "by_parts", tr), "value")
+            check(dy, *rotated(v, pos, 32, "half", "by_parts", tr), "tangent")
+    with forward_ad.dual_level(), pytest.raises(ValueError, match="tangent"):
+        r.rotate(x, pos, out=forward_ad.make_dual(x, v))

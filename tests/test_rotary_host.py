@@ -120,3 +120,56 @@ def test_cache_rows_fit_31_bits():
     c = _cache(pages=1 << 20, page_size=1 << 12)
     assert q4.load_library().q4_cache_append(ctypes.byref(c), 4096, 0, 0, 4096, 0, 0, 4096, 64, 1, None, None, 32,
                                              None, 0, 0, None, 0, 0, 0, None) == 2
+
+
+class _Plain:
+    """A rotation of heads of 4 values on the CPU, in the place of the library's."""
+    dim = 4
+
+    def _rotate(self, x, positions, transpose, out, stream):
+        import torch
+        assert not x.requires_grad and x.data_ptr()
+        c, s = positions.to(x.dtype).cos()[:, None, None], positions.to(x.dtype).sin()[:, None, None] * (-1 if transpose else 1)
+        a, b = x[..., :2], x[..., 2:]
+        return torch.cat([a * c - b * s, b * c + a * s], -1)
+
+
+def test_derivatives_backward_and_forward():
+    """What rotate() records: gradients and tangents, of each other too, against
+    differences, and through the functional transforms."""
+    import torch
+    from torch.autograd import forward_ad
+
+    plain, pos = _Plain(), torch.tensor([5, 0, -3])
+    g = torch.Generator().manual_seed(2)
+    x, v = torch.randn(2, 3, 2, 4, generator=g, dtype=torch.float64)
+
+    def rotate(t, transpose=False):
+        return q4.Rotary.rotate(plain, t, pos, transpose=transpose)
+
+    want = rotate(v)
+    with forward_ad.dual_level():
+        for tangent in (v, v.transpose(0, 2).contiguous().transpose(0, 2)):
+            y, dy = forward_ad.unpack_dual(rotate(forward_ad.make_dual(x, tangent)))
+            assert torch.equal(y, rotate(x)) and torch.equal(dy, want)
+            with torch.no_grad():
+                assert torch.equal(forward_ad.unpack_dual(rotate(forward_ad.make_dual(x, tangent))).tangent, want)
+        assert forward_ad.unpack_dual(rotate(x)).tangent is None
+    assert torch.equal(torch.func.jvp(rotate, (x,), (v,))[1], want)
+    assert torch.allclose(torch.func.grad(lambda t: (rotate(t) * v).sum())(x), rotate(v, True))
+    # (R^T R = 1: the gradient of |R x|^2 / 2 is x, its tangent v)
+    assert torch.allclose(torch.func.jvp(torch.func.grad(lambda t: (rotate(t) ** 2).sum() / 2), (x,), (v,))[1], v)
+    leaf = x.clone().requires_grad_()
+    assert torch.autograd.gradcheck(rotate, (leaf,), check_forward_ad=True)
+    assert torch.autograd.gradgradcheck(lambda t: rotate(t) ** 2, (leaf,))
+
+
+def test_outputs_with_a_tangent_are_refused():
+    import torch
+    from torch.autograd import forward_ad
+    from gptq_bit_weight_amd.attention import _writable
+    x = torch.zeros(3, 2, 4, dtype=torch.float16)
+    with forward_ad.dual_level():
+        _writable(x, "out")
+        with pytest.raises(ValueError, match="tangent"):
+            _writable(forward_ad.make_dual(x, x), "out")
