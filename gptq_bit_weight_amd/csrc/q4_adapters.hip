@@ -372,6 +372,7 @@ __global__ __launch_bounds__(MT, 2) void q4_adapter_many_kernel(ManyArgs p)
 
 struct q4_adapters {
     int slots = 0, rank = 0, rp = 0, parts = 0, K = 0, N = 0, device = -1;
+    std::vector<int> part_n;           // columns of each part
     bool bf16 = false;
     uint16_t *A = nullptr, *B = nullptr;
     float* scale = nullptr;
@@ -444,7 +445,7 @@ q4_status load_slot(q4_adapters* a, int slot, const uint16_t* A, const uint16_t*
 q4_status adapters_check(const q4_adapters* a, const q4_matrix* h, const int* index, bool bf16, const char* who)
 {
     if (!a || !index) return fail(Q4_ERR_INVALID_ARG, "%s: null bank or index", who);
-    if (a->K != h->K || a->N != h->N || a->device != h->device || a->parts != (int)h->part_n.size())
+    if (a->K != h->K || a->N != h->N || a->device != h->device || a->part_n != h->part_n)
         return fail(Q4_ERR_INVALID_ARG, "%s: the bank was made for another matrix", who);
     if (a->bf16 != bf16)
         return fail(Q4_ERR_INVALID_ARG, "%s: the bank holds %s, the activations are %s", who, a->bf16 ? "bfloat16" : "float16",
@@ -597,6 +598,13 @@ q4_adapters* q4_adapters_make(const q4_matrix* h, int slots, int rank, int bf16)
     }
     q4_adapters* a = new (std::nothrow) q4_adapters;
     if (!a) {
+        q4::fail(Q4_ERR_OOM, "%s: out of memory", who);
+        return nullptr;
+    }
+    try {
+        a->part_n = h->part_n;
+    } catch (const std::bad_alloc&) {
+        delete a;
         q4::fail(Q4_ERR_OOM, "%s: out of memory", who);
         return nullptr;
     }

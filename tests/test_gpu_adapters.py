@@ -419,3 +419,19 @@ def test_out_is_told_to_autograd():
         c.W.matmul_adapters(x, c.bank, index, b, out=out.clone().requires_grad_())
     with torch.no_grad():
         c.check(c.W.matmul_adapters(x, c.bank, index, b, out=out.clone().requires_grad_()), x, b, index)
+
+
+def test_a_bank_of_other_parts_is_refused_by_the_c_call():
+    """The same K, N and number of parts, other widths: another matrix, for callers
+    of the C call too (the binding compares them itself)."""
+    import gptq_bit_weight_amd as q4
+    c, d = Case(128, [64, 128], 128, rank=8), Case(128, [128, 64], 128, rank=8)
+    lib = q4.load_library()
+    for M in (4, 40):
+        x, b, index = c.inputs(M)
+        out = torch.zeros(M, 192, dtype=c.dt, device="cuda")
+        args = (x.data_ptr(), b.data_ptr(), index.data_ptr(), out.data_ptr(), M, 0, torch.cuda.current_stream().cuda_stream)
+        assert lib.q4_matmul_adapters(c.W._handle(), d.bank._handle(), *args) == 1
+        assert b"another matrix" in lib.q4_last_error()
+        assert lib.q4_matmul_adapters(c.W._handle(), c.bank._handle(), *args) == 0
+        c.check(out, x, b, index)
