@@ -20,7 +20,7 @@ from typing import Optional
 
 __all__ = [
     "Q4Matrix", "Q4Error", "load_library", "library_path", "check_shape", "plan_actorder",
-    "plan_gemv", "plan_gemv_gather", "plan_gemm", "Q4Adapters", "Rotary", "PagedCache", "PATH_NONE", "PATH_GEMV", "PATH_MFMA", "GEMV_MAX_M", "EXPORTED_SYMBOLS",
+    "plan_gemv", "plan_gemv_gather", "plan_gemm", "Q4Adapters", "PATH_NONE", "PATH_GEMV", "PATH_MFMA", "GEMV_MAX_M", "EXPORTED_SYMBOLS",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -577,7 +577,7 @@ _ATTENTION = ("Rotary", "PagedCache")
 
 def __getattr__(name):
     # (torch is imported with the classes that work on its tensors, not with
-    # the package, whose host-only part needs none)
+    # the package, whose host-only part needs none: hence they are not in __all__)
     if name in _ATTENTION:
         from . import attention
         return getattr(attention, name)

@@ -294,3 +294,16 @@ def test_writes_in_place_are_told_to_autograd(monkeypatch):
         c.append(make(2), make(2), pos)
     # what the calls make themselves is not written in place
     assert r.rotate(make(4), pos)._version == 0 and c.attend(make(4), starts, lengths, table)._version == 0
+
+
+def test_the_host_only_part_needs_no_torch():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = ("import sys; sys.modules['torch'] = None; from gptq_bit_weight_amd import *; check_shape(128, 64, 64); "
+            "import gptq_bit_weight_amd as q4; q4.Q4Adapters")
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-500:]
+    from gptq_bit_weight_amd import PagedCache, Rotary
+    assert PagedCache is q4.PagedCache and Rotary is q4.Rotary
