@@ -62,7 +62,15 @@ struct Args {
     q4::FastDiv div_g, div_page;           // by heads of a group; by rows of a page (or 16-row blocks of one)
 };
 
-constexpr float kLow = -3.4028234663852886e38f;   // running maximum of a row that has seen no key (the lowest finite value)
+constexpr float kLow = -3.4028234663852886e38f;   // running maximum of a row that has seen no key (the lowest finite value, lifted or not)
+
+// A row's running maximum is held less this many powers of two, so that the weights
+// of binary16 lie in the upper part of its range: unlifted, those below 2^-25 of the
+// largest vanish when they are rounded for the second product and stay in the sum
+// (12000 keys of weight 2^-25.5 beside one of 1 are 2^-12 of the result). Up to 2^15 goes in;
+// `slack` is the log2 of what a weight may already pass 1 by. (bfloat16 has fp32's range.)
+template <bool BF>
+constexpr float lift(float slack) { return BF ? 0.f : 15.f - slack; }
 
 typedef short s4v __attribute__((ext_vector_type(4)));
 typedef short s8v __attribute__((ext_vector_type(8)));

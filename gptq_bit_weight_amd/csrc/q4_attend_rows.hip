@@ -298,7 +298,7 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void q4_attend_rows_kernel(Ar
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[h][e]);
-                const float mn = fmaxf(m, max_quarters(top));
+                const float mn = fmaxf(m, max_quarters(top) - lift<BF>(0.f));
                 if (__any(mn > m)) {
                     const float a = exp2_fast(m - mn);
                     l *= a;

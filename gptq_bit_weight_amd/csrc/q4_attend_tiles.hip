@@ -19,7 +19,7 @@
 // four waves of 32-key tiles, whose outputs and queries fill the registers of two.
 //
 // The rescale of the outputs when a maximum grows is put off until it has grown by
-// 2^8: a weight is then at most 256, far inside both types.
+// 2^8: a weight is then at most 2^15 in binary16, 2^8 in bfloat16 (lift in q4_attend.h).
 //
 // Units of work are (request, row tile, cached head, split of the keys), the
 // heads fastest, so that a head's row tiles run on one XCD (workgroup i on XCD i
@@ -338,7 +338,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
         for (int h = 0; h < HH; ++h)
 #pragma unroll
             for (int e = 0; e < 16; ++e) top = fmaxf(top, cur[h][e]);
-        const float mn = fmaxf(m, max_halves(top) * p.scale);
+        const float mn = fmaxf(m, max_halves(top) * p.scale - lift<BF>(kSlack));
         const bool grow = __any(mn > m + kSlack);
         const float m1 = grow ? mn : m, a = exp2_fast(m - m1);
         float ls[2] = {l * a, 0.f};
@@ -456,7 +456,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
                         sa[h][e] = key >= klo && key <= pos ? sa[h][e] : -INFINITY;
                         top = fmaxf(top, sa[h][e]);
                     }
-                const float m1 = fmaxf(m, max_halves(top) * p.scale), a = exp2_fast(m - m1);
+                const float m1 = fmaxf(m, max_halves(top) * p.scale - lift<BF>(kSlack)), a = exp2_fast(m - m1);
                 m = m1;
                 l *= a;
 #pragma unroll

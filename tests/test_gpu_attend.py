@@ -523,3 +523,34 @@ def test_out_that_meets_an_input_is_refused():
     assert (arena[:, 2] == 0).all() and torch.equal(arena[:, 0], q)
     with pytest.raises(ValueError, match="overlaps"):
         c.attend(arena[:, 0], starts, lengths, table, out=arena.view(2, 24, 128)[:, 7:15])
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("news,lens", [([1] * 150, [6000] * 150), ([1, 3], [6000, 9000]), ([100], [12001]), ([64, 70], [6000, 5000])])
+@pytest.mark.parametrize("where", [0, -1])
+def test_many_small_weights_count(dt, D, news, lens, where):
+    """One key with the largest weight and a value of 0, thousands with weights of
+    2^-25.1 of it and values of 1: what they add up to is the whole result. Tolerance as
+    above but for the last term: a weight rounds to a step of 2^-24 from 2^15 (few rows)
+    or 2^7 (many) up, so it is off by 2^-32 of the largest at most."""
+    import gptq_bit_weight_amd as q4
+    announce(f"small weights {dt} D={D} {news[:3]} {lens[:3]} {where}")
+    q, kc, vc, starts, lengths, table = make(dt, 4, 2, D, 16, news, lens)
+    q.zero_()
+    q[..., 0] = 1
+    low = torch.tensor(-17.4).to(dt).item()
+    kc[:], vc[:] = 0, 1
+    kc[..., 0] = low
+    for b, (n, m) in enumerate(zip(news, lens)):
+        at = 0 if where == 0 else m - n          # the first key, or the first new one
+        page = int(table[b, at // 16])
+        kc[page, :, at % 16, 0] = 0
+        vc[page, :, at % 16] = 0
+    y = q4.PagedCache(kc, vc).attend(q, starts, lengths, table, scale=1.0)
+    ref, tol = reference(q, kc, vc, news, lens, table, scale=1.0)
+    if dt == torch.float16:                      # (tol has 2^-25 for each visible key in place of 2^-32)
+        keys = torch.cat([torch.arange(m - n, m) for n, m in zip(news, lens)]).to(ref)[:, None, None] + 1
+        tol = tol - (2.0 ** -25 - 2.0 ** -32) * (keys - 1) / (1 + (keys - 1) * math.exp(low))
+    assert (ref > 1e-4).all()
+    check(y, ref, tol)
