@@ -470,7 +470,7 @@ class Q4Matrix:
               (h, bank._handle(), x.data_ptr(), bias.data_ptr() if bias is not None else None, index.data_ptr(),
                out.data_ptr(), M, 1 if dt is torch.bfloat16 else 0), () if stream is None else [t for t in (x, index, out, bias) if t is not None])
         if written:
-            _wrote(out)
+            _wrote((out,))
         return out
 
     def dequant_dump(self, path: int = PATH_GEMV, stream=None, dtype=None):

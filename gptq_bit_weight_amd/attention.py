@@ -36,7 +36,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i:
 _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _dense = torch.contiguous_format
 _Tensor, _int32_t, _int64_t = torch.Tensor, torch.int32, torch.int64
-_wrote = torch.autograd.graph.increment_version      # tells autograd of tensors written in place
+_wrote = getattr(torch._C, "_increment_version", None) or torch.autograd.graph.increment_version   # tells autograd of a tuple of tensors written in place
 
 
 def _recorded(t):
@@ -258,7 +258,7 @@ class Rotary:
               (self._handle(), x.data_ptr(), xs[0], xs[1], out.data_ptr(), os_[0], os_[1], positions.data_ptr(), bits,
                T, H, 1 if transpose else 0, 1 if x.dtype == torch.bfloat16 else 0), (x, positions, out))
         if written:
-            _wrote(out)
+            _wrote((out,))
         return out
 
     def rotate(self, x, positions, *, transpose: bool = False, out=None, stream=None):
@@ -327,8 +327,9 @@ class PagedCache:
         sb = _index(slots, "slots", dev, T)
         pb, pp, rh, qa = 32, None, None, (None, 0, 0, None, 0, 0, 0)
         used, written = (k, v, slots), (self.k, self.v)
-        _writable(self.k, "the cache's k")
-        _writable(self.v, "the cache's v")
+        if self.k.requires_grad or self.v.requires_grad or forward_ad._current_level >= 0:
+            _writable(self.k, "the cache's k")
+            _writable(self.v, "the cache's v")
         if rotary is not None:
             if rotary.dim != D:
                 raise ValueError(f"rotary turns heads of {rotary.dim} values, the cache has {D}")
@@ -398,26 +399,24 @@ class PagedCache:
             _heads(out, "out", dev, dt, T, H, D)
             _writable(out, "out")
             _distinct(out, "out")
-        table, ts = _table_rows(table, stream)
+        ts = table.stride(0)
+        if ts < width:
+            table, ts = _table_rows(table, stream)
         os_ = out.stride()
-        args = (self._ref, q.data_ptr(), qs[0], qs[1], H, T, starts.data_ptr(), lengths.data_ptr(), table.data_ptr(),
-                width, ts, B, window, D ** -0.5 if scale is None else scale, out.data_ptr(), os_[0], os_[1])
-        used = (q, out, starts, lengths, table, self.k, self.v)
-        fn, need = load_library().q4_attend, self._need.get(H) or self._workspace_bytes(H)
-        if _capturing(dev, stream):
-            # (the call's own: a graph may replay beside other work of the stream it was captured on)
-            ws = _on(stream, _new_workspace, need, dev)
-            _call(fn, "q4_attend", dev, stream, args + (ws.data_ptr(), need), used)
-            if written:
-                _wrote(out)
-            return out
-        ws = _workspace(dev, stream)
+        need = self._need.get(H) or self._workspace_bytes(H)
+        # (under capture the call's own: a graph may replay beside other work of the
+        # stream it was captured on)
+        ws = _Workspace() if _capturing(dev, stream) else _workspace(dev, stream)
         with ws.lock:
             if ws.bytes < need:
                 ws.hold(_on(stream, _new_workspace, need, dev))
-            _call(fn, "q4_attend", dev, stream, args + (ws.at, ws.bytes), used)
+            _call(load_library().q4_attend, "q4_attend", dev, stream,
+                  (self._ref, q.data_ptr(), qs[0], qs[1], H, T, starts.data_ptr(), lengths.data_ptr(), table.data_ptr(),
+                   width, ts, B, window, D ** -0.5 if scale is None else scale, out.data_ptr(), os_[0], os_[1],
+                   ws.at, ws.bytes),
+                  () if stream is None else (q, out, starts, lengths, table, self.k, self.v))
         if written:
-            _wrote(out)
+            _wrote((out,))
         return out
 
     def _workspace_bytes(self, heads):

@@ -119,6 +119,15 @@ inline bool meet(const Pieces& a, const Pieces& b)
 // pieces whose strides have nothing in common: those meet if their ranges do.
 inline bool meet(const View& a, const View& b)
 {
+    // (mostly their ranges do not meet: seen without taking them apart)
+    int64_t from[2], to[2];
+    for (int i = 0; i < 2; ++i) {
+        const View& v = i ? b : a;
+        from[i] = (int64_t) reinterpret_cast<uintptr_t>(v.at);
+        to[i] = from[i] + v.inner;
+        for (const auto& d : v.dim) (d.stride < 0 ? from[i] : to[i]) += (d.count - 1) * d.stride;
+    }
+    if (from[0] >= to[1] || from[1] >= to[0]) return false;
     const detail::Pieces p(a), q(b);
     if (p.empty || q.empty) return false;
     try {
