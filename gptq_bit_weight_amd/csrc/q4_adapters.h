@@ -34,7 +34,14 @@ struct AdapterArgs {
     const AdapterRow* rows;  // [positions]
     // c A x rounded, and what that leaves: [positions / 32][width / 8][position][value]
     const uint16_t *hi, *lo;
+    // binary16: [stretch][up_pitch] what a position's values of a stretch were divided by, a
+    // power of two (1 where they are in reach of the type)
+    const float* up;
+    int up_pitch;
 };
+
+// Values of a stretch of a part's rank: what is in LDS at a time, and has one scale.
+constexpr int kStretch = 64;
 
 // Values between two 8-value chunks of one column of B, or of one position of c A x.
 constexpr int kChunk = 32 * 8;
@@ -75,8 +82,8 @@ __device__ __forceinline__ void each(F&& f)
 // workgroup of NW waves, whose columns are n0 .. n0 + 32 NW - 1, 32 a wave: acc(i) is
 // the 32 x 32 tile of positions m0 + 32 i .. (lane: column l32 of the wave's, rows 8 (r
 // / 4) + 4 lhi + r % 4). seg[i], in LDS, is the adapter of position m0 + i (-1: none,
-// or past the last; kWild added where its B has values that are not finite).
-// lds_hi and lds_lo take 64 values of c A x of every position each; no load into
+// or past the last; kWild added where its B has values that are not finite). lds_up
+// takes a factor for each (binary16); lds_hi and lds_lo take 64 values of c A x of every position each; no load into
 // them is under way, and all waves come here.
 //
 // Bound: latency. 64 values of rank at a time, the positions' c A x comes to LDS once for
@@ -89,13 +96,14 @@ __device__ __forceinline__ void each(F&& f)
 //
 // Other rows of a run's tile meet it with zeros for their c A x; where the run's B has
 // values that are not finite, its products are a result of their own, of which only
-// its rows are added: values of one request that are not finite stay its own.
+// its rows are added: values of one request that are not finite stay its own. So are
+// the products of a run with a position whose c A x was scaled into binary16's reach.
 constexpr int kWild = 1 << 20;
 template <bool BF, int MI, int NW, class Acc>
-__device__ __forceinline__ void adapter_tile(const AdapterArgs& a, const int* seg, char* lds_hi, char* lds_lo, int m0, int n0, int N,
+__device__ __forceinline__ void adapter_tile(const AdapterArgs& a, const int* seg, float* lds_up, char* lds_hi, char* lds_lo, int m0, int n0, int N,
                                              int wave, int lane, Acc&& acc)
 {
-    constexpr int RC = 64, KC = RC / 16;   // values of rank in LDS, and their 16-value steps
+    constexpr int RC = kStretch, KC = RC / 16;   // values of rank in LDS, and their 16-value steps
     // steps that runs are gone through for, runs ahead (the accumulators of 256 rows
     // leave room for less)
     constexpr int KB = 2, PF = MI <= 2 ? 4 : 2;
@@ -135,6 +143,13 @@ __device__ __forceinline__ void adapter_tile(const AdapterArgs& a, const int* se
             const int chunks = min(RC, a.rp - k) >> 3;       // 8-value chunks of this stretch
             if (!fresh) __syncthreads();
             fresh = false;
+            // (asked for before the values and written to LDS after B is asked for)
+            float up_mine = 1.f;
+            const int up_at = 64 * wave + lane;
+            if constexpr (!BF) {
+                const size_t of = (size_t)(part * ((a.rp + RC - 1) / RC) + k / RC) * a.up_pitch;
+                if (up_at < 32 * MI) up_mine = a.up[of + m0 + up_at];
+            }
 #pragma unroll
             for (int e = 0; e < MI * KC / NW; ++e) {
                 const int at = wave + NW * e, tile = at / KC, pair = at % KC;
@@ -171,9 +186,14 @@ __device__ __forceinline__ void adapter_tile(const AdapterArgs& a, const int* se
 #pragma unroll
                 for (int q = 0; q < PF; ++q) load(q, 0);
             }
+            if constexpr (!BF)
+                if (up_at < 32 * MI) lds_up[up_at] = seg[up_at] >= 0 ? up_mine : 1.f;   // (none without an adapter)
             wait_loads<0>();
             __syncthreads();
             if (!wanted) continue;
+            uint64_t scaled[J];                              // positions with a factor
+#pragma unroll
+            for (int j = 0; j < J; ++j) scaled[j] = BF ? 0 : __ballot(lds_up[64 * j + lane] != 1.f);
             for (; 2 * c0 < chunks; c0 += KB) {
                 each<0, J>([&](auto group) __attribute__((always_inline)) {
                     constexpr int j = decltype(group)::value;
@@ -205,8 +225,9 @@ __device__ __forceinline__ void adapter_tile(const AdapterArgs& a, const int* se
                                 }
                             return y;
                         };
+                        const bool up = !BF && (scaled[j] >> from << (from + 64 - to)) != 0;
                         // (256 rows' accumulators as operands in two branches would spill)
-                        if (MI <= 2 && s < kWild && first == last) {
+                        if (MI <= 2 && s < kWild && first == last && !up) {
                             if (from < 32) acc(2 * j) = products(acc(2 * j));
                             else acc(2 * j + 1) = products(acc(2 * j + 1));
                         } else {
@@ -214,12 +235,13 @@ __device__ __forceinline__ void adapter_tile(const AdapterArgs& a, const int* se
 #pragma unroll
                             for (int v = 0; v < 16; ++v) y[v] = 0.f;
                             y = products(y);
-                            if (s >= kWild || first != last) {
+                            if (s >= kWild || first != last || up) {
                                 const int lo = (from & 31) - 4 * lhi, hi = mine == part ? lo + to - from : -1;
+                                const float* f = lds_up + 64 * j + (from & 32) + 4 * lhi;
 #pragma unroll
                                 for (int v = 0; v < 16; ++v) {
                                     const int m = 8 * (v >> 2) + (v & 3);
-                                    y[v] = m >= lo && m < hi ? y[v] : 0.f;
+                                    y[v] = m >= lo && m < hi ? (BF ? y[v] : y[v] * f[m]) : 0.f;
                                 }
                             }
                             // (the two ends differ, or the compiler makes one of them, of an

@@ -130,8 +130,15 @@ struct ManyArgs {
     uint16_t *hi, *lo;
     float* partial;                    // [tile][columns' block][share][MR][64]
     uint32_t* arrived;                 // [tile][columns' block], zero between calls
+    float* up;                         // binary16: [stretch][up_pitch]
     int M, K, slots, rank, rp, parts;
+    int per_part, up_pitch;            // columns' blocks of a part (0: of the whole width)
 };
+
+// binary16 reaches from 2^-24 to 2^16. c A x whose largest value of a stretch lies outside
+// these bounds is stored over a power of two near it, so that the pair of values is never
+// off by more than 2^-16 of the largest (2^-25 of 2^-9).
+constexpr float kReachLow = 0x1p-9f, kReachHigh = 0x1p15f;
 
 template <bool BF, int NB>
 __global__ __launch_bounds__(MT, 2) void q4_adapter_many_kernel(ManyArgs p)
@@ -252,7 +259,18 @@ __global__ __launch_bounds__(MT, 2) void q4_adapter_many_kernel(ManyArgs p)
     if (none) return;
     // ---- a stage is 128 bytes of each row of x and of A; its 16-byte chunk c lies at
     // place c ^ row % 8, which spreads a product's operand over the banks
-    const int width = p.parts * p.rp, col0 = (int)blockIdx.y * MC, l32 = lane & 31, lhi = lane >> 5;
+    // (a stretch of one part each, or 64 values of the whole width)
+    const int width = p.parts * p.rp, of_part = p.per_part ? (int)blockIdx.y / p.per_part : 0;
+    const int col0 = p.per_part ? of_part * p.rp + ((int)blockIdx.y - of_part * p.per_part) * kStretch : (int)blockIdx.y * MC;
+    const int cols = p.per_part ? (of_part + 1) * p.rp : width;
+    const int l32 = lane & 31, lhi = lane >> 5;
+    // the 8 values of one row that a thread finishes, where they are in their part, and the
+    // block's columns of their stretch
+    // (binary16: a row's are neighbours, who look for its largest together)
+    const int row = BF ? tid % MR : tid / 8, c8 = (BF ? tid / MR : tid % 8) * 8, w0 = col0 + c8;
+    static_assert(MT / MR == 8, "64 columns of a row over 8 threads");
+    const int part = p.per_part ? of_part : w0 / p.rp, at_rank = w0 - part * p.rp;
+    const int from = p.per_part ? 0 : c8 - at_rank, to = p.per_part ? MC : from + p.rp;
     const char* src[LPW];
     const int chunk = (lane & 7) ^ (lane >> 3);
 #pragma unroll
@@ -311,8 +329,7 @@ __global__ __launch_bounds__(MT, 2) void q4_adapter_many_kernel(ManyArgs p)
 #pragma unroll
         for (int e = 0; e < 16; ++e) red[wave][8 * (e >> 2) + 4 * lhi + (e & 3)][32 * h + l32] = acc[h][e];
     __syncthreads();
-    const int row = tid % MR, c8 = tid / MR * 8, w0 = col0 + c8;
-    const bool mine = c8 < MC && row < n_rows && w0 < width;
+    const bool mine = c8 < MC && row < n_rows && w0 < cols;
     f4 z[2] = {f4{0.f, 0.f, 0.f, 0.f}, f4{0.f, 0.f, 0.f, 0.f}};
     if (mine)
 #pragma unroll
@@ -325,7 +342,7 @@ __global__ __launch_bounds__(MT, 2) void q4_adapter_many_kernel(ManyArgs p)
     if (shares > 1) {
         const int block = (int)blockIdx.x * (int)gridDim.y + (int)blockIdx.y;
         const rsrc_t r = make_rsrc(p.partial + (size_t)block * shares * (MR * 64), (uint32_t)shares * (MR * 64 * 4));
-        const uint32_t at = (uint32_t)(c8 * MR + row * 8) * 4u;
+        const uint32_t at = (uint32_t)tid * 32u;
         if (mine)
 #pragma unroll
             for (int h = 0; h < 2; ++h) put16(r, (uint32_t)blockIdx.z * (MR * 64 * 4) + at + 16u * h, z[h]);
@@ -349,17 +366,40 @@ __global__ __launch_bounds__(MT, 2) void q4_adapter_many_kernel(ManyArgs p)
                 if (s < shares) z[h] += o[s][h];
         }
     }
-    if (!mine) return;
     // (values past the rank meet zeros of B: they must be finite)
+    float t[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = mine && at_rank + e < p.rank ? z[e >> 2][e & 3] * scale : 0.f;
+    float down = 1.f;
+    if constexpr (!BF) {
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, __builtin_isfinite(t[e]) ? fabsf(t[e]) : 0.f);
+        // (of this part's: a block of the whole width has several)
+        const float own = top;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float other = __shfl(own, (lane & ~7) + i);
+            top = fmaxf(top, 8 * i >= from && 8 * i < to ? other : 0.f);
+        }
+        float up = 1.f;
+        if (top != 0.f && (top < kReachLow || top > kReachHigh)) {
+            const int exponent = min(max((int)(bitcast<uint32_t>(top) >> 23), 27), 253);
+            up = bitcast<float>((uint32_t)exponent << 23);
+            down = bitcast<float>((uint32_t)(254 - exponent) << 23);
+        }
+        if (mine && c8 == from) p.up[(size_t)(p.per_part ? (int)blockIdx.y : part) * p.up_pitch + pos + row] = up;
+    }
+    if (!mine) return;
     u4 hi, lo;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float y = (w0 + e) % p.rp < p.rank ? z[e >> 2][e & 3] * scale : 0.f;
-        const uint16_t t = f32_to_act<BF>(y);
+        const float y = t[e] * down;
+        const uint16_t r = f32_to_act<BF>(y);
         // what the rounding leaves; nothing of a value beyond the type's range
-        const float rest = y - act_to_f32<BF>(t);
+        const float rest = y - act_to_f32<BF>(r);
         const uint16_t u = f32_to_act<BF>(__builtin_isfinite(rest) ? rest : 0.f);
-        hi[e >> 1] = e & 1 ? hi[e >> 1] | (uint32_t)t << 16 : t;
+        hi[e >> 1] = e & 1 ? hi[e >> 1] | (uint32_t)r << 16 : r;
         lo[e >> 1] = e & 1 ? lo[e >> 1] | (uint32_t)u << 16 : u;
     }
     const int at = pos + row;
@@ -399,8 +439,18 @@ constexpr size_t kArrivedBytes = kManyGroups * sizeof(uint32_t), kPartialBytes =
 struct ManySpace {
     AdapterRow* rows;
     uint16_t *hi, *lo;
+    float* up;
     size_t bytes;
 };
+
+// Stretches of a bank; blocks of columns that c A x of many rows is made in: the whole
+// width where it has 64 values at most, else 64 at a time, of binary16 a stretch.
+int stretches(const q4_adapters* a) { return a->parts * ((a->rp + kStretch - 1) / kStretch); }
+bool whole_width(const q4_adapters* a) { return a->parts * a->rp <= kStretch; }
+int column_blocks(const q4_adapters* a)
+{
+    return whole_width(a) ? 1 : a->bf16 ? (a->parts * a->rp + kStretch - 1) / kStretch : stretches(a);
+}
 
 // What goes by rows of a bank's many-row workspace. The rows are whole output tiles.
 constexpr int kRowStep = 256;
@@ -417,6 +467,7 @@ ManySpace many_space(const q4_adapters* a, char* base, int rows)
     s.rows = reinterpret_cast<AdapterRow*>(take(m * sizeof(AdapterRow)));
     s.hi = reinterpret_cast<uint16_t*>(take(m * width * 2));
     s.lo = reinterpret_cast<uint16_t*>(take(m * width * 2));
+    s.up = reinterpret_cast<float*>(take(a->bf16 ? 0 : m * stretches(a) * sizeof(float)));
     s.bytes = at;
     return s;
 }
@@ -532,6 +583,8 @@ q4_status adapters_prepare(q4_adapters* a, const uint16_t* x, const int* index, 
     args->rows = s.rows;
     args->hi = s.hi;
     args->lo = s.lo;
+    args->up = s.up;
+    args->up_pitch = held;
     ManyArgs p;
     p.x = x;
     p.index = index;
@@ -553,7 +606,10 @@ q4_status adapters_prepare(q4_adapters* a, const uint16_t* x, const int* index, 
     // shared out while there are fewer workgroups than the chip holds, in shares of
     // 256 values and more
     const bool narrow = args->width <= 32;
-    const int tiles = M / MR + std::min(a->slots + 1, M), blocks = narrow ? 1 : (args->width + 63) / 64;
+    const int tiles = M / MR + std::min(a->slots + 1, M), blocks = column_blocks(a);
+    p.up = s.up;
+    p.up_pitch = held;
+    p.per_part = a->bf16 || whole_width(a) ? 0 : blocks / a->parts;
     const int shares = (int)std::clamp<long long>(kManyGroups / ((long long)tiles * blocks), 1, std::min(kMaxShares, std::max(a->K / 256, 1)));
     const dim3 grid(tiles, blocks, shares), block(MT);
     const size_t lds = (size_t)(a->slots + 1) * sizeof(int);

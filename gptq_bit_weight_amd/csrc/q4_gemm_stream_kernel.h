@@ -240,6 +240,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
     // (AD) the present tile's positions: their rows and their adapters
     __shared__ __attribute__((aligned(16))) uint32_t ad_row[AD ? BM : 1];
     __shared__ int ad_seg[AD ? BM : 1];
+    __shared__ __attribute__((aligned(16))) float ad_up[AD && !BF ? BM : 1];
 
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int wm = 0, wn = wave;   // (waves side by side along N)
@@ -549,7 +550,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
             if (kb == 0) {
                 lds_barrier();     // (every wave's loads have landed and its reads are done)
                 static_assert(G::A_TILE_BYTES == BM * 64 * 2 && G::BN == 32 * NW, "64 values of a position in a stage");
-                adapter_tile<BF, MI, NW>(p.ad, ad_seg, lds_a0, lds_a1, m0, n0, p.N, wave, lane,
+                adapter_tile<BF, MI, NW>(p.ad, ad_seg, ad_up, lds_a0, lds_a1, m0, n0, p.N, wave, lane,
                                          [&](int i) -> f16x& { return acc[i][0]; });
             }
         }

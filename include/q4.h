@@ -602,7 +602,7 @@ q4_status q4_check_adapters(int slots, int rank);
  * one). Every slot is empty (adds nothing). The bank holds slots * (parts * rank *
  * K + N rounded up to 32 * rank rounded up to 8) values and the workspace of its calls:
  * once M passes Q4_GEMV_MAX_M, 2 MiB and, a row, 16 bytes and 4 for each part and value of
- * rank (rounded up to 8). Rows come in 256s and at least double as M grows; what is
+ * rank (rounded up to 8; in binary16 4 more for each part and 64 of rank). Rows come in 256s and at least double as M grows; what is
  * outgrown stays until the bank is freed, which is at most as much again. It does not
  * keep h. NULL on error.
  */
@@ -627,10 +627,10 @@ q4_status q4_adapters_clear(q4_adapters* a, int slot, hipStream_t stream);
  * with A, B, c of slot index[m] and p the part of column n; an index outside
  * [0, slots) (-1) adds nothing. index is int32 [M] on the device. fp32 sums, one
  * rounding of the result. Up to Q4_GEMV_MAX_M rows c A x is kept in fp32; above, as
- * two values of the activations' type (its rounding and the rest: 16 bits of
- * bfloat16, 22 of binary16), so in binary16 its magnitude must stay below
- * 65504. Rows of other adapters, or of none, are not touched by one's values
- * that are not finite.
+ * two values of the activations' type (its rounding and the rest): off by 2^-16 of itself
+ * in bfloat16, in binary16 by 2^-22 of itself or 2^-16 of the largest of 64 values of its
+ * row and part (which a power of two brings into the type's reach). Rows of other adapters,
+ * or of none, are not touched by one's values that are not finite.
  *
  * Errors, graph capture and concurrency as q4_matmul, for the handle and the bank alike: a
  * bank's workspace for M > Q4_GEMV_MAX_M grows on the first call with a larger

@@ -435,3 +435,55 @@ def test_a_bank_of_other_parts_is_refused_by_the_c_call():
         assert b"another matrix" in lib.q4_last_error()
         assert lib.q4_matmul_adapters(c.W._handle(), c.bank._handle(), *args) == 0
         c.check(out, x, b, index)
+
+
+def scaled_reference(c, x, b, index):
+    """(result, tolerance) where c A x may lie far from 1: as in Case.check, but for a part's
+    c A x off by 2^-16 of its row's largest in place of 2^-16 of itself."""
+    xd = x.double()
+    ref = xd @ c.w + b.double()
+    tol = (BF16_GEMM_REL_A if c.fmt == "bf16" and x.shape[0] > 32 else REL_A) * (xd.abs() @ c.w.abs())
+    for s in range(c.slots):
+        rows, at = (index == s).nonzero()[:, 0], 0
+        for p, n in enumerate(c.parts):
+            a, bb = c.A[s][p].double(), c.B[s][at:at + n].double()
+            t, ta = xd[rows] @ a.t() * c.c[s], xd[rows].abs() @ a.abs().t() * abs(c.c[s])
+            off = c.K * 2.0 ** -24 * ta + 2.0 ** -16 * t.abs().amax(1, keepdim=True)
+            ref[rows, at:at + n] += t @ bb.t()
+            tol[rows, at:at + n] += off @ bb.abs().t()
+            at += n
+    return ref, tol + (BF16_REL_Y if c.fmt == "bf16" else REL_Y) * ref.abs()
+
+
+@pytest.mark.parametrize("fmt", ["f16", "bf16"])
+@pytest.mark.parametrize("parts,rank", [([264], 16), ([72, 64, 120], 8), ([72, 64, 120], 40), ([200, 64], 150)])
+@pytest.mark.parametrize("size", [1e-9, 1e-5, 1e-3, 1.0, 3e4, 1e6, 1e9])
+def test_sizes_of_the_adapters_product(fmt, parts, rank, size):
+    """c A x from far below to far above the reach of binary16 and B the other way,
+    alone (the matrix is zero): the same at 32 rows and more. Slot 0 has c A x of 1; of
+    slot 1's parts, the last has 2^20 times less than the others."""
+    import gptq_bit_weight_amd as q4
+    announce(f"adapters' product {fmt} {parts} rank={rank} of {size}")
+    c = Case(256, parts, 64, fmt, slots=3, rank=rank)
+    words = lambda *shape: torch.full(shape, -0x77777778, dtype=torch.int32, device="cuda")  # noqa: E731  (codes and zeros of 8)
+    c.W = q4.Q4Matrix.concat([(words(32, n), words(4, n // 8), torch.ones(4, n, dtype=torch.float16, device="cuda"))
+                              for n in parts], groupsize=64)
+    c.w = torch.zeros_like(c.w)
+    for s in range(c.slots):
+        c.c[s] = 1.0 if s == 0 else float(torch.tensor(size))
+        if s == 1:
+            c.A[s][-1] *= 2.0 ** -20
+        c.B[s] = (c.B[s].sign() * min(max(1.0 / c.c[s], 2.0 ** -13), 2.0 ** 12)).to(c.dt)
+        c.bank.load(s, c.A[s], c.B[s], c.c[s])
+    for M in (32, 33, 77, 300, 600):
+        x, b, index = c.inputs(M)
+        if size > 1e6:
+            x = x * 2.0 ** -9
+        b = b * 0
+        y = c.W.matmul_adapters(x, c.bank, index, b)
+        ref, tol = scaled_reference(c, x, b, index)
+        if fmt == "f16":
+            assert (ref.abs() < 6e4).all()
+            tol = tol + 2.0 ** -25                          # (half a step of the result's subnormals)
+        bad = ~((y.double() - ref).abs() <= tol)
+        assert not bad.any(), (M, int(bad.sum()), bad.nonzero()[0].tolist(), ((y.double() - ref).abs() / tol)[bad].max().item())
