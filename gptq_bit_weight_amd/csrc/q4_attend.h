@@ -30,7 +30,7 @@ using namespace q4dev;
 
 // Row tiles whose keys were split: where their rows and partial results are.
 struct Join {
-    int start, row0, rows, head, slot, parts;
+    int start, row0, rows, head, slot, parts, pos0;
 };
 constexpr int kMaxJoins = 1024;         // (at most one for each workgroup that work is split for)
 constexpr int kJoinGroups = 32;
@@ -196,6 +196,19 @@ __device__ __forceinline__ Request request(const Args& p, int b)
 __device__ __forceinline__ Request request_of_lane(const Request& r, int b)
 {
     return Request{__builtin_amdgcn_readlane(r.start, b), __builtin_amdgcn_readlane(r.n, b), __builtin_amdgcn_readlane(r.len, b)};
+}
+
+// What a row's sums are multiplied by for its output. A sum of zero: a row that sees no
+// key (its position is negative) gives zeros; one that does has scores of -inf
+// only, which have no softmax.
+__device__ __forceinline__ float over_sum(float sum, int pos)
+{
+    return sum != 0.f ? 1.f / sum : pos < 0 ? 0.f : __builtin_nanf("");
+}
+__device__ __forceinline__ f4 output_of(f4 v, float sum, float inv)
+{
+    // (what a row that sees no key has summed may not be finite)
+    return sum == 0.f ? f4{inv, inv, inv, inv} : v * inv;
 }
 
 // Four values of an output row.

@@ -461,9 +461,7 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void q4_attend_rows_kernel(Ar
                     const int unit = u * NT + tid, row = unit / (D / 4), at = unit % (D / 4) * 4;
                     if (row >= rows || at >= p.dim) continue;
                     const int r = row0 + row, token = (int)q4::fast_div((uint32_t)r, p.div_g);
-                    // (a row that sees no key: zeros)
-                    const float inv = ol[u] == 0.f ? 0.f : 1.f / ol[u];
-                    const f4 y = ol[u] == 0.f ? f4{0.f, 0.f, 0.f, 0.f} : o[u] * inv;
+                    const f4 y = output_of(o[u], ol[u], over_sum(ol[u], pos0 + token));
                     store_row4<BF>(p.out + (s.r.start + token) * p.o_t + (head * p.g + r - token * p.g) * p.o_h + at, y,
                                    p.dim - at, p.store8);
                 }

@@ -509,7 +509,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
     const float ls = sum_halves(l);
     if (parts == 1) {
         if (live) {
-            const float inv = ls == 0.f ? 0.f : 1.f / ls;       // (a row that sees no key: zeros)
+            const float inv = over_sum(ls, pos);
             uint16_t* o = p.out + (start + token) * p.o_t + qh * p.o_h;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
@@ -517,10 +517,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
                 for (int e = 0; e < 4; ++e) {
                     const int at = 32 * d + 8 * e + 4 * lhi;
                     if (at >= p.dim) continue;
-                    f4 y;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[i] = ls == 0.f ? 0.f : acc[d][4 * e + i] * inv;
-                    store_row4<BF>(o + at, y, p.dim - at, p.store8);
+                    const f4 y = f4{acc[d][4 * e], acc[d][4 * e + 1], acc[d][4 * e + 2], acc[d][4 * e + 3]};
+                    store_row4<BF>(o + at, output_of(y, ls, inv), p.dim - at, p.store8);
                 }
         }
         return;
@@ -530,7 +528,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
     if (slot0 + (uint32_t)splits > 2u * (uint32_t)p.workers) return;
     if (split == 0 && tid == 0) {
         const uint32_t i = atomicAdd(&p.joins->count, 1u);
-        if (i < (uint32_t)kMaxJoins) p.joins->item[i] = Join{start, row0, rows, head, (int)slot0, parts};
+        if (i < (uint32_t)kMaxJoins) p.joins->item[i] = Join{start, row0, rows, head, (int)slot0, parts, pos0};
     }
     if (!live) return;
     constexpr size_t SLOT = (size_t)BR * (D + 2);
@@ -590,8 +588,7 @@ __global__ __launch_bounds__(64 * JW) void q4_attend_join_kernel(Args p)
         }
         if (at >= p.dim) continue;
         const int r = j.row0 + row, token = (int)q4::fast_div((uint32_t)r, p.div_g);
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const f4 y = l == 0.f ? f4{0.f, 0.f, 0.f, 0.f} : v * inv;
+        const f4 y = output_of(v, l, over_sum(l, j.pos0 + token));
         store_row4<BF>(p.out + (j.start + token) * p.o_t + (j.head * p.g + r - token * p.g) * p.o_h + at, y, p.dim - at, p.store8);
     }
     // The last workgroup that had work leaves the list empty (counted in groups:

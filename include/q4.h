@@ -565,7 +565,7 @@ size_t q4_attend_workspace(const q4_cache* c, int heads);
  * heads; head h reads cached head h / (heads / kv_heads). Token i, at position
  * p, sees keys j <= p, with window > 0 only p - window < j:
  *   out[i][h] = sum_j softmax_j(scale q[i][h] . k[j]) v[j]
- * and zeros where it sees none. fp32 scores, softmax and sums; the weights
+ * and zeros where it sees none (NaN where every score is -inf). fp32 scores, softmax and sums; the weights
  * are rounded to the data's type for the second product.
  *
  * Only rows that some token of the tile sees are read, and of the table only

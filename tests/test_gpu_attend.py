@@ -554,3 +554,24 @@ def test_many_small_weights_count(dt, D, news, lens, where):
         tol = tol - (2.0 ** -25 - 2.0 ** -32) * (keys - 1) / (1 + (keys - 1) * math.exp(low))
     assert (ref > 1e-4).all()
     check(y, ref, tol)
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("news,lens", [([1, 1, 2], [40, 3, 900]), ([1, 5], [6000, 3]), ([70], [9001]), ([200, 90, 1], [200, 40, 5])])
+def test_scores_of_minus_infinity_have_no_softmax(dt, D, news, lens):
+    """Tokens whose every visible score is -inf are NaN, by the definition; with one
+    finite score they have that key's value; those that see no key stay zero."""
+    import gptq_bit_weight_amd as q4
+    q, kc, vc, starts, lengths, table = make(dt, 4, 2, D, 16, news, lens)
+    q.abs_().add_(0.1)
+    kc[..., 0] = torch.where(kc[..., 0].isnan(), kc[..., 0], -math.inf)
+    cache = q4.PagedCache(kc, vc)
+    y = cache.attend(q, starts, lengths, table)
+    pos = torch.cat([torch.arange(m - n, m) for n, m in zip(news, lens)]).cuda()
+    assert y[pos >= 0].isnan().all() and (y[pos < 0] == 0).all()
+    page = table[:, 0].long()
+    kc[page, :, 0] = 0
+    y = cache.attend(q, starts, lengths, table)
+    want = torch.cat([vc[p, :, 0].repeat_interleave(2, 0)[None].expand(n, -1, -1) for n, p in zip(news, page.tolist())])
+    assert torch.equal(y, torch.where((pos >= 0)[:, None, None], want, 0))
