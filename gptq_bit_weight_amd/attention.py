@@ -318,7 +318,8 @@ class PagedCache:
         """Write the keys (turned by `rotary` at `positions`, copied without
         it) and values [tokens, kv heads, dim] of new tokens to rows slots
         [tokens]: slot s is row s % page_size of page s // page_size; a slot
-        outside the cache (-1 for padding) is not written. With q [tokens,
+        outside the cache (-1 for padding) is not written, the others must differ
+        (of two tokens with one slot a mixture may be left). With q [tokens,
         heads, dim], returns it turned too (in q_out, which may be q). No
         gradient goes through it (Rotary.rotate has one)."""
         dev, dt, D, kv = self.device, self.dtype, self.dim, self.kv_heads

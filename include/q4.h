@@ -540,7 +540,9 @@ typedef struct {
  * (rotated by positions[t] when `rotary` is given, copied when it is NULL)
  * and its values go to row slots[t] % page_size of page slots[t] / page_size.
  * A token whose slot is negative or not below pages * page_size is not
- * written; two tokens with one slot leave either's row. With q, its `heads`
+ * written. Slots must differ: a row is written in pieces, so two tokens with one slot
+ * may leave pieces of both, and the keys of one with the values of the other. k and v
+ * may be rows of the cache only if each goes to where it is. With q, its `heads`
  * heads are rotated too, into q_out (which may be q itself), for every token; q_out
  * must not overlap anything else of the call (Q4_ERR_INVALID_ARG).
  */
