@@ -36,11 +36,15 @@ size_t rows_bytes(int dim, int num_cu)
 // results. (A request is split where a row tile has more than 1 / target of all
 // tiles: at most `target` row tiles are, into at most 2 target units.)
 constexpr int kTileRows = 128, kTileLeast = 8;
-// Row tiles that a window keeps to this many tiles of keys are not split where there
-// are as many as workgroups wanted, which saves the join's launch (six windowed chunks of
-// 58 row tiles and 8 heads: 34.7 -> 33.0 us; with fewer row tiles splitting is worth
-// more: one chunk of 40 tokens 20.0 us against 26.0).
-constexpr int kTileWhole = 24;
+// Row tiles that a window keeps to this many keys are not split where there are as many
+// as workgroups wanted, which saves the join's launch: 1.5 to 2.5 us a call whatever the window,
+// where requests are alike (1100 to 16000 tokens, 32 heads over 8; heads of 64, window
+// 1024: 75.3 us against 76.6, heads of 128: 111.0 and 113.3, heads of 256, window 256: 60.7
+// and 63.0). The price is paid where one request's long row tile stands beside many short ones:
+// one of 32 tokens and 40 of 28, heads of 128: window 512 21.1 us against 21.8, 1024 28.9
+// and 23.0, 2048 44.3 and 24.0, so no further than 24 tiles of 64. (With fewer row tiles splitting
+// is always worth more: one chunk of 40 tokens 20.0 us against 26.0.)
+constexpr int kWholeKeys = 24 * 64;
 int tile_target(int num_cu) { return num_cu < q4attend::kMaxJoins ? num_cu : q4attend::kMaxJoins; }
 size_t tiles_bytes(int dim, int num_cu)
 {
@@ -167,7 +171,7 @@ q4_status q4_attend(const q4_cache* c, const uint16_t* q, int64_t q_token, int64
         const long long seen = window ? (long long)window + (kTileRows + g - 1) / g : p.max_len;
         const long long most = std::min<long long>(seen, p.max_len) / keys + 2;
         const bool enough = (long long)tokens * g / kTileRows * c->kv_heads >= tile_target(cu);
-        if (window && most <= kTileWhole && enough) p.least = (int)most;
+        if (window && most * keys <= kWholeKeys && enough) p.least = (int)most;
         p.unsplit = most <= p.least;
     }
     const size_t need = many ? tiles_bytes(c->dim, cu) : rows_bytes(c->dim, cu);
