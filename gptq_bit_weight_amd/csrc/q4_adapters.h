@@ -89,10 +89,11 @@ __device__ __forceinline__ void each(F&& f)
 // Bound: latency. 64 values of rank at a time, the positions' c A x comes to LDS once for
 // all waves; then each wave goes by runs, the positions of one adapter inside one tile,
 // with the B of the next PF runs under way. The runs are bit masks, and their adapters
-// lanes of a register. Measured, as what the product's launch takes more than without
-// adapters: 2048 rows x 11008 columns, 8 adapters of rank 64: 5 us of 186 (87 with
-// operands from memory in rows of rank values, a run at a time); 77 rows, 12 of rank 32: 8
-// us of 33, about 2 of them the rows' map, the rest the latency of 8 MiB of B.
+// lanes of a register. The product's launch with adapters and without (medians in a
+// trace; the rows' gathering and scattering included): 2048 rows x 11008 columns, 8
+// adapters of rank 64: 205 us and 178 (with operands from memory in rows of rank values, a
+// run at a time, 60 more); 77 rows, 12 of rank 32: 33.1 us and 24.3, about 2 of them the
+// rows' map, the rest the latency of 8 MiB of B.
 //
 // Other rows of a run's tile meet it with zeros for their c A x; where the run's B has
 // values that are not finite, its products are a result of their own, of which only
@@ -163,23 +164,17 @@ __device__ __forceinline__ void adapter_tile(const AdapterArgs& a, const int* se
             u4 b[PF][KB];
             uint64_t ahead = 0;
             int c0 = 0;
-            // (64 rows: always as many loads, of something where there is no run left, so
-            // that the compiler can count those newer than the one it waits for; with a
-            // branch here every run waits for all, 77 rows of 12 adapters 35 us against
-            // 33. 256 rows mostly have long runs, for which the loads of nothing cost
-            // more: 2048 rows of 8 adapters 196 us against 186.)
+            // (as many loads in every run, of something where there is no run left, so that
+            // the compiler can count those newer than the one it waits for; with a branch
+            // every run waits for all: 77 rows of 12 adapters 35.5 us against 34.0, 2048 of 8,
+            // whose runs are long, the same within 1%)
             auto load = [&](int q, int j) __attribute__((always_inline)) {
-                if (MI > 2 && !ahead) return;
                 const int s = ahead ? __builtin_amdgcn_readlane(slot[j], (int)__builtin_ctzll(ahead)) : 0;
                 ahead &= ahead - 1;
-                if (MI > 2 && s < 0) return;
                 const uint16_t* of = bn + (s < 0 ? 0 : s & (kWild - 1)) * a.b_slot + (size_t)k * 32;
 #pragma unroll
-                for (int c = 0; c < KB; ++c) {
-                    const int chunk = 2 * (c0 + c) + lhi;
-                    if (MI <= 2) b[q][c] = *reinterpret_cast<const u4*>(of + min(chunk, chunks - 1) * kChunk);
-                    else if (2 * (c0 + c) < chunks) b[q][c] = chunk < chunks ? *reinterpret_cast<const u4*>(of + chunk * kChunk) : zero;
-                }
+                for (int c = 0; c < KB; ++c)
+                    b[q][c] = *reinterpret_cast<const u4*>(of + min(2 * (c0 + c) + lhi, chunks - 1) * kChunk);
             };
             if (wanted) {
                 ahead = starts[0];
@@ -220,7 +215,7 @@ __device__ __forceinline__ void adapter_tile(const AdapterArgs& a, const int* se
                                     u4 l = *reinterpret_cast<const u4*>(lds_lo + at + c * 1024);
 #pragma unroll
                                     for (int v = 0; v < 4; ++v) h[v] = in ? h[v] : 0u, l[v] = in ? l[v] : 0u;
-                                    const u4 w = MI > 2 || 2 * (c0 + c) + lhi < chunks ? b[q][c] : zero;
+                                    const u4 w = 2 * (c0 + c) + lhi < chunks ? b[q][c] : zero;
                                     y = mma(l, w, mma(h, w, y));
                                 }
                             return y;

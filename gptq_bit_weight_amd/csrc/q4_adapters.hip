@@ -12,7 +12,7 @@
 // each has a workgroup; x and A stream through a ring of LDS stages, 64 of
 // K each, filled by direct loads of whole 128-byte lines, and the last workgroup of a
 // tile to arrive adds the shares in order (K = 4096: 77 rows of 12 adapters of rank 32
-// 8.8 us, 2048 rows of 8 of rank 64 20.5 us; one workgroup a tile, operands straight from
+// 9.0 us, 2048 rows of 8 of rank 64 20.3 us; one workgroup a tile, operands straight from
 // memory: 13.4 and 33). The workgroups also leave the order of the rows for the
 // product's launch.
 #include <hip/hip_runtime.h>
@@ -603,8 +603,8 @@ q4_status adapters_prepare(q4_adapters* a, const uint16_t* x, const int* index, 
     p.arrived = reinterpret_cast<uint32_t*>(a->shares);
     p.partial = reinterpret_cast<float*>(a->shares + kArrivedBytes);
     // tiles: a whole one each MR rows, and a partial one each bin with rows; K is
-    // shared out while there are fewer workgroups than the chip holds, in shares of
-    // 256 values and more
+    // shared out while there are fewer workgroups than CUs, in shares of 256
+    // values and more
     const bool narrow = args->width <= 32;
     const int tiles = M / MR + std::min(a->slots + 1, M), blocks = column_blocks(a);
     p.up = s.up;
