@@ -92,7 +92,7 @@ __device__ __forceinline__ void each(F&& f)
 // lanes of a register. The product's launch with adapters and without (medians in a
 // trace; the rows' gathering and scattering included): 2048 rows x 11008 columns, 8
 // adapters of rank 64: 205 us and 178 (with operands from memory in rows of rank values, a
-// run at a time, 60 more); 77 rows, 12 of rank 32: 33.1 us and 24.3, about 2 of them the
+// run at a time, some 65 more); 77 rows, 12 of rank 32: 33.1 us and 24.3, about 2 of them the
 // rows' map, the rest the latency of 8 MiB of B.
 //
 // Other rows of a run's tile meet it with zeros for their c A x; where the run's B has

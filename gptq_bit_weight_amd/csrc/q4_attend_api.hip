@@ -156,7 +156,10 @@ q4_status q4_attend(const q4_cache* c, const uint16_t* q, int64_t q_token, int64
 
     // Few rows a request: the few-row kernel, above the many-row one. (64 x 8
     // rows over 4600 keys: 221 us and 237; 8 x 16 over 3000: 32 and 28; 20 x 32 over
-    // 6000: 115 and 102.)
+    // 6000: 115 and 102.) By their mean, as the host knows no more: a long chunk beside
+    // many single tokens costs more in one call than apart (63 single tokens and a chunk of
+    // 512 over 8192 keys: 8 heads over 8, few rows, 450 us, apart 359 and 37; 32 heads over 8,
+    // many rows, 546 us, apart 360 and 88).
     const long long mean_rows = ((long long)tokens * g + requests - 1) / requests;
     const bool many = mean_rows > 12;
     const int tile = many ? kTileRows : kFewRows;
