@@ -42,7 +42,8 @@ EXPORTED_SYMBOLS = (
     "q4_handle_bits", "q4_check_shape_bits", "q4_plan_gemm", "q4_plan_gemm_waves", "q4_read_probe",
     "q4_matmul_static",
     "q4_rotary_make", "q4_rotary_free", "q4_rotary_plan", "q4_rotary_apply", "q4_cache_append",
-    "q4_attend_workspace", "q4_attend",
+    "q4_attend_workspace", "q4_attend", "q4_attend_ex",
+    "q4_check_cache4", "q4_cache4_append", "q4_cache4_read", "q4_attend4_workspace", "q4_attend4",
     "q4_check_adapters", "q4_adapters_make", "q4_adapters_free", "q4_adapters_load", "q4_adapters_clear",
     "q4_matmul_adapters",
 )
@@ -133,6 +134,13 @@ def load_library():
     lib.q4_attend_workspace.argtypes = [P, I]
     lib.q4_attend_workspace.restype = ctypes.c_size_t
     lib.q4_attend.argtypes = [P, P, L, L, I, I, P, P, P, I, L, I, I, ctypes.c_float, P, L, L, P, ctypes.c_size_t, P]
+    lib.q4_attend_ex.argtypes = [P, P, L, L, I, I, P, P, P, I, L, I, I, I, ctypes.c_float, P, L, L, P, ctypes.c_size_t, P]
+    lib.q4_attend4.argtypes = lib.q4_attend_ex.argtypes[:-1] + [I, P]
+    lib.q4_attend4_workspace.argtypes = [P, I]
+    lib.q4_attend4_workspace.restype = ctypes.c_size_t
+    lib.q4_check_cache4.argtypes = [P]
+    lib.q4_cache4_append.argtypes = lib.q4_cache_append.argtypes[:-1] + [I, P]
+    lib.q4_cache4_read.argtypes = [P, P, I, I, P, L, L, P, L, L, P]
     lib.q4_check_adapters.argtypes = [I, I]
     lib.q4_adapters_make.argtypes = [P, I, I, I]
     lib.q4_adapters_make.restype = P
@@ -141,7 +149,8 @@ def load_library():
     lib.q4_adapters_load.argtypes = [P, I, P, P, I, ctypes.c_float, P]
     lib.q4_adapters_clear.argtypes = [P, I, P]
     lib.q4_matmul_adapters.argtypes = [P, P, P, P, P, P, I, I, P]
-    for f in (lib.q4_rotary_plan, lib.q4_rotary_apply, lib.q4_cache_append, lib.q4_attend, lib.q4_check_adapters,
+    for f in (lib.q4_rotary_plan, lib.q4_rotary_apply, lib.q4_cache_append, lib.q4_attend, lib.q4_attend_ex, lib.q4_check_cache4,
+              lib.q4_cache4_append, lib.q4_cache4_read, lib.q4_attend4, lib.q4_check_adapters,
               lib.q4_adapters_load, lib.q4_adapters_clear, lib.q4_matmul_adapters):
         f.restype = I
     _lib = lib
@@ -572,7 +581,7 @@ class Q4Adapters:
             pass
 
 
-_ATTENTION = ("Rotary", "PagedCache")
+_ATTENTION = ("Rotary", "PagedCache", "PagedCache4")
 
 
 def __getattr__(name):

@@ -1,11 +1,12 @@
-"""Rotary positions, a paged cache of keys and values, and attention of new
-tokens over it: what a decoder layer needs between its quantized
-projections.
+"""Rotary positions, a paged cache of keys and values (in 16 bits or in 4), and
+attention of new tokens over it: what a decoder layer needs between its
+quantized projections.
 
     rope = q4.Rotary(dim, scaling=dict(kind="linear", factor=8.0))
     cache = q4.PagedCache(k_pages, v_pages)          # [pages, kv heads, page size, dim]
     q = cache.append(k, v, slots, rotary=rope, positions=positions, q=q)
     o = cache.attend(q, starts, lengths, table)
+    cache = q4.PagedCache4.empty(pages, kv_heads, page_size, dim)       # the same in 4 bits
 
 Like the rest of the binding this only checks tensors and passes pointers and
 a HIP stream to the C ABI (``include/q4.h``).
@@ -20,7 +21,7 @@ from torch.autograd import forward_ad
 
 from . import _check, _raise, load_library
 
-__all__ = ["Rotary", "PagedCache"]
+__all__ = ["Rotary", "PagedCache", "PagedCache4"]
 
 LAYOUTS = {"half": 0, "interleaved": 1}
 SCALINGS = {"none": 0, "linear": 1, "base": 2, "by_parts": 3}
@@ -57,6 +58,13 @@ class _Cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_stride", ctypes.c_int64 * 3),
                 ("v_stride", ctypes.c_int64 * 3), ("pages", ctypes.c_int), ("kv_heads", ctypes.c_int),
                 ("page_size", ctypes.c_int), ("dim", ctypes.c_int), ("bf16", ctypes.c_int)]
+
+
+class _Cache4(ctypes.Structure):
+    """q4_cache4 of include/q4.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + [
+        (n + "_stride", ctypes.c_int64 * 3) for n in ("k", "v", "k_scale", "v_scale")] + [
+        (n, ctypes.c_int) for n in ("pages", "kv_heads", "page_size", "dim", "group")]
 
 
 def _heads(t, name, device, dtype=None, tokens=None, heads=None, dim=None):
@@ -284,7 +292,141 @@ class Rotary:
             pass
 
 
-class PagedCache:
+class _Paged:
+    """What the caches have in common: `dtype` is the tokens' (None: either 16-bit
+    type), `_tensors` what is written in place, `_four` whether it is held in 4 bits."""
+
+    dtype, _four = None, False
+
+    @property
+    def _tensors(self):
+        return self.k, self.v
+
+    def append(self, k, v, slots, *, rotary=None, positions=None, q=None, q_out=None, stream=None):
+        """Write the keys (turned by `rotary` at `positions`, as they are without
+        it) and values [tokens, kv heads, dim] of new tokens to rows slots
+        [tokens]: slot s is row s % page_size of page s // page_size; a slot
+        outside the cache (-1 for padding) is not written, the others must differ
+        (of two tokens with one slot a mixture may be left). With q [tokens,
+        heads, dim], returns it turned too (in q_out, which may be q). No
+        gradient goes through it (Rotary.rotate has one)."""
+        dev, dt, D, kv = self.device, self.dtype, self.dim, self.kv_heads
+        (T, _, _), ks = _heads(k, "k", dev, dt, None, kv, D)
+        dt = k.dtype
+        _, vs = _heads(v, "v", dev, dt, T, kv, D)
+        sb = _index(slots, "slots", dev, T)
+        pb, pp, rh, qa = 32, None, None, (None, 0, 0, None, 0, 0, 0)
+        used, written = (k, v, slots), self._tensors
+        for t in written:
+            if t.requires_grad or forward_ad._current_level >= 0:
+                _writable(t, "the cache")
+        if rotary is not None:
+            if rotary.dim != D:
+                raise ValueError(f"rotary turns heads of {rotary.dim} values, the cache has {D}")
+            if rotary.device != dev:
+                raise ValueError(f"rotary is on {rotary.device}, the cache on {dev}")
+            if positions is None:
+                raise ValueError("positions are needed with rotary")
+            pb, pp, rh = _index(positions, "positions", dev, T), positions.data_ptr(), rotary._handle()
+            used += (positions,)
+        if q is not None:
+            if rotary is None:
+                raise ValueError("q is given without rotary")
+            (_, H, _), qs = _heads(q, "q", dev, dt, T, None, D)
+            if q_out is not None:
+                written += (q_out,)
+            q_out = _out_like(q, q_out, "q_out", stream)
+            if H:
+                os_ = q_out.stride()
+                qa = (q.data_ptr(), qs[0], qs[1], q_out.data_ptr(), os_[0], os_[1], H)
+            used += (q, q_out)
+        elif q_out is not None:
+            raise ValueError("q_out is given without q")
+        four = self._four
+        what = "q4_cache4_append" if four else "q4_cache_append"
+        _call(getattr(load_library(), what), what, dev, stream,
+              (self._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], slots.data_ptr(), sb, T, rh, pp, pb)
+              + qa + ((1 if dt is torch.bfloat16 else 0,) if four else ()), used if stream is None else used + self._tensors)
+        _wrote(written)
+        return q_out
+
+    def attend(self, q, starts, lengths, table, *, window: int = 0, sinks: int = 0, scale=None, out=None, stream=None):
+        """Attention of new tokens over the cache: q [tokens, heads, dim] holds
+        the new tokens of every request one after the other, request b's are
+        rows starts[b] .. starts[b + 1] - 1 (starts int32 [requests + 1]) and
+        the last of its lengths[b] cached tokens (lengths int32 [requests]);
+        key j is row j % page_size of page table[b, j // page_size] (table int32
+        [requests, width]). A token sees the keys up to its own, with `window`
+        only the last `window` of them and the request's first `sinks`; one that
+        sees none gives zeros. heads is a multiple of the cached heads, scale
+        defaults to dim ** -0.5. Lengths stay on the device; nothing waits for
+        it. No gradient goes through it. Several threads may call at once, on one
+        stream too."""
+        dev, dt = self.device, self.dtype
+        (T, H, D), qs = _heads(q, "q", dev, dt, None, None, self.dim)
+        dt = q.dtype
+        if H % self.kv_heads or not H:
+            raise ValueError(f"q has {H} heads, the cache {self.kv_heads}")
+        _int32(starts, "starts", dev, 1)
+        _int32(lengths, "lengths", dev, 1)
+        _int32(table, "table", dev, 2)
+        B, width = table.shape
+        if lengths.shape[0] != B or starts.shape[0] != B + 1:
+            raise ValueError(f"table [{B}, {width}] takes lengths [{B}] and starts [{B + 1}], got {list(lengths.shape)} "
+                             f"and {list(starts.shape)}")
+        if (B and width == 0) or (T and not B):
+            raise ValueError("table has no pages" if B else f"{T} tokens of no request")
+        if not (starts.is_contiguous() and lengths.is_contiguous()) or (width > 1 and table.stride(1) != 1):
+            raise ValueError("starts, lengths and the rows of table must be contiguous")
+        window, sinks = min(int(window), 2 ** 31 - 1), min(int(sinks), 2 ** 31 - 1)       # (more keys than any cache has)
+        if window < 0 or sinks < 0:
+            raise ValueError(f"window and sinks must not be negative, got {window} and {sinks}")
+        if q.data_ptr() % 16 or qs[0] % 8 or qs[1] % 8:
+            if stream is not None:
+                q.record_stream(stream)
+            q = _on(stream, torch.clone, q, memory_format=_dense)
+            qs = q.stride()
+        written = out is not None
+        if not written:
+            out = _out_like(q, None, "out", stream)
+        else:
+            _heads(out, "out", dev, dt, T, H, D)
+            _writable(out, "out")
+            _distinct(out, "out")
+        ts = table.stride(0)
+        if ts < width:
+            table, ts = _table_rows(table, stream)
+        os_ = out.stride()
+        need = self._need.get(H) or self._workspace_bytes(H)
+        # (under capture the call's own: a graph may replay beside other work of the
+        # stream it was captured on)
+        ws = _Workspace() if _capturing(dev, stream) else _workspace(dev, stream)
+        with ws.lock:
+            if ws.bytes < need:
+                ws.hold(_on(stream, _new_workspace, need, dev))
+            four = self._four
+            what = "q4_attend4" if four else "q4_attend_ex" if sinks else "q4_attend"
+            _call(getattr(load_library(), what), what, dev, stream,
+                  (self._ref, q.data_ptr(), qs[0], qs[1], H, T, starts.data_ptr(), lengths.data_ptr(), table.data_ptr(),
+                   width, ts, B, window) + ((sinks,) if four or sinks else ())
+                  + (D ** -0.5 if scale is None else scale, out.data_ptr(), os_[0], os_[1], ws.at, ws.bytes)
+                  + ((1 if dt is torch.bfloat16 else 0,) if four else ()),
+                  () if stream is None else (q, out, starts, lengths, table) + self._tensors)
+        if written:
+            _wrote((out,))
+        return out
+
+    def _workspace_bytes(self, heads):
+        with torch.cuda.device(self.device):
+            what = "q4_attend4_workspace" if self._four else "q4_attend_workspace"
+            need = getattr(load_library(), what)(self._ref, heads)
+        if not need:
+            _raise(load_library().q4_last_status(), what)
+        self._need[heads] = need
+        return need
+
+
+class PagedCache(_Paged):
     """Keys and values in pages: two tensors [pages, kv heads, page size, dim]
     (float16 or bfloat16, any strides of the first three dimensions, dense
     values), which stay the caller's and are written in place."""
@@ -314,119 +456,84 @@ class PagedCache:
         self._ref = ctypes.byref(self._c)
         self._need = {}
 
-    def append(self, k, v, slots, *, rotary=None, positions=None, q=None, q_out=None, stream=None):
-        """Write the keys (turned by `rotary` at `positions`, copied without
-        it) and values [tokens, kv heads, dim] of new tokens to rows slots
-        [tokens]: slot s is row s % page_size of page s // page_size; a slot
-        outside the cache (-1 for padding) is not written, the others must differ
-        (of two tokens with one slot a mixture may be left). With q [tokens,
-        heads, dim], returns it turned too (in q_out, which may be q). No
-        gradient goes through it (Rotary.rotate has one)."""
-        dev, dt, D, kv = self.device, self.dtype, self.dim, self.kv_heads
-        (T, _, _), ks = _heads(k, "k", dev, dt, None, kv, D)
-        _, vs = _heads(v, "v", dev, dt, T, kv, D)
+
+class PagedCache4(_Paged):
+    """Keys and values in 4 bits, in pages: codes k and v, uint8 [pages, kv heads,
+    page size, dim / 2] (value 2 i of a row in the low half of byte i, 2 i + 1 in its
+    high half), and k_scale and v_scale, float16 [pages, kv heads, page size, dim /
+    group, 2]: for each group of 32, 64, 128 or 256 neighbouring values the step s and
+    the least value m. Code c stands for the float16 value s c + m. The tensors stay
+    the caller's and are written in place; their first three dimensions may have any
+    strides. Tokens are float16 or bfloat16, dim a multiple of 32 up to 256.
+
+    append() quantises: m is the group's least value in float16, s = (largest - m) /
+    15 in float16, a code the nearest (ties to even). Finite values beyond +-65440
+    are held as that; a group with a value that is not finite stands for NaN."""
+
+    _four = True
+
+    def __init__(self, k, v, k_scale, v_scale):
+        names = ("k", "v", "k_scale", "v_scale")
+        for t, nm in zip((k, v, k_scale, v_scale), names):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{nm} must be a torch.Tensor")
+            codes = "scale" not in nm
+            if t.dtype != (torch.uint8 if codes else torch.float16):
+                raise ValueError(f"{nm} must be {torch.uint8 if codes else torch.float16}, got {t.dtype}")
+            if t.dim() != (4 if codes else 5) or 0 in t.shape or (not codes and t.shape[4] != 2):
+                raise ValueError(f"{nm} must be [pages, kv heads, page size, {'dim / 2' if codes else 'dim / group, 2'}], got {list(t.shape)}")
+            if (t.stride(-1) != 1 and t.shape[-1] > 1) or (not codes and t.stride(3) != 2 and t.shape[3] > 1):
+                raise ValueError(f"{nm}: a row must be contiguous")
+            if t.device.type != "cuda":
+                raise ValueError(f"{nm} must be on the GPU, got {t.device}")
+            _distinct(t, nm)
+        for t, of, nm in ((v, k, "v"), (v_scale, k_scale, "v_scale")):
+            if t.shape != of.shape:
+                raise ValueError(f"{nm} must have the shape {list(of.shape)}, got {list(t.shape)}")
+        if k_scale.shape[:3] != k.shape[:3] or 2 * k.shape[3] % k_scale.shape[3]:
+            raise ValueError(f"scales {list(k_scale.shape)} do not go with codes {list(k.shape)}")
+        if len({t.device for t in (k, v, k_scale, v_scale)}) > 1:
+            raise ValueError("the tensors must be on one device")
+        self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, k_scale, v_scale, k.device
+        self.pages, self.kv_heads, self.page_size = (int(n) for n in k.shape[:3])
+        self.dim, self.group = 2 * int(k.shape[3]), 2 * int(k.shape[3]) // int(k_scale.shape[3])
+        if self.pages * self.page_size > 2 ** 31 - 1:
+            raise NotImplementedError("more than 2^31 - 1 rows in the cache")
+        strides = lambda t: (ctypes.c_int64 * 3)(*(x * t.element_size() for x in t.stride()[:3]))  # noqa: E731
+        self._need = {}
+        self._c = _Cache4(*(t.data_ptr() for t in self._tensors), *(strides(t) for t in self._tensors),
+                          self.pages, self.kv_heads, self.page_size, self.dim, self.group)
+        self._ref = ctypes.byref(self._c)
+        _check(load_library().q4_check_cache4(self._ref), "PagedCache4")
+
+    @property
+    def _tensors(self):
+        return self.k, self.v, self.k_scale, self.v_scale
+
+    @classmethod
+    def empty(cls, pages: int, kv_heads: int, page_size: int, dim: int, *, group: int = 32, device=None):
+        """A cache of zeros."""
+        if dim < 1 or group < 1 or dim % 2 or dim % group:
+            raise ValueError(f"groups of {group} values do not divide heads of {dim}")
+        shape, dev = (pages, kv_heads, page_size), "cuda" if device is None else device
+        codes = lambda: torch.zeros(shape + (dim // 2,), dtype=torch.uint8, device=dev)  # noqa: E731
+        scales = lambda: torch.zeros(shape + (dim // group, 2), dtype=torch.float16, device=dev)  # noqa: E731
+        return cls(codes(), codes(), scales(), scales())
+
+    def read(self, slots, *, stream=None):
+        """The keys and values that rows slots [tokens] stand for, float16 [tokens,
+        kv heads, dim] each; zeros for a slot outside the cache."""
+        dev = self.device
+        T = slots.shape[0] if isinstance(slots, _Tensor) and slots.dim() == 1 else -1
         sb = _index(slots, "slots", dev, T)
-        pb, pp, rh, qa = 32, None, None, (None, 0, 0, None, 0, 0, 0)
-        used, written = (k, v, slots), (self.k, self.v)
-        if self.k.requires_grad or self.v.requires_grad or forward_ad._current_level >= 0:
-            _writable(self.k, "the cache's k")
-            _writable(self.v, "the cache's v")
-        if rotary is not None:
-            if rotary.dim != D:
-                raise ValueError(f"rotary turns heads of {rotary.dim} values, the cache has {D}")
-            if rotary.device != dev:
-                raise ValueError(f"rotary is on {rotary.device}, the cache on {dev}")
-            if positions is None:
-                raise ValueError("positions are needed with rotary")
-            pb, pp, rh = _index(positions, "positions", dev, T), positions.data_ptr(), rotary._handle()
-            used += (positions,)
-        if q is not None:
-            if rotary is None:
-                raise ValueError("q is given without rotary")
-            (_, H, _), qs = _heads(q, "q", dev, dt, T, None, D)
-            if q_out is not None:
-                written += (q_out,)
-            q_out = _out_like(q, q_out, "q_out", stream)
-            if H:
-                os_ = q_out.stride()
-                qa = (q.data_ptr(), qs[0], qs[1], q_out.data_ptr(), os_[0], os_[1], H)
-            used += (q, q_out)
-        elif q_out is not None:
-            raise ValueError("q_out is given without q")
-        _call(load_library().q4_cache_append, "q4_cache_append", dev, stream,
-              (self._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], slots.data_ptr(), sb, T, rh, pp, pb)
-              + qa, used if stream is None else used + (self.k, self.v))
-        _wrote(written)
-        return q_out
-
-    def attend(self, q, starts, lengths, table, *, window: int = 0, scale=None, out=None, stream=None):
-        """Attention of new tokens over the cache: q [tokens, heads, dim] holds
-        the new tokens of every request one after the other, request b's are
-        rows starts[b] .. starts[b + 1] - 1 (starts int32 [requests + 1]) and
-        the last of its lengths[b] cached tokens (lengths int32 [requests]);
-        key j is row j % page_size of page table[b, j // page_size] (table int32
-        [requests, width]). A token sees the keys up to its own, with `window`
-        only the last `window` of them; one that sees none gives zeros. heads is
-        a multiple of the cached heads, scale defaults to dim ** -0.5. Lengths
-        stay on the device; nothing waits for it. No gradient goes through it.
-        Several threads may call at once, on one stream too."""
-        dev, dt = self.device, self.dtype
-        (T, H, D), qs = _heads(q, "q", dev, dt, None, None, self.dim)
-        if H % self.kv_heads or not H:
-            raise ValueError(f"q has {H} heads, the cache {self.kv_heads}")
-        _int32(starts, "starts", dev, 1)
-        _int32(lengths, "lengths", dev, 1)
-        _int32(table, "table", dev, 2)
-        B, width = table.shape
-        if lengths.shape[0] != B or starts.shape[0] != B + 1:
-            raise ValueError(f"table [{B}, {width}] takes lengths [{B}] and starts [{B + 1}], got {list(lengths.shape)} "
-                             f"and {list(starts.shape)}")
-        if (B and width == 0) or (T and not B):
-            raise ValueError("table has no pages" if B else f"{T} tokens of no request")
-        if not (starts.is_contiguous() and lengths.is_contiguous()) or (width > 1 and table.stride(1) != 1):
-            raise ValueError("starts, lengths and the rows of table must be contiguous")
-        window = min(int(window), 2 ** 31 - 1)       # (more keys than any cache has)
-        if window < 0:
-            raise ValueError(f"window must not be negative, got {window}")
-        if q.data_ptr() % 16 or qs[0] % 8 or qs[1] % 8:
-            if stream is not None:
-                q.record_stream(stream)
-            q = _on(stream, torch.clone, q, memory_format=_dense)
-            qs = q.stride()
-        written = out is not None
-        if not written:
-            out = _out_like(q, None, "out", stream)
-        else:
-            _heads(out, "out", dev, dt, T, H, D)
-            _writable(out, "out")
-            _distinct(out, "out")
-        ts = table.stride(0)
-        if ts < width:
-            table, ts = _table_rows(table, stream)
-        os_ = out.stride()
-        need = self._need.get(H) or self._workspace_bytes(H)
-        # (under capture the call's own: a graph may replay beside other work of the
-        # stream it was captured on)
-        ws = _Workspace() if _capturing(dev, stream) else _workspace(dev, stream)
-        with ws.lock:
-            if ws.bytes < need:
-                ws.hold(_on(stream, _new_workspace, need, dev))
-            _call(load_library().q4_attend, "q4_attend", dev, stream,
-                  (self._ref, q.data_ptr(), qs[0], qs[1], H, T, starts.data_ptr(), lengths.data_ptr(), table.data_ptr(),
-                   width, ts, B, window, D ** -0.5 if scale is None else scale, out.data_ptr(), os_[0], os_[1],
-                   ws.at, ws.bytes),
-                  () if stream is None else (q, out, starts, lengths, table, self.k, self.v))
-        if written:
-            _wrote((out,))
-        return out
-
-    def _workspace_bytes(self, heads):
-        with torch.cuda.device(self.device):
-            need = load_library().q4_attend_workspace(self._ref, heads)
-        if not need:
-            _raise(load_library().q4_last_status(), "q4_attend_workspace")
-        self._need[heads] = need
-        return need
+        shape = (T, self.kv_heads, self.dim)
+        k = _on(stream, torch.empty, shape, dtype=torch.float16, device=dev)
+        v = _on(stream, torch.empty, shape, dtype=torch.float16, device=dev)
+        st = k.stride()
+        _call(load_library().q4_cache4_read, "q4_cache4_read", dev, stream,
+              (self._ref, slots.data_ptr(), sb, T, k.data_ptr(), st[0], st[1], v.data_ptr(), st[0], st[1]),
+              () if stream is None else (slots,) + self._tensors)
+        return k, v
 
 
 class _Workspace:

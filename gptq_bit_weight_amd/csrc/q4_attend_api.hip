@@ -5,12 +5,17 @@
 #include <cmath>
 
 #include "q4_attend.h"
+#include "q4_cache4_host.h"
 
 namespace q4 {
 
 hipError_t launch_attend_rows(const q4attend::Args& p, bool bf16, bool pages_of_16, hipStream_t stream);
 
 hipError_t launch_attend_tiles(const q4attend::Args& p, int grid, bool bf16, bool pages_of_16, hipStream_t stream);
+
+hipError_t launch_attend4_rows(const q4attend::Args& p, bool bf16, bool pages_of_16, hipStream_t stream);
+
+hipError_t launch_attend4_tiles(const q4attend::Args& p, int grid, bool bf16, bool pages_of_16, hipStream_t stream);
 
 namespace {
 
@@ -63,6 +68,135 @@ q4_status check_attend(const q4_cache* c, int heads, const char* who)
 
 bool at16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+q4_status check_attend4(const q4_cache4* c, int heads, const char* who)
+{
+    if (q4_status st = check_cache4(c, who); st != Q4_OK) return st;
+    if (heads < 1 || heads % c->kv_heads)
+        return fail(Q4_ERR_INVALID_ARG, "%s: %d heads over %d cached heads", who, heads, c->kv_heads);
+    return Q4_OK;
+}
+
+size_t workspace_bytes_of(int dim, int cu)
+{
+    const size_t rows = rows_bytes(dim, cu), tiles = tiles_bytes(dim, cu);
+    return rows > tiles ? rows : tiles;
+}
+
+// What a call says beside its cache.
+struct Call {
+    const uint16_t* q;
+    int64_t q_token, q_head;
+    int heads, tokens;
+    const int32_t *starts, *lengths, *table;
+    int table_width;
+    int64_t table_stride;
+    int requests, window, sinks;
+    float scale;
+    uint16_t* out;
+    int64_t out_token, out_head;
+    void* workspace;
+    size_t workspace_bytes;
+    bool bf16, four;
+};
+
+// The call over a cache that p describes already (pages, page_size, KV, dim and where its
+// memory is) and that `caches` are the views of.
+q4_status attend(const char* who, q4attend::Args& p, const View* caches, int ncaches, const Call& a, hipStream_t stream)
+{
+    if (a.tokens < 0 || a.requests < 0 || a.window < 0 || a.sinks < 0)
+        return fail(Q4_ERR_INVALID_ARG, "%s: %d tokens, %d requests, window %d, %d sinks", who, a.tokens, a.requests, a.window, a.sinks);
+    if (!std::isfinite(a.scale)) return fail(Q4_ERR_INVALID_ARG, "%s: scale is not finite", who);
+    if (a.tokens == 0 || a.requests == 0) return Q4_OK;
+    if (!a.q || !a.starts || !a.lengths || !a.table || !a.out) return fail(Q4_ERR_INVALID_ARG, "%s: null pointer", who);
+    if (a.table_width < 1 || a.table_stride < a.table_width || a.table_stride > 0x7fffffff)
+        return fail(Q4_ERR_INVALID_ARG, "%s: a table of %d pages a request, %lld apart", who, a.table_width, (long long)a.table_stride);
+    if (a.q_token < 0 || a.q_token % 8 || a.q_head < 0 || a.q_head % 8)
+        return fail(Q4_ERR_UNSUPPORTED, "%s: strides of q must be multiples of 8 values", who);
+    if (!at16(a.q) || (reinterpret_cast<uintptr_t>(a.out) & 1))
+        return fail(Q4_ERR_UNSUPPORTED, "%s: q must be 16-byte aligned", who);
+    const int g = a.heads / p.KV;
+    if ((long long)a.tokens * g > (1 << 30) || (long long)a.heads * p.dim > (1 << 30))
+        return fail(Q4_ERR_UNSUPPORTED, "%s: %d tokens of %d heads", who, a.tokens, a.heads);
+    // (row tiles are stored while others still read)
+    const View to = head_view(a.out, a.out_token, a.out_head, a.tokens, a.heads, p.dim);
+    if (meet(to, head_view(a.q, a.q_token, a.q_head, a.tokens, a.heads, p.dim)))
+        return fail(Q4_ERR_INVALID_ARG, "%s: out overlaps q", who);
+    for (int i = 0; i < ncaches; ++i)
+        if (meet(to, caches[i])) return fail(Q4_ERR_INVALID_ARG, "%s: out overlaps the cache", who);
+    if (meet(to, flat_view(a.starts, ((int64_t)a.requests + 1) * 4)) || meet(to, flat_view(a.lengths, (int64_t)a.requests * 4)) ||
+        meet(to, View{a.table, (int64_t)a.table_width * 4, {{a.requests, a.table_stride * 4}, {1, 0}, {1, 0}}}))
+        return fail(Q4_ERR_INVALID_ARG, "%s: out overlaps starts, lengths or table", who);
+    int dev = -1, cu = 0;
+    if (q4_status st = device_info(&dev, &cu); st != Q4_OK) return st;
+
+    p.q = a.q;
+    p.out = a.out;
+    p.starts = a.starts;
+    p.lengths = a.lengths;
+    p.table = a.table;
+    p.q_t = a.q_token;
+    p.q_h = a.q_head;
+    p.o_t = a.out_token;
+    p.o_h = a.out_head;
+    p.T = a.tokens;
+    p.B = a.requests;
+    p.g = g;
+    p.chunks = p.dim / 8;
+    p.table_stride = (int)a.table_stride;
+    const long long rows = (long long)a.table_width * p.page_size;
+    p.max_len = (int)(rows < (1 << 30) ? rows : (1 << 30));
+    // (a window that no key can lie outside is none; the kernels' 32-bit positions less a
+    // window then stay in range)
+    p.window = a.window >= p.max_len ? 0 : a.window;
+    p.sinks = p.window ? std::min(a.sinks, p.max_len) : 0;
+    // (a negative scale turns q's signs, a scale of zero clears q)
+    p.scale = a.scale == 0.f ? 1.f : std::fabs(a.scale) * 1.4426950408889634f;
+    p.q_and = a.scale == 0.f ? 0u : ~0u;
+    p.q_xor = a.scale < 0.f ? 0x80008000u : 0u;
+    p.store8 = (reinterpret_cast<uintptr_t>(a.out) % 8 == 0) && a.out_token % 4 == 0 && a.out_head % 4 == 0;
+    p.div_g = make_fastdiv((uint32_t)g);
+    p.div_page = make_fastdiv((uint32_t)p.page_size);
+    const bool pg = p.page_size % 16 == 0;
+
+    // Few rows a request: the few-row kernel, above the many-row one. (64 x 8
+    // rows over 4600 keys: 221 us and 237; 8 x 16 over 3000: 32 and 28; 20 x 32 over
+    // 6000: 115 and 102.) By their mean, as the host knows no more: a long chunk beside
+    // many single tokens costs more in one call than apart (63 single tokens and a chunk of
+    // 512 over 8192 keys: 8 heads over 8, few rows, 450 us, apart 359 and 37; 32 heads over 8,
+    // many rows, 546 us, apart 360 and 88).
+    const long long mean_rows = ((long long)a.tokens * g + a.requests - 1) / a.requests;
+    const bool many = mean_rows > 12;
+    const int tile = many ? kTileRows : kFewRows;
+    const long long row_tiles = (long long)a.tokens * g / tile + a.requests;
+    if (row_tiles * p.KV * (p.max_len / 32 + 2) >= (1LL << 31))
+        return fail(Q4_ERR_UNSUPPORTED, "%s: more than 2^31 tiles of keys", who);
+    p.workers = many ? tile_target(cu) : cu;
+    p.least = many ? kTileLeast : kFewLeast;
+    if (many) {
+        const int keys = p.dim > 128 ? 32 : 64;
+        // (a row tile's tokens see window - 1 keys before the first's own, and the sinks)
+        const long long seen = p.window ? (long long)p.window + (kTileRows + g - 1) / g : p.max_len;
+        const long long most = std::min(std::min<long long>(seen, p.max_len) / keys + 2 + (p.sinks + keys - 1) / keys,
+                                        (long long)p.max_len / keys + 2);
+        const bool enough = (long long)a.tokens * g / kTileRows * p.KV >= tile_target(cu);
+        if (p.window && most * keys <= kWholeKeys && enough) p.least = (int)most;
+        p.unsplit = most <= p.least;
+    }
+    const size_t need = many ? tiles_bytes(p.dim, cu) : rows_bytes(p.dim, cu);
+    if (!a.workspace || a.workspace_bytes < need || !at16(a.workspace))
+        return fail(Q4_ERR_INVALID_ARG, "%s: the workspace needs %zu bytes on a 16-byte boundary (%s_workspace)", who, need,
+                    a.four ? "q4_attend4" : "q4_attend");
+    p.counters = static_cast<uint32_t*>(a.workspace);
+    p.joins = reinterpret_cast<q4attend::JoinList*>(static_cast<char*>(a.workspace) + kListAt);
+    p.slots = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kCounterBytes);
+    // (most units there can be: a whole one each share of the work, a partial one each row tile and head)
+    const int units = (int)(row_tiles * p.KV + p.workers);
+    hipError_t e;
+    if (a.four) e = many ? launch_attend4_tiles(p, units, a.bf16, pg, stream) : launch_attend4_rows(p, a.bf16, pg, stream);
+    else e = many ? launch_attend_tiles(p, units, a.bf16, pg, stream) : launch_attend_rows(p, a.bf16, pg, stream);
+    return e == hipSuccess ? Q4_OK : fail(Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
+}
+
 }  // namespace
 }  // namespace q4
 
@@ -72,8 +206,41 @@ size_t q4_attend_workspace(const q4_cache* c, int heads)
 {
     int dev = -1, cu = 0;
     if (q4::check_attend(c, heads, "q4_attend_workspace") != Q4_OK || q4::device_info(&dev, &cu) != Q4_OK) return 0;
-    const size_t rows = q4::rows_bytes(c->dim, cu), tiles = q4::tiles_bytes(c->dim, cu);
-    return rows > tiles ? rows : tiles;
+    return q4::workspace_bytes_of(c->dim, cu);
+}
+
+q4_status q4_attend_ex(const q4_cache* c, const uint16_t* q, int64_t q_token, int64_t q_head, int heads, int tokens,
+                       const int32_t* starts, const int32_t* lengths, const int32_t* table, int table_width,
+                       int64_t table_stride, int requests, int window, int sinks, float scale, uint16_t* out, int64_t out_token,
+                       int64_t out_head, void* workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    using namespace q4;
+    const char* who = "q4_attend";
+    if (q4_status st = check_attend(c, heads, who); st != Q4_OK) return st;
+    if (tokens > 0 && requests > 0) {
+        const int64_t strides[] = {c->k_stride[0], c->k_stride[1], c->k_stride[2], c->v_stride[0], c->v_stride[1], c->v_stride[2]};
+        for (int64_t s : strides)
+            if (s < 0 || s % 8) return fail(Q4_ERR_UNSUPPORTED, "%s: strides of the cache must be multiples of 8 values", who);
+        if (!at16(c->k) || !at16(c->v)) return fail(Q4_ERR_UNSUPPORTED, "%s: the cache must be 16-byte aligned", who);
+        if (c->k_stride[2] > (1 << 25) || c->v_stride[2] > (1 << 25))
+            return fail(Q4_ERR_UNSUPPORTED, "%s: rows of a page more than 2^25 values apart", who);
+    }
+    q4attend::Args p = {};
+    p.k = static_cast<const uint16_t*>(c->k);
+    p.v = static_cast<const uint16_t*>(c->v);
+    p.ks0 = c->k_stride[0];
+    p.ks1 = c->k_stride[1];
+    p.ks2 = (int)c->k_stride[2] * 2;
+    p.vs0 = c->v_stride[0];
+    p.vs1 = c->v_stride[1];
+    p.vs2 = (int)c->v_stride[2] * 2;
+    p.KV = c->kv_heads;
+    p.dim = c->dim;
+    p.pages = c->pages;
+    p.page_size = c->page_size;
+    const View caches[] = {cache_view(c, false), cache_view(c, true)};
+    return attend(who, p, caches, 2, Call{q, q_token, q_head, heads, tokens, starts, lengths, table, table_width, table_stride, requests,
+                                          window, sinks, scale, out, out_token, out_head, workspace, workspace_bytes, c->bf16 != 0, false}, stream);
 }
 
 q4_status q4_attend(const q4_cache* c, const uint16_t* q, int64_t q_token, int64_t q_head, int heads, int tokens,
@@ -81,112 +248,41 @@ q4_status q4_attend(const q4_cache* c, const uint16_t* q, int64_t q_token, int64
                     int64_t table_stride, int requests, int window, float scale, uint16_t* out, int64_t out_token,
                     int64_t out_head, void* workspace, size_t workspace_bytes, hipStream_t stream)
 {
-    using namespace q4;
-    const char* who = "q4_attend";
-    if (q4_status st = check_attend(c, heads, who); st != Q4_OK) return st;
-    if (tokens < 0 || requests < 0 || window < 0)
-        return fail(Q4_ERR_INVALID_ARG, "%s: %d tokens, %d requests, window %d", who, tokens, requests, window);
-    if (!std::isfinite(scale)) return fail(Q4_ERR_INVALID_ARG, "%s: scale is not finite", who);
-    if (tokens == 0 || requests == 0) return Q4_OK;
-    if (!q || !starts || !lengths || !table || !out) return fail(Q4_ERR_INVALID_ARG, "%s: null pointer", who);
-    if (table_width < 1 || table_stride < table_width || table_stride > 0x7fffffff)
-        return fail(Q4_ERR_INVALID_ARG, "%s: a table of %d pages a request, %lld apart", who, table_width, (long long)table_stride);
-    const int64_t strides[] = {q_token, q_head, c->k_stride[0], c->k_stride[1], c->k_stride[2], c->v_stride[0], c->v_stride[1], c->v_stride[2]};
-    for (int64_t s : strides)
-        if (s < 0 || s % 8) return fail(Q4_ERR_UNSUPPORTED, "%s: strides of q and the cache must be multiples of 8 values", who);
-    if (!at16(q) || !at16(c->k) || !at16(c->v) || (reinterpret_cast<uintptr_t>(out) & 1))
-        return fail(Q4_ERR_UNSUPPORTED, "%s: q and the cache must be 16-byte aligned", who);
-    if (c->k_stride[2] > (1 << 25) || c->v_stride[2] > (1 << 25))
-        return fail(Q4_ERR_UNSUPPORTED, "%s: rows of a page more than 2^25 values apart", who);
-    const int g = heads / c->kv_heads;
-    if ((long long)tokens * g > (1 << 30) || (long long)heads * c->dim > (1 << 30))
-        return fail(Q4_ERR_UNSUPPORTED, "%s: %d tokens of %d heads", who, tokens, heads);
-    // (row tiles are stored while others still read)
-    const View to = head_view(out, out_token, out_head, tokens, heads, c->dim);
-    if (meet(to, head_view(q, q_token, q_head, tokens, heads, c->dim))) return fail(Q4_ERR_INVALID_ARG, "%s: out overlaps q", who);
-    if (meet(to, cache_view(c, false)) || meet(to, cache_view(c, true)))
-        return fail(Q4_ERR_INVALID_ARG, "%s: out overlaps the cache", who);
-    if (meet(to, flat_view(starts, ((int64_t)requests + 1) * 4)) || meet(to, flat_view(lengths, (int64_t)requests * 4)) ||
-        meet(to, View{table, (int64_t)table_width * 4, {{requests, table_stride * 4}, {1, 0}, {1, 0}}}))
-        return fail(Q4_ERR_INVALID_ARG, "%s: out overlaps starts, lengths or table", who);
-    int dev = -1, cu = 0;
-    if (q4_status st = device_info(&dev, &cu); st != Q4_OK) return st;
+    return q4_attend_ex(c, q, q_token, q_head, heads, tokens, starts, lengths, table, table_width, table_stride, requests, window, 0,
+                        scale, out, out_token, out_head, workspace, workspace_bytes, stream);
+}
 
+size_t q4_attend4_workspace(const q4_cache4* c, int heads)
+{
+    int dev = -1, cu = 0;
+    if (q4::check_attend4(c, heads, "q4_attend4_workspace") != Q4_OK || q4::device_info(&dev, &cu) != Q4_OK) return 0;
+    return q4::workspace_bytes_of(c->dim, cu);
+}
+
+q4_status q4_attend4(const q4_cache4* c, const uint16_t* q, int64_t q_token, int64_t q_head, int heads, int tokens,
+                     const int32_t* starts, const int32_t* lengths, const int32_t* table, int table_width,
+                     int64_t table_stride, int requests, int window, int sinks, float scale, uint16_t* out, int64_t out_token,
+                     int64_t out_head, void* workspace, size_t workspace_bytes, int bf16, hipStream_t stream)
+{
+    using namespace q4;
+    const char* who = "q4_attend4";
+    if (q4_status st = check_attend4(c, heads, who); st != Q4_OK) return st;
     q4attend::Args p = {};
-    p.q = q;
-    p.out = out;
-    p.k = static_cast<const uint16_t*>(c->k);
-    p.v = static_cast<const uint16_t*>(c->v);
-    p.starts = starts;
-    p.lengths = lengths;
-    p.table = table;
-    p.q_t = q_token;
-    p.q_h = q_head;
-    p.o_t = out_token;
-    p.o_h = out_head;
-    p.ks0 = c->k_stride[0];
-    p.ks1 = c->k_stride[1];
-    p.ks2 = (int)c->k_stride[2] * 2;
-    p.vs0 = c->v_stride[0];
-    p.vs1 = c->v_stride[1];
-    p.vs2 = (int)c->v_stride[2] * 2;
-    p.T = tokens;
-    p.B = requests;
+    auto side = [&](bool values) {
+        const int64_t *s = values ? c->v_stride : c->k_stride, *w = values ? c->v_scale_stride : c->k_scale_stride;
+        return q4attend::Side{static_cast<const char*>(values ? c->v : c->k), static_cast<const char*>(values ? c->v_scale : c->k_scale),
+                              s[0], s[1], w[0], w[1], (int)s[2], (int)w[2]};
+    };
+    p.k4 = side(false);
+    p.v4 = side(true);
+    for (p.group_shift = 5; 1 << p.group_shift < c->group;) ++p.group_shift;
     p.KV = c->kv_heads;
-    p.g = g;
     p.dim = c->dim;
-    p.chunks = c->dim / 8;
     p.pages = c->pages;
     p.page_size = c->page_size;
-    p.table_stride = (int)table_stride;
-    const long long rows = (long long)table_width * c->page_size;
-    p.max_len = (int)(rows < (1 << 30) ? rows : (1 << 30));
-    // (a window that no key can lie outside is none; the kernels' 32-bit positions less a
-    // window then stay in range)
-    if (window >= p.max_len) window = 0;
-    p.window = window;
-    // (a negative scale turns q's signs, a scale of zero clears q)
-    p.scale = scale == 0.f ? 1.f : std::fabs(scale) * 1.4426950408889634f;
-    p.q_and = scale == 0.f ? 0u : ~0u;
-    p.q_xor = scale < 0.f ? 0x80008000u : 0u;
-    p.store8 = (reinterpret_cast<uintptr_t>(out) % 8 == 0) && out_token % 4 == 0 && out_head % 4 == 0;
-    p.div_g = make_fastdiv((uint32_t)g);
-    p.div_page = make_fastdiv((uint32_t)c->page_size);
-    const bool bf16 = c->bf16 != 0, pg = c->page_size % 16 == 0;
-
-    // Few rows a request: the few-row kernel, above the many-row one. (64 x 8
-    // rows over 4600 keys: 221 us and 237; 8 x 16 over 3000: 32 and 28; 20 x 32 over
-    // 6000: 115 and 102.) By their mean, as the host knows no more: a long chunk beside
-    // many single tokens costs more in one call than apart (63 single tokens and a chunk of
-    // 512 over 8192 keys: 8 heads over 8, few rows, 450 us, apart 359 and 37; 32 heads over 8,
-    // many rows, 546 us, apart 360 and 88).
-    const long long mean_rows = ((long long)tokens * g + requests - 1) / requests;
-    const bool many = mean_rows > 12;
-    const int tile = many ? kTileRows : kFewRows;
-    const long long row_tiles = (long long)tokens * g / tile + requests;
-    if (row_tiles * c->kv_heads * (p.max_len / 32 + 2) >= (1LL << 31))
-        return fail(Q4_ERR_UNSUPPORTED, "%s: more than 2^31 tiles of keys", who);
-    p.workers = many ? tile_target(cu) : cu;
-    p.least = many ? kTileLeast : kFewLeast;
-    if (many) {
-        const int keys = c->dim > 128 ? 32 : 64;
-        // (a row tile's tokens see window - 1 keys before the first's own)
-        const long long seen = window ? (long long)window + (kTileRows + g - 1) / g : p.max_len;
-        const long long most = std::min<long long>(seen, p.max_len) / keys + 2;
-        const bool enough = (long long)tokens * g / kTileRows * c->kv_heads >= tile_target(cu);
-        if (window && most * keys <= kWholeKeys && enough) p.least = (int)most;
-        p.unsplit = most <= p.least;
-    }
-    const size_t need = many ? tiles_bytes(c->dim, cu) : rows_bytes(c->dim, cu);
-    if (!workspace || workspace_bytes < need || !at16(workspace))
-        return fail(Q4_ERR_INVALID_ARG, "%s: the workspace needs %zu bytes on a 16-byte boundary (q4_attend_workspace)", who, need);
-    p.counters = static_cast<uint32_t*>(workspace);
-    p.joins = reinterpret_cast<q4attend::JoinList*>(static_cast<char*>(workspace) + kListAt);
-    p.slots = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
-    // (most units there can be: a whole one each share of the work, a partial one each row tile and head)
-    hipError_t e = many ? launch_attend_tiles(p, (int)(row_tiles * c->kv_heads + p.workers), bf16, pg, stream)
-                        : launch_attend_rows(p, bf16, pg, stream);
-    return e == hipSuccess ? Q4_OK : fail(Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
+    const View caches[] = {cache4_view(c, false, false), cache4_view(c, true, false), cache4_view(c, false, true), cache4_view(c, true, true)};
+    return attend(who, p, caches, 4, Call{q, q_token, q_head, heads, tokens, starts, lengths, table, table_width, table_stride, requests,
+                                          window, sinks, scale, out, out_token, out_head, workspace, workspace_bytes, bf16 != 0, true}, stream);
 }
 
 }  // extern "C"

@@ -1,9 +1,9 @@
 // Attention over a paged cache for few rows a request: single tokens and
 // short runs of them.
 //
-// q4_attend_rows_kernel<D, BF, PG>: head rows of D values in LDS (64, 128,
+// q4_attend_rows_kernel<D, BF, PG, SK>: head rows of D values in LDS (64, 128,
 // 256; a head's own dim may be less), BF (bfloat16), PG (pages of a multiple
-// of 16 rows). A row tile is 16 rows (token, head of the group).
+// of 16 rows), SK (sinks: first keys that stay visible beside a window). A row tile is 16 rows (token, head of the group).
 //
 // Bound: HBM. Each key and value is read once for all rows of its tile and
 // does 4 rows flops a value, far under the matrix rate. So the work is split
@@ -26,37 +26,15 @@
 // in LDS. A segment that is its whole row tile is stored; else its partial
 // result goes to a slot of its workgroup, and the last workgroup of the row
 // tile to arrive joins them in key order (the same bits whichever it is).
-#include "q4_attend.h"
+#include "q4_attend_rows.h"
 
 namespace {
 
 using namespace q4attend;
 
 constexpr int WV = 4, NT = 64 * WV;
-constexpr int KT = 32;                 // keys of a tile
-constexpr int ROWS = 16;               // rows of one
 
-// What of a request the kernel's split goes by: its row tiles, its first
-// visible key, where its tiles begin (a multiple of 32) and their number (at least
-// one: a tile of rows that see nothing still stores zeros).
-struct Span {
-    Request r;
-    int rt, lo, base, nt;
-};
-
-__device__ __forceinline__ Span span(const Args& p, const Request& r)
-{
-    Span s;
-    s.r = r;
-    s.rt = (s.r.n * p.g + ROWS - 1) / ROWS;
-    s.lo = p.window ? max(s.r.len - s.r.n - p.window + 1, 0) : 0;
-    s.lo = min(s.lo, max(s.r.len - 1, 0));
-    s.base = s.lo & ~(KT - 1);
-    s.nt = max((s.r.len - s.base + KT - 1) / KT, 1);
-    return s;
-}
-
-template <int D, bool BF, bool PG>
+template <int D, bool BF, bool PG, bool SK>
 __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void q4_attend_rows_kernel(Args p)
 {
     constexpr int PITCH = 2 * D;               // bytes of a row in LDS
@@ -88,60 +66,16 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void q4_attend_rows_kernel(Ar
         voff[e] = (uint32_t)(row * p.vs2) + chunk;
     }
 
-    // ---- this workgroup's range of tiles
-    // (the first 64 requests stay in the lanes: each look at them in memory is one
-    // more latency before the first key)
-    auto request_at = [&](int b) { return b < p.B ? request(p, b) : Request{0, 0, 0}; };
-    auto cost = [&](const Request& r) {        // (0 without tokens)
-        const Span s = span(p, r);
-        return (uint32_t)s.rt * (uint32_t)p.KV * (uint32_t)s.nt;
-    };
-    auto scan = [&](uint32_t v) {              // inclusive, over the lanes
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const uint32_t o = (uint32_t)__shfl_up((int)v, d);
-            if (lane >= d) v += o;
-        }
-        return v;
-    };
-    const Request first64 = request_at(lane);
-    const uint32_t cost64 = scan(cost(first64));
-    uint32_t total = (uint32_t)__builtin_amdgcn_readlane((int)cost64, 63);
-    for (int b0 = 64; b0 < p.B; b0 += 64) total += (uint32_t)__builtin_amdgcn_readlane((int)scan(cost(request_at(b0 + lane))), 63);
-    // equal shares, in whole rounds of the waves
-    uint32_t per = (total + (uint32_t)p.workers - 1) / (uint32_t)p.workers;
-    per = (max(per, (uint32_t)p.least) + WV - 1) / WV * WV;
-    const int me = (int)blockIdx.x;
-    uint32_t it = (uint32_t)me * per;
-    const uint32_t it_end = min(it + per, total);
-    if (it >= it_end) return;
-    int b = 0;
-    uint32_t before = 0;                       // tiles of the requests before b
-    for (int b0 = 0; b0 < p.B; b0 += 64) {
-        const uint32_t c = b0 ? scan(cost(request_at(b0 + lane))) : cost64;
-        const unsigned long long past = __ballot(before + c > it);
-        if (past) {
-            const int f = (int)__builtin_ctzll(past);
-            b = b0 + f;
-            if (f) before += (uint32_t)__builtin_amdgcn_readlane((int)c, f - 1);
-            break;
-        }
-        before += (uint32_t)__builtin_amdgcn_readlane((int)c, 63);
-        b = b0 + 64;
-    }
+    Share sh;
+    if (!share_of<SK, WV>(p, lane, sh)) return;
+    uint32_t it = sh.it;
+    uint32_t before = sh.before;
+    int b = sh.b;
 
-    for (; it < it_end && b < p.B; ++b) {
-        Request r = b < 64 ? request_of_lane(first64, b) : request(p, b);
-        r.start = uniform(r.start);
-        r.n = uniform(r.n);
-        r.len = uniform(r.len);
-        Span s = span(p, r);
-        s.rt = uniform(s.rt);
-        s.lo = uniform(s.lo);
-        s.base = uniform(s.base);
-        s.nt = uniform(s.nt);
+    for (; it < sh.end && b < p.B; ++b) {
+        const Span s = span_of<SK>(p, sh, b);
         const uint32_t pairs = (uint32_t)s.rt * (uint32_t)p.KV;
-        const uint32_t mine = min(it_end, before + pairs * (uint32_t)s.nt);
+        const uint32_t mine = min(sh.end, before + pairs * (uint32_t)s.nt);
         while (it < mine) {
             const uint32_t pair = (it - before) / (uint32_t)s.nt;
             const int tile0 = (int)(it - before - pair * (uint32_t)s.nt);
@@ -169,14 +103,14 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void q4_attend_rows_kernel(Ar
             auto batch = [&](int i) {
                 if constexpr (PG) {
                     const int tile = tile0 + wave + WV * (i + (lane >> 1));
-                    const int block = min(max((s.base + tile * KT) / 16 + (lane & 1), s.lo >> 4), last_block);
+                    const int block = min(seen_block<SK>(p, s, s.key_of(tile) / 16 + (lane & 1)), last_block);
                     locate(block * 16);
                 }
             };
             // tile i of the wave, into its buffer
             auto load = [&](int i, auto values_tag) {
                 constexpr bool values = decltype(values_tag)::value;
-                const int first = s.base + (tile0 + wave + WV * i) * KT;
+                const int first = s.key_of(tile0 + wave + WV * i);
                 const uint32_t dst = values ? own_v : own_k;
                 const char* src = values ? vh : kh;
                 const int pitch = values ? p.vs2 : p.ks2;
@@ -189,7 +123,7 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void q4_attend_rows_kernel(Ar
                         const uint32_t o1 = (uint32_t)__builtin_amdgcn_readlane((int)(off >> 32), from);
                         const char* base = src + (long long)((uint64_t)o1 << 32 | o0);
                         // rows past the last key repeat it (nothing unwritten is read)
-                        const int limit = max(s.r.len - 1, 0) - 16 * min(max((first >> 4) + h, s.lo >> 4), last_block);
+                        const int limit = max(s.r.len - 1, 0) - 16 * min(seen_block<SK>(p, s, (first >> 4) + h), last_block);
 #pragma unroll
                         for (int e0 = 0; e0 < NI / 2; e0 += NB) {
                             uint32_t at[NB];
@@ -209,7 +143,7 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void q4_attend_rows_kernel(Ar
                     for (int e = 0; e < NI; ++e) {
                         const int row = e * RPI + lane / CPR;        // of the tile
                         const int chunk = min((lane % CPR) ^ spread<D>(row), p.chunks - 1);
-                        locate(min(max(first + row, s.lo), max(s.r.len - 1, 0)));
+                        locate(min(seen_key<SK>(p, s, first + row), max(s.r.len - 1, 0)));
                         dma_lane(src + (values ? vo : ko) + chunk * 16, dst + e * 1024u);
                     }
                 }
@@ -258,7 +192,7 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void q4_attend_rows_kernel(Ar
 
             for (int i = 0; i < count; ++i) {
                 const bool more = i + 1 < count;
-                const int first = s.base + (tile0 + wave + WV * i) * KT;
+                const int first = s.key_of(tile0 + wave + WV * i);
                 __builtin_amdgcn_sched_barrier(0);
                 // the keys have landed (the values' loads, issued later, may be out)
                 wait_loads<NI>();
@@ -283,14 +217,14 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void q4_attend_rows_kernel(Ar
                 // ---- softmax: lane holds keys first + 16 h + 4 quad + e of row c16
                 sc[0] *= p.scale;
                 sc[1] *= p.scale;
-                const bool edge = first + KT - 1 > all_hi || first < all_lo;
+                const bool edge = first + KT - 1 > all_hi || (first < all_lo && !(SK && first + KT <= p.sinks));
                 if (edge) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int key = first + 16 * h + 4 * quad + e;
-                            sc[h][e] = key >= klo && key <= khi ? sc[h][e] : -INFINITY;
+                            sc[h][e] = (key >= klo || (SK && key < p.sinks)) && key <= khi ? sc[h][e] : -INFINITY;
                         }
                 }
                 float top = kLow;
@@ -344,7 +278,7 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void q4_attend_rows_kernel(Ar
                     // (key 16 h + 4 q + e of the tile is value 4 h + e of the lanes of quad q)
 #pragma clang loop unroll(disable)
                     for (int x = 0; x < KT; ++x) {
-                        const bool sees = first + x >= klo && first + x <= khi;
+                        const bool sees = (first + x >= klo || (SK && first + x < p.sinks)) && first + x <= khi;
 #pragma unroll
                         for (int d = 0; d < DT; ++d) {
                             const char* at = vb + (vx ^ (d << 5));
@@ -373,113 +307,22 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void q4_attend_rows_kernel(Ar
                 for (int d = 0; d < DT; ++d)
                     *reinterpret_cast<f4*>(lds_k[wave] + c16 * (4 * D) + (((4 * d + quad) ^ c16) << 4)) = acc[d];
             }
-            __syncthreads();
-            constexpr int UNITS = ROWS * (D / 4), UPT = UNITS / NT;   // four values of a row each
-            const bool whole = tile0 == 0 && tiles == s.nt;
-            const uint32_t pair_at = before + pair * (uint32_t)s.nt;
-            // (workgroups there are, whatever `starts` says)
-            const int wf = min((int)(pair_at / per), p.workers - 1);
-            const int wl = min((int)((pair_at + (uint32_t)s.nt - 1) / per), p.workers - 1);
-            constexpr size_t SLOT = (size_t)ROWS * (D + 2);
-            auto slot_of = [&](int w) {
-                return make_rsrc(p.slots + (size_t)(2 * w + (w == wf ? 1 : 0)) * SLOT, (uint32_t)(SLOT * 4));
-            };
-            const rsrc_t own = slot_of(me);
-            f4 o[UPT];
-            float om[UPT], ol[UPT];
-#pragma unroll
-            for (int u = 0; u < UPT; ++u) {
-                const int unit = u * NT + tid, row = unit / (D / 4), c = unit % (D / 4);
-                float mm = lds_m[0][row];
-#pragma unroll
-                for (int w = 1; w < WV; ++w) mm = fmaxf(mm, lds_m[w][row]);
-                float ll = 0.f;
-                f4 v = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int w = 0; w < WV; ++w) {
-                    const float a = exp2_fast(lds_m[w][row] - mm);
-                    const f4 x = *reinterpret_cast<const f4*>(lds_k[w] + row * (4 * D) + ((c ^ row) << 4));
-                    ll += a * lds_l[w][row];
-                    v += a * x;
-                }
-                o[u] = v;
-                om[u] = mm;
-                ol[u] = ll;
-                if (!whole && row < rows) {
-                    put16(own, (uint32_t)unit * 16u, v);
-                    if (c == 0) {
-                        put4(own, (uint32_t)(ROWS * D + row) * 4u, mm);
-                        put4(own, (uint32_t)(ROWS * D + ROWS + row) * 4u, ll);
-                    }
-                }
-            }
-            bool finish = whole;
-            if (!whole) {
-                __builtin_amdgcn_s_waitcnt(0);
-                __syncthreads();
-                if (tid == 0)
-                    s_last = __hip_atomic_fetch_add(&p.counters[wf], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-                             (uint32_t)(wl - wf);
-                __syncthreads();
-                finish = s_last != 0;
-                if (finish) {
-#pragma unroll
-                    for (int u = 0; u < UPT; ++u) {
-                        const int unit = u * NT + tid, row = unit / (D / 4);
-                        float mm = kLow, ll = 0.f;
-                        f4 v = f4{0.f, 0.f, 0.f, 0.f};
-                        constexpr int FB = 16;     // slots whose loads are under way together
-                        for (int w0 = wf; row < rows && w0 <= wl; w0 += FB) {
-                            float pm[FB], pl[FB];
-                            f4 po[FB];
-#pragma unroll
-                            for (int f = 0; f < FB; ++f) {
-                                const rsrc_t r = slot_of(min(w0 + f, wl));
-                                pm[f] = take4(r, (uint32_t)(ROWS * D + row) * 4u);
-                                pl[f] = take4(r, (uint32_t)(ROWS * D + ROWS + row) * 4u);
-                                po[f] = take16(r, (uint32_t)unit * 16u);
-                            }
-#pragma unroll
-                            for (int f = 0; f < FB; ++f) {
-                                if (w0 + f > wl) continue;
-                                const float mn = fmaxf(mm, pm[f]);
-                                const float a = exp2_fast(mm - mn), c = exp2_fast(pm[f] - mn);
-                                ll = a * ll + c * pl[f];
-                                v = a * v + c * po[f];
-                                mm = mn;
-                            }
-                        }
-                        o[u] = v;
-                        ol[u] = ll;
-                    }
-                    if (tid == 0) __hip_atomic_store(&p.counters[wf], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                }
-            }
-            if (finish) {
-#pragma unroll
-                for (int u = 0; u < UPT; ++u) {
-                    const int unit = u * NT + tid, row = unit / (D / 4), at = unit % (D / 4) * 4;
-                    if (row >= rows || at >= p.dim) continue;
-                    const int r = row0 + row, token = (int)q4::fast_div((uint32_t)r, p.div_g);
-                    const f4 y = output_of(o[u], ol[u], over_sum(ol[u], pos0 + token));
-                    store_row4<BF>(p.out + (s.r.start + token) * p.o_t + (head * p.g + r - token * p.g) * p.o_h + at, y,
-                                   p.dim - at, p.store8);
-                }
-            }
+            finish<D, BF, WV>(p, sh, s, Segment{before + pair * (uint32_t)s.nt, tile0, tiles, head, row0, rows, pos0}, lds_k[0],
+                              KT * PITCH, lds_m[0], lds_l[0], &s_last);
             __syncthreads();    // the buffers are free for the next segment
         }
         before += pairs * (uint32_t)s.nt;
     }
 }
 
-template <int D>
+template <int D, bool SK>
 hipError_t launch_rows(const Args& p, bool bf16, bool pg, hipStream_t stream)
 {
     const dim3 grid(p.workers), block(NT);
-    if (bf16 && pg) hipLaunchKernelGGL((q4_attend_rows_kernel<D, true, true>), grid, block, 0, stream, p);
-    else if (bf16) hipLaunchKernelGGL((q4_attend_rows_kernel<D, true, false>), grid, block, 0, stream, p);
-    else if (pg) hipLaunchKernelGGL((q4_attend_rows_kernel<D, false, true>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((q4_attend_rows_kernel<D, false, false>), grid, block, 0, stream, p);
+    if (bf16 && pg) hipLaunchKernelGGL((q4_attend_rows_kernel<D, true, true, SK>), grid, block, 0, stream, p);
+    else if (bf16) hipLaunchKernelGGL((q4_attend_rows_kernel<D, true, false, SK>), grid, block, 0, stream, p);
+    else if (pg) hipLaunchKernelGGL((q4_attend_rows_kernel<D, false, true, SK>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((q4_attend_rows_kernel<D, false, false, SK>), grid, block, 0, stream, p);
     return hipGetLastError();
 }
 
@@ -490,9 +333,14 @@ namespace q4 {
 hipError_t launch_attend_rows(const q4attend::Args& p, bool bf16, bool pages_of_16, hipStream_t stream)
 {
     if (p.dim < 8 || p.dim > 256 || p.dim % 8 || p.workers < 1) return hipErrorInvalidValue;
-    if (p.dim <= 64) return launch_rows<64>(p, bf16, pages_of_16, stream);
-    if (p.dim <= 128) return launch_rows<128>(p, bf16, pages_of_16, stream);
-    return launch_rows<256>(p, bf16, pages_of_16, stream);
+    if (p.sinks) {
+        if (p.dim <= 64) return launch_rows<64, true>(p, bf16, pages_of_16, stream);
+        if (p.dim <= 128) return launch_rows<128, true>(p, bf16, pages_of_16, stream);
+        return launch_rows<256, true>(p, bf16, pages_of_16, stream);
+    }
+    if (p.dim <= 64) return launch_rows<64, false>(p, bf16, pages_of_16, stream);
+    if (p.dim <= 128) return launch_rows<128, false>(p, bf16, pages_of_16, stream);
+    return launch_rows<256, false>(p, bf16, pages_of_16, stream);
 }
 
 }  // namespace q4

@@ -1,0 +1,405 @@
+// New tokens into a paged cache held in 4 bits, and rows of it back.
+//
+// q4_cache4_append_kernel<WIDE, BF>: keys and values of new tokens, the keys turned by their
+// positions, are quantised in groups of G = 32 .. 256 neighbouring values:
+//   lo, hi = least and largest value (finite ones held within +-65440)
+//   m = binary16(lo), s = binary16(fp32(hi - m) / 15)
+//   c = (x - m) / s rounded to the nearest of 0 .. 15, ties to even (0 where s is 0)
+// and a group with a value that is not finite gets s = m = NaN. What the cache then stands for
+// is s c + m (q4_cache4.h). The queries are turned in the same launch.
+//
+// x is of the tokens' 16-bit type, so (x - m) is exact in 64 bits and the remainder x - m - n s
+// of a guess n is too: whether it passes half a step decides the code exactly. Keys are
+// turned in 64 bits, rounded to fp32 and to the type, and then quantised: a code is the definition's
+// and does not hang on the last bits of fp32. (64-bit instructions run at the rate of
+// 32-bit ones here.) Queries are turned as q4_rope_kernel turns them.
+//
+// Bound: memory, for many tokens that of the queries; for a few the launch. A row of a head is
+// taken by as many lanes as it has pieces of 8 values, all in one wave: a lane reads its piece
+// and the piece that it is paired with (from the cache beside it), the group's extremes pass
+// through the lanes, a lane writes 4 bytes of codes and the group's first the scale.
+//
+// q4_cache4_read_kernel: the rows of given slots as binary16.
+#include <hip/hip_runtime.h>
+
+#include "q4_cache4.h"
+#include "q4_cache4_host.h"
+#include "q4_fastdiv.h"
+#include "q4_ops.h"
+#include "q4_turn.h"
+
+namespace {
+
+using namespace q4dev;
+using namespace q4cache4;
+
+constexpr int NT = 256;
+constexpr int kMaxTokens = 4;     // tokens of a workgroup
+
+// Keys or values of the cache: strides in bytes.
+struct Plane {
+    char *at, *scale;
+    long long page, head, row, scale_page, scale_head, scale_row;
+};
+
+struct AppendArgs {
+    const uint64_t* turns;
+    float magnitude;
+    int n, rot, interleaved, dim;     // rotated pairs (0: none), rotated values, values of a head
+    int H, KV, T, TB;                 // heads of q; heads of k and v; tokens, tokens a workgroup
+    const uint16_t *q, *k, *v;
+    uint16_t* q_out;
+    long long q_t, q_h, k_t, k_h, v_t, v_h, o_t, o_h;
+    Plane kc, vc;
+    int group_lanes, group_shift;     // lanes of a group, log2 of its values
+    const void *positions, *slots;
+    int positions64, slots64;
+    int capacity, page_size;          // rows of the cache, rows of a page
+    int lanes_shift, rows;            // log2 of a row's lanes; rows of a token: H + 2 KV
+    q4::FastDiv div_rows, div_ps, div_n;
+};
+
+// The code of a value: d = x - m against steps of s, inv = 1 / s.
+__device__ __forceinline__ uint32_t code_of(double d, double s, double inv)
+{
+    double n = __builtin_rint(d * inv);
+    const double r = 2. * __builtin_fma(-n, s, d);      // exact: what is left, twice
+    const bool odd = (int)n & 1;
+    if (r > s || (r == s && odd)) n += 1.;
+    else if (r < -s || (r == -s && odd)) n -= 1.;
+    return (uint32_t)fmin(fmax(n, 0.), 15.);
+}
+
+template <bool WIDE, bool BF>
+__global__ __launch_bounds__(NT) void q4_cache4_append_kernel(AppendArgs p)
+{
+    extern __shared__ double2 cs64[];                                   // [TB][n]
+    float2* cs = reinterpret_cast<float2*>(cs64 + p.TB * p.n);          // [TB][n]
+    const int t0 = (int)blockIdx.x * p.TB;
+    const int tb = min(p.TB, p.T - t0);
+    for (int i = threadIdx.x; i < tb * p.n; i += NT) {
+        const int tt = p.TB == 1 ? 0 : (int)q4::fast_div((uint32_t)i, p.div_n);
+        const uint64_t f = (uint64_t)index_at(p.positions, p.positions64, t0 + tt) * p.turns[i - tt * p.n];
+        float2 e = turn_cos_sin(f);
+        e.x *= p.magnitude;
+        e.y *= p.magnitude;
+        cs[i] = e;
+        double2 d = turn_cos_sin64(f);
+        d.x *= (double)p.magnitude;
+        d.y *= (double)p.magnitude;
+        cs64[i] = d;
+    }
+    __syncthreads();
+    const int step = NT * (int)gridDim.y;
+    const int total = tb * p.rows << p.lanes_shift;
+    // (a row's lanes stay together: every lane of a wave goes round as often)
+    for (int base = (int)blockIdx.y * NT; base < total; base += step) {
+        const int i = base + (int)threadIdx.x;
+        const int piece = i & ((1 << p.lanes_shift) - 1);
+        const int row = i >> p.lanes_shift;
+        const int tt = min(p.TB == 1 ? 0 : (int)q4::fast_div((uint32_t)row, p.div_rows), tb - 1);
+        const int t = t0 + tt, head = row - tt * p.rows;
+        const int at = 8 * piece;
+        const bool query = head < p.H, value = head >= p.H + p.KV;
+        const int h = query ? head : head - p.H - (value ? p.KV : 0);
+        const uint16_t* src = query ? p.q + t * p.q_t + h * p.q_h : value ? p.v + t * p.v_t + h * p.v_h : p.k + t * p.k_t + h * p.k_h;
+        long long slot = -1;
+        bool on = i < total && at < p.dim;
+        if (on && !query) {
+            slot = index_at(p.slots, p.slots64, t);
+            on = slot >= 0 && slot < p.capacity;                        // else the token is not written
+        }
+        const bool turned = !value && at < p.rot;
+        uint32_t x[8], y[8];          // the lane's values, and the ones that they are paired with
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = y[e] = 0;
+        if (on) {
+            if constexpr (WIDE) {
+                const u4 a = *reinterpret_cast<const u4*>(src + at);
+                u4 b = a;
+                if (turned && !p.interleaved) b = *reinterpret_cast<const u4*>(src + (at < p.n ? at + p.n : at - p.n));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[2 * e] = a[e] & 0xffffu;
+                    x[2 * e + 1] = a[e] >> 16;
+                    y[2 * e] = p.interleaved ? a[e] >> 16 : b[e] & 0xffffu;
+                    y[2 * e + 1] = p.interleaved ? a[e] & 0xffffu : b[e] >> 16;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int d = at + e;
+                    x[e] = src[d];
+                    if (!value && d < p.rot) y[e] = src[p.interleaved ? d ^ 1 : d < p.n ? d + p.n : d - p.n];
+                }
+            }
+        }
+        if (turned && on) {
+            const float2* f = cs + tt * p.n;
+            const double2* f64 = cs64 + tt * p.n;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int d = at + e;
+                if (!WIDE && d >= p.rot) continue;
+                const bool first = p.interleaved ? !(d & 1) : d < p.n;
+                const int pair = p.interleaved ? d >> 1 : first ? d : d - p.n;
+                const float a = act_to_f32<BF>((uint16_t)x[e]), b = act_to_f32<BF>((uint16_t)y[e]);
+                if (query) {
+                    const float2 w = f[pair];
+                    x[e] = f32_to_act<BF>(first ? a * w.x - b * w.y : a * w.x + b * w.y);
+                } else {
+                    const double2 w = f64[pair];
+                    x[e] = f32_to_act<BF>((float)((double)a * w.x + (first ? -(double)b : (double)b) * w.y));
+                }
+            }
+        }
+        if (query) {
+            if (on) {
+                uint16_t* to = p.q_out + t * p.o_t + h * p.o_h + at;
+                if constexpr (WIDE) {
+                    *reinterpret_cast<u4*>(to) = u4{x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16};
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) to[e] = (uint16_t)x[e];
+                }
+            }
+        }
+        // (not branched over: the lanes of a row pass their extremes on)
+        float lo = INFINITY, hi = -INFINITY, v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float a = act_to_f32<BF>((uint16_t)x[e]);
+            v[e] = fminf(fmaxf(a, -kLargest), kLargest);
+            lo = fminf(lo, v[e]);
+            hi = fmaxf(hi, fabsf(a) < INFINITY ? v[e] : INFINITY);
+        }
+        for (int d = 1; d < p.group_lanes; d *= 2) {
+            lo = fminf(lo, __shfl_xor(lo, d));
+            hi = fmaxf(hi, __shfl_xor(hi, d));
+        }
+        if (!on || query) continue;
+        const bool finite = hi < INFINITY;
+        const uint16_t m16 = finite ? f32_to_f16_bits(lo) : (uint16_t)0x7e00;
+        const float m = f16_bits_to_f32(m16);
+        const uint16_t s16 = finite ? f32_to_f16_bits((hi - m) / 15.f) : (uint16_t)0x7e00;
+        const double s = (double)f16_bits_to_f32(s16), inv = 1. / s;
+        uint32_t word = 0;
+        if (s > 0.)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) word |= code_of((double)v[e] - (double)m, s, inv) << 4 * e;
+        const long long page = q4::fast_div((uint32_t)slot, p.div_ps);
+        const long long r = slot - page * p.page_size;
+        const Plane& c = value ? p.vc : p.kc;
+        *reinterpret_cast<uint32_t*>(c.at + page * c.page + h * c.head + r * c.row + 4 * piece) = word;
+        if ((piece & (p.group_lanes - 1)) == 0)
+            *reinterpret_cast<uint32_t*>(c.scale + page * c.scale_page + h * c.scale_head + r * c.scale_row + 4 * (at >> p.group_shift)) =
+                (uint32_t)s16 | (uint32_t)m16 << 16;
+    }
+}
+
+struct ReadArgs {
+    Plane kc, vc;
+    uint16_t *k, *v;
+    long long k_t, k_h, v_t, v_h;
+    const void* slots;
+    int slots64, T, KV, pieces, group_shift, capacity, page_size, wide;
+    q4::FastDiv div_pieces, div_heads, div_ps;
+};
+
+__global__ __launch_bounds__(NT) void q4_cache4_read_kernel(ReadArgs p)
+{
+    const long long total = 2LL * p.T * p.KV * p.pieces;
+    for (long long base = (long long)blockIdx.x * NT; base < total; base += (long long)gridDim.x * NT) {
+        const long long at = base + threadIdx.x;
+        if (at >= total) return;
+        const uint32_t i = (uint32_t)at;
+        const uint32_t row = q4::fast_div(i, p.div_pieces);
+        const int piece = (int)(i - row * (uint32_t)p.pieces);
+        const int t = (int)q4::fast_div(row, p.div_heads), head = (int)row - t * 2 * p.KV;
+        const bool value = head >= p.KV;
+        const int h = value ? head - p.KV : head;
+        const long long slot = index_at(p.slots, p.slots64, t);
+        u4 w = u4{0, 0, 0, 0};
+        if (slot >= 0 && slot < p.capacity) {
+            const long long page = q4::fast_div((uint32_t)slot, p.div_ps);
+            const long long r = slot - page * p.page_size;
+            const Plane& c = value ? p.vc : p.kc;
+            const uint32_t code = *reinterpret_cast<const uint32_t*>(c.at + page * c.page + h * c.head + r * c.row + 4 * piece);
+            const uint32_t sm = *reinterpret_cast<const uint32_t*>(c.scale + page * c.scale_page + h * c.scale_head + r * c.scale_row +
+                                                                   4 * (8 * piece >> p.group_shift));
+            w = own_order(values8(code, both(sm), both(sm >> 16)));
+        }
+        uint16_t* to = (value ? p.v + t * p.v_t + h * p.v_h : p.k + t * p.k_t + h * p.k_h) + 8 * piece;
+        if (p.wide) {
+            *reinterpret_cast<u4*>(to) = w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                to[2 * e] = (uint16_t)w[e];
+                to[2 * e + 1] = (uint16_t)(w[e] >> 16);
+            }
+        }
+    }
+}
+
+bool mult8(long long a) { return a % 8 == 0; }
+bool at16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+int log2_of(int n)
+{
+    int l = 0;
+    while ((1 << l) < n) ++l;
+    return l;
+}
+
+Plane plane_of(const q4_cache4* c, bool values)
+{
+    const int64_t* s = values ? c->v_stride : c->k_stride;
+    const int64_t* w = values ? c->v_scale_stride : c->k_scale_stride;
+    return Plane{static_cast<char*>(values ? c->v : c->k), static_cast<char*>(values ? c->v_scale : c->k_scale),
+                 s[0], s[1], s[2], w[0], w[1], w[2]};
+}
+
+}  // namespace
+
+extern "C" {
+
+q4_status q4_cache4_append(const q4_cache4* c, const uint16_t* k, int64_t k_token, int64_t k_head, const uint16_t* v,
+                           int64_t v_token, int64_t v_head, const void* slots, int slot_bits, int tokens,
+                           const q4_rotary* r, const void* positions, int position_bits, const uint16_t* q,
+                           int64_t q_token, int64_t q_head, uint16_t* q_out, int64_t out_token, int64_t out_head,
+                           int heads, int bf16, hipStream_t stream)
+{
+    const char* who = "q4_cache4_append";
+    if (q4_status st = q4::check_cache4(c, who); st != Q4_OK) return st;
+    if (tokens < 0 || heads < 0) return q4::fail(Q4_ERR_INVALID_ARG, "%s: negative size", who);
+    if (tokens == 0) return Q4_OK;
+    if (!k || !v || !slots) return q4::fail(Q4_ERR_INVALID_ARG, "%s: null k, v or slots", who);
+    if (slot_bits != 32 && slot_bits != 64) return q4::fail(Q4_ERR_INVALID_ARG, "%s: slots of %d bits", who, slot_bits);
+    const q4::View kin = q4::head_view(k, k_token, k_head, tokens, c->kv_heads, c->dim);
+    const q4::View vin = q4::head_view(v, v_token, v_head, tokens, c->kv_heads, c->dim);
+    if (q4::meets_cache4(kin, c) || q4::meets_cache4(vin, c)) return q4::fail(Q4_ERR_INVALID_ARG, "%s: k or v overlap the cache", who);
+    if (q4::meets_cache4(q4::flat_view(slots, (int64_t)tokens * slot_bits / 8), c) ||
+        (r && positions && q4::meets_cache4(q4::flat_view(positions, (int64_t)tokens * position_bits / 8), c)))
+        return q4::fail(Q4_ERR_INVALID_ARG, "%s: slots or positions overlap the cache", who);
+    AppendArgs p = {};
+    bool wide = true;
+    if (r) {
+        if (q4_status st = q4::check_rotary(r, positions, position_bits, who); st != Q4_OK) return st;
+        if (r->dim != c->dim) return q4::fail(Q4_ERR_INVALID_ARG, "%s: rotary heads of %d values, cache of %d", who, r->dim, c->dim);
+        p.turns = r->turns;
+        p.magnitude = r->magnitude;
+        p.n = r->rot / 2;
+        p.rot = r->rot;
+        p.interleaved = r->interleaved;
+        p.positions = positions;
+        p.positions64 = position_bits == 64;
+        wide = mult8(r->rot) && (r->interleaved || mult8(r->rot / 2));
+    }
+    if (q) {
+        if (!r) return q4::fail(Q4_ERR_INVALID_ARG, "%s: q is given without a rotary", who);
+        if (!q_out || heads < 1) return q4::fail(Q4_ERR_INVALID_ARG, "%s: q without heads or output", who);
+        // (a workgroup writes its part of q_out while others read k and v)
+        const q4::View to = q4::head_view(q_out, out_token, out_head, tokens, heads, c->dim);
+        if (!q4::same_view(q, q_token, q_head, q_out, out_token, out_head, tokens, heads) &&
+            q4::meet(to, q4::head_view(q, q_token, q_head, tokens, heads, c->dim)))
+            return q4::fail(Q4_ERR_INVALID_ARG, "%s: q_out overlaps q without being the same view", who);
+        if (q4::meet(to, kin) || q4::meet(to, vin)) return q4::fail(Q4_ERR_INVALID_ARG, "%s: q_out overlaps k or v", who);
+        if (q4::meets_cache4(to, c) || q4::meets_cache4(q4::head_view(q, q_token, q_head, tokens, heads, c->dim), c))
+            return q4::fail(Q4_ERR_INVALID_ARG, "%s: q or q_out overlap the cache", who);
+        if (q4::meet(to, q4::flat_view(slots, (int64_t)tokens * slot_bits / 8)) ||
+            q4::meet(to, q4::flat_view(positions, (int64_t)tokens * position_bits / 8)))
+            return q4::fail(Q4_ERR_INVALID_ARG, "%s: q_out overlaps slots or positions", who);
+        p.H = heads;
+        p.q = q;
+        p.q_t = q_token;
+        p.q_h = q_head;
+        p.q_out = q_out;
+        p.o_t = out_token;
+        p.o_h = out_head;
+        wide = wide && at16(q) && at16(q_out) && mult8(q_token) && mult8(q_head) && mult8(out_token) && mult8(out_head);
+    }
+    if (((long long)p.H + 2LL * c->kv_heads) * c->dim > (1 << 24))
+        return q4::fail(Q4_ERR_UNSUPPORTED, "%s: more than 2^24 values a token", who);
+    wide = wide && at16(k) && at16(v) && mult8(k_token) && mult8(k_head) && mult8(v_token) && mult8(v_head);
+    p.dim = c->dim;
+    p.KV = c->kv_heads;
+    p.T = tokens;
+    p.k = k;
+    p.k_t = k_token;
+    p.k_h = k_head;
+    p.v = v;
+    p.v_t = v_token;
+    p.v_h = v_head;
+    p.kc = plane_of(c, false);
+    p.vc = plane_of(c, true);
+    p.group_lanes = c->group / 8;
+    p.group_shift = log2_of(c->group);
+    p.slots = slots;
+    p.slots64 = slot_bits == 64;
+    p.page_size = c->page_size;
+    p.capacity = c->pages * c->page_size;
+    p.lanes_shift = log2_of(c->dim / 8);
+    p.rows = p.H + 2 * p.KV;
+    // Few tokens: a workgroup for each 256 lanes of each token, so that a decode step
+    // spreads over the CUs. Many: whole tokens, kMaxTokens to a workgroup.
+    const int slices = ((p.rows << p.lanes_shift) + NT - 1) / NT;
+    const bool few = (long long)p.T * slices <= 4096;
+    p.TB = few ? 1 : kMaxTokens;
+    p.div_rows = q4::make_fastdiv((uint32_t)p.rows);
+    p.div_ps = q4::make_fastdiv((uint32_t)p.page_size);
+    p.div_n = q4::make_fastdiv((uint32_t)(p.n > 0 ? p.n : 1));
+    const dim3 grid((p.T + p.TB - 1) / p.TB, few ? slices : 1);
+    const size_t lds = (size_t)p.TB * p.n * (sizeof(float2) + sizeof(double2));
+    if (wide && bf16) hipLaunchKernelGGL((q4_cache4_append_kernel<true, true>), grid, dim3(NT), lds, stream, p);
+    else if (wide) hipLaunchKernelGGL((q4_cache4_append_kernel<true, false>), grid, dim3(NT), lds, stream, p);
+    else if (bf16) hipLaunchKernelGGL((q4_cache4_append_kernel<false, true>), grid, dim3(NT), lds, stream, p);
+    else hipLaunchKernelGGL((q4_cache4_append_kernel<false, false>), grid, dim3(NT), lds, stream, p);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? Q4_OK : q4::fail(Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
+}
+
+q4_status q4_cache4_read(const q4_cache4* c, const void* slots, int slot_bits, int tokens, uint16_t* k, int64_t k_token,
+                         int64_t k_head, uint16_t* v, int64_t v_token, int64_t v_head, hipStream_t stream)
+{
+    const char* who = "q4_cache4_read";
+    if (q4_status st = q4::check_cache4(c, who); st != Q4_OK) return st;
+    if (tokens < 0) return q4::fail(Q4_ERR_INVALID_ARG, "%s: negative size", who);
+    if (tokens == 0) return Q4_OK;
+    if (!k || !v || !slots) return q4::fail(Q4_ERR_INVALID_ARG, "%s: null k, v or slots", who);
+    if (slot_bits != 32 && slot_bits != 64) return q4::fail(Q4_ERR_INVALID_ARG, "%s: slots of %d bits", who, slot_bits);
+    if (2LL * tokens * c->kv_heads * (c->dim / 8) >= (1LL << 31))
+        return q4::fail(Q4_ERR_UNSUPPORTED, "%s: more than 2^34 values", who);
+    const q4::View to[2] = {q4::head_view(k, k_token, k_head, tokens, c->kv_heads, c->dim),
+                            q4::head_view(v, v_token, v_head, tokens, c->kv_heads, c->dim)};
+    if (q4::meet(to[0], to[1])) return q4::fail(Q4_ERR_INVALID_ARG, "%s: k and v overlap", who);
+    for (const q4::View& x : to)
+        if (q4::meets_cache4(x, c) || q4::meet(x, q4::flat_view(slots, (int64_t)tokens * slot_bits / 8)))
+            return q4::fail(Q4_ERR_INVALID_ARG, "%s: k or v overlap the cache or slots", who);
+    ReadArgs p = {};
+    p.kc = plane_of(c, false);
+    p.vc = plane_of(c, true);
+    p.k = k;
+    p.v = v;
+    p.k_t = k_token;
+    p.k_h = k_head;
+    p.v_t = v_token;
+    p.v_h = v_head;
+    p.slots = slots;
+    p.slots64 = slot_bits == 64;
+    p.T = tokens;
+    p.KV = c->kv_heads;
+    p.pieces = c->dim / 8;
+    p.group_shift = log2_of(c->group);
+    p.capacity = c->pages * c->page_size;
+    p.page_size = c->page_size;
+    p.wide = at16(k) && at16(v) && mult8(k_token) && mult8(k_head) && mult8(v_token) && mult8(v_head);
+    p.div_pieces = q4::make_fastdiv((uint32_t)p.pieces);
+    p.div_heads = q4::make_fastdiv((uint32_t)(2 * p.KV));
+    p.div_ps = q4::make_fastdiv((uint32_t)p.page_size);
+    const long long blocks = (2LL * tokens * p.KV * p.pieces + NT - 1) / NT;
+    hipLaunchKernelGGL(q4_cache4_read_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(NT), 0, stream, p);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? Q4_OK : q4::fail(Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
+}
+
+}  // extern "C"

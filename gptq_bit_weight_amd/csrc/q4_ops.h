@@ -22,6 +22,14 @@ namespace q4 {
 q4_status device_info(int* dev, int* num_cu);
 // Shape and pointers of a cache description.
 q4_status check_cache(const q4_cache* c, const char* who);
+// A rotary handle and its positions: widths, and that it was made on the current device.
+q4_status check_rotary(const q4_rotary* r, const void* positions, int position_bits, const char* who);
+
+// (of one token, or one head, the stride does not count)
+inline bool same_view(const uint16_t* a, int64_t at, int64_t ah, const uint16_t* b, int64_t bt, int64_t bh, int tokens, int heads)
+{
+    return a == b && (at == bt || tokens == 1) && (ah == bh || heads == 1);
+}
 
 // 16-bit values of `tokens` tokens and `heads` heads; the keys or values of a cache.
 inline View head_view(const void* at, int64_t token, int64_t head, int tokens, int heads, int dim)

@@ -2,7 +2,7 @@
 // and tables that need no GPU.
 #include <cmath>
 
-#include "q4_internal.h"
+#include "q4_cache4_host.h"
 
 namespace q4 {
 
@@ -14,6 +14,32 @@ q4_status check_cache(const q4_cache* c, const char* who)
                     c->kv_heads, c->page_size, c->dim);
     if ((long long)c->pages * c->page_size > 0x7fffffffLL)
         return fail(Q4_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 rows in the cache", who);
+    return Q4_OK;
+}
+
+q4_status check_cache4(const q4_cache4* c, const char* who)
+{
+    if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale) return fail(Q4_ERR_INVALID_ARG, "%s: null cache or cache pointer", who);
+    if (c->pages < 1 || c->kv_heads < 1 || c->page_size < 1 || c->dim < 1)
+        return fail(Q4_ERR_INVALID_ARG, "%s: cache of %d pages, %d heads, %d rows a page, %d values", who, c->pages,
+                    c->kv_heads, c->page_size, c->dim);
+    if ((long long)c->pages * c->page_size > 0x7fffffffLL)
+        return fail(Q4_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 rows in the cache", who);
+    if (c->dim % 32 || c->dim > 256)
+        return fail(Q4_ERR_UNSUPPORTED, "%s: heads of %d values (a multiple of 32, at most 256)", who, c->dim);
+    if ((c->group != 32 && c->group != 64 && c->group != 128 && c->group != 256) || c->dim % c->group)
+        return fail(Q4_ERR_UNSUPPORTED, "%s: groups of %d values (32, 64, 128 or 256, a divisor of %d)", who, c->group, c->dim);
+    for (int i = 0; i < 3; ++i) {
+        if (c->k_stride[i] < 0 || c->v_stride[i] < 0 || c->k_stride[i] % 16 || c->v_stride[i] % 16)
+            return fail(Q4_ERR_UNSUPPORTED, "%s: strides of the codes must be multiples of 16 bytes", who);
+        if (c->k_scale_stride[i] < 0 || c->v_scale_stride[i] < 0 || c->k_scale_stride[i] % 4 || c->v_scale_stride[i] % 4)
+            return fail(Q4_ERR_UNSUPPORTED, "%s: strides of the scales must be multiples of 4 bytes", who);
+    }
+    if (c->k_stride[2] > (1 << 26) || c->v_stride[2] > (1 << 26) || c->k_scale_stride[2] > (1 << 26) || c->v_scale_stride[2] > (1 << 26))
+        return fail(Q4_ERR_UNSUPPORTED, "%s: rows of a page more than 2^26 bytes apart", who);
+    auto off = [](const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; };
+    if (off(c->k, 16) || off(c->v, 16) || off(c->k_scale, 4) || off(c->v_scale, 4))
+        return fail(Q4_ERR_UNSUPPORTED, "%s: codes must be 16-byte, scales 4-byte aligned", who);
     return Q4_OK;
 }
 
@@ -56,3 +82,5 @@ extern "C" q4_status q4_rotary_plan(int dim, int rot, int scaling, double base, 
     *magnitude = scaling == Q4_ROTARY_BY_PARTS ? (float)(0.1L * logl(f) + 1.0L) : 1.f;
     return Q4_OK;
 }
+
+extern "C" q4_status q4_check_cache4(const q4_cache4* c) { return q4::check_cache4(c, "q4_check_cache4"); }

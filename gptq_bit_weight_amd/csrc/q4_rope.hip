@@ -27,6 +27,7 @@
 #include "q4_device.h"
 #include "q4_fastdiv.h"
 #include "q4_ops.h"
+#include "q4_turn.h"
 
 namespace {
 
@@ -54,31 +55,6 @@ struct RopeArgs {
     int r1, ipt;                  // units of a token's rotated heads, and all of them
     q4::FastDiv div_ipt, div_lph, div_lpv, div_ps, div_n;
 };
-
-__device__ __forceinline__ long long index_at(const void* p, int wide, int i)
-{
-    return wide ? static_cast<const long long*>(p)[i] : (long long)static_cast<const int*>(p)[i];
-}
-
-__device__ __forceinline__ float2 turn_cos_sin(uint64_t f)
-{
-    const uint64_t g = f + (1ull << 61);
-    const uint32_t quad = (uint32_t)(g >> 62);
-    const uint64_t r = f - ((uint64_t)quad << 62);      // signed, in [-2^61, 2^61)
-    const float t = __builtin_fmaf((float)(uint32_t)r, 0x1p-64f, (float)(int32_t)(uint32_t)(r >> 32) * 0x1p-32f);
-    const float x = t * 6.283185307179586f, y = x * x;
-    float s = __builtin_fmaf(y, 1.f / 362880, -1.f / 5040);
-    s = __builtin_fmaf(y, s, 1.f / 120);
-    s = __builtin_fmaf(y, s, -1.f / 6);
-    s = __builtin_fmaf(x * y, s, x);
-    float c = __builtin_fmaf(y, -1.f / 3628800, 1.f / 40320);
-    c = __builtin_fmaf(y, c, -1.f / 720);
-    c = __builtin_fmaf(y, c, 1.f / 24);
-    c = __builtin_fmaf(y, c, -0.5f);
-    c = __builtin_fmaf(y, c, 1.f);
-    const float a = (quad & 1) ? s : c, b = (quad & 1) ? c : s;   // |cos|, |sin| of the quadrant
-    return float2{(quad == 1 || quad == 2) ? -a : a, (quad & 2) ? -b : b};
-}
 
 // V values a load (8: 16 bytes, 1: what no alignment allows more for); IL:
 // interleaved pairs (2i, 2i + 1), else (i, i + n).
@@ -245,26 +221,24 @@ void set_rotary(RopeArgs& p, const q4_rotary* r, bool transpose)
     p.transpose = transpose;
 }
 
+}  // namespace
+
+namespace q4 {
+
 q4_status check_rotary(const q4_rotary* r, const void* positions, int position_bits, const char* who)
 {
-    if (!r || !positions) return q4::fail(Q4_ERR_INVALID_ARG, "%s: null rotary or positions", who);
+    if (!r || !positions) return fail(Q4_ERR_INVALID_ARG, "%s: null rotary or positions", who);
     if (position_bits != 32 && position_bits != 64)
-        return q4::fail(Q4_ERR_INVALID_ARG, "%s: positions of %d bits", who, position_bits);
+        return fail(Q4_ERR_INVALID_ARG, "%s: positions of %d bits", who, position_bits);
     int cur = -1;
     hipError_t e = hipGetDevice(&cur);
-    if (e != hipSuccess) return q4::fail(Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
+    if (e != hipSuccess) return fail(Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
     if (cur != r->device)
-        return q4::fail(Q4_ERR_INVALID_ARG, "%s: the rotary table was made on device %d, the current device is %d", who, r->device, cur);
+        return fail(Q4_ERR_INVALID_ARG, "%s: the rotary table was made on device %d, the current device is %d", who, r->device, cur);
     return Q4_OK;
 }
 
-// (of one token, or one head, the stride does not count)
-bool same_view(const uint16_t* a, int64_t at, int64_t ah, const uint16_t* b, int64_t bt, int64_t bh, int tokens, int heads)
-{
-    return a == b && (at == bt || tokens == 1) && (ah == bh || heads == 1);
-}
-
-}  // namespace
+}  // namespace q4
 
 extern "C" {
 
@@ -314,11 +288,11 @@ q4_status q4_rotary_apply(const q4_rotary* r, const uint16_t* x, int64_t x_token
     const char* who = "q4_rotary_apply";
     if (tokens < 0 || heads < 0) return q4::fail(Q4_ERR_INVALID_ARG, "%s: negative size", who);
     if (tokens == 0 || heads == 0) return Q4_OK;
-    if (q4_status st = check_rotary(r, positions, position_bits, who); st != Q4_OK) return st;
+    if (q4_status st = q4::check_rotary(r, positions, position_bits, who); st != Q4_OK) return st;
     if (!x || !out) return q4::fail(Q4_ERR_INVALID_ARG, "%s: null pointer", who);
     if ((long long)heads * r->dim > (1 << 24)) return q4::fail(Q4_ERR_UNSUPPORTED, "%s: more than 2^24 values a token", who);
     const q4::View to = q4::head_view(out, out_token, out_head, tokens, heads, r->dim);
-    if (!same_view(x, x_token, x_head, out, out_token, out_head, tokens, heads) &&
+    if (!q4::same_view(x, x_token, x_head, out, out_token, out_head, tokens, heads) &&
         q4::meet(to, q4::head_view(x, x_token, x_head, tokens, heads, r->dim)))
         return q4::fail(Q4_ERR_INVALID_ARG, "%s: out overlaps its input without being the same view", who);
     if (q4::meet(to, q4::flat_view(positions, (int64_t)tokens * position_bits / 8)))
@@ -356,7 +330,7 @@ q4_status q4_cache_append(const q4_cache* c, const uint16_t* k, int64_t k_token,
     RopeArgs p = {};
     bool wide = mult8(c->dim), il = false;
     if (r) {
-        if (q4_status st = check_rotary(r, positions, position_bits, who); st != Q4_OK) return st;
+        if (q4_status st = q4::check_rotary(r, positions, position_bits, who); st != Q4_OK) return st;
         if (r->dim != c->dim) return q4::fail(Q4_ERR_INVALID_ARG, "%s: rotary heads of %d values, cache of %d", who, r->dim, c->dim);
         set_rotary(p, r, false);
         wide = wide_rotation(r);
@@ -369,7 +343,7 @@ q4_status q4_cache_append(const q4_cache* c, const uint16_t* k, int64_t k_token,
         if (!q_out || heads < 1) return q4::fail(Q4_ERR_INVALID_ARG, "%s: q without heads or output", who);
         // (a workgroup writes its part of q_out while others read k and v)
         const q4::View to = q4::head_view(q_out, out_token, out_head, tokens, heads, c->dim);
-        if (!same_view(q, q_token, q_head, q_out, out_token, out_head, tokens, heads) &&
+        if (!q4::same_view(q, q_token, q_head, q_out, out_token, out_head, tokens, heads) &&
             q4::meet(to, q4::head_view(q, q_token, q_head, tokens, heads, c->dim)))
             return q4::fail(Q4_ERR_INVALID_ARG, "%s: q_out overlaps q without being the same view", who);
         if (q4::meet(to, q4::head_view(k, k_token, k_head, tokens, c->kv_heads, c->dim)) ||

@@ -588,6 +588,84 @@ q4_status q4_attend(const q4_cache* c, const uint16_t* q, int64_t q_token, int64
                     int64_t table_stride, int requests, int window, float scale, uint16_t* out, int64_t out_token,
                     int64_t out_head, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * q4_attend_ex -- q4_attend with sinks: with window > 0 a token at position p
+ * sees key j <= p if p - window < j or j < sinks: the first `sinks` keys of
+ * every request stay visible. (Without a window they are visible anyway.) Of
+ * the table only the entries of pages that hold a visible key are read, so
+ * those between the sinks and the window may name no page.
+ */
+q4_status q4_attend_ex(const q4_cache* c, const uint16_t* q, int64_t q_token, int64_t q_head, int heads, int tokens,
+                       const int32_t* starts, const int32_t* lengths, const int32_t* table, int table_width,
+                       int64_t table_stride, int requests, int window, int sinks, float scale, uint16_t* out,
+                       int64_t out_token, int64_t out_head, void* workspace, size_t workspace_bytes,
+                       hipStream_t stream);
+
+/*
+ * A paged cache held in 4 bits. Row r of head h of page p is dim / 2 bytes of
+ * codes at k + p k_stride[0] + h k_stride[1] + r k_stride[2] (value 2 i in the low
+ * half of byte i, 2 i + 1 in its high half) and, at k_scale + p k_scale_stride[0]
+ * + ..., for each group of `group` neighbouring values a binary16 pair: the step s
+ * and the least value m. Strides count bytes. Code c stands for the binary16
+ * value RNE(s c + m). v likewise. dim is a multiple of 32, at most 256; group is
+ * 32, 64, 128 or 256 and divides dim; code strides are multiples of 16 bytes (base
+ * 16-byte aligned), scale strides of 4; rows lie at most 2^26 bytes apart.
+ * Device memory is the caller's.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    void* k_scale;
+    void* v_scale;
+    int64_t k_stride[3];
+    int64_t v_stride[3];
+    int64_t k_scale_stride[3];
+    int64_t v_scale_stride[3];
+    int pages, kv_heads, page_size, dim, group;
+} q4_cache4;
+
+/* The checks of a cache held in 4 bits that need no device. */
+q4_status q4_check_cache4(const q4_cache4* c);
+
+/*
+ * q4_cache4_append -- q4_cache_append into a cache held in 4 bits; k, v and q are
+ * binary16 or (bf16 != 0) bfloat16. A key is turned (in 64 bits, rounded to fp32 and
+ * then to that type) and quantised, a value is quantised, by groups:
+ *   lo, hi = the group's least and largest value, held within +-65440
+ *   m = binary16(lo), s = binary16(fp32(hi - m) / 15)
+ *   code = (x - m) / s rounded to the nearest of 0 .. 15, ties to even; 0 where s is 0.
+ * A group with a value that is not finite gets s = m = NaN: it stands for NaN as a
+ * whole. q is turned as q4_rotary_apply does. k, v, q, q_out, slots and positions must not
+ * overlap the cache (Q4_ERR_INVALID_ARG).
+ */
+q4_status q4_cache4_append(const q4_cache4* c, const uint16_t* k, int64_t k_token, int64_t k_head, const uint16_t* v,
+                           int64_t v_token, int64_t v_head, const void* slots, int slot_bits, int tokens,
+                           const q4_rotary* rotary, const void* positions, int position_bits, const uint16_t* q,
+                           int64_t q_token, int64_t q_head, uint16_t* q_out, int64_t out_token, int64_t out_head,
+                           int heads, int bf16, hipStream_t stream);
+
+/*
+ * q4_cache4_read -- the keys and values that rows slots[t] stand for, in binary16;
+ * zeros for a slot outside the cache. k and v must not overlap each other, the cache or
+ * the slots.
+ */
+q4_status q4_cache4_read(const q4_cache4* c, const void* slots, int slot_bits, int tokens, uint16_t* k, int64_t k_token,
+                         int64_t k_head, uint16_t* v, int64_t v_token, int64_t v_head, hipStream_t stream);
+
+/*
+ * q4_attend4 -- q4_attend_ex over the values that a cache held in 4 bits stands for;
+ * q and out are binary16 or (bf16 != 0) bfloat16. Both products take those
+ * binary16 values as they are; queries of bfloat16 are brought into binary16 by a power
+ * of two a row (values below 2^-31 of the row's largest lose bits), and the weights are
+ * rounded to binary16 whatever the type. The workspace is as for q4_attend.
+ */
+size_t q4_attend4_workspace(const q4_cache4* c, int heads);
+q4_status q4_attend4(const q4_cache4* c, const uint16_t* q, int64_t q_token, int64_t q_head, int heads, int tokens,
+                     const int32_t* starts, const int32_t* lengths, const int32_t* table, int table_width,
+                     int64_t table_stride, int requests, int window, int sinks, float scale, uint16_t* out,
+                     int64_t out_token, int64_t out_head, void* workspace, size_t workspace_bytes, int bf16,
+                     hipStream_t stream);
+
 /* ------------------------------------------------------------------------
  * Adapters of many requests beside one quantized product.
  * ---------------------------------------------------------------------- */
