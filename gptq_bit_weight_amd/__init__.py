@@ -44,6 +44,7 @@ EXPORTED_SYMBOLS = (
     "q4_rotary_make", "q4_rotary_free", "q4_rotary_plan", "q4_rotary_apply", "q4_cache_append",
     "q4_attend_workspace", "q4_attend", "q4_attend_ex",
     "q4_check_cache4", "q4_cache4_append", "q4_cache4_read", "q4_attend4_workspace", "q4_attend4",
+    "q4_copy_pages", "q4_pages_workspace", "q4_pages_extend", "q4_pages_fork", "q4_pages_free", "q4_pages_trim", "q4_pages_compact",
     "q4_check_adapters", "q4_adapters_make", "q4_adapters_free", "q4_adapters_load", "q4_adapters_clear",
     "q4_matmul_adapters",
 )
@@ -141,6 +142,14 @@ def load_library():
     lib.q4_check_cache4.argtypes = [P]
     lib.q4_cache4_append.argtypes = lib.q4_cache_append.argtypes[:-1] + [I, P]
     lib.q4_cache4_read.argtypes = [P, P, I, I, P, L, L, P, L, L, P]
+    lib.q4_copy_pages.argtypes = [P, P, I, P, I, I, P]
+    lib.q4_pages_workspace.argtypes = [I, I]
+    lib.q4_pages_workspace.restype = ctypes.c_size_t
+    lib.q4_pages_extend.argtypes = [P, P, I, P, P]
+    lib.q4_pages_fork.argtypes = [P, P, P, I, P, I, I, P, P]
+    lib.q4_pages_free.argtypes = [P, P, I, I, P]
+    lib.q4_pages_trim.argtypes = [P, I, I, P]
+    lib.q4_pages_compact.argtypes = [P, P, P, P]
     lib.q4_check_adapters.argtypes = [I, I]
     lib.q4_adapters_make.argtypes = [P, I, I, I]
     lib.q4_adapters_make.restype = P
@@ -150,7 +159,8 @@ def load_library():
     lib.q4_adapters_clear.argtypes = [P, I, P]
     lib.q4_matmul_adapters.argtypes = [P, P, P, P, P, P, I, I, P]
     for f in (lib.q4_rotary_plan, lib.q4_rotary_apply, lib.q4_cache_append, lib.q4_attend, lib.q4_attend_ex, lib.q4_check_cache4,
-              lib.q4_cache4_append, lib.q4_cache4_read, lib.q4_attend4, lib.q4_check_adapters,
+              lib.q4_cache4_append, lib.q4_cache4_read, lib.q4_attend4, lib.q4_copy_pages, lib.q4_pages_extend, lib.q4_pages_fork,
+              lib.q4_pages_free, lib.q4_pages_trim, lib.q4_pages_compact, lib.q4_check_adapters,
               lib.q4_adapters_load, lib.q4_adapters_clear, lib.q4_matmul_adapters):
         f.restype = I
     _lib = lib
@@ -581,13 +591,13 @@ class Q4Adapters:
             pass
 
 
-_ATTENTION = ("Rotary", "PagedCache", "PagedCache4")
+_ATTENTION = {"Rotary": "attention", "PagedCache": "attention", "PagedCache4": "attention", "Pages": "pages"}
 
 
 def __getattr__(name):
     # (torch is imported with the classes that work on its tensors, not with
     # the package, whose host-only part needs none: hence they are not in __all__)
     if name in _ATTENTION:
-        from . import attention
-        return getattr(attention, name)
+        import importlib
+        return getattr(importlib.import_module("." + _ATTENTION[name], __name__), name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -67,6 +67,17 @@ class _Cache4(ctypes.Structure):
         (n, ctypes.c_int) for n in ("pages", "kv_heads", "page_size", "dim", "group")]
 
 
+class _Plane(ctypes.Structure):
+    """q4_plane of include/q4.h."""
+    _fields_ = [("at", ctypes.c_void_p), ("page", ctypes.c_int64), ("head", ctypes.c_int64), ("row", ctypes.c_int64),
+                ("heads", ctypes.c_int), ("rows", ctypes.c_int), ("bytes", ctypes.c_int)]
+
+
+class _Pool(ctypes.Structure):
+    """q4_pool of include/q4.h."""
+    _fields_ = [("plane", _Plane * 4), ("planes", ctypes.c_int), ("pages", ctypes.c_int)]
+
+
 def _heads(t, name, device, dtype=None, tokens=None, heads=None, dim=None):
     """Check a [tokens, heads, dim] tensor whose head values are dense; returns
     its shape and strides."""
@@ -349,6 +360,37 @@ class _Paged:
               + qa + ((1 if dt is torch.bfloat16 else 0,) if four else ()), used if stream is None else used + self._tensors)
         _wrote(written)
         return q_out
+
+    def _pool(self):
+        """The tensors as a pool of pages (made once)."""
+        pool = self.__dict__.get("_pool_made")
+        if pool is None:
+            pool = _Pool()
+            for x, t in zip(pool.plane, self._tensors):
+                n = t.element_size()
+                x.at, x.page, x.head, x.row = t.data_ptr(), *(s * n for s in t.stride()[:3])
+                x.heads, x.rows, x.bytes = t.shape[1], t.shape[2], n * t[0, 0, 0].numel()
+            pool.planes, pool.pages = len(self._tensors), self.pages
+            self._pool_made = pool
+        return pool
+
+    def _writes(self):
+        """The cache's tensors, about to be written in place."""
+        for t in self._tensors:
+            _writable(t, "the cache")
+        return self._tensors
+
+    def copy_pages(self, src, dst, *, stream=None):
+        """Page dst[i] becomes a copy of page src[i] (int32 or int64 [n]); a pair with
+        one outside the cache is left out. The pages of dst must differ from each
+        other and from those of src (a mixture may be left)."""
+        dev = self.device
+        n = src.shape[0] if isinstance(src, _Tensor) and src.dim() == 1 else -1
+        sb, db = _index(src, "src", dev, n), _index(dst, "dst", dev, n)
+        written = self._writes()
+        _call(load_library().q4_copy_pages, "q4_copy_pages", dev, stream,
+              (ctypes.byref(self._pool()), src.data_ptr(), sb, dst.data_ptr(), db, n), () if stream is None else (src, dst) + written)
+        _wrote(written)
 
     def attend(self, q, starts, lengths, table, *, window: int = 0, sinks: int = 0, scale=None, out=None, stream=None):
         """Attention of new tokens over the cache: q [tokens, heads, dim] holds

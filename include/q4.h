@@ -667,6 +667,94 @@ q4_status q4_attend4(const q4_cache4* c, const uint16_t* q, int64_t q_token, int
                      hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * The pages of a cache, of either kind.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * One tensor of a cache: of each page `heads` heads of `rows` rows of `bytes` dense
+ * bytes, row r of head h of page p at `at` + p page + h head + r row (strides in bytes,
+ * non-negative). A pool is the one to four tensors of a cache.
+ */
+typedef struct {
+    void* at;
+    int64_t page, head, row;
+    int heads, rows, bytes;
+} q4_plane;
+typedef struct {
+    q4_plane plane[4];
+    int planes, pages;
+} q4_pool;
+
+/*
+ * q4_copy_pages -- page dst[i] becomes a copy of page src[i], in all tensors of the
+ * pool, for i < n. src and dst are device integers of 32 or 64 bits; a pair with one outside
+ * [0, pages) is left out. The pages of dst must differ from each other and from those of src
+ * (a mixture may be left); indexes must not overlap the cache.
+ */
+q4_status q4_copy_pages(const q4_pool* pool, const void* src, int src_bits, const void* dst, int dst_bits, int n,
+                        hipStream_t stream);
+
+/*
+ * Which pages hold which request's tokens, as dense device arrays of the caller's. Request r
+ * has lengths[r] tokens, in pages table[r width + i] for i < ceil(lengths[r] /
+ * page_size) (an entry outside [0, pages) names none). counts[p] is the number of
+ * those entries that name page p; a page whose count is not positive is free. work is
+ * scratch of q4_pages_workspace(requests, pages) bytes; calls that share the arrays are ordered
+ * on one stream. Nothing waits for the device, every call may be captured, and results do
+ * not depend on the order in which anything runs.
+ */
+typedef struct {
+    int32_t* table;
+    int32_t* lengths;
+    int32_t* counts;
+    int32_t* work;
+    int requests, width, pages, page_size;
+} q4_pages;
+
+size_t q4_pages_workspace(int requests, int pages);
+
+/*
+ * q4_pages_extend -- room for new tokens: request r gets starts[r + 1] - starts[r] more
+ * (starts: requests + 1 values from 0 to `tokens`, as in q4_attend), the lowest free pages for
+ * them where its last one does not suffice, in the order of the requests, and slots[t] is where
+ * token t goes (as q4_cache_append takes it). A request whose table row is too short gets
+ * nothing; one that the free pages do not suffice for gets nothing either, nor does any after it
+ * that needs some: lengths stay, slots are -1.
+ */
+q4_status q4_pages_extend(const q4_pages* pages, const int32_t* starts, int tokens, int32_t* slots, hipStream_t stream);
+
+/*
+ * q4_pages_fork -- for i < n, request children[i] becomes a copy of request parents[i]: its
+ * pages are the same ones but the last, which is copied to the lowest free page where it is not
+ * full, so that both go on in their own. done[i] is 1, or 0 for a pair with an index outside
+ * [0, requests), a child that holds tokens or that an earlier pair names, and one for which no
+ * free page is left. All pairs see the requests as they were before the call. done has room
+ * for 2 n values (the second n are scratch). pool describes the cache, pool->pages = pages.
+ */
+q4_status q4_pages_fork(const q4_pages* pages, const q4_pool* pool, const void* parents, int parent_bits, const void* children,
+                        int child_bits, int n, int32_t* done, hipStream_t stream);
+
+/*
+ * q4_pages_free -- gives back the pages of n requests (one named twice is freed once): their
+ * lengths are 0 and their entries -1.
+ */
+q4_status q4_pages_free(const q4_pages* pages, const void* requests, int bits, int n, hipStream_t stream);
+
+/*
+ * q4_pages_trim -- gives back the pages that no token after the present ones sees anything of,
+ * with a window >= 1 and sinks as in q4_attend_ex; their entries are -1. (Tokens that are in the
+ * cache but have not been attended for yet still need theirs: trim after that.)
+ */
+q4_status q4_pages_trim(const q4_pages* pages, int window, int sinks, hipStream_t stream);
+
+/*
+ * q4_pages_compact -- moves pages so that the U in use are pages 0 .. U - 1: the k-th one in use
+ * from page U on goes to the k-th free page below it. Tables and counts follow; to[p] is
+ * where page p went, -1 for one that was free.
+ */
+q4_status q4_pages_compact(const q4_pages* pages, const q4_pool* pool, int32_t* to, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * Adapters of many requests beside one quantized product.
  * ---------------------------------------------------------------------- */
 
