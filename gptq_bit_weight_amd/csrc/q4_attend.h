@@ -148,6 +148,14 @@ __device__ __forceinline__ u2 read_tr(const char* p)
     return bitcast<u2>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)p));
 }
 
+// What this wave has read from LDS is in registers, what it wrote is there.
+__device__ __forceinline__ void wait_lds()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
@@ -218,6 +226,21 @@ __device__ __forceinline__ f4 output_of(f4 v, float sum, float inv)
 {
     // (what a row that sees no key has summed may not be finite)
     return sum == 0.f ? f4{inv, inv, inv, inv} : v * inv;
+}
+
+// The kernel's arguments (Args is its only one), read anew where this stands: what
+// rare parts of a loop take from them does not stay in registers across it.
+__device__ __forceinline__ const Args& args_again()
+{
+    auto p = (const __attribute__((address_space(4))) Args*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const Args*)p;
+}
+// A value whose uses are not computed ahead of here.
+__device__ __forceinline__ int here(int v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
 }
 
 // Four values of an output row.

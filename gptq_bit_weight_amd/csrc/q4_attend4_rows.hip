@@ -10,16 +10,21 @@
 // the queries' type; queries of bfloat16 are brought into binary16's range by a power of two a
 // row, which the scores are multiplied by again: exact but for values below 2^-32 of the row's largest.
 //
-// Bound: HBM, with the vector instructions that unpack close behind. A 32-key tile of a head of
-// 128 is 4 KiB of codes and up to 1 KiB of scales, and takes a wave some 350 vector instructions
-// (1.7 a value), so the codes go from memory straight to registers: with the scores' products
-// taken as S^T = K Q^T, a lane's operand is a piece of one key's row, and its 8 values per
-// instruction may be any 8 of the head as long as the queries' are the same 8. For O^T = V^T P^T a
-// lane's operand is 8 keys' values of one column; it loads 8 keys' codes of D / 16 neighbouring
-// columns and pairs the keys by byte permutes, which makes D / 16 operands.
+// Bound: HBM, with the vector instructions that unpack close behind: a 32-key tile of a head of
+// 128 is 4 KiB of codes and up to 1 KiB of scales, and takes a wave some 300 vector instructions
+// (unpacking 13 for 8 values of a key, 7 for 4 of a value). So four waves a SIMD share them, and what they hold
+// in registers is little: a wave's tile of codes lies in LDS of its own, filled by direct loads
+// and asked for as soon as the present one is in registers; no barrier stands in the loop.
+//
+// With the scores taken as S^T = K Q^T a lane's operand is a piece of one key's row, and its 8
+// values an instruction may be any 8 of the head as long as the queries' are the same 8: D / 4
+// neighbouring ones a lane, one LDS read and one scale. For O^T = V^T P^T a lane's operand is 8 keys'
+// values of one column; it reads 8 keys' codes of D / 16 neighbouring columns and pairs the keys
+// by byte permutes, which makes D / 16 operands. Row i of the scores' product is key i / 4 +
+// 4 (i % 4) of 16, so that the four rows which the lanes of a read touch are neighbours and fall on
+// banks of their own; pieces of 16 bytes lie at place piece ^ spread4(row) of a row for the reads of keys.
 //
 // Work is shared out, joined and stored as in the kernel for 16 bits (q4_attend_rows.h).
-// Each wave has the next tile's codes under way while it computes with the present one's.
 #include "q4_attend_rows.h"
 #include "q4_cache4.h"
 
@@ -28,9 +33,19 @@ namespace {
 using namespace q4attend;
 using namespace q4cache4;
 
+constexpr float kSlack = 8.f;    // log2 of the growth of a maximum that is let pass: a weight is at most 2^15
+
 template <int D>
 struct Shape {
-    static constexpr int WV = D == 256 ? 4 : 8;        // waves of a workgroup
+    static constexpr int WV = D == 256 ? 8 : 12;       // waves of a workgroup
+    static constexpr int ROW = D / 2;                  // bytes of a row of codes
+    static constexpr int CPR = D / 32;                 // pieces of 16 bytes of it, and scales of it in LDS (one for 32 values)
+    static constexpr int RPI = 64 / CPR > 16 ? 16 : 64 / CPR;      // rows that one direct load fills
+    static constexpr int NL = 16 / RPI;                // direct loads of 16 rows of codes; of scales as many
+    static constexpr int NI = 4 * NL;                  // and of a tile's keys (or values)
+    static constexpr int CODES = KT * ROW, SCALES = KT * CPR * 4, TILE = 2 * (CODES + SCALES);
+    static constexpr int OUT = ROWS * 4 * D;           // a wave's outputs take the same place in the end
+    static constexpr int WAVE = OUT > TILE ? OUT : TILE;
     static constexpr int KS = D / 32;                  // k-steps of the scores: words of a lane's piece of a key
     static constexpr int KG = D == 256 ? 2 : 1;        // scales of that piece
     static constexpr int VD = D / 16;                  // columns of a lane's piece of a value row
@@ -38,20 +53,28 @@ struct Shape {
     static constexpr int VW = VD > 8 ? 2 : 1;          // and words
 };
 
-// Codes and scales of a tile in a lane's registers: of keys c16 and 16 + c16, dims
-// D / 4 quad ..; of values 4 quad + e and 16 + 4 quad + e, columns VD c16 ..
 template <int D>
-struct Tile {
-    using S = Shape<D>;
-    uint32_t k[2][S::KS], ks[2][S::KG], v[8][S::VW], vs[8];
-};
+__device__ __forceinline__ int spread4(int row)        // (of 16)
+{
+    return D == 64 ? row >> 3 & 1 : D == 128 ? row >> 2 & 3 : row >> 1 & 7;
+}
+
+// 4 bytes a lane from memory straight into LDS: lane l's land at dst + 4 l (q4_attend.h, dma).
+__device__ __forceinline__ void dma_words(const char* base, uint32_t off, uint32_t dst)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(reinterpret_cast<uint64_t>(base)), "s"(dst) : "memory");
+}
+__device__ __forceinline__ void dma_words_lane(const char* src, uint32_t dst)
+{
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 4\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(dst) : "memory");
+}
 
 template <int D, bool BF, bool PG>
-__global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 1 : 2) void q4_attend4_rows_kernel(Args p)
+__global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 2 : 3) void q4_attend4_rows_kernel(Args p)
 {
     using S = Shape<D>;
-    constexpr int WV = S::WV, KS = S::KS, KG = S::KG, VD = S::VD;
-    __shared__ __attribute__((aligned(1024))) char lds_o[WV][ROWS * 4 * D];
+    constexpr int WV = S::WV, KS = S::KS, KG = S::KG, VD = S::VD, NL = S::NL, CPR = S::CPR;
+    __shared__ __attribute__((aligned(1024))) char lds[WV][S::WAVE];
     __shared__ float lds_m[WV][ROWS], lds_l[WV][ROWS];
     __shared__ int s_last;
 
@@ -60,23 +83,34 @@ __global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 1 : 2) void q4_attend
     const int lane = tid & 63;
     const int c16 = lane & 15, quad = lane >> 4;
 
-    // the lane's bytes of a row: a piece past the head's end is another one, with
-    // scales of zero
-    uint32_t kcol[KG], kscol[KG], vcol, vscol;
-    bool kin[KG], vin;
+    // ---- direct loads: the lane's bytes in 16 rows of keys and of values (the queries are
+    // zero where the head has ended, and the outputs not stored: a piece past its end is the first one)
+    const int lrow = lane / CPR, lpiece = lane % CPR;        // (of D = 64 half of the lanes load)
+    const bool loads = D > 64 || lane < 32;
+    auto column = [&](int piece) { return 32 * piece < p.dim ? piece : 0; };
+    uint32_t koff[NL], voff[NL], ksoff[NL], vsoff[NL];
 #pragma unroll
-    for (int t = 0; t < KG; ++t) {
-        const int d = D / 4 * quad + 32 * t;
-        kin[t] = d < p.dim;
-        kcol[t] = kin[t] ? (uint32_t)d / 2u : 0u;
-        kscol[t] = kin[t] ? (uint32_t)(d >> p.group_shift) * 4u : 0u;
+    for (int e = 0; e < NL; ++e) {
+        const int row = e * S::RPI + lrow;
+        const int c = column(lpiece ^ spread4<D>(row)) * 16, sc = (32 * column(lpiece) >> p.group_shift) * 4;
+        koff[e] = (uint32_t)(row * p.k4.row + c);
+        voff[e] = (uint32_t)(row * p.v4.row + c);
+        ksoff[e] = (uint32_t)(row * p.k4.scale_row + sc);
+        vsoff[e] = (uint32_t)(row * p.v4.scale_row + sc);
     }
-    {
-        const int d = VD * c16;
-        vin = d < p.dim;
-        vcol = vin ? (uint32_t)d / 2u : 0u;
-        vscol = vin ? (uint32_t)(d >> p.group_shift) * 4u : 0u;
-    }
+    const uint32_t own = lds_address(lds[wave]);
+    // ---- reads of them: key 16 h + krow, dims D / 4 quad ..; values 16 h + 4 e + quad, columns VD c16 ..
+    const int krow = (c16 >> 2) + 4 * (c16 & 3);
+    const char* kb = lds[wave] + krow * S::ROW;
+    const char* ksb = lds[wave] + S::CODES + krow * (CPR * 4) + (D / 4 * quad / 32) * 4;
+    const char* vb = lds[wave] + S::CODES + S::SCALES + quad * S::ROW;
+    const char* vsb = lds[wave] + 2 * S::CODES + S::SCALES + quad * (CPR * 4) + (VD * c16 / 32) * 4;
+    bool kin[KG];
+#pragma unroll
+    for (int t = 0; t < KG; ++t) kin[t] = D / 4 * quad + 32 * t < p.dim;
+    const bool vin = VD * c16 < p.dim;
+
+    const Magic mg = magic();
 
     Share sh;
     if (!share_of<true, WV>(p, lane, sh)) return;
@@ -99,111 +133,88 @@ __global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 1 : 2) void q4_attend
             // ---- the wave's tiles: tile0 + wave, + WV, ...
             const int count = (tiles - wave + WV - 1) / WV;      // (0 or less: none)
             const int last_key = max(s.r.len - 1, 0), last_block = last_key >> 4;
-            const char *kh = p.k4.at + head * p.k4.head, *ksh = p.k4.scale + head * p.k4.scale_head;
-            const char *vh = p.v4.at + head * p.v4.head, *vsh = p.v4.scale + head * p.v4.scale_head;
-            // page and row of a key
-            auto locate = [&](int key, int& row) {
-                const int slot = (int)q4::fast_div((uint32_t)key, p.div_page);
-                row = key - slot * p.page_size;
-                return (int)min((uint32_t)p.table[(long long)b * p.table_stride + slot], (uint32_t)p.pages - 1u);
-            };
-            // of the 16-row block that lane l / 2 steps on, half l % 2 (one load of
+            // addresses of the 16-row block that lane l / 2 steps on, half l % 2 (one load of
             // page numbers for 32 tiles)
-            int page_of = 0, row_of = 0;
+            const char *kat = nullptr, *ksat = nullptr, *vat = nullptr, *vsat = nullptr;
+            auto locate = [&](int key) {
+                const Args& a = args_again();
+                const int slot = (int)q4::fast_div((uint32_t)key, a.div_page);
+                const long long page = min((uint32_t)a.table[(long long)b * a.table_stride + slot], (uint32_t)a.pages - 1u);
+                const long long row = key - slot * a.page_size;
+                kat = a.k4.at + head * a.k4.head + page * a.k4.page + row * a.k4.row;
+                ksat = a.k4.scale + head * a.k4.scale_head + page * a.k4.scale_page + row * a.k4.scale_row;
+                vat = a.v4.at + head * a.v4.head + page * a.v4.page + row * a.v4.row;
+                vsat = a.v4.scale + head * a.v4.scale_head + page * a.v4.scale_page + row * a.v4.scale_row;
+            };
             auto batch = [&](int i) {
                 if constexpr (PG) {
-                    const int tile = tile0 + wave + WV * (i + (lane >> 1));
-                    page_of = locate(16 * min(seen_block<true>(p, s, s.key_of(tile) / 16 + (lane & 1)), last_block), row_of);
+                    const int at = here(lane), tile = tile0 + wave + WV * (i + (at >> 1));
+                    locate(16 * min(seen_block<true>(p, s, s.key_of(tile) / 16 + (at & 1)), last_block));
                 }
             };
-            auto take_v = [&](uint32_t (&v)[S::VW], const char* at) {
-                if constexpr (S::VB == 2) v[0] = *reinterpret_cast<const uint16_t*>(at);
-                else if constexpr (S::VB == 4) v[0] = *reinterpret_cast<const uint32_t*>(at);
-                else {
-                    const u2 w = *reinterpret_cast<const u2*>(at);
-                    v[0] = w[0];
-                    v[1] = w[1];
-                }
+            auto at_lane = [](const char* p, int from) {
+                const uint64_t v = reinterpret_cast<uint64_t>(p);
+                const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)v, from), hi = (uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), from);
+                return reinterpret_cast<const char*>((uint64_t)hi << 32 | lo);
             };
-            auto take_k = [&](uint32_t (&k)[KS], const char* at, const uint32_t (&off)[KG]) {
-                if constexpr (KS == 2) {
-                    const u2 w = *reinterpret_cast<const u2*>(at + off[0]);
-                    k[0] = w[0];
-                    k[1] = w[1];
-                } else {
+            auto load = [&](int i, auto values_tag) {
+                constexpr bool values = decltype(values_tag)::value;
+                const int first = s.key_of(tile0 + wave + WV * i);
+                const uint32_t to = own + (values ? S::CODES + S::SCALES : 0);
 #pragma unroll
-                    for (int t = 0; t < KG; ++t) {
-                        const u4 w = *reinterpret_cast<const u4*>(at + off[t]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) k[4 * t + e] = w[e];
-                    }
-                }
-            };
-            auto load = [&](int i, Tile<D>& t) {
-                if constexpr (PG) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < 2; ++h) {
+                    if constexpr (PG) {
                         const int from = 2 * (i & 31) + h;
-                        const long long page = __builtin_amdgcn_readlane(page_of, from);
-                        const long long row = __builtin_amdgcn_readlane(row_of, from);
-                        const char* kb = kh + page * p.k4.page + row * p.k4.row;
-                        const char* ksb = ksh + page * p.k4.scale_page + row * p.k4.scale_row;
-                        const char* vb = vh + page * p.v4.page + row * p.v4.row;
-                        const char* vsb = vsh + page * p.v4.scale_page + row * p.v4.scale_row;
-                        const int first = s.key_of(tile0 + wave + WV * i) / 16 + h;
+                        const char *base = at_lane(values ? vat : kat, from), *scale_base = at_lane(values ? vsat : ksat, from);
                         // rows past the last key repeat it (nothing unwritten is read)
-                        const int limit = last_key - 16 * min(seen_block<true>(p, s, first), last_block);
-                        const uint32_t kr = (uint32_t)min(c16, limit);
-                        uint32_t koff[KG];
+                        const int limit = last_key - 16 * min(seen_block<true>(p, s, (first >> 4) + h), last_block);
 #pragma unroll
-                        for (int g = 0; g < KG; ++g) koff[g] = kr * (uint32_t)p.k4.row + kcol[g];
-                        take_k(t.k[h], kb, koff);
-#pragma unroll
-                        for (int g = 0; g < KG; ++g)
-                            t.ks[h][g] = *reinterpret_cast<const uint32_t*>(ksb + (kr * (uint32_t)p.k4.scale_row + kscol[g]));
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t vr = (uint32_t)min(4 * quad + e, limit);
-                            take_v(t.v[4 * h + e], vb + (vr * (uint32_t)p.v4.row + vcol));
-                            t.vs[4 * h + e] = *reinterpret_cast<const uint32_t*>(vsb + (vr * (uint32_t)p.v4.scale_row + vscol));
+                        for (int e = 0; e < NL; ++e) {
+                            uint32_t at[1] = {values ? voff[e] : koff[e]}, sat = values ? vsoff[e] : ksoff[e];
+                            if (limit < 15) {
+                                const Side& side = values ? args_again().v4 : args_again().k4;
+                                const int row = e * S::RPI + here(lane) / CPR, back = row - min(row, limit);
+                                at[0] -= (uint32_t)(back * side.row);
+                                sat -= (uint32_t)(back * side.scale_row);
+                            }
+                            if (loads) {
+                                dma<1>(base, at, to + (uint32_t)(h * NL + e) * (S::RPI * S::ROW));
+                                dma_words(scale_base, sat, to + S::CODES + (uint32_t)(h * NL + e) * (S::RPI * CPR * 4));
+                            }
                         }
-                    }
-                } else {
-                    const int first = s.key_of(tile0 + wave + WV * i);
+                    } else {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        int row;
-                        long long page = locate(min(seen_key<true>(p, s, first + 16 * h + c16), last_key), row);
-                        take_k(t.k[h], kh + page * p.k4.page + (long long)row * p.k4.row, kcol);
-#pragma unroll
-                        for (int g = 0; g < KG; ++g)
-                            t.ks[h][g] = *reinterpret_cast<const uint32_t*>(ksh + page * p.k4.scale_page + (long long)row * p.k4.scale_row + kscol[g]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            page = locate(min(seen_key<true>(p, s, first + 16 * h + 4 * quad + e), last_key), row);
-                            take_v(t.v[4 * h + e], vh + page * p.v4.page + (long long)row * p.v4.row + vcol);
-                            t.vs[4 * h + e] = *reinterpret_cast<const uint32_t*>(vsh + page * p.v4.scale_page + (long long)row * p.v4.scale_row + vscol);
+                        for (int e = 0; e < NL; ++e) {
+                            const int row = e * S::RPI + lrow;
+                            locate(min(seen_key<true>(p, s, first + 16 * h + (row & 15)), last_key));
+                            const int c = column(lpiece ^ spread4<D>(row)) * 16, sc = (32 * column(lpiece) >> p.group_shift) * 4;
+                            if (loads) {
+                                dma_lane((values ? vat : kat) + c, to + (uint32_t)(h * NL + e) * (S::RPI * S::ROW));
+                                dma_words_lane((values ? vsat : ksat) + sc, to + S::CODES + (uint32_t)(h * NL + e) * (S::RPI * CPR * 4));
+                            }
                         }
                     }
                 }
             };
-            Tile<D> ta, tb;
+            constexpr std::false_type KEYS;
+            constexpr std::true_type VALUES;
             if (count > 0) {
                 batch(0);
-                load(0, ta);
+                load(0, KEYS);
+                load(0, VALUES);
             }
 
             // ---- queries: lane holds row c16, values D / 4 quad + 8 ks .. in the order of the unpacked codes
             u4 qf[KS];
-            int klo, khi;                      // the row's visible keys
+            int khi;                           // the row's last visible key (-1: a row that is none)
             float scale = p.scale;
             {
+                const int c16 = here(lane) & 15, quad = here(lane) >> 4;
                 const int r = row0 + c16;
                 const bool live = c16 < rows;
                 const int token = (int)q4::fast_div((uint32_t)r, p.div_g);
                 const int pos = pos0 + token;
                 khi = live ? pos : -1;
-                klo = p.window ? pos - p.window + 1 : 0;
                 const uint16_t* qp = p.q + (s.r.start + (live ? token : 0)) * p.q_t
                                    + (head * p.g + (live ? r - token * p.g : 0)) * p.q_h;
 #pragma unroll
@@ -233,24 +244,56 @@ __global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 1 : 2) void q4_attend
             for (int d = 0; d < VD; ++d) acc[d] = f4{0.f, 0.f, 0.f, 0.f};
             // keys of a tile that every live row sees
             const int all_hi = pos0 + (int)q4::fast_div((uint32_t)row0, p.div_g);
+            const int back = p.window ? p.window : 1 << 30;
+            auto visible = [&](int key) { return (key > khi - back || key < p.sinks) && key <= khi; };
             const int all_lo = p.window ? pos0 + (int)q4::fast_div((uint32_t)(row0 + rows - 1), p.div_g) - p.window + 1 : 0;
 
-            auto compute = [&](int i, const Tile<D>& t) {
+            for (int i = 0; i < count; ++i) {
+                const bool more = i + 1 < count;
                 const int first = s.key_of(tile0 + wave + WV * i);
+                __builtin_amdgcn_sched_barrier(0);
+                // the keys have landed (the values' loads, issued later, may be out)
+                wait_loads<S::NI>();
+                __builtin_amdgcn_sched_barrier(0);
+                uint32_t kc[2][KS], ksm[2][KG];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const char* at = kb + h * 16 * S::ROW;
+                    if constexpr (D == 64) {
+                        const u2 w = *reinterpret_cast<const u2*>(at + (((quad >> 1) ^ spread4<D>(krow)) << 4) + (quad & 1) * 8);
+                        kc[h][0] = w[0];
+                        kc[h][1] = w[1];
+                    } else {
+#pragma unroll
+                        for (int t = 0; t < KG; ++t) {
+                            const u4 w = *reinterpret_cast<const u4*>(at + (((KG * quad + t) ^ spread4<D>(krow)) << 4));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) kc[h][4 * t + e] = w[e];
+                        }
+                    }
+#pragma unroll
+                    for (int t = 0; t < KG; ++t) ksm[h][t] = *reinterpret_cast<const uint32_t*>(ksb + h * 16 * CPR * 4 + 4 * t);
+                }
+                wait_lds();
+                if (more) {
+                    if (((i + 1) & 31) == 0) batch(i + 1);
+                    load(i + 1, KEYS);
+                }
+                __builtin_amdgcn_sched_barrier(0);
                 f4 sc[2] = {f4{0.f, 0.f, 0.f, 0.f}, f4{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int g = 0; g < KG; ++g) {
-                        const uint32_t sm = kin[g] ? t.ks[h][g] : 0u;
+                        const uint32_t sm = kin[g] ? ksm[h][g] : 0u;
                         const h2 step = both(sm), least = both(sm >> 16);
 #pragma unroll
                         for (int e = 0; e < KS / KG; ++e) {
                             const int ks = g * (KS / KG) + e;
-                            sc[h] = mfma16(bitcast<h8>(values8(t.k[h][ks], step, least)), bitcast<h8>(qf[ks]), sc[h]);
+                            sc[h] = mfma16(bitcast<h8>(values8(kc[h][ks], step, least, mg)), bitcast<h8>(qf[ks]), sc[h]);
                         }
                     }
-                // ---- softmax: lane holds keys first + 16 h + 4 quad + e of row c16
+                // ---- softmax: lane holds keys first + 16 h + 4 e + quad of row c16
                 sc[0] *= scale;
                 sc[1] *= scale;
                 const bool edge = first + KT - 1 > all_hi || (first < all_lo && first + KT > p.sinks);
@@ -259,8 +302,8 @@ __global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 1 : 2) void q4_attend
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int key = first + 16 * h + 4 * quad + e;
-                            sc[h][e] = (key >= klo || key < p.sinks) && key <= khi ? sc[h][e] : -INFINITY;
+                            const int key = first + 16 * h + 4 * e + quad;
+                            sc[h][e] = visible(key) ? sc[h][e] : -INFINITY;
                         }
                 }
                 float top = kLow;
@@ -268,8 +311,8 @@ __global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 1 : 2) void q4_attend
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[h][e]);
-                const float mn = fmaxf(m, max_quarters(top) - lift<false>(0.f));
-                if (__any(mn > m)) {
+                const float mn = fmaxf(m, max_quarters(top) - lift<false>(kSlack));
+                if (__any(mn > m + kSlack)) {
                     const float a = exp2_fast(m - mn);
                     l *= a;
 #pragma unroll
@@ -285,83 +328,91 @@ __global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 1 : 2) void q4_attend
                         l += w[4 * h + e];
                     }
                 const u4 pt = u4{pack2<false>(w[0], w[1]), pack2<false>(w[2], w[3]), pack2<false>(w[4], w[5]), pack2<false>(w[6], w[7])};
+                __builtin_amdgcn_sched_barrier(0);
+                if (more) wait_loads<S::NI>();
+                else wait_loads<0>();
+                __builtin_amdgcn_sched_barrier(0);
+                uint32_t vc[8][S::VW], vsm[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const int row = 16 * (x >> 2) + 4 * (x & 3);             // (and quad)
+                    const char* at = vb + row * S::ROW;
+                    const int byte = S::VB * c16, place = ((byte >> 4) ^ spread4<D>((row & 15) + quad)) << 4 | (byte & 15);
+                    if constexpr (S::VB == 2) vc[x][0] = *reinterpret_cast<const uint16_t*>(at + place);
+                    else if constexpr (S::VB == 4) vc[x][0] = *reinterpret_cast<const uint32_t*>(at + place);
+                    else {
+                        const u2 w = *reinterpret_cast<const u2*>(at + place);
+                        vc[x][0] = w[0];
+                        vc[x][1] = w[1];
+                    }
+                    vsm[x] = *reinterpret_cast<const uint32_t*>(vsb + row * (CPR * 4));
+                }
+                wait_lds();
+                if (more) load(i + 1, VALUES);
+                __builtin_amdgcn_sched_barrier(0);
                 // ---- O^T += V^T P^T: column VD c16 + d of the lane's eight keys, in the order in which the lanes hold P^T
                 h2 step[4], least[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const uint32_t s0 = vin ? t.vs[2 * x] : 0u, s1 = vin ? t.vs[2 * x + 1] : 0u;
+                    const uint32_t s0 = vin ? vsm[2 * x] : 0u, s1 = vin ? vsm[2 * x + 1] : 0u;
                     step[x] = bitcast<h2>(__builtin_amdgcn_perm(s1, s0, 0x05040100u));
                     least[x] = bitcast<h2>(__builtin_amdgcn_perm(s1, s0, 0x07060302u));
                 }
-                auto columns = [&](int byte, u4& even, u4& odd) {
+                if (edge) {
+                    // A weight of zero does not keep a group that is not finite out of a sum. Such a group (its values
+                    // lie between those of its codes 0 and 15) is left out here, and what rows see of it is
+                    // NaN: counted by a product of marks, of the keys in the lane's columns and of what its row sees.
+                    uint32_t bad[4];
+                    bool any = false;
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        const u2 y = values_of_pair(t.v[2 * x][byte / 4], t.v[2 * x + 1][byte / 4], byte % 4, step[x], least[x]);
-                        even[x] = y[0];
-                        odd[x] = y[1];
+                        const h2 most = __builtin_elementwise_fma(bitcast<h2>(0x4b804b80u), step[x], least[x]);
+                        const uint32_t a = bitcast<uint32_t>(most), c = bitcast<uint32_t>(least[x]);
+                        const bool lo = (a & 0x7c00u) == 0x7c00u || (c & 0x7c00u) == 0x7c00u;
+                        const bool hi = (a & 0x7c000000u) == 0x7c000000u || (c & 0x7c000000u) == 0x7c000000u;
+                        bad[x] = (lo ? 0x3c00u : 0u) | (hi ? 0x3c000000u : 0u);
+                        any |= lo || hi;
                     }
-                };
-                auto mma = [&](u4 a, f4 c) { return mfma16(bitcast<h8>(a), bitcast<h8>(pt), c); };
-                bool apart = false;
-                if (edge) {
+                    if (__any(any)) {
+                        u4 sees;
 #pragma unroll
-                    for (int y = 0; y < VD / 2; ++y) {
-                        u4 e, o;
-                        columns(y, e, o);
+                        for (int x = 0; x < 4; ++x) {
+                            uint32_t mark[2];
 #pragma unroll
-                        for (int x = 0; x < 4; x += 2) apart |= not_finite<false>(u2{e[x], e[x + 1]}) || not_finite<false>(u2{o[x], o[x + 1]});
-                    }
-                    apart = __any(apart);
-                }
-                if (!apart) {
-#pragma unroll
-                    for (int y = 0; y < VD / 2; ++y) {
-                        u4 e, o;
-                        columns(y, e, o);
-                        acc[2 * y] = mma(e, acc[2 * y]);
-                        acc[2 * y + 1] = mma(o, acc[2 * y + 1]);
-                    }
-                } else {
-                    // (key 16 h + 4 q + e of the tile is value 4 h + e of the lanes of quad q)
-#pragma clang loop unroll(disable)
-                    for (int x = 0; x < KT; ++x) {
-                        const bool sees = (first + x >= klo || first + x < p.sinks) && first + x <= khi;
-                        const int key = x >> 4 << 2 | (x & 3);
-                        const bool lanes = quad == (x >> 2 & 3);
-#pragma unroll
-                        for (int y = 0; y < VD / 2; ++y) {
-                            u4 e, o;
-                            columns(y, e, o);
-#pragma unroll
-                            for (int z = 0; z < 2; ++z) {
-                                const u4 a = z ? o : e;
-                                const f4 r = mma(lone(u2{a[0], a[1]}, u2{a[2], a[3]}, key, lanes), f4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) acc[2 * y + z][q] += sees ? r[q] : 0.f;
+                            for (int y = 0; y < 2; ++y) {
+                                const int key = first + 16 * (x >> 1) + 4 * (2 * (x & 1) + y) + quad;
+                                mark[y] = visible(key) ? 0x3c00u : 0u;
                             }
-                            __builtin_amdgcn_sched_barrier(0);
+                            sees[x] = mark[0] | mark[1] << 16;
+                            const uint32_t keep = (bad[x] & 0x3c00u ? 0u : 0xffffu) | (bad[x] >> 16 ? 0u : 0xffff0000u);
+                            step[x] = bitcast<h2>(bitcast<uint32_t>(step[x]) & keep);
+                            least[x] = bitcast<h2>(bitcast<uint32_t>(least[x]) & keep);
                         }
+                        const f4 seen = mfma16(bitcast<h8>(u4{bad[0], bad[1], bad[2], bad[3]}), bitcast<h8>(sees), f4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                        for (int d = 0; d < VD; ++d)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[d][e] = seen[e] > 0.f ? __builtin_nanf("") : acc[d][e];
                     }
                 }
-            };
-            for (int i = 0; i < count; i += 2) {
-                if (i + 1 < count) load(i + 1, tb);
-                __builtin_amdgcn_sched_barrier(0);
-                compute(i, ta);
-                if (i + 1 >= count) break;
-                __builtin_amdgcn_sched_barrier(0);
-                if (i + 2 < count) {
-                    if (((i + 2) & 31) == 0) batch(i + 2);
-                    load(i + 2, ta);
+#pragma unroll
+                for (int y = 0; y < VD / 2; ++y) {
+                    u4 even, odd;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const u2 w = values_of_pair(vc[2 * x][y / 4], vc[2 * x + 1][y / 4], y % 4, step[x], least[x], mg);
+                        even[x] = w[0];
+                        odd[x] = w[1];
+                    }
+                    acc[2 * y] = mfma16(bitcast<h8>(even), bitcast<h8>(pt), acc[2 * y]);
+                    acc[2 * y + 1] = mfma16(bitcast<h8>(odd), bitcast<h8>(pt), acc[2 * y + 1]);
                 }
-                __builtin_amdgcn_sched_barrier(0);
-                compute(i + 1, tb);
-                __builtin_amdgcn_sched_barrier(0);
             }
             it += (uint32_t)tiles;
 
-            // ---- join the waves
+            // ---- join the waves (a wave's outputs lie where its codes did)
             {
+                const int c16 = here(lane) & 15, quad = here(lane) >> 4;
                 const float ls = sum_quarters(l);
                 if (quad == 0) {
                     lds_m[wave][c16] = m;
@@ -372,11 +423,11 @@ __global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 1 : 2) void q4_attend
                 for (int e = 0; e < 4; ++e)
 #pragma unroll
                     for (int d = 0; d < VD; d += 4)
-                        *reinterpret_cast<f4*>(lds_o[wave] + c16 * (4 * D) + (((VD / 4 * (4 * quad + e) + d / 4) ^ c16) << 4)) =
+                        *reinterpret_cast<f4*>(lds[wave] + c16 * (4 * D) + (((VD / 4 * (4 * quad + e) + d / 4) ^ c16) << 4)) =
                             f4{acc[d][e], acc[d + 1][e], acc[d + 2][e], acc[d + 3][e]};
             }
-            finish<D, BF, WV>(p, sh, s, Segment{before + pair * (uint32_t)s.nt, tile0, tiles, head, row0, rows, pos0}, lds_o[0],
-                              ROWS * 4 * D, lds_m[0], lds_l[0], &s_last);
+            finish<D, BF, WV>(args_again(), sh, s, Segment{before + pair * (uint32_t)s.nt, tile0, tiles, head, row0, rows, pos0}, lds[0],
+                              S::WAVE, lds_m[0], lds_l[0], &s_last);
             __syncthreads();    // the buffers are free for the next segment
         }
         before += pairs * (uint32_t)s.nt;

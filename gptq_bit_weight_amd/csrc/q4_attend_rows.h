@@ -134,8 +134,8 @@ __device__ __forceinline__ void finish(const Args& p, const Share& sh, const Spa
                                        const float* lds_m, const float* lds_l, int* s_last)
 {
     constexpr int NT = 64 * WV, UNITS = ROWS * (D / 4), UPT = UNITS < NT ? 1 : UNITS / NT;   // four values of a row each
-    static_assert(UNITS % NT == 0 || NT % UNITS == 0, "whole rounds");
-    const int tid = threadIdx.x;
+    static_assert(UNITS % NT == 0 || UNITS < NT, "whole rounds");
+    const int tid = here((int)threadIdx.x);
     __syncthreads();
     const bool whole = g.tile0 == 0 && g.tiles == s.nt;
     // (workgroups there are, whatever `starts` says)

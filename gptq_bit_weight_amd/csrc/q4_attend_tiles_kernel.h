@@ -292,6 +292,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
         }
         x.scale = *reinterpret_cast<const uint32_t*>(scale_at + (so + pscol));
     };
+    const q4cache4::Magic magic = q4cache4::magic();
     auto put = [&](const Piece& x, auto values_tag, int stage) {
         constexpr bool values = decltype(values_tag)::value;
         char* to = (values ? lds_v[0] : lds_k[0]) + stage * (KT * PITCH) + prow * PITCH;
@@ -299,7 +300,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
         const h2 step = q4cache4::both(sm), least = q4cache4::both(sm >> 16);
 #pragma unroll
         for (int e = 0; e < PD / 8; ++e) {
-            const u4 w = q4cache4::values8(x.code[e], step, least);
+            const u4 w = q4cache4::values8(x.code[e], step, least, magic);
             *reinterpret_cast<u4*>(to + (((pdim / 8 + e) ^ spread<D>(prow)) << 4)) = values ? q4cache4::own_order(w) : w;
         }
     };
@@ -417,10 +418,6 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
                 const u2 a1 = read_tr(va[1][d] + stage * STAGE + s * 16 * PITCH);
                 acc[d] = mma(u4{a0[0], a0[1], a1[0], a1[1]}, pt[s], acc[d]);
             }
-    };
-    auto wait_lds = [&]() {                    // (what this wave wrote is there before the others pass the barrier)
-        __builtin_amdgcn_sched_barrier(0);
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     };
     auto barrier = [&]() {
         __builtin_amdgcn_sched_barrier(0);

@@ -23,22 +23,34 @@ __device__ __forceinline__ h2 both(uint32_t half)
     return bitcast<h2>((half & 0xffffu) * 0x00010001u);
 }
 
-// (codes in bits 0..3 and 16..19; in bits 4..7 and 20..23)
-__device__ __forceinline__ uint32_t value_low(uint32_t w, h2 step, h2 least)
+// The constants that codes are or-ed into, 1024 and 64 in both halves. (One v_and_or_b32
+// takes its mask from a scalar register and this from a vector one; the compiler must not see the values.)
+struct Magic {
+    uint32_t low, high;
+};
+__device__ __forceinline__ Magic magic()
 {
-    const h2 c = bitcast<h2>((w & 0x000f000fu) | 0x64006400u) - bitcast<h2>(0x64006400u);
+    Magic m{0x64006400u, 0x54005400u};
+    asm volatile("" : "+v"(m.low), "+v"(m.high));
+    return m;
+}
+
+// (codes in bits 0..3 and 16..19; in bits 4..7 and 20..23)
+__device__ __forceinline__ uint32_t value_low(uint32_t w, h2 step, h2 least, const Magic& g)
+{
+    const h2 c = bitcast<h2>(and_or(w, 0x000f000fu, g.low)) - bitcast<h2>(0x64006400u);
     return bitcast<uint32_t>(__builtin_elementwise_fma(c, step, least));
 }
-__device__ __forceinline__ uint32_t value_high(uint32_t w, h2 step, h2 least)
+__device__ __forceinline__ uint32_t value_high(uint32_t w, h2 step, h2 least, const Magic& g)
 {
-    const h2 c = bitcast<h2>((w & 0x00f000f0u) | 0x54005400u) - bitcast<h2>(0x54005400u);
+    const h2 c = bitcast<h2>(and_or(w, 0x00f000f0u, g.high)) - bitcast<h2>(0x54005400u);
     return bitcast<uint32_t>(__builtin_elementwise_fma(c, step, least));
 }
 
 // A word's eight values, in the order 0 4, 1 5, 2 6, 3 7.
-__device__ __forceinline__ u4 values8(uint32_t w, h2 step, h2 least)
+__device__ __forceinline__ u4 values8(uint32_t w, h2 step, h2 least, const Magic& g)
 {
-    return u4{value_low(w, step, least), value_high(w, step, least), value_low(w >> 8, step, least), value_high(w >> 8, step, least)};
+    return u4{value_low(w, step, least, g), value_high(w, step, least, g), value_low(w >> 8, step, least, g), value_high(w >> 8, step, least, g)};
 }
 
 // Eight 16-bit values in that order.
@@ -56,10 +68,10 @@ __device__ __forceinline__ u4 own_order(u4 x)
 
 // Two rows' values of byte b of a word of each: its first (even) and second (odd)
 // column, in the low half the first row's, with the rows' steps and least values in pairs.
-__device__ __forceinline__ u2 values_of_pair(uint32_t w0, uint32_t w1, int b, h2 step, h2 least)
+__device__ __forceinline__ u2 values_of_pair(uint32_t w0, uint32_t w1, int b, h2 step, h2 least, const Magic& g)
 {
     const uint32_t x = __builtin_amdgcn_perm(w1, w0, 0x0c040c00u + 0x00010001u * (uint32_t)b);
-    return u2{value_low(x, step, least), value_high(x, step, least)};
+    return u2{value_low(x, step, least, g), value_high(x, step, least, g)};
 }
 
 // Queries of bfloat16 as binary16: a row is multiplied by the power of two that brings its
