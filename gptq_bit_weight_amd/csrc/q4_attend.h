@@ -164,7 +164,7 @@ template <bool BF>
 __device__ __forceinline__ uint32_t pack2(float a, float b)
 {
     if constexpr (BF) return pack_bf16(a, b);
-    else return (uint32_t)f32_to_f16_bits(a) | (uint32_t)f32_to_f16_bits(b) << 16;
+    else return bitcast<uint32_t>(__builtin_convertvector(ff2{a, b}, h2));
 }
 
 // Maximum over the lanes l, l ^ 32 (and l ^ 16).

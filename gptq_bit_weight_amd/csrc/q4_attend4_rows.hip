@@ -37,15 +37,15 @@ constexpr float kSlack = 8.f;    // log2 of the growth of a maximum that is let 
 
 template <int D>
 struct Shape {
-    static constexpr int WV = D == 256 ? 8 : 12;       // waves of a workgroup
+    static constexpr int WV = D == 256 ? 4 : 8;       // waves of a workgroup
     static constexpr int ROW = D / 2;                  // bytes of a row of codes
     static constexpr int CPR = D / 32;                 // pieces of 16 bytes of it, and scales of it in LDS (one for 32 values)
     static constexpr int RPI = 64 / CPR > 16 ? 16 : 64 / CPR;      // rows that one direct load fills
     static constexpr int NL = 16 / RPI;                // direct loads of 16 rows of codes; of scales as many
     static constexpr int NI = 4 * NL;                  // and of a tile's keys (or values)
     static constexpr int CODES = KT * ROW, SCALES = KT * CPR * 4, TILE = 2 * (CODES + SCALES);
-    static constexpr int OUT = ROWS * 4 * D;           // a wave's outputs take the same place in the end
-    static constexpr int WAVE = OUT > TILE ? OUT : TILE;
+    static constexpr int NS = D == 256 ? 1 : 2;        // tiles of a wave in LDS
+    static constexpr int OUT = ROWS * 4 * D;           // bytes of its outputs
     static constexpr int KS = D / 32;                  // k-steps of the scores: words of a lane's piece of a key
     static constexpr int KG = D == 256 ? 2 : 1;        // scales of that piece
     static constexpr int VD = D / 16;                  // columns of a lane's piece of a value row
@@ -74,7 +74,8 @@ __global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 2 : 3) void q4_attend
 {
     using S = Shape<D>;
     constexpr int WV = S::WV, KS = S::KS, KG = S::KG, VD = S::VD, NL = S::NL, CPR = S::CPR;
-    __shared__ __attribute__((aligned(1024))) char lds[WV][S::WAVE];
+    __shared__ __attribute__((aligned(1024))) char lds[WV][S::NS * S::TILE];
+    __shared__ __attribute__((aligned(1024))) char lds_o[WV][S::OUT];
     __shared__ float lds_m[WV][ROWS], lds_l[WV][ROWS];
     __shared__ int s_last;
 
@@ -105,105 +106,129 @@ __global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 2 : 3) void q4_attend
     const char* ksb = lds[wave] + S::CODES + krow * (CPR * 4) + (D / 4 * quad / 32) * 4;
     const char* vb = lds[wave] + S::CODES + S::SCALES + quad * S::ROW;
     const char* vsb = lds[wave] + 2 * S::CODES + S::SCALES + quad * (CPR * 4) + (VD * c16 / 32) * 4;
-    bool kin[KG];
-#pragma unroll
-    for (int t = 0; t < KG; ++t) kin[t] = D / 4 * quad + 32 * t < p.dim;
-    const bool vin = VD * c16 < p.dim;
 
     const Magic mg = magic();
 
     Share sh;
-    if (!share_of<true, WV>(p, lane, sh)) return;
+    if (!share_of<true, WV, true>(p, lane, sh)) return;
     uint32_t it = sh.it;
-    uint32_t before = sh.before;
-    int b = sh.b;
-    for (; it < sh.end && b < p.B; ++b) {
-        const Span s = span_of<true>(p, sh, b);
-        const uint32_t pairs = (uint32_t)s.rt * (uint32_t)p.KV;
-        const uint32_t mine = min(sh.end, before + pairs * (uint32_t)s.nt);
-        while (it < mine) {
-            const uint32_t pair = (it - before) / (uint32_t)s.nt;
-            const int tile0 = (int)(it - before - pair * (uint32_t)s.nt);
-            const int tiles = min(s.nt - tile0, (int)(mine - it));
-            // (row tiles of one head side by side: they read the same keys)
-            const int head = (int)(pair / (uint32_t)s.rt), row0 = (int)(pair - (uint32_t)head * (uint32_t)s.rt) * ROWS;
-            const int rows = min(ROWS, s.r.n * p.g - row0);
-            const int pos0 = s.r.len - s.r.n;
+    // ---- the share's next piece of a row tile
+    Span s;
+    Segment g;
+    int b = sh.b;                              // its request
+    uint32_t before = sh.before;               // tiles of the requests before it
+    bool more = true;
+    auto next_segment = [&]() __attribute__((always_inline)) {
+        for (;; ++b) {
+            if (it >= sh.end || b >= p.B) {
+                more = false;
+                return;
+            }
+            s = span_of<true>(p, sh, b);
+            const uint32_t pairs = (uint32_t)s.rt * (uint32_t)p.KV, nt = sh.padded(s.nt);
+            const uint32_t after = before + pairs * nt;
+            if (it < after) {
+                const uint32_t pair = (it - before) / nt;
+                g.pair_at = before + pair * nt;
+                g.tile0 = (int)(it - g.pair_at);
+                g.tiles = min(s.nt - g.tile0, (int)(min(sh.end, after) - it));
+                // (row tiles of one head side by side: they read the same keys)
+                g.head = (int)(pair / (uint32_t)s.rt);
+                g.row0 = (int)(pair - (uint32_t)g.head * (uint32_t)s.rt) * ROWS;
+                g.rows = min(ROWS, s.r.n * p.g - g.row0);
+                g.pos0 = s.r.len - s.r.n;
+                it = g.tile0 + g.tiles == s.nt ? g.pair_at + nt : it + (uint32_t)g.tiles;
+                return;
+            }
+            before = after;
+        }
+    };
 
-            // ---- the wave's tiles: tile0 + wave, + WV, ...
-            const int count = (tiles - wave + WV - 1) / WV;      // (0 or less: none)
-            const int last_key = max(s.r.len - 1, 0), last_block = last_key >> 4;
-            // addresses of the 16-row block that lane l / 2 steps on, half l % 2 (one load of
-            // page numbers for 32 tiles)
-            const char *kat = nullptr, *ksat = nullptr, *vat = nullptr, *vsat = nullptr;
-            auto locate = [&](int key) {
-                const Args& a = args_again();
-                const int slot = (int)q4::fast_div((uint32_t)key, a.div_page);
-                const long long page = min((uint32_t)a.table[(long long)b * a.table_stride + slot], (uint32_t)a.pages - 1u);
-                const long long row = key - slot * a.page_size;
-                kat = a.k4.at + head * a.k4.head + page * a.k4.page + row * a.k4.row;
-                ksat = a.k4.scale + head * a.k4.scale_head + page * a.k4.scale_page + row * a.k4.scale_row;
-                vat = a.v4.at + head * a.v4.head + page * a.v4.page + row * a.v4.row;
-                vsat = a.v4.scale + head * a.v4.scale_head + page * a.v4.scale_page + row * a.v4.scale_row;
-            };
-            auto batch = [&](int i) {
-                if constexpr (PG) {
-                    const int at = here(lane), tile = tile0 + wave + WV * (i + (at >> 1));
-                    locate(16 * min(seen_block<true>(p, s, s.key_of(tile) / 16 + (at & 1)), last_block));
-                }
-            };
-            auto at_lane = [](const char* p, int from) {
-                const uint64_t v = reinterpret_cast<uint64_t>(p);
-                const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)v, from), hi = (uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), from);
-                return reinterpret_cast<const char*>((uint64_t)hi << 32 | lo);
-            };
-            auto load = [&](int i, auto values_tag) {
-                constexpr bool values = decltype(values_tag)::value;
-                const int first = s.key_of(tile0 + wave + WV * i);
-                const uint32_t to = own + (values ? S::CODES + S::SCALES : 0);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
+    // ---- the wave's tiles of it: tile0 + wave, + WV, ... (0 or less: none)
+    auto count_of = [&]() { return (g.tiles - wave + WV - 1) / WV; };
+    auto last_key = [&]() { return max(s.r.len - 1, 0); };
+                // addresses of the 16-row block that lane l / 2 steps on, half l % 2 (one load of
+                // page numbers for 32 tiles)
+                const char *kat = nullptr, *ksat = nullptr, *vat = nullptr, *vsat = nullptr;
+                auto locate = [&](int key) __attribute__((always_inline)) {
+                    const Args& a = args_again();
+                    const int slot = (int)q4::fast_div((uint32_t)key, a.div_page);
+                    const long long page = min((uint32_t)a.table[(long long)b * a.table_stride + slot], (uint32_t)a.pages - 1u);
+                    const long long row = key - slot * a.page_size;
+                    kat = a.k4.at + g.head * a.k4.head + page * a.k4.page + row * a.k4.row;
+                    ksat = a.k4.scale + g.head * a.k4.scale_head + page * a.k4.scale_page + row * a.k4.scale_row;
+                    vat = a.v4.at + g.head * a.v4.head + page * a.v4.page + row * a.v4.row;
+                    vsat = a.v4.scale + g.head * a.v4.scale_head + page * a.v4.scale_page + row * a.v4.scale_row;
+                };
+                auto batch = [&](int i) __attribute__((always_inline)) {
                     if constexpr (PG) {
-                        const int from = 2 * (i & 31) + h;
-                        const char *base = at_lane(values ? vat : kat, from), *scale_base = at_lane(values ? vsat : ksat, from);
-                        // rows past the last key repeat it (nothing unwritten is read)
-                        const int limit = last_key - 16 * min(seen_block<true>(p, s, (first >> 4) + h), last_block);
-#pragma unroll
-                        for (int e = 0; e < NL; ++e) {
-                            uint32_t at[1] = {values ? voff[e] : koff[e]}, sat = values ? vsoff[e] : ksoff[e];
-                            if (limit < 15) {
-                                const Side& side = values ? args_again().v4 : args_again().k4;
-                                const int row = e * S::RPI + here(lane) / CPR, back = row - min(row, limit);
-                                at[0] -= (uint32_t)(back * side.row);
-                                sat -= (uint32_t)(back * side.scale_row);
+                        const int at = here(lane), tile = g.tile0 + wave + WV * (i + (at >> 1));
+                        locate(16 * min(seen_block<true>(p, s, s.key_of(tile) / 16 + (at & 1)), last_key() >> 4));
+                    }
+                };
+                auto at_lane = [](const char* p, int from) {
+                    const uint64_t v = reinterpret_cast<uint64_t>(p);
+                    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)v, from), hi = (uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), from);
+                    return reinterpret_cast<const char*>((uint64_t)hi << 32 | lo);
+                };
+                auto load = [&](int i, auto values_tag, int stage) __attribute__((always_inline)) {
+                    constexpr bool values = decltype(values_tag)::value;
+                    const int first = s.key_of(g.tile0 + wave + WV * i);
+                    const uint32_t to = own + (uint32_t)(stage * S::TILE + (values ? S::CODES + S::SCALES : 0));
+    #pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if constexpr (PG) {
+                            const int from = 2 * (i & 31) + h;
+                            const char *base = at_lane(values ? vat : kat, from), *scale_base = at_lane(values ? vsat : ksat, from);
+                            // rows past the last key repeat it (nothing unwritten is read)
+                            const int limit = last_key() - 16 * min(seen_block<true>(p, s, (first >> 4) + h), last_key() >> 4);
+    #pragma unroll
+                            for (int e = 0; e < NL; ++e) {
+                                uint32_t at[1] = {values ? voff[e] : koff[e]}, sat = values ? vsoff[e] : ksoff[e];
+                                if (limit < 15) {
+                                    const Side& side = values ? args_again().v4 : args_again().k4;
+                                    const int row = e * S::RPI + here(lane) / CPR, back = row - min(row, limit);
+                                    at[0] -= (uint32_t)(back * side.row);
+                                    sat -= (uint32_t)(back * side.scale_row);
+                                }
+                                if (loads) {
+                                    dma<1>(base, at, to + (uint32_t)(h * NL + e) * (S::RPI * S::ROW));
+                                    dma_words(scale_base, sat, to + S::CODES + (uint32_t)(h * NL + e) * (S::RPI * CPR * 4));
+                                }
                             }
-                            if (loads) {
-                                dma<1>(base, at, to + (uint32_t)(h * NL + e) * (S::RPI * S::ROW));
-                                dma_words(scale_base, sat, to + S::CODES + (uint32_t)(h * NL + e) * (S::RPI * CPR * 4));
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < NL; ++e) {
-                            const int row = e * S::RPI + lrow;
-                            locate(min(seen_key<true>(p, s, first + 16 * h + (row & 15)), last_key));
-                            const int c = column(lpiece ^ spread4<D>(row)) * 16, sc = (32 * column(lpiece) >> p.group_shift) * 4;
-                            if (loads) {
-                                dma_lane((values ? vat : kat) + c, to + (uint32_t)(h * NL + e) * (S::RPI * S::ROW));
-                                dma_words_lane((values ? vsat : ksat) + sc, to + S::CODES + (uint32_t)(h * NL + e) * (S::RPI * CPR * 4));
+                        } else {
+    #pragma unroll
+                            for (int e = 0; e < NL; ++e) {
+                                const int row = e * S::RPI + lrow;
+                                locate(min(seen_key<true>(p, s, first + 16 * h + (row & 15)), last_key()));
+                                const int c = column(lpiece ^ spread4<D>(row)) * 16, sc = (32 * column(lpiece) >> p.group_shift) * 4;
+                                if (loads) {
+                                    dma_lane((values ? vat : kat) + c, to + (uint32_t)(h * NL + e) * (S::RPI * S::ROW));
+                                    dma_words_lane((values ? vsat : ksat) + sc, to + S::CODES + (uint32_t)(h * NL + e) * (S::RPI * CPR * 4));
+                                }
                             }
                         }
                     }
-                }
-            };
-            constexpr std::false_type KEYS;
-            constexpr std::true_type VALUES;
-            if (count > 0) {
-                batch(0);
-                load(0, KEYS);
-                load(0, VALUES);
+                };
+    constexpr std::false_type KEYS;
+    constexpr std::true_type VALUES;
+    auto begin = [&]() __attribute__((always_inline)) {
+        const int count = count_of();
+        if (count <= 0) return;
+        batch(0);
+#pragma unroll
+        for (int i = 0; i < S::NS; ++i)
+            if (i < count) {
+                load(i, KEYS, i);
+                load(i, VALUES, i);
             }
+    };
 
+    next_segment();
+    if (more) begin();
+    while (more) {
+            const int count = count_of();
+            const int row0 = g.row0, rows = g.rows, pos0 = g.pos0, head = g.head;
             // ---- queries: lane holds row c16, values D / 4 quad + 8 ks .. in the order of the unpacked codes
             u4 qf[KS];
             int khi;                           // the row's last visible key (-1: a row that is none)
@@ -248,17 +273,28 @@ __global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 2 : 3) void q4_attend
             auto visible = [&](int key) { return (key > khi - back || key < p.sinks) && key <= khi; };
             const int all_lo = p.window ? pos0 + (int)q4::fast_div((uint32_t)(row0 + rows - 1), p.div_g) - p.window + 1 : 0;
 
-            for (int i = 0; i < count; ++i) {
-                const bool more = i + 1 < count;
-                const int first = s.key_of(tile0 + wave + WV * i);
+            // Tile i, in stage i % NS; the tile NS further on is asked for into the same stage, its keys as soon as
+            // these keys are in registers, its values when these values are.
+            auto step = [&](auto stage_tag, int i) __attribute__((always_inline)) {
+                constexpr int ST = decltype(stage_tag)::value;
+                const int after = count - 1 - i;       // tiles after this one
+                const bool more = after >= S::NS;
+                const int first = s.key_of(g.tile0 + wave + WV * i);
+                // (the waves of a SIMD would be served in the order of their age, and the oldest be done when
+                // the youngest has half of its tiles left: who has more of them left goes first)
+                if (4 * after >= 3 * count) __builtin_amdgcn_s_setprio(3);
+                else if (2 * after >= count) __builtin_amdgcn_s_setprio(2);
+                else if (4 * after >= count) __builtin_amdgcn_s_setprio(1);
+                else __builtin_amdgcn_s_setprio(0);
                 __builtin_amdgcn_sched_barrier(0);
-                // the keys have landed (the values' loads, issued later, may be out)
-                wait_loads<S::NI>();
+                // the keys have landed (what was issued later may be out: the values, and the next tiles)
+                if (S::NS == 2 && after >= 1) wait_loads<3 * S::NI>();
+                else wait_loads<S::NI>();
                 __builtin_amdgcn_sched_barrier(0);
                 uint32_t kc[2][KS], ksm[2][KG];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const char* at = kb + h * 16 * S::ROW;
+                    const char* at = kb + ST * S::TILE + h * 16 * S::ROW;
                     if constexpr (D == 64) {
                         const u2 w = *reinterpret_cast<const u2*>(at + (((quad >> 1) ^ spread4<D>(krow)) << 4) + (quad & 1) * 8);
                         kc[h][0] = w[0];
@@ -272,12 +308,12 @@ __global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 2 : 3) void q4_attend
                         }
                     }
 #pragma unroll
-                    for (int t = 0; t < KG; ++t) ksm[h][t] = *reinterpret_cast<const uint32_t*>(ksb + h * 16 * CPR * 4 + 4 * t);
+                    for (int t = 0; t < KG; ++t) ksm[h][t] = *reinterpret_cast<const uint32_t*>(ksb + ST * S::TILE + h * 16 * CPR * 4 + 4 * t);
                 }
                 wait_lds();
                 if (more) {
-                    if (((i + 1) & 31) == 0) batch(i + 1);
-                    load(i + 1, KEYS);
+                    if (((i + S::NS) & 31) == 0) batch(i + S::NS);
+                    load(i + S::NS, KEYS, ST);
                 }
                 __builtin_amdgcn_sched_barrier(0);
                 f4 sc[2] = {f4{0.f, 0.f, 0.f, 0.f}, f4{0.f, 0.f, 0.f, 0.f}};
@@ -285,8 +321,7 @@ __global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 2 : 3) void q4_attend
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int g = 0; g < KG; ++g) {
-                        const uint32_t sm = kin[g] ? ksm[h][g] : 0u;
-                        const h2 step = both(sm), least = both(sm >> 16);
+                        const h2 step = low_half(ksm[h][g]), least = high_half(ksm[h][g]);
 #pragma unroll
                         for (int e = 0; e < KS / KG; ++e) {
                             const int ks = g * (KS / KG) + e;
@@ -294,8 +329,6 @@ __global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 2 : 3) void q4_attend
                         }
                     }
                 // ---- softmax: lane holds keys first + 16 h + 4 e + quad of row c16
-                sc[0] *= scale;
-                sc[1] *= scale;
                 const bool edge = first + KT - 1 > all_hi || (first < all_lo && first + KT > p.sinks);
                 if (edge) {
 #pragma unroll
@@ -306,12 +339,12 @@ __global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 2 : 3) void q4_attend
                             sc[h][e] = visible(key) ? sc[h][e] : -INFINITY;
                         }
                 }
-                float top = kLow;
+                float top = sc[0][0];
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[h][e]);
-                const float mn = fmaxf(m, max_quarters(top) - lift<false>(kSlack));
+                const float mn = fmaxf(m, max_quarters(top) * scale - lift<false>(kSlack));
                 if (__any(mn > m + kSlack)) {
                     const float a = exp2_fast(m - mn);
                     l *= a;
@@ -324,19 +357,20 @@ __global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 2 : 3) void q4_attend
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        w[4 * h + e] = exp2_fast(sc[h][e] - m);
+                        w[4 * h + e] = exp2_fast(__builtin_fmaf(sc[h][e], scale, -m));
                         l += w[4 * h + e];
                     }
                 const u4 pt = u4{pack2<false>(w[0], w[1]), pack2<false>(w[2], w[3]), pack2<false>(w[4], w[5]), pack2<false>(w[6], w[7])};
                 __builtin_amdgcn_sched_barrier(0);
-                if (more) wait_loads<S::NI>();
+                if (more) wait_loads<(2 * S::NS - 1) * S::NI>();
+                else if (S::NS == 2 && after == 1) wait_loads<2 * S::NI>();
                 else wait_loads<0>();
                 __builtin_amdgcn_sched_barrier(0);
                 uint32_t vc[8][S::VW], vsm[8];
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
                     const int row = 16 * (x >> 2) + 4 * (x & 3);             // (and quad)
-                    const char* at = vb + row * S::ROW;
+                    const char* at = vb + ST * S::TILE + row * S::ROW;
                     const int byte = S::VB * c16, place = ((byte >> 4) ^ spread4<D>((row & 15) + quad)) << 4 | (byte & 15);
                     if constexpr (S::VB == 2) vc[x][0] = *reinterpret_cast<const uint16_t*>(at + place);
                     else if constexpr (S::VB == 4) vc[x][0] = *reinterpret_cast<const uint32_t*>(at + place);
@@ -345,18 +379,17 @@ __global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 2 : 3) void q4_attend
                         vc[x][0] = w[0];
                         vc[x][1] = w[1];
                     }
-                    vsm[x] = *reinterpret_cast<const uint32_t*>(vsb + row * (CPR * 4));
+                    vsm[x] = *reinterpret_cast<const uint32_t*>(vsb + ST * S::TILE + row * (CPR * 4));
                 }
                 wait_lds();
-                if (more) load(i + 1, VALUES);
+                if (more) load(i + S::NS, VALUES, ST);
                 __builtin_amdgcn_sched_barrier(0);
                 // ---- O^T += V^T P^T: column VD c16 + d of the lane's eight keys, in the order in which the lanes hold P^T
                 h2 step[4], least[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const uint32_t s0 = vin ? vsm[2 * x] : 0u, s1 = vin ? vsm[2 * x + 1] : 0u;
-                    step[x] = bitcast<h2>(__builtin_amdgcn_perm(s1, s0, 0x05040100u));
-                    least[x] = bitcast<h2>(__builtin_amdgcn_perm(s1, s0, 0x07060302u));
+                    step[x] = bitcast<h2>(__builtin_amdgcn_perm(vsm[2 * x + 1], vsm[2 * x], 0x05040100u));
+                    least[x] = bitcast<h2>(__builtin_amdgcn_perm(vsm[2 * x + 1], vsm[2 * x], 0x07060302u));
                 }
                 if (edge) {
                     // A weight of zero does not keep a group that is not finite out of a sum. Such a group (its values
@@ -407,10 +440,16 @@ __global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 2 : 3) void q4_attend
                     acc[2 * y] = mfma16(bitcast<h8>(even), bitcast<h8>(pt), acc[2 * y]);
                     acc[2 * y + 1] = mfma16(bitcast<h8>(odd), bitcast<h8>(pt), acc[2 * y + 1]);
                 }
+            };
+            for (int i = 0; i < count;) {
+                step(std::integral_constant<int, 0>{}, i);
+                if (++i >= count) break;
+                if constexpr (S::NS == 2) {
+                    step(std::integral_constant<int, 1>{}, i);
+                    ++i;
+                }
             }
-            it += (uint32_t)tiles;
-
-            // ---- join the waves (a wave's outputs lie where its codes did)
+            // ---- join the waves. The next piece's first tiles are asked for before.
             {
                 const int c16 = here(lane) & 15, quad = here(lane) >> 4;
                 const float ls = sum_quarters(l);
@@ -423,14 +462,15 @@ __global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 2 : 3) void q4_attend
                 for (int e = 0; e < 4; ++e)
 #pragma unroll
                     for (int d = 0; d < VD; d += 4)
-                        *reinterpret_cast<f4*>(lds[wave] + c16 * (4 * D) + (((VD / 4 * (4 * quad + e) + d / 4) ^ c16) << 4)) =
+                        *reinterpret_cast<f4*>(lds_o[wave] + c16 * (4 * D) + (((VD / 4 * (4 * quad + e) + d / 4) ^ c16) << 4)) =
                             f4{acc[d][e], acc[d + 1][e], acc[d + 2][e], acc[d + 3][e]};
             }
-            finish<D, BF, WV>(args_again(), sh, s, Segment{before + pair * (uint32_t)s.nt, tile0, tiles, head, row0, rows, pos0}, lds[0],
-                              S::WAVE, lds_m[0], lds_l[0], &s_last);
-            __syncthreads();    // the buffers are free for the next segment
-        }
-        before += pairs * (uint32_t)s.nt;
+            const Span s_done = s;
+            const Segment g_done = g;
+            next_segment();
+            if (more) begin();
+            finish<D, BF, WV, true>(args_again(), sh, s_done, g_done, lds_o[0], S::OUT, lds_m[0], lds_l[0], &s_last);
+            __syncthreads();    // the buffers are free for the next piece
     }
 }
 

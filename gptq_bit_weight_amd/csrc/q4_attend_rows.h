@@ -46,22 +46,27 @@ __device__ __forceinline__ int seen_block(const Args& p, const Span& s, int bloc
 }
 
 // A workgroup's range of all tiles: `it` up to `end`, in shares of `per`; it begins
-// in request b, which `before` tiles come before. (The first 64 requests stay in the
-// lanes: each look at them in memory is one more latency before the first key.)
+// in request b, which `before` tiles come before. A row tile's tiles count as the next multiple
+// of `pad`. (The first 64 requests stay in the lanes: each look at them in memory is one
+// more latency before the first key.)
 struct Share {
     Request first64;
-    uint32_t per, it, end, before;
+    uint32_t per, it, end, before, pad;
     int b;
+    __device__ __forceinline__ uint32_t padded(int tiles) const { return pad == 1 ? (uint32_t)tiles : ((uint32_t)tiles + pad - 1) / pad * pad; }
 };
 
 // (the lanes of a wave each look at a request; false: no work for this workgroup)
-template <bool SK, int WV>
+// EVEN: where there are workgroups enough, every row tile gets whole shares of its own, so that
+// no workgroup has pieces of two.
+template <bool SK, int WV, bool EVEN>
 __device__ __forceinline__ bool share_of(const Args& p, int lane, Share& sh)
 {
     auto request_at = [&](int b) { return b < p.B ? request(p, b) : Request{0, 0, 0}; };
+    sh.pad = 1;
     auto cost = [&](const Request& r) {        // (0 without tokens)
         const Span s = span<SK>(p, r);
-        return (uint32_t)s.rt * (uint32_t)p.KV * (uint32_t)s.nt;
+        return (uint32_t)s.rt * (uint32_t)p.KV * sh.padded(s.nt);
     };
     auto scan = [&](uint32_t v) {              // inclusive, over the lanes
 #pragma unroll
@@ -72,13 +77,26 @@ __device__ __forceinline__ bool share_of(const Args& p, int lane, Share& sh)
         return v;
     };
     sh.first64 = request_at(lane);
-    const uint32_t cost64 = scan(cost(sh.first64));
+    uint32_t cost64 = scan(cost(sh.first64));
     uint32_t total = (uint32_t)__builtin_amdgcn_readlane((int)cost64, 63);
     for (int b0 = 64; b0 < p.B; b0 += 64) total += (uint32_t)__builtin_amdgcn_readlane((int)scan(cost(request_at(b0 + lane))), 63);
     // equal shares, in whole rounds of the waves
     uint32_t per = (total + (uint32_t)p.workers - 1) / (uint32_t)p.workers;
     per = (max(per, (uint32_t)p.least) + WV - 1) / WV * WV;
     sh.per = per;
+    if constexpr (EVEN) {
+        auto shares = [&](const Request& r) {
+            const Span s = span<SK>(p, r);
+            return (uint32_t)s.rt * (uint32_t)p.KV * (((uint32_t)s.nt + per - 1) / per);
+        };
+        uint32_t n = (uint32_t)__builtin_amdgcn_readlane((int)scan(shares(sh.first64)), 63);
+        for (int b0 = 64; b0 < p.B; b0 += 64) n += (uint32_t)__builtin_amdgcn_readlane((int)scan(shares(request_at(b0 + lane))), 63);
+        if (n <= (uint32_t)p.workers) {
+            sh.pad = per;
+            total = n * per;
+            cost64 = scan(cost(sh.first64));
+        }
+    }
     sh.it = (uint32_t)blockIdx.x * per;
     sh.end = min(sh.it + per, total);
     if (sh.it >= sh.end) return false;
@@ -129,8 +147,8 @@ struct Segment {
 // tile. Else its partial result goes to a slot of the workgroup, and the last workgroup of the
 // row tile to arrive joins them in key order. Begins with a barrier; the caller has another
 // before it writes to the buffers again.
-template <int D, bool BF, int WV>
-__device__ __forceinline__ void finish(const Args& p, const Share& sh, const Span& s, const Segment& g, const char* out, int out_pitch,
+template <int D, bool BF, int WV, bool SPREAD>
+__device__ __forceinline__ void finish(const Args& p, const Share& sh, const Span& s, const Segment& g, char* out, int out_pitch,
                                        const float* lds_m, const float* lds_l, int* s_last)
 {
     constexpr int NT = 64 * WV, UNITS = ROWS * (D / 4), UPT = UNITS < NT ? 1 : UNITS / NT;   // four values of a row each
@@ -182,6 +200,65 @@ __device__ __forceinline__ void finish(const Args& p, const Share& sh, const Spa
             *s_last = __hip_atomic_fetch_add(&p.counters[wf], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)(wl - wf);
         __syncthreads();
         all_here = *s_last != 0;
+        if (SPREAD && all_here) {
+            // Unit `unit` (of `live` ones) of part `part` of the slots is lane unit + live part's, where there are
+            // lanes for several parts.
+            const int live = g.rows * (D / 4), parts = max(NT / live, 1), slots = wl - wf + 1;
+            for (int u0 = 0; u0 < live; u0 += NT) {
+                const int part = parts == 1 ? 0 : tid / live, unit = u0 + tid - part * live, row = unit / (D / 4);
+                const bool on = part < parts && unit < live;
+                const int w0 = wf + slots * part / parts, w1 = wf + slots * (part + 1) / parts;
+                float mm = kLow, ll = 0.f;
+                f4 v = f4{0.f, 0.f, 0.f, 0.f};
+                constexpr int FB = 4;      // slots whose loads are under way together
+                for (int w = w0; on && w < w1; w += FB) {
+                    float pm[FB], pl[FB];
+                    f4 po[FB];
+#pragma unroll
+                    for (int f = 0; f < FB; ++f) {
+                        const int x = min(w + f, w1 - 1);
+                        const uint32_t at = (uint32_t)(2 * x + (x == wf ? 1 : 0)) * (uint32_t)(SLOT * 4);
+                        const rsrc_t r = make_rsrc(p.slots, (uint32_t)(2 * p.workers * SLOT * 4));
+                        pm[f] = take4(r, at + (uint32_t)(ROWS * D + row) * 4u);
+                        pl[f] = take4(r, at + (uint32_t)(ROWS * D + ROWS + row) * 4u);
+                        po[f] = take16(r, at + (uint32_t)unit * 16u);
+                    }
+#pragma unroll
+                    for (int f = 0; f < FB; ++f) {
+                        if (w + f >= w1) continue;
+                        const float mn = fmaxf(mm, pm[f]);
+                        const float a = exp2_fast(mm - mn), c = exp2_fast(pm[f] - mn);
+                        ll = a * ll + c * pl[f];
+                        v = a * v + c * po[f];
+                        mm = mn;
+                    }
+                }
+                if (parts > 1) {
+                    f4* lv = reinterpret_cast<f4*>(out);
+                    float *lm = reinterpret_cast<float*>(out + NT * 16), *lsum = lm + NT;
+                    lv[tid] = v;
+                    lm[tid] = mm;
+                    lsum[tid] = ll;
+                    __syncthreads();
+                    for (int x = 1; part == 0 && x < parts; ++x) {
+                        const int at = tid + x * live;
+                        const float mn = fmaxf(mm, lm[at]);
+                        const float a = exp2_fast(mm - mn), c = exp2_fast(lm[at] - mn);
+                        ll = a * ll + c * lsum[at];
+                        v = a * v + c * lv[at];
+                        mm = mn;
+                    }
+                }
+                const int at = unit % (D / 4) * 4;
+                if (on && part == 0 && at < p.dim) {
+                    const int r = g.row0 + row, token = (int)q4::fast_div((uint32_t)r, p.div_g);
+                    const f4 y = output_of(v, ll, over_sum(ll, g.pos0 + token));
+                    store_row4<BF>(p.out + (s.r.start + token) * p.o_t + (g.head * p.g + r - token * p.g) * p.o_h + at, y, p.dim - at, p.store8);
+                }
+            }
+            if (tid == 0) __hip_atomic_store(&p.counters[wf], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            return;
+        }
         if (all_here) {
 #pragma unroll
             for (int u = 0; u < UPT; ++u) {

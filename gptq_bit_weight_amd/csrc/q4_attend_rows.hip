@@ -67,7 +67,7 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void q4_attend_rows_kernel(Ar
     }
 
     Share sh;
-    if (!share_of<SK, WV>(p, lane, sh)) return;
+    if (!share_of<SK, WV, false>(p, lane, sh)) return;
     uint32_t it = sh.it;
     uint32_t before = sh.before;
     int b = sh.b;
@@ -307,7 +307,7 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void q4_attend_rows_kernel(Ar
                 for (int d = 0; d < DT; ++d)
                     *reinterpret_cast<f4*>(lds_k[wave] + c16 * (4 * D) + (((4 * d + quad) ^ c16) << 4)) = acc[d];
             }
-            finish<D, BF, WV>(p, sh, s, Segment{before + pair * (uint32_t)s.nt, tile0, tiles, head, row0, rows, pos0}, lds_k[0],
+            finish<D, BF, WV, false>(p, sh, s, Segment{before + pair * (uint32_t)s.nt, tile0, tiles, head, row0, rows, pos0}, lds_k[0],
                               KT * PITCH, lds_m[0], lds_l[0], &s_last);
             __syncthreads();    // the buffers are free for the next segment
         }

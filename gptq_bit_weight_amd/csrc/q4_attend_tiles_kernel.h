@@ -297,7 +297,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
         constexpr bool values = decltype(values_tag)::value;
         char* to = (values ? lds_v[0] : lds_k[0]) + stage * (KT * PITCH) + prow * PITCH;
         const uint32_t sm = pin ? x.scale : 0u;
-        const h2 step = q4cache4::both(sm), least = q4cache4::both(sm >> 16);
+        const h2 step = q4cache4::low_half(sm), least = q4cache4::high_half(sm);
 #pragma unroll
         for (int e = 0; e < PD / 8; ++e) {
             const u4 w = q4cache4::values8(x.code[e], step, least, magic);

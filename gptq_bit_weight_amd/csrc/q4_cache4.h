@@ -18,9 +18,16 @@ using namespace q4dev;
 
 constexpr float kLargest = 65440.f;     // finite values beyond it are held as it: s 15 + m, with s rounded up, stays finite
 
-__device__ __forceinline__ h2 both(uint32_t half)
+// A half of a word in both halves (the packed instructions select it).
+__device__ __forceinline__ h2 low_half(uint32_t w)
 {
-    return bitcast<h2>((half & 0xffffu) * 0x00010001u);
+    const h2 v = bitcast<h2>(w);
+    return h2{v[0], v[0]};
+}
+__device__ __forceinline__ h2 high_half(uint32_t w)
+{
+    const h2 v = bitcast<h2>(w);
+    return h2{v[1], v[1]};
 }
 
 // The constants that codes are or-ed into, 1024 and 64 in both halves. (One v_and_or_b32

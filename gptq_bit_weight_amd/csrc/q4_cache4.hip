@@ -227,7 +227,7 @@ __global__ __launch_bounds__(NT) void q4_cache4_read_kernel(ReadArgs p)
             const uint32_t code = *reinterpret_cast<const uint32_t*>(c.at + page * c.page + h * c.head + r * c.row + 4 * piece);
             const uint32_t sm = *reinterpret_cast<const uint32_t*>(c.scale + page * c.scale_page + h * c.scale_head + r * c.scale_row +
                                                                    4 * (8 * piece >> p.group_shift));
-            w = own_order(values8(code, both(sm), both(sm >> 16), magic()));
+            w = own_order(values8(code, low_half(sm), high_half(sm), magic()));
         }
         uint16_t* to = (value ? p.v + t * p.v_t + h * p.v_h : p.k + t * p.k_t + h * p.k_h) + 8 * piece;
         if (p.wide) {
