@@ -33,18 +33,22 @@ namespace {
 using namespace q4attend;
 using namespace q4cache4;
 
+// A piece of a row tile takes 4 to 5 us beside its tiles (the first loads, the join), a tile of a
+// workgroup 0.5.
+constexpr int kExtra = 8;
+
 constexpr float kSlack = 8.f;    // log2 of the growth of a maximum that is let pass: a weight is at most 2^15
 
 template <int D>
 struct Shape {
-    static constexpr int WV = D == 256 ? 4 : 8;       // waves of a workgroup
     static constexpr int ROW = D / 2;                  // bytes of a row of codes
     static constexpr int CPR = D / 32;                 // pieces of 16 bytes of it, and scales of it in LDS (one for 32 values)
     static constexpr int RPI = 64 / CPR > 16 ? 16 : 64 / CPR;      // rows that one direct load fills
     static constexpr int NL = 16 / RPI;                // direct loads of 16 rows of codes; of scales as many
     static constexpr int NI = 4 * NL;                  // and of a tile's keys (or values)
     static constexpr int CODES = KT * ROW, SCALES = KT * CPR * 4, TILE = 2 * (CODES + SCALES);
-    static constexpr int NS = D == 256 ? 1 : 2;        // tiles of a wave in LDS
+    static constexpr int NS = 1;                       // tiles of a wave in LDS
+    static constexpr bool OVER = D == 256;             // a wave's outputs take the place of its tiles in the end
     static constexpr int OUT = ROWS * 4 * D;           // bytes of its outputs
     static constexpr int KS = D / 32;                  // k-steps of the scores: words of a lane's piece of a key
     static constexpr int KG = D == 256 ? 2 : 1;        // scales of that piece
@@ -69,13 +73,18 @@ __device__ __forceinline__ void dma_words_lane(const char* src, uint32_t dst)
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 4\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(dst) : "memory");
 }
 
-template <int D, bool BF, bool PG>
-__global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 2 : 3) void q4_attend4_rows_kernel(Args p)
+template <int D, bool BF, bool PG, int WV>
+__global__ __launch_bounds__(64 * WV, D == 256 ? 2 : 3) void q4_attend4_rows_kernel(Args p)
 {
     using S = Shape<D>;
-    constexpr int WV = S::WV, KS = S::KS, KG = S::KG, VD = S::VD, NL = S::NL, CPR = S::CPR;
-    __shared__ __attribute__((aligned(1024))) char lds[WV][S::NS * S::TILE];
-    __shared__ __attribute__((aligned(1024))) char lds_o[WV][S::OUT];
+    constexpr int KS = S::KS, KG = S::KG, VD = S::VD, NL = S::NL, CPR = S::CPR;
+    constexpr int WAVE = S::OVER && S::OUT > S::NS * S::TILE ? S::OUT : S::NS * S::TILE;
+    __shared__ __attribute__((aligned(1024))) char lds[WV][WAVE];
+    __shared__ __attribute__((aligned(1024))) char lds_other[S::OVER ? 1 : WV][S::OUT];
+    auto& lds_o = [&]() -> auto& {
+        if constexpr (S::OVER) return lds;
+        else return lds_other;
+    }();
     __shared__ float lds_m[WV][ROWS], lds_l[WV][ROWS];
     __shared__ int s_last;
 
@@ -110,7 +119,7 @@ __global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 2 : 3) void q4_attend
     const Magic mg = magic();
 
     Share sh;
-    if (!share_of<true, WV, true>(p, lane, sh)) return;
+    if (!share_of<true, WV, kExtra>(p, lane, sh)) return;
     uint32_t it = sh.it;
     // ---- the share's next piece of a row tile
     Span s;
@@ -125,19 +134,20 @@ __global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 2 : 3) void q4_attend
                 return;
             }
             s = span_of<true>(p, sh, b);
-            const uint32_t pairs = (uint32_t)s.rt * (uint32_t)p.KV, nt = sh.padded(s.nt);
+            const uint32_t pairs = (uint32_t)s.rt * (uint32_t)p.KV, nt = sh.counted(s.nt);
             const uint32_t after = before + pairs * nt;
-            if (it < after) {
-                const uint32_t pair = (it - before) / nt;
-                g.pair_at = before + pair * nt;
-                g.tile0 = (int)(it - g.pair_at);
-                g.tiles = min(s.nt - g.tile0, (int)(min(sh.end, after) - it));
+            while (it < after && it < sh.end) {
+                const uint32_t pair = (it - before) / nt, from = before + pair * nt;
+                g.pair_at = from + sh.extra;
+                g.tile0 = max((int)(it - g.pair_at), 0);
+                g.tiles = min((int)(min(sh.end, from + nt) - g.pair_at), s.nt) - g.tile0;
+                it = from + nt;
+                if (g.tiles <= 0) continue;        // (what comes before a row tile's first only)
                 // (row tiles of one head side by side: they read the same keys)
                 g.head = (int)(pair / (uint32_t)s.rt);
                 g.row0 = (int)(pair - (uint32_t)g.head * (uint32_t)s.rt) * ROWS;
                 g.rows = min(ROWS, s.r.n * p.g - g.row0);
                 g.pos0 = s.r.len - s.r.n;
-                it = g.tile0 + g.tiles == s.nt ? g.pair_at + nt : it + (uint32_t)g.tiles;
                 return;
             }
             before = after;
@@ -468,20 +478,21 @@ __global__ __launch_bounds__(64 * Shape<D>::WV, D == 256 ? 2 : 3) void q4_attend
             const Span s_done = s;
             const Segment g_done = g;
             next_segment();
-            if (more) begin();
-            finish<D, BF, WV, true>(args_again(), sh, s_done, g_done, lds_o[0], S::OUT, lds_m[0], lds_l[0], &s_last);
+            if (more && !S::OVER) begin();
+            finish<D, BF, WV, true>(args_again(), sh, s_done, g_done, lds_o[0], S::OVER ? WAVE : S::OUT, lds_m[0], lds_l[0], &s_last);
             __syncthreads();    // the buffers are free for the next piece
+            if (more && S::OVER) begin();
     }
 }
 
-template <int D>
+template <int D, int WV>
 hipError_t launch_rows(const Args& p, bool bf16, bool pg, hipStream_t stream)
 {
-    const dim3 grid(p.workers), block(64 * Shape<D>::WV);
-    if (bf16 && pg) hipLaunchKernelGGL((q4_attend4_rows_kernel<D, true, true>), grid, block, 0, stream, p);
-    else if (bf16) hipLaunchKernelGGL((q4_attend4_rows_kernel<D, true, false>), grid, block, 0, stream, p);
-    else if (pg) hipLaunchKernelGGL((q4_attend4_rows_kernel<D, false, true>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((q4_attend4_rows_kernel<D, false, false>), grid, block, 0, stream, p);
+    const dim3 grid(p.workers), block(64 * WV);
+    if (bf16 && pg) hipLaunchKernelGGL((q4_attend4_rows_kernel<D, true, true, WV>), grid, block, 0, stream, p);
+    else if (bf16) hipLaunchKernelGGL((q4_attend4_rows_kernel<D, true, false, WV>), grid, block, 0, stream, p);
+    else if (pg) hipLaunchKernelGGL((q4_attend4_rows_kernel<D, false, true, WV>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((q4_attend4_rows_kernel<D, false, false, WV>), grid, block, 0, stream, p);
     return hipGetLastError();
 }
 
@@ -489,12 +500,17 @@ hipError_t launch_rows(const Args& p, bool bf16, bool pg, hipStream_t stream)
 
 namespace q4 {
 
-hipError_t launch_attend4_rows(const q4attend::Args& p, bool bf16, bool pages_of_16, hipStream_t stream)
+hipError_t launch_attend4_rows(const q4attend::Args& p, bool bf16, bool pages_of_16, bool wide, hipStream_t stream)
 {
     if (p.dim < 32 || p.dim > 256 || p.dim % 32 || p.workers < 1) return hipErrorInvalidValue;
-    if (p.dim <= 64) return launch_rows<64>(p, bf16, pages_of_16, stream);
-    if (p.dim <= 128) return launch_rows<128>(p, bf16, pages_of_16, stream);
-    return launch_rows<256>(p, bf16, pages_of_16, stream);
+    if (wide) {
+        if (p.dim <= 64) return launch_rows<64, 8>(p, bf16, pages_of_16, stream);
+        if (p.dim <= 128) return launch_rows<128, 8>(p, bf16, pages_of_16, stream);
+        return launch_rows<256, 8>(p, bf16, pages_of_16, stream);
+    }
+    if (p.dim <= 64) return launch_rows<64, 4>(p, bf16, pages_of_16, stream);
+    if (p.dim <= 128) return launch_rows<128, 4>(p, bf16, pages_of_16, stream);
+    return launch_rows<256, 4>(p, bf16, pages_of_16, stream);
 }
 
 }  // namespace q4

@@ -13,7 +13,7 @@ hipError_t launch_attend_rows(const q4attend::Args& p, bool bf16, bool pages_of_
 
 hipError_t launch_attend_tiles(const q4attend::Args& p, int grid, bool bf16, bool pages_of_16, hipStream_t stream);
 
-hipError_t launch_attend4_rows(const q4attend::Args& p, bool bf16, bool pages_of_16, hipStream_t stream);
+hipError_t launch_attend4_rows(const q4attend::Args& p, bool bf16, bool pages_of_16, bool wide, hipStream_t stream);
 
 hipError_t launch_attend4_tiles(const q4attend::Args& p, int grid, bool bf16, bool pages_of_16, hipStream_t stream);
 
@@ -30,6 +30,7 @@ static_assert(kListAt + sizeof(q4attend::JoinList) <= kCounterBytes, "workspace"
 // The few-row kernel: rows of a tile, least tiles of a workgroup (of which there
 // is one a CU).
 constexpr int kFewRows = 16, kFewLeast = 4;
+constexpr int kFew4 = 2;
 size_t rows_bytes(int dim, int num_cu)
 {
     return kCounterBytes + (size_t)num_cu * 2 * kFewRows * (padded_dim(dim) + 2) * sizeof(float);
@@ -76,9 +77,9 @@ q4_status check_attend4(const q4_cache4* c, int heads, const char* who)
     return Q4_OK;
 }
 
-size_t workspace_bytes_of(int dim, int cu)
+size_t workspace_bytes_of(int dim, int cu, bool four)
 {
-    const size_t rows = rows_bytes(dim, cu), tiles = tiles_bytes(dim, cu);
+    const size_t rows = rows_bytes(dim, four ? kFew4 * cu : cu), tiles = tiles_bytes(dim, cu);
     return rows > tiles ? rows : tiles;
 }
 
@@ -168,9 +169,10 @@ q4_status attend(const char* who, q4attend::Args& p, const View* caches, int nca
     const bool many = mean_rows > 12;
     const int tile = many ? kTileRows : kFewRows;
     const long long row_tiles = (long long)a.tokens * g / tile + a.requests;
-    if (row_tiles * p.KV * (p.max_len / 32 + 2) >= (1LL << 31))
+    if (row_tiles * p.KV * (p.max_len / 32 + 2 + (a.four ? 8 : 0)) >= (1LL << 31))
         return fail(Q4_ERR_UNSUPPORTED, "%s: more than 2^31 tiles of keys", who);
-    p.workers = many ? tile_target(cu) : cu;
+    const bool wide = (long long)a.requests * p.KV * 16 <= cu;
+    p.workers = many ? tile_target(cu) : a.four && !wide ? kFew4 * cu : cu;
     p.least = many ? kTileLeast : kFewLeast;
     if (many) {
         const int keys = p.dim > 128 ? 32 : 64;
@@ -182,7 +184,7 @@ q4_status attend(const char* who, q4attend::Args& p, const View* caches, int nca
         if (p.window && most * keys <= kWholeKeys && enough) p.least = (int)most;
         p.unsplit = most <= p.least;
     }
-    const size_t need = many ? tiles_bytes(p.dim, cu) : rows_bytes(p.dim, cu);
+    const size_t need = many ? tiles_bytes(p.dim, cu) : rows_bytes(p.dim, p.workers);
     if (!a.workspace || a.workspace_bytes < need || !at16(a.workspace))
         return fail(Q4_ERR_INVALID_ARG, "%s: the workspace needs %zu bytes on a 16-byte boundary (%s_workspace)", who, need,
                     a.four ? "q4_attend4" : "q4_attend");
@@ -192,7 +194,7 @@ q4_status attend(const char* who, q4attend::Args& p, const View* caches, int nca
     // (most units there can be: a whole one each share of the work, a partial one each row tile and head)
     const int units = (int)(row_tiles * p.KV + p.workers);
     hipError_t e;
-    if (a.four) e = many ? launch_attend4_tiles(p, units, a.bf16, pg, stream) : launch_attend4_rows(p, a.bf16, pg, stream);
+    if (a.four) e = many ? launch_attend4_tiles(p, units, a.bf16, pg, stream) : launch_attend4_rows(p, a.bf16, pg, wide, stream);
     else e = many ? launch_attend_tiles(p, units, a.bf16, pg, stream) : launch_attend_rows(p, a.bf16, pg, stream);
     return e == hipSuccess ? Q4_OK : fail(Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
 }
@@ -206,7 +208,7 @@ size_t q4_attend_workspace(const q4_cache* c, int heads)
 {
     int dev = -1, cu = 0;
     if (q4::check_attend(c, heads, "q4_attend_workspace") != Q4_OK || q4::device_info(&dev, &cu) != Q4_OK) return 0;
-    return q4::workspace_bytes_of(c->dim, cu);
+    return q4::workspace_bytes_of(c->dim, cu, false);
 }
 
 q4_status q4_attend_ex(const q4_cache* c, const uint16_t* q, int64_t q_token, int64_t q_head, int heads, int tokens,
@@ -256,7 +258,7 @@ size_t q4_attend4_workspace(const q4_cache4* c, int heads)
 {
     int dev = -1, cu = 0;
     if (q4::check_attend4(c, heads, "q4_attend4_workspace") != Q4_OK || q4::device_info(&dev, &cu) != Q4_OK) return 0;
-    return q4::workspace_bytes_of(c->dim, cu);
+    return q4::workspace_bytes_of(c->dim, cu, true);
 }
 
 q4_status q4_attend4(const q4_cache4* c, const uint16_t* q, int64_t q_token, int64_t q_head, int heads, int tokens,

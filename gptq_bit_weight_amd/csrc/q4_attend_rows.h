@@ -46,27 +46,32 @@ __device__ __forceinline__ int seen_block(const Args& p, const Span& s, int bloc
 }
 
 // A workgroup's range of all tiles: `it` up to `end`, in shares of `per`; it begins
-// in request b, which `before` tiles come before. A row tile's tiles count as the next multiple
-// of `pad`. (The first 64 requests stay in the lanes: each look at them in memory is one
+// in request b, which `before` tiles come before. A row tile counts as its tiles and `extra`
+// before them, or as the next multiple of `pad`. (The first 64 requests stay in the lanes: each look at them in memory is one
 // more latency before the first key.)
 struct Share {
     Request first64;
-    uint32_t per, it, end, before, pad;
+    uint32_t per, it, end, before, pad, extra;
     int b;
-    __device__ __forceinline__ uint32_t padded(int tiles) const { return pad == 1 ? (uint32_t)tiles : ((uint32_t)tiles + pad - 1) / pad * pad; }
+    __device__ __forceinline__ uint32_t counted(int tiles) const
+    {
+        return pad == 1 ? (uint32_t)tiles + extra : ((uint32_t)tiles + pad - 1) / pad * pad;
+    }
 };
 
 // (the lanes of a wave each look at a request; false: no work for this workgroup)
-// EVEN: where there are workgroups enough, every row tile gets whole shares of its own, so that
-// no workgroup has pieces of two.
-template <bool SK, int WV, bool EVEN>
+// EXTRA: the time that a piece of a row tile takes beside its tiles, in tiles; and where there are
+// workgroups enough, every row tile gets whole shares of its own, so that no workgroup has pieces
+// of two. (0: neither.)
+template <bool SK, int WV, int EXTRA>
 __device__ __forceinline__ bool share_of(const Args& p, int lane, Share& sh)
 {
     auto request_at = [&](int b) { return b < p.B ? request(p, b) : Request{0, 0, 0}; };
     sh.pad = 1;
+    sh.extra = EXTRA;
     auto cost = [&](const Request& r) {        // (0 without tokens)
         const Span s = span<SK>(p, r);
-        return (uint32_t)s.rt * (uint32_t)p.KV * sh.padded(s.nt);
+        return (uint32_t)s.rt * (uint32_t)p.KV * sh.counted(s.nt);
     };
     auto scan = [&](uint32_t v) {              // inclusive, over the lanes
 #pragma unroll
@@ -84,7 +89,7 @@ __device__ __forceinline__ bool share_of(const Args& p, int lane, Share& sh)
     uint32_t per = (total + (uint32_t)p.workers - 1) / (uint32_t)p.workers;
     per = (max(per, (uint32_t)p.least) + WV - 1) / WV * WV;
     sh.per = per;
-    if constexpr (EVEN) {
+    if constexpr (EXTRA) {
         auto shares = [&](const Request& r) {
             const Span s = span<SK>(p, r);
             return (uint32_t)s.rt * (uint32_t)p.KV * (((uint32_t)s.nt + per - 1) / per);
@@ -93,6 +98,7 @@ __device__ __forceinline__ bool share_of(const Args& p, int lane, Share& sh)
         for (int b0 = 64; b0 < p.B; b0 += 64) n += (uint32_t)__builtin_amdgcn_readlane((int)scan(shares(request_at(b0 + lane))), 63);
         if (n <= (uint32_t)p.workers) {
             sh.pad = per;
+            sh.extra = 0;
             total = n * per;
             cost64 = scan(cost(sh.first64));
         }
@@ -134,7 +140,7 @@ __device__ __forceinline__ Span span_of(const Args& p, const Share& sh, int b)
     return s;
 }
 
-// A share's piece of a row tile: the tiles before the row tile's first of all, and of
+// A share's piece of a row tile: what comes before the row tile's first tile of all, and of
 // the row tile `tiles` from `tile0`.
 struct Segment {
     uint32_t pair_at;
@@ -210,8 +216,9 @@ __device__ __forceinline__ void finish(const Args& p, const Share& sh, const Spa
                 const int w0 = wf + slots * part / parts, w1 = wf + slots * (part + 1) / parts;
                 float mm = kLow, ll = 0.f;
                 f4 v = f4{0.f, 0.f, 0.f, 0.f};
-                constexpr int FB = 4;      // slots whose loads are under way together
-                for (int w = w0; on && w < w1; w += FB) {
+                // (FB slots whose loads are under way together)
+                auto take = [&](int w, auto fb) {
+                    constexpr int FB = decltype(fb)::value;
                     float pm[FB], pl[FB];
                     f4 po[FB];
 #pragma unroll
@@ -231,6 +238,15 @@ __device__ __forceinline__ void finish(const Args& p, const Share& sh, const Spa
                         ll = a * ll + c * pl[f];
                         v = a * v + c * po[f];
                         mm = mn;
+                    }
+                };
+                for (int w = w0; on && w < w1;) {
+                    if (w1 - w > 4) {
+                        take(w, std::integral_constant<int, 16>{});
+                        w += 16;
+                    } else {
+                        take(w, std::integral_constant<int, 4>{});
+                        w += 4;
                     }
                 }
                 if (parts > 1) {

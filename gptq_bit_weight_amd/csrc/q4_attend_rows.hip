@@ -67,7 +67,7 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void q4_attend_rows_kernel(Ar
     }
 
     Share sh;
-    if (!share_of<SK, WV, false>(p, lane, sh)) return;
+    if (!share_of<SK, WV, 0>(p, lane, sh)) return;
     uint32_t it = sh.it;
     uint32_t before = sh.before;
     int b = sh.b;
