@@ -8,11 +8,12 @@
 // and a group with a value that is not finite gets s = m = NaN. What the cache then stands for
 // is s c + m (q4_cache4.h). The queries are turned in the same launch.
 //
-// x is of the tokens' 16-bit type, so (x - m) is exact in 64 bits and the remainder x - m - n s
-// of a guess n is too: whether it passes half a step decides the code exactly. Keys are
-// turned in 64 bits, rounded to fp32 and to the type, and then quantised: a code is the definition's
-// and does not hang on the last bits of fp32. (64-bit instructions run at the rate of
-// 32-bit ones here.) Queries are turned as q4_rope_kernel turns them.
+// (x - m) / s in fp32, by the reciprocal, is off by 4 2^-24 of itself at most, 4e-6: a code that it leaves in doubt, within 1e-5
+// of half way between two, is decided in 64 bits (some waves in a hundred). x is of the tokens' 16-bit
+// type, so x - m is exact there and the remainder x - m - n s of a guess n is too: whether it passes half a
+// step. Keys are turned in 64 bits, rounded to fp32 and to the type, and then quantised: a code is the
+// definition's and does not hang on the last bits of fp32. (64-bit instructions run at the
+// rate of 32-bit ones here.) Queries are turned as q4_rope_kernel turns them.
 //
 // Bound: memory, for many tokens that of the queries; for a few the launch. A row of a head is
 // taken by as many lanes as it has pieces of 8 values, all in one wave: a lane reads its piece
@@ -35,6 +36,7 @@ using namespace q4cache4;
 
 constexpr int NT = 256;
 constexpr int kMaxTokens = 4;     // tokens of a workgroup
+constexpr int kSplitRows = 16384; // rows of queries that get a launch of their own
 
 // Keys or values of the cache: strides in bytes.
 struct Plane {
@@ -45,19 +47,23 @@ struct Plane {
 struct AppendArgs {
     const uint64_t* turns;
     float magnitude;
-    int n, rot, interleaved, dim;     // rotated pairs (0: none), rotated values, values of a head
+    int n, rot, dim;                  // rotated pairs (0: none), rotated values, values of a head
     int H, KV, T, TB;                 // heads of q; heads of k and v; tokens, tokens a workgroup
     const uint16_t *q, *k, *v;
     uint16_t* q_out;
-    long long q_t, q_h, k_t, k_h, v_t, v_h, o_t, o_h;
+    uint32_t q_t, q_h, k_t, k_h, v_t, v_h, o_t, o_h;
     Plane kc, vc;
     int group_lanes, group_shift;     // lanes of a group, log2 of its values
     const void *positions, *slots;
     int positions64, slots64;
     int capacity, page_size;          // rows of the cache, rows of a page
-    int lanes_shift, rows;            // log2 of a row's lanes; rows of a token: H + 2 KV
-    q4::FastDiv div_rows, div_ps, div_n;
+    int lanes_shift;                  // log2 of a row's lanes
+    q4::FastDiv div_kv, div_heads, div_ps, div_n;
 };
+
+// Place of pair i among a token's 64-bit cosines and sines: a lane reads eight neighbours, and 8
+// of them fall on 2 banks without the gap.
+__host__ __device__ constexpr int place64(int i) { return i + (i >> 3); }
 
 // The code of a value: d = x - m against steps of s, inv = 1 / s.
 __device__ __forceinline__ uint32_t code_of(double d, double s, double inv)
@@ -70,131 +76,176 @@ __device__ __forceinline__ uint32_t code_of(double d, double s, double inv)
     return (uint32_t)fmin(fmax(n, 0.), 15.);
 }
 
-template <bool WIDE, bool BF>
+// WIDE: pieces on 16 bytes, rotated by whole ones; IL: interleaved pairs (2i, 2i + 1), else (i, i + n).
+template <bool WIDE, bool IL, bool BF>
 __global__ __launch_bounds__(NT) void q4_cache4_append_kernel(AppendArgs p)
 {
-    extern __shared__ double2 cs64[];                                   // [TB][n]
-    float2* cs = reinterpret_cast<float2*>(cs64 + p.TB * p.n);          // [TB][n]
+    extern __shared__ double2 cs64[];                                   // [TB][place64(n)]
+    const int row64 = place64(p.n);
+    float2* cs = reinterpret_cast<float2*>(cs64);                       // or [TB][n]
     const int t0 = (int)blockIdx.x * p.TB;
     const int tb = min(p.TB, p.T - t0);
-    for (int i = threadIdx.x; i < tb * p.n; i += NT) {
+    // a workgroup has rows of keys, of values or of queries only
+    const bool value = blockIdx.z == 1, query = blockIdx.z == 2;
+    const int rows = query ? p.H : p.KV, step = (int)gridDim.y * (NT >> p.lanes_shift), total = tb * rows;
+    if ((int)blockIdx.y * (NT >> p.lanes_shift) >= total) return;
+    for (int i = threadIdx.x; !value && i < tb * p.n; i += NT) {
         const int tt = p.TB == 1 ? 0 : (int)q4::fast_div((uint32_t)i, p.div_n);
         const uint64_t f = (uint64_t)index_at(p.positions, p.positions64, t0 + tt) * p.turns[i - tt * p.n];
-        float2 e = turn_cos_sin(f);
-        e.x *= p.magnitude;
-        e.y *= p.magnitude;
-        cs[i] = e;
-        double2 d = turn_cos_sin64(f);
-        d.x *= (double)p.magnitude;
-        d.y *= (double)p.magnitude;
-        cs64[i] = d;
+        if (query) {
+            float2 e = turn_cos_sin(f);
+            e.x *= p.magnitude;
+            e.y *= p.magnitude;
+            cs[i] = e;
+        } else {
+            double2 d = turn_cos_sin64(f);
+            d.x *= (double)p.magnitude;
+            d.y *= (double)p.magnitude;
+            cs64[tt * row64 + place64(i - tt * p.n)] = d;
+        }
     }
     __syncthreads();
-    const int step = NT * (int)gridDim.y;
-    const int total = tb * p.rows << p.lanes_shift;
-    // (a row's lanes stay together: every lane of a wave goes round as often)
-    for (int base = (int)blockIdx.y * NT; base < total; base += step) {
-        const int i = base + (int)threadIdx.x;
-        const int piece = i & ((1 << p.lanes_shift) - 1);
-        const int row = i >> p.lanes_shift;
-        const int tt = min(p.TB == 1 ? 0 : (int)q4::fast_div((uint32_t)row, p.div_rows), tb - 1);
-        const int t = t0 + tt, head = row - tt * p.rows;
-        const int at = 8 * piece;
-        const bool query = head < p.H, value = head >= p.H + p.KV;
-        const int h = query ? head : head - p.H - (value ? p.KV : 0);
-        const uint16_t* src = query ? p.q + t * p.q_t + h * p.q_h : value ? p.v + t * p.v_t + h * p.v_h : p.k + t * p.k_t + h * p.k_h;
-        long long slot = -1;
-        bool on = i < total && at < p.dim;
-        if (on && !query) {
-            slot = index_at(p.slots, p.slots64, t);
-            on = slot >= 0 && slot < p.capacity;                        // else the token is not written
-        }
-        const bool turned = !value && at < p.rot;
-        uint32_t x[8], y[8];          // the lane's values, and the ones that they are paired with
+    const uint16_t* from = query ? p.q + t0 * (uint64_t)p.q_t : value ? p.v + t0 * (uint64_t)p.v_t : p.k + t0 * (uint64_t)p.k_t;
+    const uint32_t token = query ? p.q_t : value ? p.v_t : p.k_t, per_head = query ? p.q_h : value ? p.v_h : p.k_h;
+    const Plane& c = value ? p.vc : p.kc;
+    const q4::FastDiv div_rows = query ? p.div_heads : p.div_kv;
+    // A lane's piece is the same in every round, and the lanes of a row stay together. (Lanes past the row's or the
+    // rows' end go along with the last piece and row, and store nothing.)
+    const int piece = (int)threadIdx.x & ((1 << p.lanes_shift) - 1);
+    const bool inside = 8 * piece < p.dim;
+    const int at = inside ? 8 * piece : p.dim - 8;
+    const bool turned = !value && at < p.rot, second = !IL && at >= p.n;    // (second half of the rotated values, WIDE)
+    for (int row0 = (int)blockIdx.y * (NT >> p.lanes_shift); row0 < total; row0 += step) {
+        const int my_row = row0 + ((int)threadIdx.x >> p.lanes_shift), row = min(my_row, total - 1);
+        const int tt = p.TB == 1 ? 0 : (int)q4::fast_div((uint32_t)row, div_rows);
+        const int t = t0 + tt, h = row - tt * rows;
+        const uint16_t* src = from + (uint64_t)(uint32_t)tt * token + (uint64_t)(uint32_t)h * per_head;
+        const long long slot = query ? 0 : index_at(p.slots, p.slots64, t);
+        u4 x;                                  // the lane's values
+        if constexpr (WIDE) {
+            x = *reinterpret_cast<const u4*>(src + at);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = y[e] = 0;
-        if (on) {
+            for (int e = 0; e < 4; ++e) x[e] = (uint32_t)src[at + 2 * e] | (uint32_t)src[at + 2 * e + 1] << 16;
+        }
+        if (turned) {
+            float b[8];                        // what they are paired with, negative for the first of a pair
             if constexpr (WIDE) {
-                const u4 a = *reinterpret_cast<const u4*>(src + at);
-                u4 b = a;
-                if (turned && !p.interleaved) b = *reinterpret_cast<const u4*>(src + (at < p.n ? at + p.n : at - p.n));
+                u4 o = x;
+                if constexpr (!IL) o = *reinterpret_cast<const u4*>(src + (second ? at - p.n : at + p.n));
+                const uint32_t flip = second ? 0u : 0x80008000u;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    x[2 * e] = a[e] & 0xffffu;
-                    x[2 * e + 1] = a[e] >> 16;
-                    y[2 * e] = p.interleaved ? a[e] >> 16 : b[e] & 0xffffu;
-                    y[2 * e + 1] = p.interleaved ? a[e] & 0xffffu : b[e] >> 16;
+                    const uint32_t w = IL ? (x[e] >> 16 | x[e] << 16) ^ 0x8000u : o[e] ^ flip;
+                    b[2 * e] = act_to_f32<BF>((uint16_t)w);
+                    b[2 * e + 1] = act_to_f32<BF>((uint16_t)(w >> 16));
                 }
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int d = at + e;
-                    x[e] = src[d];
-                    if (!value && d < p.rot) y[e] = src[p.interleaved ? d ^ 1 : d < p.n ? d + p.n : d - p.n];
+                    b[e] = 0.f;
+                    if (d >= p.rot) continue;
+                    const bool first = IL ? !(d & 1) : d < p.n;
+                    b[e] = act_to_f32<BF>((uint16_t)(src[IL ? d ^ 1 : first ? d + p.n : d - p.n] ^ (first ? 0x8000u : 0u)));
                 }
             }
-        }
-        if (turned && on) {
-            const float2* f = cs + tt * p.n;
-            const double2* f64 = cs64 + tt * p.n;
+            auto pair_of = [&](int e) { return IL ? (at + e) >> 1 : at + e >= p.n ? at + e - p.n : at + e; };
+            const int pair0 = second ? at - p.n : at;
+            float y[8];
+            if (query) {
+                const float2* f = cs + tt * p.n;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int d = at + e;
-                if (!WIDE && d >= p.rot) continue;
-                const bool first = p.interleaved ? !(d & 1) : d < p.n;
-                const int pair = p.interleaved ? d >> 1 : first ? d : d - p.n;
-                const float a = act_to_f32<BF>((uint16_t)x[e]), b = act_to_f32<BF>((uint16_t)y[e]);
-                if (query) {
-                    const float2 w = f[pair];
-                    x[e] = f32_to_act<BF>(first ? a * w.x - b * w.y : a * w.x + b * w.y);
-                } else {
-                    const double2 w = f64[pair];
-                    x[e] = f32_to_act<BF>((float)((double)a * w.x + (first ? -(double)b : (double)b) * w.y));
+                for (int e = 0; e < 8; ++e) {
+                    y[e] = act_to_f32<BF>((uint16_t)(x[e / 2] >> 16 * (e & 1)));
+                    if (!WIDE && at + e >= p.rot) continue;
+                    const float2 w = f[WIDE && !IL ? pair0 + e : pair_of(e)];
+                    y[e] = y[e] * w.x + b[e] * w.y;
+                }
+            } else {
+                const double2* f = cs64 + tt * row64;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    y[e] = act_to_f32<BF>((uint16_t)(x[e / 2] >> 16 * (e & 1)));
+                    if (!WIDE && at + e >= p.rot) continue;
+                    // (eight neighbours from a multiple of 8 have no gap between them)
+                    const double2 w = f[WIDE && !IL ? place64(pair0) + e : place64(pair_of(e))];
+                    y[e] = (float)__builtin_fma((double)y[e], w.x, (double)b[e] * w.y);
                 }
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (BF) x[e] = pack_bf16(y[2 * e], y[2 * e + 1]);
+                else x[e] = bitcast<uint32_t>(__builtin_convertvector(ff2{y[2 * e], y[2 * e + 1]}, h2));
+            }
         }
+        const bool on = my_row < total && inside;
         if (query) {
-            if (on) {
-                uint16_t* to = p.q_out + t * p.o_t + h * p.o_h + at;
-                if constexpr (WIDE) {
-                    *reinterpret_cast<u4*>(to) = u4{x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16};
-                } else {
+            if (!on) continue;
+            uint16_t* to = p.q_out + (uint64_t)(uint32_t)t * p.o_t + (uint64_t)(uint32_t)h * p.o_h + at;
+            if constexpr (WIDE) {
+                *reinterpret_cast<u4*>(to) = x;
+            } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) to[e] = (uint16_t)x[e];
-                }
+                for (int e = 0; e < 8; ++e) to[e] = (uint16_t)(x[e / 2] >> 16 * (e & 1));
             }
+            continue;
         }
         // (not branched over: the lanes of a row pass their extremes on)
-        float lo = INFINITY, hi = -INFINITY, v[8];
+        float lo = INFINITY, hi = -INFINITY, odd = 0.f, v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float a = act_to_f32<BF>((uint16_t)x[e]);
+            const float a = act_to_f32<BF>((uint16_t)(x[e / 2] >> 16 * (e & 1)));
             v[e] = fminf(fmaxf(a, -kLargest), kLargest);
             lo = fminf(lo, v[e]);
-            hi = fmaxf(hi, fabsf(a) < INFINITY ? v[e] : INFINITY);
+            hi = fmaxf(hi, v[e]);
+            odd = __builtin_fmaf(a, 0.f, odd); // NaN once a value is not finite
         }
+        if (!(odd == 0.f)) hi = INFINITY;
         for (int d = 1; d < p.group_lanes; d *= 2) {
             lo = fminf(lo, __shfl_xor(lo, d));
             hi = fmaxf(hi, __shfl_xor(hi, d));
         }
-        if (!on || query) continue;
+        if (!on || slot < 0 || slot >= p.capacity) continue;            // (else the token is not written)
         const bool finite = hi < INFINITY;
         const uint16_t m16 = finite ? f32_to_f16_bits(lo) : (uint16_t)0x7e00;
         const float m = f16_bits_to_f32(m16);
         const uint16_t s16 = finite ? f32_to_f16_bits((hi - m) / 15.f) : (uint16_t)0x7e00;
-        const double s = (double)f16_bits_to_f32(s16), inv = 1. / s;
+        const float s = f16_bits_to_f32(s16), inv = __builtin_amdgcn_rcpf(s);
         uint32_t word = 0;
-        if (s > 0.)
+        float doubt = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) word |= code_of((double)v[e] - (double)m, s, inv) << 4 * e;
+        for (int e = 0; e < 8; ++e) {
+            const float c = (v[e] - m) * inv, n = __builtin_rintf(c);
+            doubt = fmaxf(doubt, fabsf(c - n));
+            word |= (uint32_t)fminf(fmaxf(n, 0.f), 15.f) << 4 * e;
+        }
+        if (doubt > 0.49999f) {
+            const double inv64 = 1. / (double)s;
+            word = 0;
+#pragma clang loop unroll(disable)
+            for (int e = 0; e < 8; ++e) {
+                float y = v[0];
+#pragma unroll
+                for (int z = 1; z < 8; ++z) y = z == e ? v[z] : y;
+                word |= code_of((double)y - (double)m, (double)s, inv64) << 4 * e;
+            }
+        }
+        if (!(s > 0.f)) word = 0;
         const long long page = q4::fast_div((uint32_t)slot, p.div_ps);
         const long long r = slot - page * p.page_size;
-        const Plane& c = value ? p.vc : p.kc;
         *reinterpret_cast<uint32_t*>(c.at + page * c.page + h * c.head + r * c.row + 4 * piece) = word;
         if ((piece & (p.group_lanes - 1)) == 0)
             *reinterpret_cast<uint32_t*>(c.scale + page * c.scale_page + h * c.scale_head + r * c.scale_row + 4 * (at >> p.group_shift)) =
                 (uint32_t)s16 | (uint32_t)m16 << 16;
     }
+}
+
+template <bool WIDE, bool IL>
+void launch_append(const AppendArgs& p, dim3 grid, size_t lds, bool bf16, hipStream_t stream)
+{
+    if (bf16) hipLaunchKernelGGL((q4_cache4_append_kernel<WIDE, IL, true>), grid, dim3(NT), lds, stream, p);
+    else hipLaunchKernelGGL((q4_cache4_append_kernel<WIDE, IL, false>), grid, dim3(NT), lds, stream, p);
 }
 
 struct ReadArgs {
@@ -275,6 +326,8 @@ q4_status q4_cache4_append(const q4_cache4* c, const uint16_t* k, int64_t k_toke
     if (tokens == 0) return Q4_OK;
     if (!k || !v || !slots) return q4::fail(Q4_ERR_INVALID_ARG, "%s: null k, v or slots", who);
     if (slot_bits != 32 && slot_bits != 64) return q4::fail(Q4_ERR_INVALID_ARG, "%s: slots of %d bits", who, slot_bits);
+    for (int64_t x : {k_token, k_head, v_token, v_head, q ? q_token : 0, q ? q_head : 0, q ? out_token : 0, q ? out_head : 0})
+        if (x < 0 || x > 0x7fffffff) return q4::fail(Q4_ERR_UNSUPPORTED, "%s: tokens or heads more than 2^31 - 1 values apart", who);
     const q4::View kin = q4::head_view(k, k_token, k_head, tokens, c->kv_heads, c->dim);
     const q4::View vin = q4::head_view(v, v_token, v_head, tokens, c->kv_heads, c->dim);
     if (q4::meets_cache4(kin, c) || q4::meets_cache4(vin, c)) return q4::fail(Q4_ERR_INVALID_ARG, "%s: k or v overlap the cache", who);
@@ -290,7 +343,6 @@ q4_status q4_cache4_append(const q4_cache4* c, const uint16_t* k, int64_t k_toke
         p.magnitude = r->magnitude;
         p.n = r->rot / 2;
         p.rot = r->rot;
-        p.interleaved = r->interleaved;
         p.positions = positions;
         p.positions64 = position_bits == 64;
         wide = mult8(r->rot) && (r->interleaved || mult8(r->rot / 2));
@@ -311,11 +363,11 @@ q4_status q4_cache4_append(const q4_cache4* c, const uint16_t* k, int64_t k_toke
             return q4::fail(Q4_ERR_INVALID_ARG, "%s: q_out overlaps slots or positions", who);
         p.H = heads;
         p.q = q;
-        p.q_t = q_token;
-        p.q_h = q_head;
+        p.q_t = (uint32_t)q_token;
+        p.q_h = (uint32_t)q_head;
         p.q_out = q_out;
-        p.o_t = out_token;
-        p.o_h = out_head;
+        p.o_t = (uint32_t)out_token;
+        p.o_h = (uint32_t)out_head;
         wide = wide && at16(q) && at16(q_out) && mult8(q_token) && mult8(q_head) && mult8(out_token) && mult8(out_head);
     }
     if (((long long)p.H + 2LL * c->kv_heads) * c->dim > (1 << 24))
@@ -325,11 +377,11 @@ q4_status q4_cache4_append(const q4_cache4* c, const uint16_t* k, int64_t k_toke
     p.KV = c->kv_heads;
     p.T = tokens;
     p.k = k;
-    p.k_t = k_token;
-    p.k_h = k_head;
+    p.k_t = (uint32_t)k_token;
+    p.k_h = (uint32_t)k_head;
     p.v = v;
-    p.v_t = v_token;
-    p.v_h = v_head;
+    p.v_t = (uint32_t)v_token;
+    p.v_h = (uint32_t)v_head;
     p.kc = plane_of(c, false);
     p.vc = plane_of(c, true);
     p.group_lanes = c->group / 8;
@@ -339,21 +391,27 @@ q4_status q4_cache4_append(const q4_cache4* c, const uint16_t* k, int64_t k_toke
     p.page_size = c->page_size;
     p.capacity = c->pages * c->page_size;
     p.lanes_shift = log2_of(c->dim / 8);
-    p.rows = p.H + 2 * p.KV;
+    // Many tokens' queries go by q4_rope_kernel, which reads a value once and has more of them under way
+    // (16384 tokens of 64 heads of 128 over 8: 225 us in one launch, ??? in two).
+    if (p.H && (long long)tokens * heads > kSplitRows) {
+        if (q4_status st = q4_rotary_apply(r, q, q_token, q_head, q_out, out_token, out_head, positions, position_bits, tokens, heads, 0,
+                                           bf16, stream); st != Q4_OK) return st;
+        p.H = 0;
+    }
     // Few tokens: a workgroup for each 256 lanes of each token, so that a decode step
     // spreads over the CUs. Many: whole tokens, kMaxTokens to a workgroup.
-    const int slices = ((p.rows << p.lanes_shift) + NT - 1) / NT;
+    const int slices = (((p.H > p.KV ? p.H : p.KV) << p.lanes_shift) + NT - 1) / NT;
     const bool few = (long long)p.T * slices <= 4096;
     p.TB = few ? 1 : kMaxTokens;
-    p.div_rows = q4::make_fastdiv((uint32_t)p.rows);
+    p.div_kv = q4::make_fastdiv((uint32_t)p.KV);
+    p.div_heads = q4::make_fastdiv((uint32_t)(p.H > 0 ? p.H : 1));
     p.div_ps = q4::make_fastdiv((uint32_t)p.page_size);
     p.div_n = q4::make_fastdiv((uint32_t)(p.n > 0 ? p.n : 1));
-    const dim3 grid((p.T + p.TB - 1) / p.TB, few ? slices : 1);
-    const size_t lds = (size_t)p.TB * p.n * (sizeof(float2) + sizeof(double2));
-    if (wide && bf16) hipLaunchKernelGGL((q4_cache4_append_kernel<true, true>), grid, dim3(NT), lds, stream, p);
-    else if (wide) hipLaunchKernelGGL((q4_cache4_append_kernel<true, false>), grid, dim3(NT), lds, stream, p);
-    else if (bf16) hipLaunchKernelGGL((q4_cache4_append_kernel<false, true>), grid, dim3(NT), lds, stream, p);
-    else hipLaunchKernelGGL((q4_cache4_append_kernel<false, false>), grid, dim3(NT), lds, stream, p);
+    const dim3 grid((p.T + p.TB - 1) / p.TB, few ? slices : 1, p.H ? 3 : 2);
+    const size_t lds = (size_t)p.TB * place64(p.n) * sizeof(double2);
+    const bool il = r && r->interleaved;
+    if (wide) il ? launch_append<true, true>(p, grid, lds, bf16 != 0, stream) : launch_append<true, false>(p, grid, lds, bf16 != 0, stream);
+    else il ? launch_append<false, true>(p, grid, lds, bf16 != 0, stream) : launch_append<false, false>(p, grid, lds, bf16 != 0, stream);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? Q4_OK : q4::fail(Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
 }

@@ -635,7 +635,8 @@ q4_status q4_check_cache4(const q4_cache4* c);
  *   m = binary16(lo), s = binary16(fp32(hi - m) / 15)
  *   code = (x - m) / s rounded to the nearest of 0 .. 15, ties to even; 0 where s is 0.
  * A group with a value that is not finite gets s = m = NaN: it stands for NaN as a
- * whole. q is turned as q4_rotary_apply does. k, v, q, q_out, slots and positions must not
+ * whole. q is turned as q4_rotary_apply does. Tokens and heads lie at most 2^31 - 1 values
+ * apart. k, v, q, q_out, slots and positions must not
  * overlap the cache (Q4_ERR_INVALID_ARG).
  */
 q4_status q4_cache4_append(const q4_cache4* c, const uint16_t* k, int64_t k_token, int64_t k_head, const uint16_t* v,
