@@ -7,7 +7,8 @@
 // what can go in parallel (page copies, table rows) is a second launch that reads the plan.
 //
 // A copy goes by pieces of 16 KiB, each read whole before it is written: 64 bytes a lane
-// under way, 128 KiB a CU.
+// under way, 128 KiB a CU. Stores pass the caches by (nobody reads a page next): 940 pages
+// of 256 KiB in 80 us, 6.1 TB/s read and written, against 99 with ordinary stores.
 #include <hip/hip_runtime.h>
 
 #include "q4_device.h"
@@ -45,44 +46,58 @@ struct CopyArgs {
 template <class T>
 __device__ __forceinline__ void copy_piece(const CopyPlane& c, const char* from, char* to, int first)
 {
+    const int i0 = first + (int)threadIdx.x;
     T v[kEach];
+    if (c.whole && first + kEach * CT <= c.count) {
+        const T* a = reinterpret_cast<const T*>(from) + i0;
+        T* b = reinterpret_cast<T*>(to) + i0;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) v[e] = a[e * CT];
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) __builtin_nontemporal_store(v[e], b + e * CT);
+        return;
+    }
     long long off[kEach];
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
-        const int i = first + e * CT + (int)threadIdx.x;
-        if (i >= c.count) continue;
-        if (c.whole) {
-            off[e] = (long long)i * (int)sizeof(T);
-        } else {
-            const int run = (int)q4::fast_div((uint32_t)i, c.div_run), head = (int)q4::fast_div((uint32_t)run, c.div_rows);
-            off[e] = head * c.head + (run - head * c.rows) * c.row + (long long)(i - run * c.run) * (int)sizeof(T);
-        }
+        const int i = min(i0 + e * CT, c.count - 1);
+        const int run = (int)q4::fast_div((uint32_t)i, c.div_run), head = (int)q4::fast_div((uint32_t)run, c.div_rows);
+        off[e] = head * c.head + (run - head * c.rows) * c.row + (long long)(i - run * c.run) * (int)sizeof(T);
         v[e] = *reinterpret_cast<const T*>(from + off[e]);
     }
 #pragma unroll
     for (int e = 0; e < kEach; ++e)
-        if (first + e * CT + (int)threadIdx.x < c.count) *reinterpret_cast<T*>(to + off[e]) = v[e];
+        if (i0 + e * CT < c.count) *reinterpret_cast<T*>(to + off[e]) = v[e];
+}
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Piece `piece` of page s to page d. (The planes are read from the kernel's arguments, of which
+// CopyArgs is the first, where they lie: a parameter that is indexed is copied to memory of each lane's own.)
+__device__ __forceinline__ void copy_piece_of(int s, int d, int piece)
+{
+    auto p = (const __attribute__((address_space(4))) CopyArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+    int x = 0;
+    while (piece >= p->plane[x].pieces) piece -= p->plane[x++].pieces;
+    const CopyPlane& c = *(const CopyPlane*)&p->plane[x];
+    const char* from = c.at + s * c.page;
+    char* to = c.at + d * c.page;
+    const int first = piece * CT * kEach;
+    if (c.width == 16) copy_piece<u4>(c, from, to, first);
+    else if (c.width == 4) copy_piece<uint32_t>(c, from, to, first);
+    else if (c.width == 2) copy_piece<uint16_t>(c, from, to, first);
+    else copy_piece<uint8_t>(c, from, to, first);
 }
 
 __device__ __forceinline__ void copy_pages(const CopyArgs& p, int n)
 {
-    const long long total = (long long)n * p.pieces;
-    for (long long w = blockIdx.x; w < total; w += gridDim.x) {
-        // (a pair's pieces by 31-bit division: the host keeps n pieces below 2^31)
-        const int pair = (int)q4::fast_div((uint32_t)w, p.div_pieces);
-        int piece = (int)w - pair * p.pieces;
+    // (the host keeps n pieces below 2^31)
+    const uint32_t total = (uint32_t)uniform(n) * (uint32_t)p.pieces;
+    for (uint32_t w = blockIdx.x; w < total; w += gridDim.x) {
+        const int pair = (int)q4::fast_div(w, p.div_pieces);
         const long long s = index_at(p.src, p.src64, pair), d = index_at(p.dst, p.dst64, pair);
         if (s < 0 || s >= p.pages || d < 0 || d >= p.pages || s == d) continue;
-        int x = 0;
-        while (piece >= p.plane[x].pieces) piece -= p.plane[x++].pieces;
-        const CopyPlane& c = p.plane[x];
-        const char* from = c.at + s * c.page;
-        char* to = c.at + d * c.page;
-        const int first = piece * CT * kEach;
-        if (c.width == 16) copy_piece<u4>(c, from, to, first);
-        else if (c.width == 4) copy_piece<uint32_t>(c, from, to, first);
-        else if (c.width == 2) copy_piece<uint16_t>(c, from, to, first);
-        else copy_piece<uint8_t>(c, from, to, first);
+        copy_piece_of(uniform((int)s), uniform((int)d), (int)w - pair * p.pieces);
     }
 }
 
@@ -297,23 +312,14 @@ __global__ __launch_bounds__(CT) void q4_pages_fork_copy_kernel(CopyArgs p, Book
         }
         if (threadIdx.x == 0) b.lengths[chi] = len;
     }
-    const long long total = (long long)n * p.pieces;
-    for (long long w = blockIdx.x; w < total; w += gridDim.x) {
-        const int i = (int)q4::fast_div((uint32_t)w, p.div_pieces);
+    const uint32_t total = (uint32_t)n * (uint32_t)p.pieces;
+    for (uint32_t w = blockIdx.x; w < total; w += gridDim.x) {
+        const int i = (int)q4::fast_div(w, p.div_pieces);
         if (!done[i] || to[i] < 0) continue;
         const int par = (int)index_at(parents, parents64, i);
         const int s = b.table[(long long)par * b.W + pages_of(b, length_of(b, par)) - 1];
         if (s < 0 || s >= b.P) continue;
-        int piece = (int)w - i * p.pieces, x = 0;
-        while (piece >= p.plane[x].pieces) piece -= p.plane[x++].pieces;
-        const CopyPlane& c = p.plane[x];
-        const char* from = c.at + s * c.page;
-        char* dst = c.at + to[i] * c.page;
-        const int first = piece * CT * kEach;
-        if (c.width == 16) copy_piece<u4>(c, from, dst, first);
-        else if (c.width == 4) copy_piece<uint32_t>(c, from, dst, first);
-        else if (c.width == 2) copy_piece<uint16_t>(c, from, dst, first);
-        else copy_piece<uint8_t>(c, from, dst, first);
+        copy_piece_of(uniform(s), uniform(to[i]), (int)w - i * p.pieces);
     }
 }
 
