@@ -195,7 +195,11 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
     struct Piece {
         uint32_t code[PD / 8], scale;
     };
-    const int prow = WR * wave + lane / PR, pdim = lane % PR * PD;
+    // (in an order of the rows in which the pieces that 16 lanes write together fall on all banks:
+    // row by row 4 of them met, which took a quarter of the kernel's time)
+    const int pq = lane / PR;
+    const int prow = WR * wave + (D == 64 ? (pq & 9) | (pq & 2) << 1 | (pq & 4) >> 1 : D == 128 ? (pq & 3) << 2 | pq >> 2 : (pq & 1) << 2 | pq >> 1);
+    const int pdim = lane % PR * PD;
     const bool pin = pdim < p.dim;
     const uint32_t pcol = pin ? (uint32_t)pdim / 2u : 0u, pscol = pin ? (uint32_t)(pdim >> p.group_shift) * 4u : 0u;
     int page_of = 0, row_of = 0;
@@ -273,7 +277,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
             // rows past the last key repeat it (nothing unwritten is read)
             row = min(prow & 15, last_key - 16 * min(seen_block(first >> 4), last_key >> 4));
         } else {
-            const int key = first + lane / PR;
+            const int key = first + prow - WR * wave;
             const long long page = locate4(min(key < p.sinks ? key : max(key, lo), last_key), row);
             at += page * side.page;
             scale_at += page * side.scale_page;
