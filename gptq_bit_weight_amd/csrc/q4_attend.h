@@ -111,6 +111,16 @@ __device__ __forceinline__ void dma(const char* base, const uint32_t (&off)[N], 
                      ::"v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(b), "s"(dst) : "memory", "scc");
 }
 
+// 4 bytes a lane from memory straight into LDS: lane l's land at dst + 4 l.
+__device__ __forceinline__ void dma_words(const char* base, uint32_t off, uint32_t dst)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(reinterpret_cast<uint64_t>(base)), "s"(dst) : "memory");
+}
+__device__ __forceinline__ void dma_words_lane(const char* src, uint32_t dst)
+{
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 4\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(dst) : "memory");
+}
+
 // A weight of zero does not keep a value that is not finite out of a sum. Where a
 // tile of keys is not wholly visible to a tile's rows, the kernels therefore look
 // for such values, and multiply key by key if there are any: `lone` leaves one of

@@ -63,16 +63,6 @@ __device__ __forceinline__ int spread4(int row)        // (of 16)
     return D == 64 ? row >> 3 & 1 : D == 128 ? row >> 2 & 3 : row >> 1 & 7;
 }
 
-// 4 bytes a lane from memory straight into LDS: lane l's land at dst + 4 l (q4_attend.h, dma).
-__device__ __forceinline__ void dma_words(const char* base, uint32_t off, uint32_t dst)
-{
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(reinterpret_cast<uint64_t>(base)), "s"(dst) : "memory");
-}
-__device__ __forceinline__ void dma_words_lane(const char* src, uint32_t dst)
-{
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 4\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(dst) : "memory");
-}
-
 template <int D, bool BF, bool PG, int WV>
 __global__ __launch_bounds__(64 * WV, D == 256 ? 2 : 3) void q4_attend4_rows_kernel(Args p)
 {

@@ -97,7 +97,7 @@ struct Call {
     int64_t out_token, out_head;
     void* workspace;
     size_t workspace_bytes;
-    bool bf16, four;
+    bool bf16, four, far;     // far: row blocks of a page must not be told by 32-bit numbers of units
 };
 
 // The call over a cache that p describes already (pages, page_size, KV, dim and where its
@@ -157,7 +157,7 @@ q4_status attend(const char* who, q4attend::Args& p, const View* caches, int nca
     p.store8 = (reinterpret_cast<uintptr_t>(a.out) % 8 == 0) && a.out_token % 4 == 0 && a.out_head % 4 == 0;
     p.div_g = make_fastdiv((uint32_t)g);
     p.div_page = make_fastdiv((uint32_t)p.page_size);
-    const bool pg = p.page_size % 16 == 0;
+    const bool pg = p.page_size % 16 == 0 && !a.far;
 
     // Few rows a request: the few-row kernel, above the many-row one. (64 x 8
     // rows over 4600 keys: 221 us and 237; 8 x 16 over 3000: 32 and 28; 20 x 32 over
@@ -242,7 +242,7 @@ q4_status q4_attend_ex(const q4_cache* c, const uint16_t* q, int64_t q_token, in
     p.page_size = c->page_size;
     const View caches[] = {cache_view(c, false), cache_view(c, true)};
     return attend(who, p, caches, 2, Call{q, q_token, q_head, heads, tokens, starts, lengths, table, table_width, table_stride, requests,
-                                          window, sinks, scale, out, out_token, out_head, workspace, workspace_bytes, c->bf16 != 0, false}, stream);
+                                          window, sinks, scale, out, out_token, out_head, workspace, workspace_bytes, c->bf16 != 0, false, false}, stream);
 }
 
 q4_status q4_attend(const q4_cache* c, const uint16_t* q, int64_t q_token, int64_t q_head, int heads, int tokens,
@@ -282,9 +282,16 @@ q4_status q4_attend4(const q4_cache4* c, const uint16_t* q, int64_t q_token, int
     p.dim = c->dim;
     p.pages = c->pages;
     p.page_size = c->page_size;
+    // (many rows: 32 bits count the codes' 16 bytes and the scales' 4)
+    bool far = false;
+    for (int v = 0; v < 2; ++v) {
+        const int64_t *s = v ? c->v_stride : c->k_stride, *w = v ? c->v_scale_stride : c->k_scale_stride;
+        far = far || (double)c->pages * (double)s[0] + (double)c->page_size * (double)s[2] >= 0x1p36 ||
+              (double)c->pages * (double)w[0] + (double)c->page_size * (double)w[2] >= 0x1p34;
+    }
     const View caches[] = {cache4_view(c, false, false), cache4_view(c, true, false), cache4_view(c, false, true), cache4_view(c, true, true)};
     return attend(who, p, caches, 4, Call{q, q_token, q_head, heads, tokens, starts, lengths, table, table_width, table_stride, requests,
-                                          window, sinks, scale, out, out_token, out_head, workspace, workspace_bytes, bf16 != 0, true}, stream);
+                                          window, sinks, scale, out, out_token, out_head, workspace, workspace_bytes, bf16 != 0, true, far}, stream);
 }
 
 }  // extern "C"

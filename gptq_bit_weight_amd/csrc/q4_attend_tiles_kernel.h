@@ -90,6 +90,12 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
     constexpr int KS = D / 16, DT = D / 32;    // k-steps of the scores, 32-value tiles of the output
     __shared__ __attribute__((aligned(1024))) char lds_k[NS][KT * PITCH];
     __shared__ __attribute__((aligned(1024))) char lds_v[NS][KT * PITCH];
+    // 4 bits, heads of 128: codes and scales on their way, a wave's 16 rows of keys and of values.
+    // (In registers, ten of them for the time of a step, they left the compiler none to read the
+    // products' operands ahead with, and every product waited for its own.)
+    constexpr bool RAW = C4 && D == 128;
+    constexpr int RAW_PIECES = 1024 + 256;
+    __shared__ __attribute__((aligned(1024))) char lds_raw[RAW ? NW : 1][RAW ? 2 * RAW_PIECES : 16];
 
     const int tid = threadIdx.x;
     const int wave = uniform(tid >> 6);
@@ -189,7 +195,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
         return page * page_stride * 2 + (long long)(key - slot * p.page_size) * row_stride;
     };
     // 4 bits: a lane has PD neighbouring values of one of the wave's rows. They go through
-    // registers, asked for a step before the direct loads would be; a row's keys lie in LDS in
+    // registers; a row's keys lie in LDS in
     // the order of the unpacked codes (the queries' values too), its values in their own.
     constexpr int PR = 64 / WR, PD = D / PR;   // pieces of a row, values of one
     struct Piece {
@@ -202,7 +208,14 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
     const int pdim = lane % PR * PD;
     const bool pin = pdim < p.dim;
     const uint32_t pcol = pin ? (uint32_t)pdim / 2u : 0u, pscol = pin ? (uint32_t)(pdim >> p.group_shift) * 4u : 0u;
-    int page_of = 0, row_of = 0;
+    const uint32_t raw = RAW ? lds_address(lds_raw[wave]) : 0u;
+    uint32_t pkoff = 0, pksoff = 0, pvoff = 0, pvsoff = 0;     // the lane's bytes in the 16 rows
+    if constexpr (C4) {
+        pkoff = (uint32_t)((prow & 15) * p.k4.row) + pcol;
+        pksoff = (uint32_t)((prow & 15) * p.k4.scale_row) + pscol;
+        pvoff = (uint32_t)((prow & 15) * p.v4.row) + pcol;
+        pvsoff = (uint32_t)((prow & 15) * p.v4.scale_row) + pscol;
+    }
     auto locate4 = [&](int key, int& row) {
         const int slot = (int)q4::fast_div((uint32_t)key, p.div_page);
         row = key - slot * p.page_size;
@@ -252,76 +265,114 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
             }
         }
     };
-    // (both sides of a step's tiles are within two blocks of 64 tiles: of keys ahead, of values behind)
-    int page_before = 0, row_before = 0;
-    auto batch4 = [&](int j) {
+    // Pages of 16 rows: the lane's block (block_of), in units of the codes' 16 bytes and the scales' 4
+    // (the host sees to it that they fit in 32 bits).
+    uint32_t kblock = 0, ksblock = 0, vblock = 0, vsblock = 0;
+    auto batch4 = [&](int j, auto values_tag) {
         if constexpr (PG && C4) {
-            page_before = page_of;
-            row_before = row_of;
-            page_of = locate4(block_of(j), row_of);
+            const Args& a = args_again();
+            const Side& side = decltype(values_tag)::value ? a.v4 : a.k4;
+            int row;
+            const uint64_t page = (uint64_t)locate4(block_of(j), row);
+            const uint32_t at = (uint32_t)((page * (uint64_t)side.page + (uint64_t)row * (uint64_t)side.row) >> 4);
+            const uint32_t scale_at = (uint32_t)((page * (uint64_t)side.scale_page + (uint64_t)row * (uint64_t)side.scale_row) >> 2);
+            if constexpr (decltype(values_tag)::value) {
+                vblock = at;
+                vsblock = scale_at;
+            } else {
+                kblock = at;
+                ksblock = scale_at;
+            }
         }
     };
-    int held = j0;                             // tiles from here on are in page_of
+    const char *kh4 = p.k4.at + head * p.k4.head, *ksh4 = p.k4.scale + head * p.k4.scale_head;
+    const char *vh4 = p.v4.at + head * p.v4.head, *vsh4 = p.v4.scale + head * p.v4.scale_head;
     auto fetch = [&](int j, auto values_tag, Piece& x) {
         constexpr bool values = decltype(values_tag)::value;
-        const Side& side = values ? p.v4 : p.k4;
         const int first = key_of(j) + WR * wave;
-        const char *at = side.at + head * side.head, *scale_at = side.scale + head * side.scale_head;
-        int row;
+        const char *at = values ? vh4 : kh4, *scale_at = values ? vsh4 : ksh4;
+        uint64_t ro, so;
         if constexpr (PG) {
             const int from = (j - j0) & 63;
-            const long long page = __builtin_amdgcn_readlane(j < held ? page_before : page_of, from);
-            const int row0 = __builtin_amdgcn_readlane(j < held ? row_before : row_of, from);
-            at += page * side.page + (long long)row0 * side.row;
-            scale_at += page * side.scale_page + (long long)row0 * side.scale_row;
+            at += (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(values ? vblock : kblock), from) << 4;
+            scale_at += (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(values ? vsblock : ksblock), from) << 2;
+            uint32_t r = values ? pvoff : pkoff, q = values ? pvsoff : pksoff;
             // rows past the last key repeat it (nothing unwritten is read)
-            row = min(prow & 15, last_key - 16 * min(seen_block(first >> 4), last_key >> 4));
+            const int limit = last_key - 16 * min(seen_block(first >> 4), last_key >> 4);
+            if (limit < 15) {
+                const Side& side = values ? args_again().v4 : args_again().k4;
+                const int back = (prow & 15) - min(prow & 15, limit);
+                r -= (uint32_t)(back * side.row);
+                q -= (uint32_t)(back * side.scale_row);
+            }
+            ro = r;
+            so = q;
         } else {
+            const Side& side = values ? args_again().v4 : args_again().k4;
             const int key = first + prow - WR * wave;
-            const long long page = locate4(min(key < p.sinks ? key : max(key, lo), last_key), row);
-            at += page * side.page;
-            scale_at += page * side.scale_page;
+            int row;
+            const uint64_t page = (uint64_t)locate4(min(key < p.sinks ? key : max(key, lo), last_key), row);
+            ro = page * (uint64_t)side.page + (uint64_t)row * (uint64_t)side.row + pcol;
+            so = page * (uint64_t)side.scale_page + (uint64_t)row * (uint64_t)side.scale_row + pscol;
         }
-        // (row strides of at most 2^26 bytes; of a whole page they may pass 32 bits)
-        const uint64_t ro = PG ? (uint64_t)((uint32_t)row * (uint32_t)side.row) : (uint64_t)row * (uint64_t)side.row;
-        const uint64_t so = PG ? (uint64_t)((uint32_t)row * (uint32_t)side.scale_row) : (uint64_t)row * (uint64_t)side.scale_row;
-        if constexpr (PD == 16) {
-            const u2 w = *reinterpret_cast<const u2*>(at + (ro + pcol));
+        if constexpr (RAW) {
+            const uint32_t to = raw + (values ? RAW_PIECES : 0);
+            if constexpr (PG) {
+                const uint32_t off[1] = {(uint32_t)ro};
+                dma<1>(at, off, to);
+                dma_words(scale_at, (uint32_t)so, to + 1024u);
+            } else {
+                dma_lane(at + ro, to);
+                dma_words_lane(scale_at + so, to + 1024u);
+            }
+        } else if constexpr (PD == 16) {
+            const u2 w = *reinterpret_cast<const u2*>(at + ro);
             x.code[0] = w[0];
             x.code[1] = w[1];
         } else {
-            const u4 w = *reinterpret_cast<const u4*>(at + (ro + pcol));
+            const u4 w = *reinterpret_cast<const u4*>(at + ro);
 #pragma unroll
             for (int e = 0; e < 4; ++e) x.code[e] = w[e];
         }
-        x.scale = *reinterpret_cast<const uint32_t*>(scale_at + (so + pscol));
+        if constexpr (!RAW) x.scale = *reinterpret_cast<const uint32_t*>(scale_at + so);
     };
-    const q4cache4::Magic magic = q4cache4::magic();
-    auto put = [&](const Piece& x, auto values_tag, int stage) {
+    // (piece e of the lane's, from a multiple of their number, is at place (pdim / 8 ^ spread) ^ e of the row)
+    const int pplace = prow * PITCH + (((pdim / 8) ^ spread<D>(prow)) << 4);
+    auto put = [&](Piece x, auto values_tag, int stage) {
         constexpr bool values = decltype(values_tag)::value;
-        char* to = (values ? lds_v[0] : lds_k[0]) + stage * (KT * PITCH) + prow * PITCH;
+        if constexpr (RAW) {
+            const char* from = lds_raw[wave] + (values ? RAW_PIECES : 0);
+            const u4 w = *reinterpret_cast<const u4*>(from + lane * 16);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x.code[e] = w[e];
+            x.scale = *reinterpret_cast<const uint32_t*>(from + 1024 + lane * 4);
+        }
+        const int place = here(pplace);
+        const q4cache4::Magic magic = q4cache4::magic();
         const uint32_t sm = pin ? x.scale : 0u;
         const h2 step = q4cache4::low_half(sm), least = q4cache4::high_half(sm);
 #pragma unroll
         for (int e = 0; e < PD / 8; ++e) {
             const u4 w = q4cache4::values8(x.code[e], step, least, magic);
-            *reinterpret_cast<u4*>(to + (((pdim / 8 + e) ^ spread<D>(prow)) << 4)) = values ? q4cache4::own_order(w) : w;
+            *reinterpret_cast<u4*>((values ? lds_v[0] : lds_k[0]) + (place ^ (e << 4)) + stage * (KT * PITCH)) =
+                values ? q4cache4::own_order(w) : w;
         }
     };
     constexpr std::false_type KEYS;
     constexpr std::true_type VALUES;
-    Piece pk[2], pv[2];
+    Piece pk = {}, pv = {};
     if constexpr (C4) {
-        batch4(j0);
+        batch4(j0, KEYS);
+        batch4(j0, VALUES);
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-            fetch(min(j0 + i, j1 - 1), KEYS, pk[0]);
-            if (i < NS - 2) fetch(min(j0 + i, j1 - 1), VALUES, pv[0]);
-            put(pk[0], KEYS, i);
-            if (i < NS - 2) put(pv[0], VALUES, i);
+            fetch(min(j0 + i, j1 - 1), KEYS, pk);
+            if (i < NS - 2) fetch(min(j0 + i, j1 - 1), VALUES, pv);
+            if constexpr (RAW) wait_loads<0>();
+            put(pk, KEYS, i);
+            if (i < NS - 2) put(pv, VALUES, i);
+            wait_lds();
         }
-        fetch(min(j0 + NS, j1 - 1), KEYS, pk[0]);
-        fetch(min(j0 + NS - 2, j1 - 1), VALUES, pv[0]);
     } else {
     batch(j0, KEYS);
     batch(j0, VALUES);
@@ -446,13 +497,12 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
         constexpr int ST = decltype(par)::value;      // i % NS
         const int j = j0 + i;
         if constexpr (C4) {
-            // (asked for here, put into LDS at the end of the next step)
-            if (((i + NS + 1) & 63) == 0 && j + NS + 1 < j1) {
-                batch4(j + NS + 1);
-                held = j + NS + 1;
-            }
-            fetch(min(j + NS + 1, j1 - 1), KEYS, pk[(ST + 1) & 1]);
-            fetch(min(j + NS - 1, j1 - 1), VALUES, pv[(ST + 1) & 1]);
+            // (asked for here, unpacked into LDS at the end of the step: a step later would be
+            // ten registers more, which the reads of the operands ahead of the products need)
+            if (((i + NS) & 63) == 0 && j + NS < j1) batch4(j + NS, KEYS);
+            fetch(min(j + NS, j1 - 1), KEYS, pk);
+            if (((i + NS - 2) & 63) == 0 && j + NS - 2 < j1) batch4(j + NS - 2, VALUES);
+            fetch(min(j + NS - 2, j1 - 1), VALUES, pv);
         } else {
         if (((i + NS - 2) & 63) == 0 && j + NS - 2 < j1) batch(j + NS - 2, VALUES);
         load(min(j + NS - 2, j1 - 1), VALUES, (ST + NS - 2) % NS);
@@ -525,8 +575,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
         }
         }
         if constexpr (C4) {
-            put(pk[ST & 1], KEYS, ST);
-            put(pv[ST & 1], VALUES, (ST + NS - 2) % NS);
+            if constexpr (RAW) wait_loads<0>();
+            put(pk, KEYS, ST);
+            put(pv, VALUES, (ST + NS - 2) % NS);
             wait_lds();
         } else {
             wait_loads<(NS - 2) * 2 * NI>();
@@ -583,13 +634,14 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
         for (int j = j0; j < j1; ++j) {
             if constexpr (C4) {
                 if (((j - j0) & 63) == 0) {
-                    batch4(j);
-                    held = j;
+                    batch4(j, KEYS);
+                    batch4(j, VALUES);
                 }
-                fetch(j, KEYS, pk[0]);
-                fetch(j, VALUES, pv[0]);
-                put(pk[0], KEYS, 0);
-                put(pv[0], VALUES, 0);
+                fetch(j, KEYS, pk);
+                fetch(j, VALUES, pv);
+                if constexpr (RAW) wait_loads<0>();
+                put(pk, KEYS, 0);
+                put(pv, VALUES, 0);
             } else {
                 if (((j - j0) & 63) == 0) {
                     batch(j, KEYS);
