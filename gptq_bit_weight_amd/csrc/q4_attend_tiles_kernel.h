@@ -201,11 +201,11 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
     struct Piece {
         uint32_t code[PD / 8], scale;
     };
-    // (in an order of the rows in which the pieces that 16 lanes write together fall on all banks:
-    // row by row 4 of them met, which took a quarter of the kernel's time)
-    const int pq = lane / PR;
-    const int prow = WR * wave + (D == 64 ? (pq & 9) | (pq & 2) << 1 | (pq & 4) >> 1 : D == 128 ? (pq & 3) << 2 | pq >> 2 : (pq & 1) << 2 | pq >> 1);
-    const int pdim = lane % PR * PD;
+    // (in an order in which the pieces that 8 lanes write together, and 16, fall on banks of their own:
+    // row by row 4 of them met, which took a quarter of the kernel's time; of heads of 256 two still do)
+    const int pq = D == 128 ? (lane >> 1 & 3) | lane >> 4 << 2 : lane / PR;
+    const int prow = WR * wave + (D == 64 ? (pq & 1) << 2 | (pq & 6) >> 1 | (pq & 8) : D == 128 ? (pq & 3) << 2 | pq >> 2 : (pq & 1) << 2 | pq >> 1);
+    const int pdim = (D == 128 ? (lane & 1) | (lane >> 3 & 1) << 1 : lane % PR) * PD;
     const bool pin = pdim < p.dim;
     const uint32_t pcol = pin ? (uint32_t)pdim / 2u : 0u, pscol = pin ? (uint32_t)(pdim >> p.group_shift) * 4u : 0u;
     const uint32_t raw = RAW ? lds_address(lds_raw[wave]) : 0u;
