@@ -30,7 +30,10 @@ static_assert(kListAt + sizeof(q4attend::JoinList) <= kCounterBytes, "workspace"
 // The few-row kernel: rows of a tile, least tiles of a workgroup (of which there
 // is one a CU).
 constexpr int kFewRows = 16, kFewLeast = 4;
-constexpr int kFew4 = 2;
+// Of 4 bits: two workgroups of four waves a CU, so that one multiplies while the other begins or joins
+// a piece; where there are no more than 1 / 16 row tiles a CU, one of eight, whose partial results are half as many
+// (64 single tokens of 8 cached heads, 4600 keys on average, 93 us against 113; 1 over 131000 49 against 42).
+constexpr int kFew4 = 2, kFewWide4 = 16;
 size_t rows_bytes(int dim, int num_cu)
 {
     return kCounterBytes + (size_t)num_cu * 2 * kFewRows * (padded_dim(dim) + 2) * sizeof(float);
@@ -164,14 +167,16 @@ q4_status attend(const char* who, q4attend::Args& p, const View* caches, int nca
     // 6000: 115 and 102.) By their mean, as the host knows no more: a long chunk beside
     // many single tokens costs more in one call than apart (63 single tokens and a chunk of
     // 512 over 8192 keys: 8 heads over 8, few rows, 450 us, apart 359 and 37; 32 heads over 8,
-    // many rows, 546 us, apart 360 and 88).
+    // many rows, 546 us, apart 360 and 88.) In 4 bits the many-row kernel has its vector instructions to share
+    // with the unpacking, and the border lies higher: 20 x 48 rows over 6000 keys 108 us and 125,
+    // 20 x 64 125 and 121, 20 x 96 174 and 125; 16 x 64 of heads of 64 over 2000 32 and 34.
     const long long mean_rows = ((long long)a.tokens * g + a.requests - 1) / a.requests;
-    const bool many = mean_rows > 12;
+    const bool many = mean_rows > (a.four ? 64 : 12);
     const int tile = many ? kTileRows : kFewRows;
     const long long row_tiles = (long long)a.tokens * g / tile + a.requests;
     if (row_tiles * p.KV * (p.max_len / 32 + 2 + (a.four ? 8 : 0)) >= (1LL << 31))
         return fail(Q4_ERR_UNSUPPORTED, "%s: more than 2^31 tiles of keys", who);
-    const bool wide = (long long)a.requests * p.KV * 16 <= cu;
+    const bool wide = a.four && (long long)a.requests * p.KV * kFewWide4 <= cu;
     p.workers = many ? tile_target(cu) : a.four && !wide ? kFew4 * cu : cu;
     p.least = many ? kTileLeast : kFewLeast;
     if (many) {
