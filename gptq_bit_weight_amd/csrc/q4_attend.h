@@ -65,10 +65,11 @@ struct Args {
     uint32_t* counters;                    // few rows: arrivals
     JoinList* joins;                       // many rows
     int workers, least;                    // workgroups, and least tiles of one
-    Side k4, v4;                           // 4 bits, in place of k, v and their strides
-    int group_shift;                       // log2 of the values that share a scale
     int unsplit;                           // many rows: no row tile has more than `least` tiles
     q4::FastDiv div_g, div_page;           // by heads of a group; by rows of a page (or 16-row blocks of one)
+    // (4 bits; last, as the other kernels do not read them)
+    Side k4, v4;                           // 4 bits, in place of k, v and their strides
+    int group_shift;                       // log2 of the values that share a scale
 };
 
 constexpr float kLow = -3.4028234663852886e38f;   // running maximum of a row that has seen no key (the lowest finite value, lifted or not)

@@ -159,7 +159,7 @@ __device__ __forceinline__ void finish(const Args& p, const Share& sh, const Spa
 {
     constexpr int NT = 64 * WV, UNITS = ROWS * (D / 4), UPT = UNITS < NT ? 1 : UNITS / NT;   // four values of a row each
     static_assert(UNITS % NT == 0 || UNITS < NT, "whole rounds");
-    const int tid = here((int)threadIdx.x);
+    const int tid = SPREAD ? here((int)threadIdx.x) : (int)threadIdx.x;
     __syncthreads();
     const bool whole = g.tile0 == 0 && g.tiles == s.nt;
     // (workgroups there are, whatever `starts` says)
@@ -175,7 +175,7 @@ __device__ __forceinline__ void finish(const Args& p, const Share& sh, const Spa
     float ol[UPT];
 #pragma unroll
     for (int u = 0; u < UPT; ++u) {
-        const int unit = u * NT + tid, row = unit / (D / 4) % ROWS, c = unit % (D / 4);
+        const int unit = u * NT + tid, row = UNITS < NT ? unit / (D / 4) % ROWS : unit / (D / 4), c = unit % (D / 4);
         float mm = lds_m[row];
 #pragma unroll
         for (int w = 1; w < WV; ++w) mm = fmaxf(mm, lds_m[w * ROWS + row]);
