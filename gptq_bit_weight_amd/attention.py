@@ -510,7 +510,9 @@ class PagedCache4(_Paged):
 
     append() quantises: m is the group's least value in float16, s = (largest - m) /
     15 in float16, a code the nearest (ties to even). Finite values beyond +-65440
-    are held as that; a group with a value that is not finite stands for NaN."""
+    are held as that; a group with a value that is not finite stands for NaN. (Where
+    the caller makes codes and scales otherwise, a group whose code 0 or 15 stands for
+    a value that is not finite may count as NaN as a whole in attend().)"""
 
     _four = True
 

@@ -419,8 +419,9 @@ q4_status check_pool(const q4_pool* c, const char* who)
         const q4_plane& x = c->plane[i];
         if (!x.at || x.heads < 1 || x.rows < 1 || x.bytes < 1 || x.page < 0 || x.head < 0 || x.row < 0)
             return q4::fail(Q4_ERR_INVALID_ARG, "%s: plane %d: %d heads of %d rows of %d bytes", who, i, x.heads, x.rows, x.bytes);
-        if ((long long)x.heads * x.rows * x.bytes >= (1LL << 31))
-            return q4::fail(Q4_ERR_UNSUPPORTED, "%s: plane %d: pages of 2^31 bytes", who, i);
+        // (a lane's elements lie up to a piece past the last one: their numbers fit in an int)
+        if ((long long)x.heads * x.rows > (1 << 30) / x.bytes)
+            return q4::fail(Q4_ERR_UNSUPPORTED, "%s: plane %d: pages of more than 2^30 bytes", who, i);
     }
     return Q4_OK;
 }

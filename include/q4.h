@@ -658,7 +658,9 @@ q4_status q4_cache4_read(const q4_cache4* c, const void* slots, int slot_bits, i
  * q and out are binary16 or (bf16 != 0) bfloat16. Both products take those
  * binary16 values as they are; queries of bfloat16 are brought into binary16 by a power
  * of two a row (values below 2^-31 of the row's largest lose bits), and the weights are
- * rounded to binary16 whatever the type. The workspace is as for q4_attend.
+ * rounded to binary16 whatever the type. A group whose codes 0 or 15 stand for a value that is
+ * not finite (q4_cache4_append makes none but NaN as a whole) may count as NaN as a
+ * whole. The workspace is as for q4_attend.
  */
 size_t q4_attend4_workspace(const q4_cache4* c, int heads);
 q4_status q4_attend4(const q4_cache4* c, const uint16_t* q, int64_t q_token, int64_t q_head, int heads, int tokens,
@@ -674,7 +676,7 @@ q4_status q4_attend4(const q4_cache4* c, const uint16_t* q, int64_t q_token, int
 /*
  * One tensor of a cache: of each page `heads` heads of `rows` rows of `bytes` dense
  * bytes, row r of head h of page p at `at` + p page + h head + r row (strides in bytes,
- * non-negative). A pool is the one to four tensors of a cache.
+ * non-negative), 2^30 of them a page at most. A pool is the one to four tensors of a cache.
  */
 typedef struct {
     void* at;
