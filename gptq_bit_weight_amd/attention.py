@@ -362,23 +362,25 @@ class _Paged:
         return q_out
 
     def _pool(self):
-        """The tensors as a pool of pages (made once)."""
-        pool = self.__dict__.get("_pool_made")
-        if pool is None:
+        """The tensors as a pool of pages, by reference (made once)."""
+        ref = self.__dict__.get("_pool_made")
+        if ref is None:
             pool = _Pool()
             for x, t in zip(pool.plane, self._tensors):
                 n = t.element_size()
                 x.at, x.page, x.head, x.row = t.data_ptr(), *(s * n for s in t.stride()[:3])
                 x.heads, x.rows, x.bytes = t.shape[1], t.shape[2], n * t[0, 0, 0].numel()
             pool.planes, pool.pages = len(self._tensors), self.pages
-            self._pool_made = pool
-        return pool
+            ref = self._pool_made = ctypes.byref(pool)
+        return ref
 
     def _writes(self):
         """The cache's tensors, about to be written in place."""
-        for t in self._tensors:
-            _writable(t, "the cache")
-        return self._tensors
+        written = self._tensors
+        for t in written:
+            if t.requires_grad or forward_ad._current_level >= 0:
+                _writable(t, "the cache")
+        return written
 
     def copy_pages(self, src, dst, *, stream=None):
         """Page dst[i] becomes a copy of page src[i] (int32 or int64 [n]); a pair with
@@ -389,7 +391,7 @@ class _Paged:
         sb, db = _index(src, "src", dev, n), _index(dst, "dst", dev, n)
         written = self._writes()
         _call(load_library().q4_copy_pages, "q4_copy_pages", dev, stream,
-              (ctypes.byref(self._pool()), src.data_ptr(), sb, dst.data_ptr(), db, n), () if stream is None else (src, dst) + written)
+              (self._pool(), src.data_ptr(), sb, dst.data_ptr(), db, n), () if stream is None else (src, dst) + written)
         _wrote(written)
 
     def attend(self, q, starts, lengths, table, *, window: int = 0, sinks: int = 0, scale=None, out=None, stream=None):
@@ -570,12 +572,11 @@ class PagedCache4(_Paged):
         dev = self.device
         T = slots.shape[0] if isinstance(slots, _Tensor) and slots.dim() == 1 else -1
         sb = _index(slots, "slots", dev, T)
-        shape = (T, self.kv_heads, self.dim)
-        k = _on(stream, torch.empty, shape, dtype=torch.float16, device=dev)
-        v = _on(stream, torch.empty, shape, dtype=torch.float16, device=dev)
-        st = k.stride()
+        kv, D = self.kv_heads, self.dim
+        k = _on(stream, self.k_scale.new_empty, (T, kv, D))
+        v = _on(stream, self.k_scale.new_empty, (T, kv, D))
         _call(load_library().q4_cache4_read, "q4_cache4_read", dev, stream,
-              (self._ref, slots.data_ptr(), sb, T, k.data_ptr(), st[0], st[1], v.data_ptr(), st[0], st[1]),
+              (self._ref, slots.data_ptr(), sb, T, k.data_ptr(), kv * D, D, v.data_ptr(), kv * D, D),
               () if stream is None else (slots,) + self._tensors)
         return k, v
 

@@ -78,7 +78,7 @@ class Pages:
         tokens = int(tokens)
         if starts.shape[0] != self.requests + 1 or not starts.is_contiguous() or not 0 <= tokens <= 1 << 30:
             raise ValueError(f"starts must be contiguous with shape [{self.requests + 1}], got {list(starts.shape)} for {tokens} tokens")
-        slots = _on(stream, torch.empty, tokens, dtype=torch.int32, device=self.device)
+        slots = _on(stream, self.lengths.new_empty, tokens)
         self._run("q4_pages_extend", stream, (starts.data_ptr(), tokens, slots.data_ptr()), (starts,))
         return slots
 
@@ -91,10 +91,10 @@ class Pages:
         pp, pb, n = self._list(parents, "parents")
         cp, cb, _ = self._list(children, "children", n)
         written = self.cache._writes()
-        done = _on(stream, torch.empty, (2, n), dtype=torch.int32, device=self.device)
-        self._run("q4_pages_fork", stream, (ctypes.byref(self.cache._pool()), pp, pb, cp, cb, n, done.data_ptr()),
+        done = _on(stream, self.lengths.new_empty, (2, n))
+        self._run("q4_pages_fork", stream, (self.cache._pool(), pp, pb, cp, cb, n, done.data_ptr()),
                   (parents, children), written)
-        return done[0]
+        return done.select(0, 0)
 
     def free(self, requests, *, stream=None):
         """Gives back the pages of requests (int32 or int64 [n]; one named twice is freed
@@ -115,6 +115,6 @@ class Pages:
         """Moves pages so that those in use come first. Returns int32 [pages]: where each page
         went, -1 for one that was free."""
         written = self.cache._writes()
-        to = _on(stream, torch.empty, self.cache.pages, dtype=torch.int32, device=self.device)
-        self._run("q4_pages_compact", stream, (ctypes.byref(self.cache._pool()), to.data_ptr()), (), written)
+        to = _on(stream, self.counts.new_empty, self.cache.pages)
+        self._run("q4_pages_compact", stream, (self.cache._pool(), to.data_ptr()), (), written)
         return to
