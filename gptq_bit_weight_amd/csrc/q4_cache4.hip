@@ -1,6 +1,6 @@
 // New tokens into a paged cache held in 4 bits, and rows of it back.
 //
-// q4_cache4_append_kernel<WIDE, BF>: keys and values of new tokens, the keys turned by their
+// q4_cache4_append_kernel<WIDE, IL, BF, Q>: keys and values of new tokens, the keys turned by their
 // positions, are quantised in groups of G = 32 .. 256 neighbouring values:
 //   lo, hi = least and largest value (finite ones held within +-65440)
 //   m = binary16(lo), s = binary16(fp32(hi - m) / 15)
@@ -15,13 +15,17 @@
 // definition's and does not hang on the last bits of fp32. (64-bit instructions run at the
 // rate of 32-bit ones here.) Queries are turned as q4_rope_kernel turns them.
 //
-// Bound: memory, for many tokens that of the queries; for a few the launch. A row of a head is
-// taken by as many lanes as it has pieces of 8 values, all in one wave: a lane reads its piece
+// Bound: memory, for many tokens that of the queries (16384 tokens of 64 heads of 128 over 8: 622 MB in 146 us, 4.3
+// TB/s; keys and values alone 49 us, bound by their vector instructions); for a few the launch. A row of keys or
+// values is taken by as many lanes as it has pieces of 8 values, all in one wave: a lane reads its piece
 // and the piece that it is paired with (from the cache beside it), the group's extremes pass
-// through the lanes, a lane writes 4 bytes of codes and the group's first the scale.
+// through the lanes, a lane writes 4 bytes of codes and the group's first the scale. A lane of queries takes both
+// pieces of a pair, several at once.
 //
 // q4_cache4_read_kernel: the rows of given slots as binary16.
 #include <hip/hip_runtime.h>
+
+#include <algorithm>
 
 #include "q4_cache4.h"
 #include "q4_cache4_host.h"
@@ -36,7 +40,7 @@ using namespace q4cache4;
 
 constexpr int NT = 256;
 constexpr int kMaxTokens = 4;     // tokens of a workgroup
-constexpr int kSplitRows = 16384; // rows of queries that get a launch of their own
+constexpr int kUnits = 4;         // units of queries that a lane has in flight
 
 // Keys or values of the cache: strides in bytes.
 struct Plane {
@@ -58,8 +62,18 @@ struct AppendArgs {
     int positions64, slots64;
     int capacity, page_size;          // rows of the cache, rows of a page
     int lanes_shift;                  // log2 of a row's lanes
-    q4::FastDiv div_kv, div_heads, div_ps, div_n;
+    int groups;                       // workgroups (of grid.x) of keys, and of values
+    int units, rotated;               // units of a head of q, those of them that are turned
+    q4::FastDiv div_kv, div_heads, div_units, div_ps, div_n;
 };
+
+// Two values of the tokens' type, rounded.
+template <bool BF>
+__device__ __forceinline__ uint32_t pack_act(float x, float y)
+{
+    if constexpr (BF) return pack_bf16(x, y);
+    else return bitcast<uint32_t>(__builtin_convertvector(ff2{x, y}, h2));
+}
 
 // Place of pair i among a token's 64-bit cosines and sines: a lane reads eight neighbours, and 8
 // of them fall on 2 banks without the gap.
@@ -76,19 +90,89 @@ __device__ __forceinline__ uint32_t code_of(double d, double s, double inv)
     return (uint32_t)fmin(fmax(n, 0.), 15.);
 }
 
-// WIDE: pieces on 16 bytes, rotated by whole ones; IL: interleaved pairs (2i, 2i + 1), else (i, i + n).
+// The queries of tb tokens from t0, in units of one chunk (interleaved pairs, the rest of a head) or of two
+// that are paired, so that a value is read once; cs: cosines and sines [tb][n]. In fp32, rounded once.
 template <bool WIDE, bool IL, bool BF>
-__global__ __launch_bounds__(NT) void q4_cache4_append_kernel(AppendArgs p)
+__device__ __forceinline__ void turn_queries(const AppendArgs& p, const float2* cs, int t0, int tb)
+{
+    constexpr int V = WIDE ? 8 : 1, CR = WIDE ? 8 : IL ? 2 : 1;      // values of a chunk that is copied, and turned
+    const int step = NT * (int)gridDim.y, total = tb * p.H * p.units;
+    for (int base = (int)blockIdx.y * NT + (int)threadIdx.x; base < total; base += kUnits * step) {
+        u4 a[kUnits], b[kUnits];
+        uint16_t* dst[kUnits];
+        int at[kUnits];                // first pair in cs, or -1: a copy
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            const int i = base + u * step;
+            if (i >= total) continue;
+            const int row = (int)q4::fast_div((uint32_t)i, p.div_units), un = i - row * p.units;
+            const int tt = p.TB == 1 ? 0 : (int)q4::fast_div((uint32_t)row, p.div_heads), h = row - tt * p.H;
+            const bool turned = un < p.rotated;
+            const int off = turned ? un * CR : p.rot + (un - p.rotated) * V;
+            const uint16_t* src = p.q + (uint64_t)(uint32_t)(t0 + tt) * p.q_t + (uint64_t)(uint32_t)h * p.q_h + off;
+            dst[u] = p.q_out + (uint64_t)(uint32_t)(t0 + tt) * p.o_t + (uint64_t)(uint32_t)h * p.o_h + off;
+            at[u] = turned ? tt * p.n + (IL ? off / 2 : off) : -1;
+            if constexpr (WIDE) {
+                a[u] = *reinterpret_cast<const u4*>(src);
+                if (!IL && turned) b[u] = *reinterpret_cast<const u4*>(src + p.n);
+            } else {
+                a[u][0] = src[0];
+                if (turned) b[u][0] = src[IL ? 1 : p.n];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            if (base + u * step >= total) continue;
+            const float2* f = cs + max(at[u], 0);
+            if constexpr (WIDE) {
+                if (at[u] >= 0) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float a0 = act_to_f32<BF>((uint16_t)a[u][e]), a1 = act_to_f32<BF>((uint16_t)(a[u][e] >> 16));
+                        if constexpr (IL) {
+                            a[u][e] = pack_act<BF>(a0 * f[e].x - a1 * f[e].y, a1 * f[e].x + a0 * f[e].y);
+                        } else {
+                            const float b0 = act_to_f32<BF>((uint16_t)b[u][e]), b1 = act_to_f32<BF>((uint16_t)(b[u][e] >> 16));
+                            const float2 g0 = f[2 * e], g1 = f[2 * e + 1];
+                            a[u][e] = pack_act<BF>(a0 * g0.x - b0 * g0.y, a1 * g1.x - b1 * g1.y);
+                            b[u][e] = pack_act<BF>(b0 * g0.x + a0 * g0.y, b1 * g1.x + a1 * g1.y);
+                        }
+                    }
+                    if constexpr (!IL) *reinterpret_cast<u4*>(dst[u] + p.n) = b[u];
+                }
+                *reinterpret_cast<u4*>(dst[u]) = a[u];
+            } else {
+                if (at[u] >= 0) {
+                    const float a0 = act_to_f32<BF>((uint16_t)a[u][0]), b0 = act_to_f32<BF>((uint16_t)b[u][0]);
+                    dst[u][0] = f32_to_act<BF>(a0 * f->x - b0 * f->y);
+                    dst[u][IL ? 1 : p.n] = f32_to_act<BF>(b0 * f->x + a0 * f->y);
+                } else {
+                    dst[u][0] = (uint16_t)a[u][0];
+                }
+            }
+        }
+    }
+}
+
+// WIDE: pieces on 16 bytes, rotated by whole ones; IL: interleaved pairs (2i, 2i + 1), else (i, i + n).
+// Q: with queries. (Eight waves a SIMD without them, 48 us against 55 for 16384 tokens of 8 heads of 128; with them memory
+// decides, and the registers are worth more: 146 against 152.)
+template <bool WIDE, bool IL, bool BF, bool Q>
+__global__ __launch_bounds__(NT, Q ? 1 : 8) void q4_cache4_append_kernel(AppendArgs p)
 {
     extern __shared__ double2 cs64[];                                   // [TB][place64(n)]
     const int row64 = place64(p.n);
     float2* cs = reinterpret_cast<float2*>(cs64);                       // or [TB][n]
-    const int t0 = (int)blockIdx.x * p.TB;
+    // A workgroup has rows of keys, of values or of queries only. The three of the same tokens are neighbours, so that the
+    // keys' vector instructions run beside the queries' memory traffic (16384 tokens of 64 heads of 128 over 8: 146 us; the
+    // queries in a launch of their own before 178, last in this one 225). Without queries all keys come first, which
+    // take longest (each beside its values: 60 us against 49, as half of the XCDs have the keys then).
+    const int role = Q ? (int)(blockIdx.x % 3u) : (int)(blockIdx.x >= (uint32_t)p.groups);
+    const int t0 = (Q ? (int)(blockIdx.x / 3u) : (int)blockIdx.x - role * p.groups) * p.TB;
     const int tb = min(p.TB, p.T - t0);
-    // a workgroup has rows of keys, of values or of queries only
-    const bool value = blockIdx.z == 1, query = blockIdx.z == 2;
-    const int rows = query ? p.H : p.KV, step = (int)gridDim.y * (NT >> p.lanes_shift), total = tb * rows;
-    if ((int)blockIdx.y * (NT >> p.lanes_shift) >= total) return;
+    const bool value = role == 1, query = Q && role == 2;
+    const int rows = p.KV, step = (int)gridDim.y * (NT >> p.lanes_shift), total = tb * rows;
+    if (query ? (int)blockIdx.y * NT >= tb * p.H * p.units : (int)blockIdx.y * (NT >> p.lanes_shift) >= total) return;
     for (int i = threadIdx.x; !value && i < tb * p.n; i += NT) {
         const int tt = p.TB == 1 ? 0 : (int)q4::fast_div((uint32_t)i, p.div_n);
         const uint64_t f = (uint64_t)index_at(p.positions, p.positions64, t0 + tt) * p.turns[i - tt * p.n];
@@ -105,10 +189,14 @@ __global__ __launch_bounds__(NT) void q4_cache4_append_kernel(AppendArgs p)
         }
     }
     __syncthreads();
-    const uint16_t* from = query ? p.q + t0 * (uint64_t)p.q_t : value ? p.v + t0 * (uint64_t)p.v_t : p.k + t0 * (uint64_t)p.k_t;
-    const uint32_t token = query ? p.q_t : value ? p.v_t : p.k_t, per_head = query ? p.q_h : value ? p.v_h : p.k_h;
+    if constexpr (Q)
+        if (query) {
+            turn_queries<WIDE, IL, BF>(p, cs, t0, tb);
+            return;
+        }
+    const uint16_t* from = value ? p.v + t0 * (uint64_t)p.v_t : p.k + t0 * (uint64_t)p.k_t;
+    const uint32_t token = value ? p.v_t : p.k_t, per_head = value ? p.v_h : p.k_h;
     const Plane& c = value ? p.vc : p.kc;
-    const q4::FastDiv div_rows = query ? p.div_heads : p.div_kv;
     // A lane's piece is the same in every round, and the lanes of a row stay together. (Lanes past the row's or the
     // rows' end go along with the last piece and row, and store nothing.)
     const int piece = (int)threadIdx.x & ((1 << p.lanes_shift) - 1);
@@ -117,10 +205,10 @@ __global__ __launch_bounds__(NT) void q4_cache4_append_kernel(AppendArgs p)
     const bool turned = !value && at < p.rot, second = !IL && at >= p.n;    // (second half of the rotated values, WIDE)
     for (int row0 = (int)blockIdx.y * (NT >> p.lanes_shift); row0 < total; row0 += step) {
         const int my_row = row0 + ((int)threadIdx.x >> p.lanes_shift), row = min(my_row, total - 1);
-        const int tt = p.TB == 1 ? 0 : (int)q4::fast_div((uint32_t)row, div_rows);
+        const int tt = p.TB == 1 ? 0 : (int)q4::fast_div((uint32_t)row, p.div_kv);
         const int t = t0 + tt, h = row - tt * rows;
         const uint16_t* src = from + (uint64_t)(uint32_t)tt * token + (uint64_t)(uint32_t)h * per_head;
-        const long long slot = query ? 0 : index_at(p.slots, p.slots64, t);
+        const long long slot = index_at(p.slots, p.slots64, t);
         u4 x;                                  // the lane's values
         if constexpr (WIDE) {
             x = *reinterpret_cast<const u4*>(src + at);
@@ -153,16 +241,7 @@ __global__ __launch_bounds__(NT) void q4_cache4_append_kernel(AppendArgs p)
             auto pair_of = [&](int e) { return IL ? (at + e) >> 1 : at + e >= p.n ? at + e - p.n : at + e; };
             const int pair0 = second ? at - p.n : at;
             float y[8];
-            if (query) {
-                const float2* f = cs + tt * p.n;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    y[e] = act_to_f32<BF>((uint16_t)(x[e / 2] >> 16 * (e & 1)));
-                    if (!WIDE && at + e >= p.rot) continue;
-                    const float2 w = f[WIDE && !IL ? pair0 + e : pair_of(e)];
-                    y[e] = y[e] * w.x + b[e] * w.y;
-                }
-            } else {
+            {
                 const double2* f = cs64 + tt * row64;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -175,22 +254,10 @@ __global__ __launch_bounds__(NT) void q4_cache4_append_kernel(AppendArgs p)
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                if constexpr (BF) x[e] = pack_bf16(y[2 * e], y[2 * e + 1]);
-                else x[e] = bitcast<uint32_t>(__builtin_convertvector(ff2{y[2 * e], y[2 * e + 1]}, h2));
+                x[e] = pack_act<BF>(y[2 * e], y[2 * e + 1]);
             }
         }
         const bool on = my_row < total && inside;
-        if (query) {
-            if (!on) continue;
-            uint16_t* to = p.q_out + (uint64_t)(uint32_t)t * p.o_t + (uint64_t)(uint32_t)h * p.o_h + at;
-            if constexpr (WIDE) {
-                *reinterpret_cast<u4*>(to) = x;
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) to[e] = (uint16_t)(x[e / 2] >> 16 * (e & 1));
-            }
-            continue;
-        }
         // (not branched over: the lanes of a row pass their extremes on)
         float lo = INFINITY, hi = -INFINITY, odd = 0.f, v[8];
 #pragma unroll
@@ -241,11 +308,17 @@ __global__ __launch_bounds__(NT) void q4_cache4_append_kernel(AppendArgs p)
     }
 }
 
+template <bool WIDE, bool IL, bool BF>
+void launch_append(const AppendArgs& p, dim3 grid, size_t lds, hipStream_t stream)
+{
+    if (p.H) hipLaunchKernelGGL((q4_cache4_append_kernel<WIDE, IL, BF, true>), grid, dim3(NT), lds, stream, p);
+    else hipLaunchKernelGGL((q4_cache4_append_kernel<WIDE, IL, BF, false>), grid, dim3(NT), lds, stream, p);
+}
+
 template <bool WIDE, bool IL>
 void launch_append(const AppendArgs& p, dim3 grid, size_t lds, bool bf16, hipStream_t stream)
 {
-    if (bf16) hipLaunchKernelGGL((q4_cache4_append_kernel<WIDE, IL, true>), grid, dim3(NT), lds, stream, p);
-    else hipLaunchKernelGGL((q4_cache4_append_kernel<WIDE, IL, false>), grid, dim3(NT), lds, stream, p);
+    bf16 ? launch_append<WIDE, IL, true>(p, grid, lds, stream) : launch_append<WIDE, IL, false>(p, grid, lds, stream);
 }
 
 struct ReadArgs {
@@ -391,25 +464,23 @@ q4_status q4_cache4_append(const q4_cache4* c, const uint16_t* k, int64_t k_toke
     p.page_size = c->page_size;
     p.capacity = c->pages * c->page_size;
     p.lanes_shift = log2_of(c->dim / 8);
-    // Many tokens' queries go by q4_rope_kernel, which reads a value once and has more of them under way
-    // (16384 tokens of 64 heads of 128 over 8: 225 us in one launch, 161 in two).
-    if (p.H && (long long)tokens * heads > kSplitRows) {
-        if (q4_status st = q4_rotary_apply(r, q, q_token, q_head, q_out, out_token, out_head, positions, position_bits, tokens, heads, 0,
-                                           bf16, stream); st != Q4_OK) return st;
-        p.H = 0;
-    }
     // Few tokens: a workgroup for each 256 lanes of each token, so that a decode step
     // spreads over the CUs. Many: whole tokens, kMaxTokens to a workgroup.
-    const int slices = (((p.H > p.KV ? p.H : p.KV) << p.lanes_shift) + NT - 1) / NT;
+    const bool il = r && r->interleaved;
+    const int turn = wide ? 8 : il ? 2 : 1;
+    p.rotated = p.rot / (il ? turn : 2 * turn);
+    p.units = p.rotated + (p.dim - p.rot) / (wide ? 8 : 1);
+    const int lanes = std::max(p.KV << p.lanes_shift, p.H * p.units), slices = (lanes + NT - 1) / NT;
     const bool few = (long long)p.T * slices <= 4096;
     p.TB = few ? 1 : kMaxTokens;
     p.div_kv = q4::make_fastdiv((uint32_t)p.KV);
     p.div_heads = q4::make_fastdiv((uint32_t)(p.H > 0 ? p.H : 1));
+    p.div_units = q4::make_fastdiv((uint32_t)p.units);
     p.div_ps = q4::make_fastdiv((uint32_t)p.page_size);
     p.div_n = q4::make_fastdiv((uint32_t)(p.n > 0 ? p.n : 1));
-    const dim3 grid((p.T + p.TB - 1) / p.TB, few ? slices : 1, p.H ? 3 : 2);
+    p.groups = (p.T + p.TB - 1) / p.TB;
+    const dim3 grid((p.H ? 3u : 2u) * (unsigned)p.groups, few ? slices : 1);
     const size_t lds = (size_t)p.TB * place64(p.n) * sizeof(double2);
-    const bool il = r && r->interleaved;
     if (wide) il ? launch_append<true, true>(p, grid, lds, bf16 != 0, stream) : launch_append<true, false>(p, grid, lds, bf16 != 0, stream);
     else il ? launch_append<false, true>(p, grid, lds, bf16 != 0, stream) : launch_append<false, false>(p, grid, lds, bf16 != 0, stream);
     const hipError_t e = hipGetLastError();
