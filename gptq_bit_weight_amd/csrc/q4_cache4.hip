@@ -158,7 +158,7 @@ __device__ __forceinline__ void turn_queries(const AppendArgs& p, const float2* 
 // Q: with queries. (Eight waves a SIMD without them, 48 us against 55 for 16384 tokens of 8 heads of 128; with them memory
 // decides, and the registers are worth more: 146 against 152.)
 template <bool WIDE, bool IL, bool BF, bool Q>
-__global__ __launch_bounds__(NT, Q ? 1 : 8) void q4_cache4_append_kernel(AppendArgs p)
+__global__ __launch_bounds__(NT, WIDE && !Q ? 8 : 1) void q4_cache4_append_kernel(AppendArgs p)
 {
     extern __shared__ double2 cs64[];                                   // [TB][place64(n)]
     const int row64 = place64(p.n);

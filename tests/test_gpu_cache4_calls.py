@@ -124,7 +124,7 @@ def test_no_tokens_and_no_requests():
 @pytest.mark.parametrize("dt", [F16, BF16])
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 def test_many_tokens_with_queries(dt, layout):
-    """Queries that a launch of their own turns, bit for bit as Rotary does, in place too."""
+    """Queries beside many keys and values, bit for bit as Rotary turns them, in place too."""
     import gptq_bit_weight_amd as q4
     announce(f"append4 many queries {dt} {layout}")
     T, H, kv, D, ps = 3001, 8, 2, 128, 16
@@ -140,11 +140,11 @@ def test_many_tokens_with_queries(dt, layout):
     assert torch.equal(q, want)
 
 
-def spaced(cache, gap):
-    """The same cache with pages `gap` bytes of codes and gap / 8 of scales apart."""
+def spaced(cache, k_gap, v_gap):
+    """The same cache with pages k_gap and v_gap bytes of codes and an eighth of that of scales apart."""
     import gptq_bit_weight_amd as q4
     out = []
-    for t, step in ((cache.k, gap), (cache.v, gap), (cache.k_scale, gap // 16), (cache.v_scale, gap // 16)):
+    for t, step in ((cache.k, k_gap), (cache.v, v_gap), (cache.k_scale, k_gap // 16), (cache.v_scale, v_gap // 16)):
         span = (t.shape[0] - 1) * step + t[0].numel()
         mem = torch.empty(span, dtype=t.dtype, device="cuda")
         s = mem.as_strided(t.shape, (step,) + t[0].stride())
@@ -153,17 +153,17 @@ def spaced(cache, gap):
     return q4.PagedCache4(*out)
 
 
-@pytest.mark.parametrize("gap", [1 << 20, 3 << 30, 5 << 30])
-def test_offsets_past_32_bits(gap):
-    """Pages gigabytes apart (14 of them: to 42 GiB, where 32 bits count 16 bytes each, and to 70 GiB, where they
+@pytest.mark.parametrize("k_gap,v_gap", [(1 << 20, 1 << 20), (3 << 30, 1 << 20), (1 << 20, 3 << 30), (1 << 20, 5 << 30)])
+def test_offsets_past_32_bits(k_gap, v_gap):
+    """Pages of keys or of values gigabytes apart (14 of them: to 42 GiB, where 32 bits count 16 bytes each, and to 70 GiB, where they
     do not) give what neighbouring ones do."""
     H, kv, D, G, ps = 8, 2, 128, 64, 16
     for dt, news, lens in ((F16, [1, 1], [100, 60]), (BF16, [100, 40], [100, 60])):
-        announce(f"attend4 pages {gap} bytes apart {dt} news={news}")
+        announce(f"attend4 pages {k_gap} and {v_gap} bytes apart {dt} news={news}")
         q, cache, starts, lengths, table = make(dt, H, kv, D, G, ps, news, lens, seed=3)
         want = cache.attend(q, starts, lengths, table)
-        far = spaced(cache, gap)
-        assert far.k.stride(0) == gap
+        far = spaced(cache, k_gap, v_gap)
+        assert far.k.stride(0) == k_gap and far.v.stride(0) == v_gap
         got = far.attend(q, starts, lengths, table)
         # (where 32 bits do not suffice the keys are found one by one, by the same kernel: the sums are the same)
         assert torch.equal(got, want)
