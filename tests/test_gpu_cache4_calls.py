@@ -277,3 +277,53 @@ def test_two_captured_graphs(news, lens):
             assert torch.equal(graphs[k][1], want), (i, k)
             for a, b in zip(sides[k][1]._tensors, sides[2 + k][1]._tensors):
                 assert torch.equal(a, b), (i, k)
+
+
+@pytest.mark.parametrize("ps", [1, 3, 512])
+def test_pages_of_one_row_and_of_many(ps):
+    run(F16, 4, 2, 64, 32, ps, [1, 1], [70, 515], seed=ps)
+    run(BF16, 4, 2, 128, 128, ps, [90, 1], [300, 65], window=80, sinks=2, seed=ps)
+
+
+@pytest.mark.parametrize("dt", [F16, BF16])
+@pytest.mark.parametrize("H,kv,D", [(17, 1, 64), (64, 1, 128), (65, 1, 64), (120, 1, 32), (80, 40, 64)])
+def test_large_groups_and_many_heads(dt, H, kv, D):
+    run(dt, H, kv, D, 32, 16, [1, 1, 2], [90, 700, 33], seed=H)
+
+
+def test_thousands_of_requests():
+    lens = [1 + (7 * i) % 90 for i in range(3000)]
+    run(F16, 4, 2, 64, 64, 16, [1] * 3000, lens, seed=1)
+
+
+@pytest.mark.parametrize("dt", [F16, BF16])
+@pytest.mark.parametrize("news,lens", [([1] * 20, [50 + i for i in range(20)]), ([70], [200])])
+def test_queries_that_are_not_finite(dt, news, lens):
+    """Such a token's heads are NaN, the others are what they are without it. (Not always to the bit: rows of one wave
+    put a growth of their maxima off together, so a row's weights may be rounded at another power of its sum; the derived
+    tolerance holds at any.)"""
+    announce(f"attend4 queries not finite {dt} news={news[:3]}")
+    q, cache, starts, lengths, table = make(dt, 4, 2, 128, 32, 16, news, lens, seed=4)
+    bad = torch.zeros(q.shape[:2], dtype=torch.bool)
+    k, v = (rows_of(x, table, lens) for x in pools(cache))
+    ref, tol = attention(q, k, v, news, lens, 0, 0, None, F16)
+    for i, x in ((0, math.inf), (3, -math.inf), (17, math.nan)):
+        q[i, i % 4, 5] = x
+        bad[i, i % 4] = True
+    got = cache.attend(q, starts, lengths, table)
+    assert not got[bad].isfinite().any()
+    check(got[~bad], ref[~bad], tol[~bad])
+
+
+@pytest.mark.parametrize("index", [torch.int32, torch.int64])
+def test_read_by_either_index(index):
+    import gptq_bit_weight_amd as q4
+    announce(f"read4 {index}")
+    cache = q4.PagedCache4.empty(5, 3, 7, 96)
+    k, v = tokens(F16, 35, 3, 96, 1), tokens(F16, 35, 3, 96, 2)
+    cache.append(k, v, torch.arange(35, device="cuda"))
+    slots = torch.tensor([34, 0, -1, 35, 12, 12], dtype=index, device="cuda")
+    a, b = cache.read(slots)
+    whole = cache.read(torch.arange(35, device="cuda"))
+    for x, y in zip((a, b), whole):
+        assert torch.equal(x[[0, 1, 4, 5]], y[[34, 0, 12, 12]]) and not x[[2, 3]].any()
