@@ -36,7 +36,7 @@
 // codes, one packed multiply-add for two values, in the steps between the products, so the products
 // are those of a binary16 cache whatever the queries' type (bfloat16 queries brought into binary16's
 // range by a power of two a row). The unpacking is some 126 vector instructions a wave and 64-key tile beside
-// the 950: 2048 new tokens over 8192 keys, 32 heads of 128 over 8, 294 us, 820 TFLOP/s, of
+// the 950: 2048 new tokens over 8192 keys, 32 heads of 128 over 8, 290 us, 830 TFLOP/s, of
 // which 5 join (the same call over a bfloat16 cache 270).
 #pragma once
 

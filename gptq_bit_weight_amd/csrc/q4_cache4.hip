@@ -15,8 +15,8 @@
 // definition's and does not hang on the last bits of fp32. (64-bit instructions run at the
 // rate of 32-bit ones here.) Queries are turned as q4_rope_kernel turns them.
 //
-// Bound: memory, for many tokens that of the queries (16384 tokens of 64 heads of 128 over 8: 622 MB in 146 us, 4.3
-// TB/s; keys and values alone 49 us, bound by their vector instructions); for a few the launch. A row of keys or
+// Bound: memory, for many tokens that of the queries (16384 tokens of 64 heads of 128 over 8: 599 MB in 120 us, 5.0
+// TB/s; keys and values alone 48 us, bound by their vector instructions); for a few the launch. A row of keys or
 // values is taken by as many lanes as it has pieces of 8 values, all in one wave: a lane reads its piece
 // and the piece that it is paired with (from the cache beside it), the group's extremes pass
 // through the lanes, a lane writes 4 bytes of codes and the group's first the scale. A lane of queries takes both
@@ -164,8 +164,8 @@ __global__ __launch_bounds__(NT, WIDE && !Q ? 8 : 1) void q4_cache4_append_kerne
     const int row64 = place64(p.n);
     float2* cs = reinterpret_cast<float2*>(cs64);                       // or [TB][n]
     // A workgroup has rows of keys, of values or of queries only. The three of the same tokens are neighbours, so that the
-    // keys' vector instructions run beside the queries' memory traffic (16384 tokens of 64 heads of 128 over 8: 146 us; the
-    // queries in a launch of their own before 178, last in this one 225). Without queries all keys come first, which
+    // keys' vector instructions run beside the queries' memory traffic (16384 tokens of 64 heads of 128 over 8, each
+    // call after one that fills the cache: 146 us; the queries in a launch of their own before 178, last in this one 225). Without queries all keys come first, which
     // take longest (each beside its values: 60 us against 49, as half of the XCDs have the keys then).
     const int role = Q ? (int)(blockIdx.x % 3u) : (int)(blockIdx.x >= (uint32_t)p.groups);
     const int t0 = (Q ? (int)(blockIdx.x / 3u) : (int)blockIdx.x - role * p.groups) * p.TB;
