@@ -43,7 +43,8 @@ EXPORTED_SYMBOLS = (
     "q4_matmul_static",
     "q4_rotary_make", "q4_rotary_free", "q4_rotary_plan", "q4_rotary_apply", "q4_cache_append",
     "q4_attend_workspace", "q4_attend", "q4_attend_ex",
-    "q4_check_cache4", "q4_cache4_append", "q4_cache4_read", "q4_attend4_workspace", "q4_attend4",
+    "q4_check_cache4", "q4_cache4_append", "q4_cache4_read", "q4_attend4_workspace",
+    "q4_attend4_workspace_for", "q4_attend4",
     "q4_copy_pages", "q4_pages_workspace", "q4_pages_extend", "q4_pages_fork", "q4_pages_free", "q4_pages_trim", "q4_pages_compact",
     "q4_check_adapters", "q4_adapters_make", "q4_adapters_free", "q4_adapters_load", "q4_adapters_clear",
     "q4_matmul_adapters",
@@ -139,6 +140,8 @@ def load_library():
     lib.q4_attend4.argtypes = lib.q4_attend_ex.argtypes[:-1] + [I, P]
     lib.q4_attend4_workspace.argtypes = [P, I]
     lib.q4_attend4_workspace.restype = ctypes.c_size_t
+    lib.q4_attend4_workspace_for.argtypes = [P, I, I, I, I]
+    lib.q4_attend4_workspace_for.restype = ctypes.c_size_t
     lib.q4_check_cache4.argtypes = [P]
     lib.q4_cache4_append.argtypes = lib.q4_cache_append.argtypes[:-1] + [I, P]
     lib.q4_cache4_read.argtypes = [P, P, I, I, P, L, L, P, L, L, P]

@@ -442,6 +442,8 @@ class _Paged:
             table, ts = _table_rows(table, stream)
         os_ = out.stride()
         need = self._need.get(H) or self._workspace_bytes(H)
+        if self._four and T * H > 256 * self.kv_heads * B:       # (chunks that may be long)
+            need = load_library().q4_attend4_workspace_for(self._ref, H, T, B, width)
         # (under capture the call's own: a graph may replay beside other work of the
         # stream it was captured on)
         ws = _Workspace() if _capturing(dev, stream) else _workspace(dev, stream)

@@ -17,6 +17,10 @@ hipError_t launch_attend4_rows(const q4attend::Args& p, bool bf16, bool pages_of
 
 hipError_t launch_attend4_tiles(const q4attend::Args& p, int grid, bool bf16, bool pages_of_16, hipStream_t stream);
 
+// (0: more than 2^30 bytes)
+size_t attend4_halves_bytes(int requests, int kv_heads, int max_len, int dim);
+hipError_t launch_attend4_halves(q4attend::Args p, int grid, bool bf16, char* scratch, hipStream_t stream);
+
 namespace {
 
 int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
@@ -78,6 +82,19 @@ q4_status check_attend4(const q4_cache4* c, int heads, const char* who)
     if (heads < 1 || heads % c->kv_heads)
         return fail(Q4_ERR_INVALID_ARG, "%s: %d heads over %d cached heads", who, heads, c->kv_heads);
     return Q4_OK;
+}
+
+// Of 4 bits: keys and values are brought into binary16 first where a request has so many rows on average, so that
+// enough workgroups read what was unpacked once. (Rows, keys; unpacked by every workgroup and once: 32 heads of 128
+// over 8, 32768 over 8192 669 us and 569, 8192 over 8192 302 and 276, 8192 over 2048 71 and 69, 4 requests of
+// 2048 over 8192 325 and 307, 8 of 1024 over 4000 175 and 179; over 32, 2048 over 2048 72 and 76, 4 of 1024 over
+// 2000 159 and 175; heads of 64, 6 of 2800 in a window of 1024 95 and 92; heads of 256, 8192 over 4096 262 and 237.)
+constexpr int kHalvesRows = 2560;
+int max_length(int table_width, int page_size) { return (int)std::min<long long>((long long)table_width * page_size, 1 << 30); }
+size_t halves_bytes(int kv_heads, int dim, int g, int tokens, int requests, int max_len)
+{
+    if ((long long)tokens * g < (long long)kHalvesRows * requests) return 0;
+    return attend4_halves_bytes(requests, kv_heads, max_len, dim);
 }
 
 size_t workspace_bytes_of(int dim, int cu, bool four)
@@ -147,8 +164,7 @@ q4_status attend(const char* who, q4attend::Args& p, const View* caches, int nca
     p.g = g;
     p.chunks = p.dim / 8;
     p.table_stride = (int)a.table_stride;
-    const long long rows = (long long)a.table_width * p.page_size;
-    p.max_len = (int)(rows < (1 << 30) ? rows : (1 << 30));
+    p.max_len = max_length(a.table_width, p.page_size);
     // (a window that no key can lie outside is none; the kernels' 32-bit positions less a
     // window then stay in range)
     p.window = a.window >= p.max_len ? 0 : a.window;
@@ -199,7 +215,10 @@ q4_status attend(const char* who, q4attend::Args& p, const View* caches, int nca
     // (most units there can be: a whole one each share of the work, a partial one each row tile and head)
     const int units = (int)(row_tiles * p.KV + p.workers);
     hipError_t e;
-    if (a.four) e = many ? launch_attend4_tiles(p, units, a.bf16, pg, stream) : launch_attend4_rows(p, a.bf16, pg, wide, stream);
+    const size_t halves = a.four && many ? halves_bytes(p.KV, p.dim, g, a.tokens, a.requests, p.max_len) : 0;
+    if (halves && a.workspace_bytes >= need + halves)
+        e = launch_attend4_halves(p, units, a.bf16, static_cast<char*>(a.workspace) + need, stream);
+    else if (a.four) e = many ? launch_attend4_tiles(p, units, a.bf16, pg, stream) : launch_attend4_rows(p, a.bf16, pg, wide, stream);
     else e = many ? launch_attend_tiles(p, units, a.bf16, pg, stream) : launch_attend_rows(p, a.bf16, pg, stream);
     return e == hipSuccess ? Q4_OK : fail(Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
 }
@@ -264,6 +283,16 @@ size_t q4_attend4_workspace(const q4_cache4* c, int heads)
     int dev = -1, cu = 0;
     if (q4::check_attend4(c, heads, "q4_attend4_workspace") != Q4_OK || q4::device_info(&dev, &cu) != Q4_OK) return 0;
     return q4::workspace_bytes_of(c->dim, cu, true);
+}
+
+size_t q4_attend4_workspace_for(const q4_cache4* c, int heads, int tokens, int requests, int table_width)
+{
+    const size_t least = q4_attend4_workspace(c, heads);
+    if (!least || tokens < 1 || requests < 1 || table_width < 1) return least;
+    int dev = -1, cu = 0;
+    if (q4::device_info(&dev, &cu) != Q4_OK) return 0;
+    const size_t halves = q4::halves_bytes(c->kv_heads, c->dim, heads / c->kv_heads, tokens, requests, q4::max_length(table_width, c->page_size));
+    return std::max(least, halves ? q4::tiles_bytes(c->dim, cu) + halves : 0);
 }
 
 q4_status q4_attend4(const q4_cache4* c, const uint16_t* q, int64_t q_token, int64_t q_head, int heads, int tokens,

@@ -1,8 +1,9 @@
 // Attention over a paged cache for many rows a request: chunks of prompts.
 //
-// q4_attend_tiles_kernel<D, BF, PG, SK, C4>: head rows of D values in LDS, BF
+// q4_attend_tiles_kernel<D, BF, PG, SK, C4, H16>: head rows of D values in LDS, BF
 // (bfloat16), PG (pages of a multiple of 16 rows), SK (sinks: first keys that stay
-// visible beside a window), C4 (a cache held in 4 bits, q4_cache4.h).
+// visible beside a window), C4 (a cache held in 4 bits, q4_cache4.h), H16 (keys and values
+// of binary16 whatever the queries are).
 //
 // Bound: the matrix cores (4 dim flops for each visible key of a row), with the
 // exponentials close behind: a 64-key tile of 32 rows is 32 products of 32 cycles
@@ -85,11 +86,11 @@ __device__ __forceinline__ Span span(const Args& p, const Request& r)
     return s;
 }
 
-template <int D, bool BF, bool PG, bool SK, bool C4>
+template <int D, bool BF, bool PG, bool SK, bool C4, bool H16>
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_kernel(Args p)
 {
     using SH = Shape<D>;
-    constexpr bool BI = BF && !C4;             // the products' operands are bfloat16
+    constexpr bool BI = BF && !H16;            // the products' operands are bfloat16
     constexpr int KT = SH::KT, NS = SH::NS, WR = SH::WR;
     constexpr int HH = KT / 32;                // 32-key halves of a tile
     constexpr int PITCH = 2 * D, CPR = D / 8, RPI = 64 / CPR;
@@ -405,7 +406,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
             const int at = 16 * ks + 8 * lhi;
             qf[ks] = at < p.dim ? *reinterpret_cast<const u4*>(qp + at) : u4{0, 0, 0, 0};
         }
-        if constexpr (C4 && BF) {
+        if constexpr (H16 && BF) {
             uint32_t top = 0;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) top = max(top, q4cache4::largest_bf16(qf[ks]));
@@ -821,19 +822,34 @@ __global__ __launch_bounds__(64 * JW) void q4_attend_join_kernel(Args p)
     p.joins->count = 0;
 }
 
-template <int D, bool SK, bool C4>
-hipError_t launch_tiles(const Args& p, int grid, bool bf16, bool pg, hipStream_t stream)
+// What joins the splits of a launch before it.
+template <int D>
+hipError_t launch_join(const Args& p, bool bf16, hipStream_t stream)
 {
-    const dim3 g(grid), block(64 * NW);
-    if (bf16 && pg) hipLaunchKernelGGL((q4_attend_tiles_kernel<D, true, true, SK, C4>), g, block, 0, stream, p);
-    else if (bf16) hipLaunchKernelGGL((q4_attend_tiles_kernel<D, true, false, SK, C4>), g, block, 0, stream, p);
-    else if (pg) hipLaunchKernelGGL((q4_attend_tiles_kernel<D, false, true, SK, C4>), g, block, 0, stream, p);
-    else hipLaunchKernelGGL((q4_attend_tiles_kernel<D, false, false, SK, C4>), g, block, 0, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.unsplit) return e;
     if (bf16) hipLaunchKernelGGL((q4_attend_join_kernel<D, true>), dim3(kJoinGrid), dim3(64 * JW), 0, stream, p);
     else hipLaunchKernelGGL((q4_attend_join_kernel<D, false>), dim3(kJoinGrid), dim3(64 * JW), 0, stream, p);
     return hipGetLastError();
+}
+
+template <int D, bool SK, bool C4>
+hipError_t launch_tiles(const Args& p, int grid, bool bf16, bool pg, hipStream_t stream)
+{
+    const dim3 g(grid), block(64 * NW);
+    if (bf16 && pg) hipLaunchKernelGGL((q4_attend_tiles_kernel<D, true, true, SK, C4, C4>), g, block, 0, stream, p);
+    else if (bf16) hipLaunchKernelGGL((q4_attend_tiles_kernel<D, true, false, SK, C4, C4>), g, block, 0, stream, p);
+    else if (pg) hipLaunchKernelGGL((q4_attend_tiles_kernel<D, false, true, SK, C4, C4>), g, block, 0, stream, p);
+    else hipLaunchKernelGGL((q4_attend_tiles_kernel<D, false, false, SK, C4, C4>), g, block, 0, stream, p);
+    return launch_join<D>(p, bf16, stream);
+}
+
+// Queries of bfloat16 over keys and values of binary16, in pages of a multiple of 16 rows.
+template <int D, bool SK>
+hipError_t launch_halves(const Args& p, int grid, hipStream_t stream)
+{
+    hipLaunchKernelGGL((q4_attend_tiles_kernel<D, true, true, SK, false, true>), dim3(grid), dim3(64 * NW), 0, stream, p);
+    return launch_join<D>(p, true, stream);
 }
 
 }  // namespace

@@ -663,6 +663,12 @@ q4_status q4_cache4_read(const q4_cache4* c, const void* slots, int slot_bits, i
  * whole. The workspace is as for q4_attend.
  */
 size_t q4_attend4_workspace(const q4_cache4* c, int heads);
+
+/* The workspace with which a call of these sizes is fastest, at least that of
+ * q4_attend4_workspace: chunks of some thousand rows (tokens times heads of a group) a request on average
+ * and more bring the keys and values into binary16 there first, if they take no more than 2^30
+ * bytes (2 dim a row and side, of requests * table_width pages). */
+size_t q4_attend4_workspace_for(const q4_cache4* c, int heads, int tokens, int requests, int table_width);
 q4_status q4_attend4(const q4_cache4* c, const uint16_t* q, int64_t q_token, int64_t q_head, int heads, int tokens,
                      const int32_t* starts, const int32_t* lengths, const int32_t* table, int table_width,
                      int64_t table_stride, int requests, int window, int sinks, float scale, uint16_t* out,

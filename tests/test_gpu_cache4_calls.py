@@ -228,7 +228,7 @@ def test_threads_and_streams():
     assert not wrong
 
 
-@pytest.mark.parametrize("news,lens", [([1] * 5, [900, 30, 50, 700, 2000]), ([80, 3], [400, 700])])
+@pytest.mark.parametrize("news,lens", [([1] * 5, [900, 30, 50, 700, 2000]), ([80, 3], [400, 700]), ([1400], [1700])])
 def test_two_captured_graphs(news, lens):
     """Two graphs of append and attend over caches of their own, replayed in turn while lengths grow on the
     device, against eager calls."""
@@ -327,3 +327,70 @@ def test_read_by_either_index(index):
     whole = cache.read(torch.arange(35, device="cuda"))
     for x, y in zip((a, b), whole):
         assert torch.equal(x[[0, 1, 4, 5]], y[[34, 0, 12, 12]]) and not x[[2, 3]].any()
+
+
+@pytest.mark.parametrize("dt", [F16, BF16])
+@pytest.mark.parametrize("H,kv,D,G,ps", [(8, 2, 128, 32, 16), (16, 2, 64, 64, 7), (12, 3, 256, 128, 64), (8, 2, 96, 32, 1)])
+@pytest.mark.parametrize("news,lens,window,sinks", [
+    ([700], [900], 0, 0), ([1300, 0, 700], [1300, 50, 2500], 0, 0), ([900, 1100], [400, 1111], 0, 0), ([800], [3000], 300, 0),
+    ([800, 1400], [3001, 2000], 170, 37), ([700], [0], 0, 0)])
+def test_long_chunks(dt, H, kv, D, G, ps, news, lens, window, sinks):
+    """Chunks whose keys and values are brought into binary16 once."""
+    import ctypes
+    import gptq_bit_weight_amd as q4
+    from gptq_bit_weight_amd.attention import _Cache4
+    assert sum(news) * H // kv >= 2560 * len(news)
+    width = max(max(-(-m // ps) for m in lens), 1)
+    c = _Cache4(*[1 << 20] * 4, *[(ctypes.c_int64 * 3)(0, 0, 0)] * 4, width * len(lens) + 3, kv, ps, D, G)
+    lib = q4.load_library()
+    full = lib.q4_attend4_workspace_for(ctypes.byref(c), H, sum(news), len(news), width)
+    assert full > 4 * len(news) * kv * width * ps * D
+    run(dt, H, kv, D, G, ps, news, lens, window=window, sinks=sinks, seed=D + len(news))
+
+
+def test_long_chunks_in_less_memory():
+    """With the least workspace every workgroup unpacks for itself: another order of the sums, the same bound."""
+    import ctypes
+    import gptq_bit_weight_amd as q4
+    announce("attend4 long chunk, least workspace")
+    H, kv, D, ps, news, lens = 8, 2, 128, 16, [1000, 700], [1300, 2000]
+    lib = q4.load_library()
+    for dt in (F16, BF16):
+        q, cache, starts, lengths, table = make(dt, H, kv, D, 32, ps, news, lens, seed=9)
+        least = lib.q4_attend4_workspace(cache._ref, H)
+        full = lib.q4_attend4_workspace_for(cache._ref, H, sum(news), 2, table.shape[1])
+        assert 0 < least < full
+        # few rows, or more than 2^30 bytes: no more than the least
+        assert lib.q4_attend4_workspace_for(cache._ref, H, 100, 2, table.shape[1]) == least
+        assert lib.q4_attend4_workspace_for(cache._ref, H, 4000, 2, 1 << 20) == least
+        assert lib.q4_attend4_workspace_for(cache._ref, H, 0, 0, 0) == least
+        ws = torch.zeros(least, dtype=torch.uint8, device="cuda")
+        out = torch.empty_like(q)
+        st = lib.q4_attend4(cache._ref, q.data_ptr(), q.stride(0), q.stride(1), H, q.shape[0], starts.data_ptr(), lengths.data_ptr(),
+                            table.data_ptr(), table.shape[1], table.stride(0), 2, 0, 0, D ** -0.5, out.data_ptr(), out.stride(0), out.stride(1),
+                            ws.data_ptr(), least, int(dt is BF16), torch.cuda.current_stream().cuda_stream)
+        assert st == 0
+        k, v = (rows_of(x, table, lens) for x in pools(cache))
+        ref, tol = attention(q, k, v, news, lens, 0, 0, None, F16)
+        check(out, ref, tol)
+        check(cache.attend(q, starts, lengths, table), ref, tol)
+
+
+@pytest.mark.parametrize("dt", [F16, BF16])
+def test_what_is_not_finite_in_long_chunks(dt):
+    H, kv, D, G, ps, window, sinks = 8, 2, 64, 32, 16, 150, 5
+    news, lens = [700, 900], [1000, 950]
+    announce(f"attend4 long chunks not finite {dt}")
+    q, cache, starts, lengths, table = make(dt, H, kv, D, G, ps, news, lens, seed=5)
+    plain_k, plain_v = (rows_of(x, table, lens) for x in pools(cache))
+    none = torch.zeros(q.shape, dtype=torch.bool)
+    see, at = seen_by(news, lens, window, sinks), [0, 700, 1600]
+    for b, j, h, g, t in ((0, 7, 0, 1, "k"), (0, 400, 1, 0, "v"), (0, 999, 0, 0, "v"), (1, 60, 1, 1, "k"), (1, 300, 0, 1, "v"), (1, 949, 1, 0, "k")):
+        (cache.k_scale if t == "k" else cache.v_scale)[int(table[b, j // ps]), h, j % ps, g] = math.nan
+        cols = slice(None) if t == "k" else slice(g * G, (g + 1) * G)
+        none[at[b]:at[b + 1], h * (H // kv):(h + 1) * (H // kv), cols] |= see[b][:, j, None, None]
+    got = cache.attend(q, starts, lengths, table, window=window, sinks=sinks)
+    ref, tol = attention(q, plain_k, plain_v, news, lens, window, sinks, None, F16)
+    none = none.cuda()
+    assert torch.equal(got.isnan(), none)
+    check(torch.where(none, 0, got), torch.where(none, 0, ref), torch.where(none, 0, tol))
