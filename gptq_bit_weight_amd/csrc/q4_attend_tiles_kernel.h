@@ -38,7 +38,7 @@
 // are those of a binary16 cache whatever the queries' type (bfloat16 queries brought into binary16's
 // range by a power of two a row). The unpacking is some 126 vector instructions a wave and 64-key tile beside
 // the 950: 2048 new tokens over 8192 keys, 32 heads of 128 over 8, 290 us, 830 TFLOP/s, of
-// which 5 join (the same call over a bfloat16 cache 270).
+// which 5 join; over tiles that were unpacked once before (q4_attend4_halves.hip) 265 with the unpacking.
 #pragma once
 
 #include "q4_attend.h"

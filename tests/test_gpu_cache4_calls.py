@@ -394,3 +394,23 @@ def test_what_is_not_finite_in_long_chunks(dt):
     none = none.cuda()
     assert torch.equal(got.isnan(), none)
     check(torch.where(none, 0, got), torch.where(none, 0, ref), torch.where(none, 0, tol))
+
+
+@pytest.mark.parametrize("news,lens", [([1, 1], [900, 1300]), ([40, 30], [900, 1300]), ([700, 800], [1600, 2300])])
+@pytest.mark.parametrize("ps", [16, 7])
+def test_pages_between_sinks_and_window_are_not_named(news, lens, ps):
+    """Entries of pages that no token sees name nothing, and the page that is read in their stead holds NaN."""
+    H, kv, D, window, sinks = 8, 2, 64, 200, 9
+    announce(f"attend4 pages not named news={news} ps={ps}")
+    for dt in (F16, BF16):
+        q, cache, starts, lengths, table = make(dt, H, kv, D, 32, ps, news, lens, seed=6)
+        k, v = (rows_of(x, table, lens) for x in pools(cache))
+        spare = cache.pages - 1
+        free = [p for p in range(cache.pages) if not (table == p).any()][0]
+        cache.copy_pages(torch.tensor([spare], device="cuda"), torch.tensor([free], device="cuda"))
+        table[table == spare] = free
+        cache.k_scale[spare], cache.v_scale[spare] = math.nan, math.nan
+        for b, (n, m) in enumerate(zip(news, lens)):
+            table[b, -(-sinks // ps):max(m - n - window + 1, 0) // ps] = -1
+        got = cache.attend(q, starts, lengths, table, window=window, sinks=sinks)
+        check(got, *attention(q, k, v, news, lens, window, sinks, None, F16))
