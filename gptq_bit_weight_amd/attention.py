@@ -443,7 +443,7 @@ class _Paged:
         os_ = out.stride()
         need = self._need.get(H) or self._workspace_bytes(H)
         if self._four and T * H > 256 * self.kv_heads * B:       # (chunks that may be long)
-            need = load_library().q4_attend4_workspace_for(self._ref, H, T, B, width)
+            need = max(need, self._chunk_bytes(H, T, B, width))
         # (under capture the call's own: a graph may replay beside other work of the
         # stream it was captured on)
         ws = _Workspace() if _capturing(dev, stream) else _workspace(dev, stream)
@@ -461,6 +461,12 @@ class _Paged:
         if written:
             _wrote((out,))
         return out
+
+    def _chunk_bytes(self, *sizes):
+        if _device() == self.device.index:
+            return load_library().q4_attend4_workspace_for(self._ref, *sizes)
+        with torch.cuda.device(self.device):
+            return load_library().q4_attend4_workspace_for(self._ref, *sizes)
 
     def _workspace_bytes(self, heads):
         with torch.cuda.device(self.device):
