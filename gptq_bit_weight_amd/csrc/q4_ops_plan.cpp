@@ -83,4 +83,13 @@ extern "C" q4_status q4_rotary_plan(int dim, int rot, int scaling, double base, 
     return Q4_OK;
 }
 
-extern "C" q4_status q4_check_cache4(const q4_cache4* c) { return q4::check_cache4(c, "q4_check_cache4"); }
+extern "C" q4_status q4_check_cache4(const q4_cache4* c)
+{
+    const char* who = "q4_check_cache4";
+    if (q4_status st = q4::check_cache4(c, who); st != Q4_OK) return st;
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < i; ++j)
+            if (q4::meet(q4::cache4_view(c, i & 1, i & 2), q4::cache4_view(c, j & 1, j & 2)))
+                return q4::fail(Q4_ERR_INVALID_ARG, "%s: keys, values and their scales overlap", who);
+    return Q4_OK;
+}

@@ -624,7 +624,8 @@ typedef struct {
     int pages, kv_heads, page_size, dim, group;
 } q4_cache4;
 
-/* The checks of a cache held in 4 bits that need no device. */
+/* The checks of a cache held in 4 bits that need no device, and, what the calls themselves do not
+ * look at, that codes and scales do not overlap each other. */
 q4_status q4_check_cache4(const q4_cache4* c);
 
 /*

@@ -221,3 +221,14 @@ def test_python_refuses_before_the_gpu():
     for a in ((2, 1, 16, 33), (2, 1, 16, 0), (2, 1, 16, 48)):
         with pytest.raises(ValueError):
             q4.PagedCache4.empty(*a, device="cpu")
+
+
+@pytest.mark.parametrize("cache,meets", [
+    (dict(v=1 << 20), True), (dict(v=(1 << 20) + 16), True), (dict(k_scale=2 << 20), True), (dict(v_scale=(3 << 20) + 4), True),
+    (dict(v=(1 << 20) + 4096), False), (dict(v_scale=(3 << 20) + 1024), False),
+    # rows of keys and of values in turn
+    (dict(k_stride=(2048, 1024, 64), v_stride=(2048, 1024, 64), v=(1 << 20) + 32), False),
+    (dict(k_stride=(2048, 1024, 64), v_stride=(2048, 1024, 64), v=(1 << 20) + 16), True)])
+def test_tensors_that_overlap(cache, meets):
+    lib = q4.load_library()
+    assert lib.q4_check_cache4(ctypes.byref(_cache(**cache))) == (1 if meets else 0)

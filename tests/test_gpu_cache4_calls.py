@@ -414,3 +414,13 @@ def test_pages_between_sinks_and_window_are_not_named(news, lens, ps):
             table[b, -(-sinks // ps):max(m - n - window + 1, 0) // ps] = -1
         got = cache.attend(q, starts, lengths, table, window=window, sinks=sinks)
         check(got, *attention(q, k, v, news, lens, window, sinks, None, F16))
+
+
+def test_a_cache_of_one_tensor_twice():
+    import gptq_bit_weight_amd as q4
+    announce("cache4 of one tensor twice")
+    c = q4.PagedCache4.empty(3, 2, 16, 64)
+    with pytest.raises(ValueError, match="overlap"):
+        q4.PagedCache4(c.k, c.k, c.k_scale, c.v_scale)
+    with pytest.raises(ValueError, match="overlap"):
+        q4.PagedCache4(c.k, c.v, c.v_scale, c.v_scale)
