@@ -57,7 +57,7 @@ struct Args {
     int ks2, vs2;                          // row strides, bytes
     int T, B, KV, g;                       // tokens, requests, cached heads, heads of a group
     int dim, chunks;                       // values of a head and its 16-byte pieces
-    int pages, page_size, table_stride, max_len, window, sinks;   // (no sinks without a window)
+    int pages, page_size, table_stride, max_len, window;
     float scale;                           // on the scores, times log2 e; positive
     uint32_t q_and, q_xor;                 // on two of q's values: a scale of 0 clears them, a negative one turns them
     int store8;                            // 8-byte stores reach every output row
@@ -67,7 +67,8 @@ struct Args {
     int workers, least;                    // workgroups, and least tiles of one
     int unsplit;                           // many rows: no row tile has more than `least` tiles
     q4::FastDiv div_g, div_page;           // by heads of a group; by rows of a page (or 16-row blocks of one)
-    // (4 bits; last, as the other kernels do not read them)
+    // (last, as not all kernels read them)
+    int sinks;                             // none without a window
     Side k4, v4;                           // 4 bits, in place of k, v and their strides
     int group_shift;                       // log2 of the values that share a scale
 };
