@@ -729,7 +729,8 @@ size_t q4_pages_workspace(int requests, int pages);
  * them where its last one does not suffice, in the order of the requests, and slots[t] is where
  * token t goes (as q4_cache_append takes it). A request whose table row is too short gets
  * nothing; one that the free pages do not suffice for gets nothing either, nor does any after it
- * that needs some: lengths stay, slots are -1.
+ * that needs some: lengths stay, slots are -1. (One that needs none is served. Tokens without a slot are not
+ * in the cache: the caller leaves them out of what follows, q4_attend would take them for its last ones.)
  */
 q4_status q4_pages_extend(const q4_pages* pages, const int32_t* starts, int tokens, int32_t* slots, hipStream_t stream);
 

@@ -26,7 +26,7 @@ class Sim:
                 continue
             more = -(-new // self.ps) - self.need(r)
             at += more
-            if n == 0 or at > len(free):
+            if n == 0 or (more and at > len(free)):
                 continue
             first = self.need(r)
             for e in range(more):
