@@ -251,7 +251,7 @@ __global__ __launch_bounds__(64 * WV, D == 256 ? 2 : 3) void q4_attend4_rows_ker
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) top = max(top, largest_bf16(qf[ks]));
                 const float most = max_quarters(bitcast<float>(top));
-                scale *= halve_range(most);
+                scale = row_scale(scale, most);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) qf[ks] = bf16_to_f16(qf[ks], most);
             }

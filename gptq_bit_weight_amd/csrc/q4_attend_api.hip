@@ -3,6 +3,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <limits>
 
 #include "q4_attend.h"
 #include "q4_cache4_host.h"
@@ -170,7 +171,8 @@ q4_status attend(const char* who, q4attend::Args& p, const View* caches, int nca
     p.window = a.window >= p.max_len ? 0 : a.window;
     p.sinks = p.window ? std::min(a.sinks, p.max_len) : 0;
     // (a negative scale turns q's signs, a scale of zero clears q)
-    p.scale = a.scale == 0.f ? 1.f : std::fabs(a.scale) * 1.4426950408889634f;
+    // (finite with log2 e too: infinity times a score of 0 would be NaN)
+    p.scale = a.scale == 0.f ? 1.f : std::min(std::fabs(a.scale) * 1.4426950408889634f, std::numeric_limits<float>::max());
     p.q_and = a.scale == 0.f ? 0u : ~0u;
     p.q_xor = a.scale < 0.f ? 0x80008000u : 0u;
     p.store8 = (reinterpret_cast<uintptr_t>(a.out) % 8 == 0) && a.out_token % 4 == 0 && a.out_head % 4 == 0;

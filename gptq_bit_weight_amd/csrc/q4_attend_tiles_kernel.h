@@ -411,7 +411,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) top = max(top, q4cache4::largest_bf16(qf[ks]));
             const float most = max_halves(bitcast<float>(top));
-            scale *= q4cache4::halve_range(most);
+            scale = q4cache4::row_scale(scale, most);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) qf[ks] = q4cache4::bf16_to_f16(qf[ks], most);
         }

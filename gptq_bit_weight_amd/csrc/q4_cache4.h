@@ -93,6 +93,12 @@ __device__ __forceinline__ uint32_t largest_bf16(u4 x)
 }
 __device__ __forceinline__ uint32_t exponent_of(float most) { return min(max(bitcast<uint32_t>(most) >> 23 & 255u, 15u), 254u); }
 __device__ __forceinline__ float halve_range(float most) { return bitcast<float>((exponent_of(most) - 14u) << 23); }
+// The scores' factor with that inverse, held within fp32's range: at 0 a masked score of -inf would
+// be NaN, and at infinity one of 0. (Scores under the least factor are all 0 to what a weight is rounded to.)
+__device__ __forceinline__ float row_scale(float scale, float most)
+{
+    return fminf(fmaxf(scale * halve_range(most), 1.1754943508222875e-38f), 3.4028234663852886e38f);
+}
 __device__ __forceinline__ u4 bf16_to_f16(u4 x, float most)
 {
     const float f = bitcast<float>((268u - exponent_of(most)) << 23);
