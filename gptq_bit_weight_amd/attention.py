@@ -441,15 +441,17 @@ class _Paged:
         if ts < width:
             table, ts = _table_rows(table, stream)
         os_ = out.stride()
-        need = self._need.get(H) or self._workspace_bytes(H)
+        need = want = self._need.get(H) or self._workspace_bytes(H)
         if self._four and T * H > 256 * self.kv_heads * B:       # (chunks that may be long)
-            need = max(need, self._chunk_bytes(H, T, B, width))
+            want = max(need, self._chunk_bytes(H, T, B, width))
+            if want >= _refused.get(dev.index, want + 1):
+                want = need
         # (under capture the call's own: a graph may replay beside other work of the
         # stream it was captured on)
         ws = _Workspace() if _capturing(dev, stream) else _workspace(dev, stream)
         with ws.lock:
-            if ws.bytes < need:
-                ws.hold(_on(stream, _new_workspace, need, dev))
+            if ws.bytes < want:
+                ws.grow(need, want, stream, dev)
             four = self._four
             what = "q4_attend4" if four else "q4_attend_ex" if sinks else "q4_attend"
             _call(getattr(load_library(), what), what, dev, stream,
@@ -602,8 +604,20 @@ class _Workspace:
     def hold(self, memory):
         self.at, self.bytes, self.memory = memory.data_ptr(), memory.numel(), memory
 
+    def grow(self, need, want, stream, device):
+        """At least `need` bytes, `want` where there is memory for them."""
+        if want > need:
+            try:
+                return self.hold(_on(stream, _new_workspace, want, device))
+            except torch.cuda.OutOfMemoryError:
+                # (not asked for again: each attempt empties the allocator's cache and waits for the device)
+                _refused[device.index] = min(want, _refused.get(device.index, want))
+        if self.bytes < need:
+            self.hold(_on(stream, _new_workspace, need, device))
+
 
 _workspaces: dict = {}      # (device, stream) -> its _Workspace
+_refused: dict = {}         # device -> least bytes beyond its need that a call found no memory for
 
 
 def _workspace(device, stream):
