@@ -58,7 +58,7 @@ def test_no_memory_for_the_scratch(dt, little_memory):
         y = cache.attend(*args, stream=s)
         s.synchronize()
         check(y, *want)
-    # a short call before and after goes on as ever
+    # a short call on that stream
     short = (args[0][:3], torch.tensor([0, 3], dtype=torch.int32, device="cuda")) + args[2:]
     torch.cuda.synchronize()
     a = cache.attend(*short, stream=s)
@@ -81,3 +81,22 @@ def test_a_size_without_memory_is_asked_for_once(little_memory, monkeypatch):
         s.synchronize()
         check(y, *want)
     assert len([n for n in asked if n > 512 << 20]) == 1
+
+
+def test_a_large_scratch_is_not_held():
+    """After the call its memory is the allocator's again; what a stream holds is 64 MiB more than any call needs, at most."""
+    import gptq_bit_weight_amd as q4
+    announce("attend4 long chunk: what a stream holds after it")
+    args, cache, want = wide_call(BF16, 3)
+    least = q4.load_library().q4_attend4_workspace(cache._ref, 32)
+    narrow = args[:3] + (args[3][:, :2048 // 16].contiguous(),)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    for call in (args, narrow, args, narrow):
+        before = torch.cuda.memory_allocated()
+        y = cache.attend(*call, stream=s)
+        s.synchronize()
+        check(y, *want)
+        del y
+        assert torch.cuda.memory_allocated() - before <= (least if call is args else least + (64 << 20)) + 4096
