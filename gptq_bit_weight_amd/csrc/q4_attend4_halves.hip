@@ -39,10 +39,12 @@ __global__ __launch_bounds__(UT) void q4_attend4_unpack_kernel(Args p, Unpack u)
     if (block == 0 && side == 0 && threadIdx.x == 0) u.table[b] = b;
     const Request r = request(p, b);
     if (r.n == 0) return;
-    // (the blocks of 16 rows that the kernel reads: the sinks', and from the first visible key's on)
+    // (the blocks of 16 rows that the kernel reads: the sinks', and from the first visible key's on. What no
+    // token sees in them holds that key's row: its own page may be another request's, or none)
     const int row0 = UR * block, last = max(r.len - 1, 0);
-    const int lo = p.window ? min(max(r.len - r.n - p.window + 1, 0), last) & ~15 : 0;
-    if (row0 > last || (row0 + UR <= lo && row0 >= ((p.sinks + 15) & ~15))) return;
+    const int lo = p.window ? min(max(r.len - r.n - p.window + 1, 0), last) : 0;
+    const int sink_rows = (p.sinks + 15) & ~15, window_row0 = lo & ~15;
+    if (row0 > last || (row0 + UR <= window_row0 && row0 >= sink_rows)) return;
     const Side& c = values ? p.v4 : p.k4;
     uint16_t* to = u.to + (((values ? (long long)p.B : 0) + b) * p.KV + head) * ((long long)u.rows * p.dim);
     const int total = UR * u.pieces;
@@ -55,7 +57,7 @@ __global__ __launch_bounds__(UT) void q4_attend4_unpack_kernel(Args p, Unpack u)
             const int x = (int)q4::fast_div((uint32_t)i, u.div_pieces);
             piece[e] = i - x * u.pieces;
             row[e] = row0 + x;
-            const int key = min(row[e], last), slot = (int)q4::fast_div((uint32_t)key, p.div_page);
+            const int key = min(row[e] < p.sinks ? row[e] : max(row[e], lo), last), slot = (int)q4::fast_div((uint32_t)key, p.div_page);
             const long long page = min((uint32_t)p.table[(long long)b * p.table_stride + slot], (uint32_t)p.pages - 1u);
             const long long in = key - slot * p.page_size;
             code[e] = *reinterpret_cast<const uint32_t*>(c.at + head * c.head + page * c.page + in * c.row + 4 * piece[e]);
@@ -64,7 +66,7 @@ __global__ __launch_bounds__(UT) void q4_attend4_unpack_kernel(Args p, Unpack u)
         }
 #pragma unroll
         for (int e = 0; e < kEach; ++e)
-            if (base + e * UT < total && row[e] <= last)
+            if (base + e * UT < total && row[e] <= last && (row[e] < sink_rows || row[e] >= window_row0))
                 *reinterpret_cast<u4*>(to + (long long)row[e] * p.dim + 8 * piece[e]) =
                     own_order(values8(code[e], low_half(scale[e]), high_half(scale[e]), magic()));
     }
