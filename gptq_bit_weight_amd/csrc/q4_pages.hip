@@ -486,6 +486,43 @@ q4_status check_pages(const q4_pages* b, const char* who)
     return Q4_OK;
 }
 
+// The books' arrays, all of which calls write (work as the scratch).
+constexpr int kArrays = 4;
+q4::View array_view(const q4_pages* b, int i)
+{
+    switch (i) {
+    case 0: return q4::flat_view(b->table, (int64_t)b->requests * b->width * 4);
+    case 1: return q4::flat_view(b->lengths, (int64_t)b->requests * 4);
+    case 2: return q4::flat_view(b->counts, (int64_t)b->pages * 4);
+    default: return q4::flat_view(b->work, (int64_t)q4_pages_workspace(b->requests, b->pages));
+    }
+}
+
+// The books lie apart from each other and from the cache (which calls with a pool write).
+q4_status check_apart(const q4_pages* b, const q4_pool* pool, const char* who)
+{
+    for (int i = 0; i < kArrays; ++i) {
+        const q4::View v = array_view(b, i);
+        for (int j = 0; j < i; ++j)
+            if (q4::meet(v, array_view(b, j))) return q4::fail(Q4_ERR_INVALID_ARG, "%s: table, lengths, counts and work overlap", who);
+        for (int j = 0; pool && j < pool->planes; ++j)
+            if (q4::meet(v, plane_view(pool, j))) return q4::fail(Q4_ERR_INVALID_ARG, "%s: the books overlap the cache", who);
+    }
+    return Q4_OK;
+}
+
+// An index or an output lies apart from the books, the cache and `other`.
+q4_status check_apart(const q4::View& v, const char* what, const q4_pages* b, const q4_pool* pool, const q4::View* other, const char* who)
+{
+    for (int i = 0; i < kArrays; ++i)
+        if (q4::meet(v, array_view(b, i))) return q4::fail(Q4_ERR_INVALID_ARG, "%s: %s overlaps the books", who, what);
+    for (int i = 0; pool && i < pool->planes; ++i)
+        if (q4::meet(v, plane_view(pool, i))) return q4::fail(Q4_ERR_INVALID_ARG, "%s: %s overlaps the cache", who, what);
+    return other && q4::meet(v, *other) ? q4::fail(Q4_ERR_INVALID_ARG, "%s: %s overlaps the output", who, what) : Q4_OK;
+}
+
+q4::View index_view(const void* p, int bits, int n) { return q4::flat_view(p, (int64_t)n * bits / 8); }
+
 Books books_of(const q4_pages* x)
 {
     Books b = {};
@@ -564,6 +601,10 @@ q4_status q4_pages_extend(const q4_pages* pages, const int32_t* starts, int toke
     if (tokens == 0) return Q4_OK;
     if (tokens > (1 << 30)) return q4::fail(Q4_ERR_UNSUPPORTED, "%s: %d tokens", who, tokens);
     if (!starts || !slots) return q4::fail(Q4_ERR_INVALID_ARG, "%s: null pointer", who);
+    const q4::View to = q4::flat_view(slots, (int64_t)tokens * 4), from = q4::flat_view(starts, ((int64_t)pages->requests + 1) * 4);
+    if (q4_status st = check_apart(pages, nullptr, who); st != Q4_OK) return st;
+    if (q4_status st = check_apart(to, "slots", pages, nullptr, nullptr, who); st != Q4_OK) return st;
+    if (q4_status st = check_apart(from, "starts", pages, nullptr, &to, who); st != Q4_OK) return st;
     hipLaunchKernelGGL(q4_pages_extend_kernel, dim3(1), dim3(PT), 0, stream, books_of(pages), starts, tokens, slots);
     return launched(who);
 }
@@ -580,6 +621,11 @@ q4_status q4_pages_fork(const q4_pages* pages, const q4_pool* pool, const void* 
     if (q4_status st = check_index(children, child_bits, n, who); st != Q4_OK) return st;
     if (n == 0) return Q4_OK;
     if (!done) return q4::fail(Q4_ERR_INVALID_ARG, "%s: null pointer", who);
+    const q4::View to = q4::flat_view(done, (int64_t)n * 8);
+    if (q4_status st = check_apart(pages, pool, who); st != Q4_OK) return st;
+    if (q4_status st = check_apart(to, "done", pages, pool, nullptr, who); st != Q4_OK) return st;
+    if (q4_status st = check_apart(index_view(parents, parent_bits, n), "parents", pages, pool, &to, who); st != Q4_OK) return st;
+    if (q4_status st = check_apart(index_view(children, child_bits, n), "children", pages, pool, &to, who); st != Q4_OK) return st;
     const CopyArgs p = copy_args(pool);
     if (q4_status st = pieces_fit(p, n, who); st != Q4_OK) return st;
     const Books b = books_of(pages);
@@ -599,6 +645,8 @@ q4_status q4_pages_free(const q4_pages* pages, const void* requests, int bits, i
     if (n < 0) return q4::fail(Q4_ERR_INVALID_ARG, "%s: negative size", who);
     if (q4_status st = check_index(requests, bits, n, who); st != Q4_OK) return st;
     if (n == 0) return Q4_OK;
+    if (q4_status st = check_apart(pages, nullptr, who); st != Q4_OK) return st;
+    if (q4_status st = check_apart(index_view(requests, bits, n), "requests", pages, nullptr, nullptr, who); st != Q4_OK) return st;
     hipLaunchKernelGGL(q4_pages_free_kernel, dim3(n < kCopyGrid ? n : kCopyGrid), dim3(CT), 0, stream, books_of(pages), requests, bits == 64, n);
     return launched(who);
 }
@@ -608,6 +656,7 @@ q4_status q4_pages_trim(const q4_pages* pages, int window, int sinks, hipStream_
     const char* who = "q4_pages_trim";
     if (q4_status st = check_pages(pages, who); st != Q4_OK) return st;
     if (window < 1 || sinks < 0) return q4::fail(Q4_ERR_INVALID_ARG, "%s: window %d, %d sinks", who, window, sinks);
+    if (q4_status st = check_apart(pages, nullptr, who); st != Q4_OK) return st;
     hipLaunchKernelGGL(q4_pages_trim_kernel, dim3(pages->requests < kCopyGrid ? pages->requests : kCopyGrid), dim3(CT), 0, stream,
                        books_of(pages), window, sinks);
     return launched(who);
@@ -620,6 +669,8 @@ q4_status q4_pages_compact(const q4_pages* pages, const q4_pool* pool, int32_t* 
     if (q4_status st = check_pool(pool, who); st != Q4_OK) return st;
     if (pool->pages != pages->pages) return q4::fail(Q4_ERR_INVALID_ARG, "%s: %d pages, the pool has %d", who, pages->pages, pool->pages);
     if (!to) return q4::fail(Q4_ERR_INVALID_ARG, "%s: null pointer", who);
+    if (q4_status st = check_apart(pages, pool, who); st != Q4_OK) return st;
+    if (q4_status st = check_apart(q4::flat_view(to, (int64_t)pages->pages * 4), "to", pages, pool, nullptr, who); st != Q4_OK) return st;
     CopyArgs p = copy_args(pool);
     if (q4_status st = pieces_fit(p, pool->pages, who); st != Q4_OK) return st;
     const Books b = books_of(pages);

@@ -711,7 +711,8 @@ q4_status q4_copy_pages(const q4_pool* pool, const void* src, int src_bits, cons
  * those entries that name page p; a page whose count is not positive is free. work is
  * scratch of q4_pages_workspace(requests, pages) bytes; calls that share the arrays are ordered
  * on one stream. Nothing waits for the device, every call may be captured, and results do
- * not depend on the order in which anything runs.
+ * not depend on the order in which anything runs. The arrays, a call's indexes and its output must
+ * not overlap each other or the cache (Q4_ERR_INVALID_ARG; indexes may overlap indexes).
  */
 typedef struct {
     int32_t* table;
