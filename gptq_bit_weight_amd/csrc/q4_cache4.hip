@@ -41,6 +41,9 @@ using namespace q4cache4;
 constexpr int NT = 256;
 constexpr int kMaxTokens = 4;     // tokens of a workgroup
 constexpr int kUnits = 4;         // units of queries that a lane has in flight
+// Tokens of a launch: 2^32 lanes and more (of 3 workgroups for 4 tokens) are a launch of their number modulo 2^32, without an error.
+constexpr int kMostTokens = 1 << 24;
+static_assert(3LL * kMostTokens / kMaxTokens * NT < 1LL << 32, "lanes of a launch");
 
 // Keys or values of the cache: strides in bytes.
 struct Plane {
@@ -416,7 +419,6 @@ q4_status q4_cache4_append(const q4_cache4* c, const uint16_t* k, int64_t k_toke
         p.magnitude = r->magnitude;
         p.n = r->rot / 2;
         p.rot = r->rot;
-        p.positions = positions;
         p.positions64 = position_bits == 64;
         wide = mult8(r->rot) && (r->interleaved || mult8(r->rot / 2));
     }
@@ -435,10 +437,8 @@ q4_status q4_cache4_append(const q4_cache4* c, const uint16_t* k, int64_t k_toke
             q4::meet(to, q4::flat_view(positions, (int64_t)tokens * position_bits / 8)))
             return q4::fail(Q4_ERR_INVALID_ARG, "%s: q_out overlaps slots or positions", who);
         p.H = heads;
-        p.q = q;
         p.q_t = (uint32_t)q_token;
         p.q_h = (uint32_t)q_head;
-        p.q_out = q_out;
         p.o_t = (uint32_t)out_token;
         p.o_h = (uint32_t)out_head;
         wide = wide && at16(q) && at16(q_out) && mult8(q_token) && mult8(q_head) && mult8(out_token) && mult8(out_head);
@@ -449,17 +449,14 @@ q4_status q4_cache4_append(const q4_cache4* c, const uint16_t* k, int64_t k_toke
     p.dim = c->dim;
     p.KV = c->kv_heads;
     p.T = tokens;
-    p.k = k;
     p.k_t = (uint32_t)k_token;
     p.k_h = (uint32_t)k_head;
-    p.v = v;
     p.v_t = (uint32_t)v_token;
     p.v_h = (uint32_t)v_head;
     p.kc = plane_of(c, false);
     p.vc = plane_of(c, true);
     p.group_lanes = c->group / 8;
     p.group_shift = log2_of(c->group);
-    p.slots = slots;
     p.slots64 = slot_bits == 64;
     p.page_size = c->page_size;
     p.capacity = c->pages * c->page_size;
@@ -478,11 +475,20 @@ q4_status q4_cache4_append(const q4_cache4* c, const uint16_t* k, int64_t k_toke
     p.div_units = q4::make_fastdiv((uint32_t)p.units);
     p.div_ps = q4::make_fastdiv((uint32_t)p.page_size);
     p.div_n = q4::make_fastdiv((uint32_t)(p.n > 0 ? p.n : 1));
-    p.groups = (p.T + p.TB - 1) / p.TB;
-    const dim3 grid((p.H ? 3u : 2u) * (unsigned)p.groups, few ? slices : 1);
     const size_t lds = (size_t)p.TB * place64(p.n) * sizeof(double2);
-    if (wide) il ? launch_append<true, true>(p, grid, lds, bf16 != 0, stream) : launch_append<true, false>(p, grid, lds, bf16 != 0, stream);
-    else il ? launch_append<false, true>(p, grid, lds, bf16 != 0, stream) : launch_append<false, false>(p, grid, lds, bf16 != 0, stream);
+    for (int t = 0; t < tokens; t += std::min(tokens - t, kMostTokens)) {
+        p.T = std::min(tokens - t, kMostTokens);
+        p.q = q ? q + t * q_token : nullptr;
+        p.q_out = q ? q_out + t * out_token : nullptr;
+        p.k = k + t * k_token;
+        p.v = v + t * v_token;
+        p.slots = static_cast<const char*>(slots) + (int64_t)t * (slot_bits / 8);
+        p.positions = r ? static_cast<const char*>(positions) + (int64_t)t * (position_bits / 8) : nullptr;
+        p.groups = (p.T + p.TB - 1) / p.TB;
+        const dim3 grid((p.H ? 3u : 2u) * (unsigned)p.groups, few ? slices : 1);
+        if (wide) il ? launch_append<true, true>(p, grid, lds, bf16 != 0, stream) : launch_append<true, false>(p, grid, lds, bf16 != 0, stream);
+        else il ? launch_append<false, true>(p, grid, lds, bf16 != 0, stream) : launch_append<false, false>(p, grid, lds, bf16 != 0, stream);
+    }
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? Q4_OK : q4::fail(Q4_ERR_HIP, "%s: %s", who, hipGetErrorString(e));
 }
