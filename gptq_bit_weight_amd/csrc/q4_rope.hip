@@ -22,6 +22,7 @@
 // and rotates in fp32, rounded once.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <new>
 
 #include "q4_device.h"
@@ -36,6 +37,9 @@ using namespace q4dev;
 constexpr int NT = 256;
 constexpr int kMaxTokens = 4;     // tokens of a workgroup
 constexpr int kUnits = 4;         // units a lane has in flight
+// Tokens of a launch: 2^32 lanes and more are a launch of their number modulo 2^32, without an error.
+constexpr int kMostTokens = 1 << 25;
+static_assert((long long)kMostTokens / kMaxTokens * NT < 1LL << 32, "lanes of a launch");
 
 struct RopeArgs {
     const uint64_t* turns;
@@ -200,10 +204,23 @@ hipError_t launch(RopeArgs& p, bool interleaved, bool wide, bool bf16, hipStream
     p.div_lpv = q4::make_fastdiv((uint32_t)p.lpv);
     p.div_n = q4::make_fastdiv((uint32_t)(p.n > 0 ? p.n : 1));
     p.div_ps = q4::make_fastdiv((uint32_t)(p.page_size > 0 ? p.page_size : 1));
-    const dim3 grid((p.T + p.TB - 1) / p.TB, few ? slices : 1);
     const size_t lds = (size_t)p.TB * (p.n > 0 ? p.n : 1) * sizeof(float2);
-    if (wide) return interleaved ? launch_v<8, true>(p, grid, lds, bf16, stream) : launch_v<8, false>(p, grid, lds, bf16, stream);
-    return interleaved ? launch_v<1, true>(p, grid, lds, bf16, stream) : launch_v<1, false>(p, grid, lds, bf16, stream);
+    for (int left = p.T;;) {
+        p.T = std::min(left, kMostTokens);
+        const dim3 grid((p.T + p.TB - 1) / p.TB, few ? slices : 1);
+        hipError_t e;
+        if (wide) e = interleaved ? launch_v<8, true>(p, grid, lds, bf16, stream) : launch_v<8, false>(p, grid, lds, bf16, stream);
+        else e = interleaved ? launch_v<1, true>(p, grid, lds, bf16, stream) : launch_v<1, false>(p, grid, lds, bf16, stream);
+        if (e != hipSuccess || (left -= p.T) == 0) return e;
+        auto on = [&](auto*& at, long long stride) { at = at ? at + p.T * stride : at; };
+        on(p.q, p.q_t);
+        on(p.q_out, p.o_t);
+        on(p.k, p.k_t);
+        on(p.v, p.v_t);
+        auto on_index = [&](const void*& at, int wide) { at = at ? static_cast<const char*>(at) + (long long)p.T * (wide ? 8 : 4) : at; };
+        on_index(p.positions, p.positions64);
+        on_index(p.slots, p.slots64);
+    }
 }
 
 bool mult8(long long a) { return a % 8 == 0; }
