@@ -214,8 +214,11 @@ q4_status attend(const char* who, q4attend::Args& p, const View* caches, int nca
     p.counters = static_cast<uint32_t*>(a.workspace);
     p.joins = reinterpret_cast<q4attend::JoinList*>(static_cast<char*>(a.workspace) + kListAt);
     p.slots = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kCounterBytes);
-    // (most units there can be: a whole one each share of the work, a partial one each row tile and head)
+    // (most units there can be: a whole one each share of the work, a partial one each row tile and head. They are workgroups
+    // of 256 lanes, and 2^32 lanes and more HIP launches modulo 2^32, without an error)
     const int units = (int)(row_tiles * p.KV + p.workers);
+    if (many && units >= 1 << 24)
+        return fail(Q4_ERR_UNSUPPORTED, "%s: %d units of 128 rows of a request and cached head, 2^24 and more", who, units);
     hipError_t e;
     const size_t halves = a.four && many ? halves_bytes(p.KV, p.dim, g, a.tokens, a.requests, p.max_len) : 0;
     if (halves && a.workspace_bytes >= need + halves)
