@@ -33,7 +33,12 @@ class Pages:
     (tokens in the cache, as attend() takes them) and `counts` int32 [pages], how many
     entries of requests name a page (0: it is free). The tensors may be read, and
     written by who keeps them in step. All calls are asynchronous, may be captured, and
-    belong on one stream at a time."""
+    belong on one stream at a time.
+
+    fork() and compact() copy pages of `cache` alone. Layers that share one table are
+    therefore heads of one pool: k [pages, layers * kv heads, page size, dim], of which
+    layer l appends to and attends over a cache of the slice k[:, l * kv:(l + 1) * kv],
+    and Pages gets the cache over all of it."""
 
     def __init__(self, cache, requests: int, width: int):
         if not isinstance(cache, _Paged):
