@@ -404,7 +404,9 @@ class _Paged:
         only the last `window` of them and the request's first `sinks`; one that
         sees none gives zeros. heads is a multiple of the cached heads, scale
         defaults to dim ** -0.5. Lengths stay on the device; nothing waits for
-        it. No gradient goes through it. Several threads may call at once, on one
+        it. One kernel is chosen for the call, by its tokens a request on average, those
+        without tokens among them: a long chunk is called with its own rows of a
+        table of many requests (table[b:b + 1], lengths[b:b + 1]). No gradient goes through it. Several threads may call at once, on one
         stream too."""
         dev, dt = self.device, self.dtype
         (T, H, D), qs = _heads(q, "q", dev, dt, None, None, self.dim)

@@ -8,7 +8,7 @@
 // The cache stands for binary16 values v = RNE(s c + m) (q4_cache4.h), which one packed
 // multiply-add makes of two codes, so the products are those of a binary16 cache whatever
 // the queries' type; queries of bfloat16 are brought into binary16's range by a power of two a
-// row, which the scores are multiplied by again: exact but for values below 2^-32 of the row's largest.
+// row, which the scores are multiplied by again: exact but for values below 2^-31 of the row's largest.
 //
 // Bound: HBM, with the vector instructions that unpack close behind: a 32-key tile of a head of
 // 128 is 4 KiB of codes and up to 1 KiB of scales, and takes a wave some 300 vector instructions

@@ -33,10 +33,12 @@
 // tile's splits leave partial results and its first one an entry in a list, which
 // a second launch goes through.
 //
-// Over 4 bits the tiles in LDS are of binary16: each wave makes its 16 rows of them out of the
-// codes, one packed multiply-add for two values, in the steps between the products, so the products
+// Over 4 bits the tiles in LDS are of binary16: each wave makes its KT / NW rows of them out of the
+// codes, one packed multiply-add for two values, so the products
 // are those of a binary16 cache whatever the queries' type (bfloat16 queries brought into binary16's
-// range by a power of two a row). The unpacking is some 126 vector instructions a wave and 64-key tile beside
+// range by a power of two a row). Codes and scales are asked for at a step's start (by direct loads into LDS
+// for heads of 128, into registers for the others), waited for at its end, all of them, and unpacked there into
+// the stage that they are for: only the step's own products stand between a load and its use. The unpacking is some 126 vector instructions a wave and 64-key tile beside
 // the 950: 2048 new tokens over 8192 keys, 32 heads of 128 over 8, 290 us, 830 TFLOP/s, of
 // which 5 join; over tiles that were unpacked once before (q4_attend4_halves.hip) 265 with the unpacking.
 #pragma once
@@ -500,7 +502,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void q4_attend_tiles_ker
     // i - 1 read last; those that step i + 1 reads have landed at the end of step
     // i, the newer ones stay under way. (A load's latency is longer than a step, 1.7
     // to 2 us against 1: with two stages every step took that. Past the last tile the
-    // loads repeat it, so that the count of those under way holds.)
+    // loads repeat it, so that the count of those under way holds.) Over 4 bits no load stays under way from one
+    // step to the next: what is fetched in step i is in its stage at the end of it.
     auto step = [&](auto par, int i, f16x (&cur)[HH], f16x (&nxt)[HH]) {
         constexpr int ST = decltype(par)::value;      // i % NS
         const int j = j0 + i;

@@ -580,7 +580,8 @@ size_t q4_attend_workspace(const q4_cache* c, int heads);
  * multiples of 8 values, their base 16-byte aligned. `workspace` is device
  * memory of at least q4_attend_workspace bytes whose first 64 KiB are zero before
  * its first use (each call leaves them fit for the next); calls that share it must not overlap
- * in time. out must not overlap an input (Q4_ERR_INVALID_ARG). Host and device never
+ * in time. out must not overlap an input (Q4_ERR_INVALID_ARG). A call of 2^24 units and more of 128 rows
+ * (token, head of a group) of one request and cached head is refused (Q4_ERR_UNSUPPORTED). Host and device never
  * synchronize; the call may be captured.
  */
 q4_status q4_attend(const q4_cache* c, const uint16_t* q, int64_t q_token, int64_t q_head, int heads, int tokens,
@@ -665,8 +666,8 @@ q4_status q4_cache4_read(const q4_cache4* c, const void* slots, int slot_bits, i
  */
 size_t q4_attend4_workspace(const q4_cache4* c, int heads);
 
-/* The workspace with which a call of these sizes is fastest, at least that of
- * q4_attend4_workspace: chunks of some thousand rows (tokens times heads of a group) a request on average
+/* The workspace with which a call of these sizes is fastest (any from q4_attend4_workspace on will
+ * do), at least that of q4_attend4_workspace: chunks of some thousand rows (tokens times heads of a group) a request on average
  * and more bring the keys and values into binary16 there first, if they take no more than 2^30
  * bytes (2 dim a row and side, of requests * table_width pages). */
 size_t q4_attend4_workspace_for(const q4_cache4* c, int heads, int tokens, int requests, int table_width);
