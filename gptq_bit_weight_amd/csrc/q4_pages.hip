@@ -223,7 +223,8 @@ __global__ __launch_bounds__(PT) void q4_pages_extend_kernel(Books b, const int*
         bool mine = false;
         if (r < b.R) {
             int start;
-            const int n = tokens_of(r, start), len = length_of(b, r), at = b.list_a[r], need = pages_of(b, len + n) - pages_of(b, len);
+            const int n = tokens_of(r, start), len = length_of(b, r), at = b.list_a[r];
+            const int need = at < 0 ? 0 : pages_of(b, len + n) - pages_of(b, len);      // (-1: len + n may not fit in an int)
             // (who needs no page does not wait for those who find none)
             const bool served = n > 0 && at >= 0 && (need == 0 || at + need <= have);
             if (served && n > kFew) many[atomicAdd(&s_many, 1)] = r;
