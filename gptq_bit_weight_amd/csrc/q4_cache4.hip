@@ -11,7 +11,8 @@
 // (x - m) / s in fp32, by the reciprocal, is off by 4 2^-24 of itself at most, 4e-6: a code that it leaves in doubt, within 1e-5
 // of half way between two, is decided in 64 bits (some waves in a hundred). x is of the tokens' 16-bit
 // type, so x - m is exact there and the remainder x - m - n s of a guess n is too: whether it passes half a
-// step. Keys are turned in 64 bits, rounded to fp32 and to the type, and then quantised: a code is the
+// step. (Of bfloat16 values under 2^-29 a difference from a large m is rounded to 53 bits: one within 2^-37 of
+// a tie counts as the tie.) Keys are turned in 64 bits, rounded to fp32 and to the type, and then quantised: a code is the
 // definition's and does not hang on the last bits of fp32. (64-bit instructions run at the
 // rate of 32-bit ones here.) Queries are turned as q4_rope_kernel turns them.
 //
