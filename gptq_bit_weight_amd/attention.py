@@ -406,8 +406,8 @@ class _Paged:
         defaults to dim ** -0.5. Lengths stay on the device; nothing waits for
         it. One kernel is chosen for the call, by its tokens a request on average, those
         without tokens among them: a long chunk is called with its own rows of a
-        table of many requests (table[b:b + 1], lengths[b:b + 1]). No gradient goes through it. Several threads may call at once, on one
-        stream too."""
+        table of many requests (table[b:b + 1], lengths[b:b + 1]). No gradient goes
+        through it. Several threads may call at once, on one stream too."""
         dev, dt = self.device, self.dtype
         (T, H, D), qs = _heads(q, "q", dev, dt, None, None, self.dim)
         dt = q.dtype
@@ -619,7 +619,7 @@ class _Workspace:
 
 
 _workspaces: dict = {}      # (device, stream) -> its _Workspace
-_refused: dict = {}         # device -> least bytes beyond its need that a call found no memory for
+_refused: dict = {}         # device -> least size with scratch that a call found no memory for
 
 
 def _workspace(device, stream):
